@@ -185,6 +185,53 @@ mns_status normuon_scale(void* O, int dtype, int64_t batch, int64_t rows, int64_
                          float* v, float beta2, float eps, void* workspace,
                          size_t workspace_bytes, void* stream);
 
+/* ---- Products grouped by expert -----------------------------------------------------------
+ * The products of a layer of experts and of its gradients, for rows sorted by expert: expert e
+ * owns rows offsets[e] .. offsets[e+1]-1 of the token matrices, and one n x k matrix W_e (or
+ * gradient G_e) of a contiguous [groups][n][k] stack. bfloat16 products are accumulated in
+ * float32 and rounded once; float32 ones run in float32.
+ *   offsets   (device) int64 [groups + 1], non-decreasing, read by the kernels only (no host
+ *             copy, no synchronisation; a captured call reads the values of each replay). Values
+ *             are clamped to 0 .. total_rows and an end below its begin is an empty expert:
+ *             offsets that are not non-decreasing give unspecified values in the outputs, but no
+ *             access outside the buffers.
+ *   Token matrices have a row pitch in elements (>= their width; rows need not be contiguous) and
+ *   need only the alignment of their dtype, as do W and G. 16-byte aligned pointers with widths
+ *   and pitches of whole 16 bytes run faster.
+ *   Sizes: 1 <= groups <= 65536; 0 <= total_rows <= 2^31 - 1 (the token pointers may be NULL when
+ *   it is 0); 1 <= n, k <= 65536, n*k <= 2^31 - 1; pitches <= 2^21; at most 2^31 - 1 output tiles
+ *   of 16 x 64; else MNS_ERR_SHAPE.
+ *   workspace (may be NULL when the size query returns 0) must be 256-byte aligned.
+ *   Rounding: the order of a sum's float32 additions depends on the sizes and the number of CUs
+ *   only, so equal calls give equal bits. */
+
+/* Workspace bytes of grouped_matmul (weight_grad = 0) or grouped_weight_grad (1). */
+mns_status mns_grouped_workspace_size(int weight_grad, int dtype, int64_t groups,
+                                      int64_t total_rows, int64_t n, int64_t k,
+                                      size_t* bytes /* (host) out */);
+
+/* transpose_w = 0: Y_e = X_e W_e^T (the layer's forward; X total_rows x k, Y total_rows x n);
+ * transpose_w = 1: Y_e = X_e W_e (the gradient of its input; X total_rows x n, Y total_rows x k).
+ *   X in, W in, Y out, all of dtype; ldx, ldy: row pitches of X and Y. Y may not overlap X or W.
+ *   fill_rest  0: rows of Y that belong to no expert (before offsets[0], from offsets[groups] on)
+ *              are left as they are; 1: they are written as zeros. */
+mns_status grouped_matmul(const void* X, int64_t ldx, const void* W, void* Y, int64_t ldy,
+                          int dtype, const int64_t* offsets, int64_t groups, int64_t total_rows,
+                          int64_t n, int64_t k, int transpose_w, int fill_rest, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Weight gradients: G_e = beta C_e + dY_e^T X_e, the product summed over the expert's rows (an
+ * expert without rows gets beta C_e).
+ *   dY in  dtype, total_rows x n, pitch lddy;   X in  dtype, total_rows x k, pitch ldx
+ *   C  in  out_dtype [groups][n][k], or NULL (taken as zero); not read when beta is 0
+ *   G  out out_dtype [groups][n][k]; may be C itself, may not overlap it otherwise
+ *   out_dtype  dtype, or MNS_F32 (a float32 momentum: beta = mu gives M <- mu M + dY^T X). */
+mns_status grouped_weight_grad(const void* dY, int64_t lddy, const void* X, int64_t ldx,
+                               int dtype, const int64_t* offsets, int64_t groups,
+                               int64_t total_rows, int64_t n, int64_t k, const void* C, float beta,
+                               void* G, int out_dtype, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
 /* ---- Instrumentation ---------------------------------------------------------------------
  * Between mns_profile_begin() and mns_profile_end() every kernel launch the library makes is
  * bracketed by a pair of hipEvents recorded on the launch's stream. mns_profile_end() waits

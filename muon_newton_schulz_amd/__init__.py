@@ -7,6 +7,7 @@ library must be built (``python -m muon_newton_schulz_amd.build``); there is no 
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Iterable, Sequence
 
@@ -18,6 +19,7 @@ from ._abi import (MNS_BF16, MNS_F32, MNS_NS_GRAM, MNS_NS_STANDARD, MnsError,  #
 
 __all__ = ["muon_step", "ns_orthogonalize", "ns_orthogonalize_noalloc",
            "gram_ns_orthogonalize", "normuon_scale",
+           "grouped_matmul", "grouped_weight_grad",
            "step_workspace_size", "ns_workspace_size", "normuon_workspace_size",
            "restart_mask", "profile_begin", "profile_set_flush", "profile_end", "MnsError",
            "load"]
@@ -311,6 +313,188 @@ def normuon_scale(O: torch.Tensor, v: torch.Tensor, beta2: float = 0.95, eps: fl
                             ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)),
           "normuon_scale")
     return O
+
+
+class _OnStream:
+    """The device of a call's tensors and the stream it runs on (a torch stream, a raw
+    hipStream_t, or None for that device's current stream). Inside the context the device is
+    current and torch allocates on that stream, so an output or workspace made there is not
+    handed out again before the call's kernels are done with it."""
+
+    def __init__(self, device: torch.device, stream):
+        self._ctx = None
+        if stream is None:
+            if device.index != torch.cuda.current_device():
+                self._ctx = torch.cuda.device(device)
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+            return
+        if not hasattr(stream, "cuda_stream"):
+            handle = int(stream)
+            if handle == 0:
+                stream = torch.cuda.default_stream(device)
+            else:
+                stream = torch.cuda.ExternalStream(handle, device=device)
+        elif stream.device != device:
+            raise ValueError(f"stream on {stream.device}, tensors on {device}")
+        self.handle = stream.cuda_stream
+        self._ctx = contextlib.ExitStack()
+        self._ctx.enter_context(torch.cuda.device(device))
+        self._ctx.enter_context(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        if isinstance(self._ctx, torch.cuda.device):
+            self._ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+        return False
+
+
+def _pitch(t: torch.Tensor, name: str, what: str) -> int:
+    """Row pitch of a 2-D tensor whose rows are contiguous and do not overlap."""
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: the rows of {name} must be contiguous")
+    if rows <= 1:
+        return cols
+    if t.stride(0) < cols:
+        raise ValueError(f"{what}: the rows of {name} overlap")
+    return t.stride(0)
+
+
+def _extent(t: torch.Tensor):
+    """First byte and the byte behind the last one a (strided) tensor reaches."""
+    if t.numel() == 0:
+        return 0, 0
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+def _apart(a: torch.Tensor, b: torch.Tensor) -> bool:
+    a0, a1 = _extent(a)
+    b0, b1 = _extent(b)
+    return a1 <= b0 or b1 <= a0
+
+
+def _grouped_checks(tokens, stack, offsets, groups: int, what: str) -> torch.device:
+    for name, t in tokens:
+        if t.dim() != 2:
+            raise ValueError(f"{what}: {name} must be 2-D (rows x width)")
+    if offsets.dim() != 1 or offsets.dtype != torch.int64 or offsets.shape[0] != groups + 1:
+        raise ValueError(f"{what}: offsets must be int64 of shape ({groups + 1},)")
+    if not offsets.is_contiguous():
+        raise ValueError(f"{what}: offsets must be contiguous")
+    return _on_one_gpu([t for _, t in tokens] + list(stack) + [offsets], what)
+
+
+def _grouped_workspace(weight_grad: int, code: int, groups: int, rows: int, n: int, k: int,
+                       device, workspace):
+    need = ctypes.c_size_t(0)
+    check(load().mns_grouped_workspace_size(weight_grad, code, groups, rows, n, k,
+                                            ctypes.byref(need)), "mns_grouped_workspace_size")
+    if need.value == 0:
+        return None, 0, 0
+    ws = _workspace(need.value, device, workspace)
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def grouped_matmul(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, *,
+                   transpose_w: bool = False, out: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rows sorted by expert times their expert's matrix: Y_e = X_e W_e^T (the forward product
+    of a layer of experts), or Y_e = X_e W_e with ``transpose_w`` (the gradient of its input).
+
+    W is a contiguous (experts, n, k) stack; expert e owns rows offsets[e]:offsets[e + 1] of X
+    (offsets: int64 on the GPU, read by the kernels only). X and ``out`` are 2-D with contiguous
+    rows at any row pitch. Rows that belong to no expert come back as zeros in a new output and
+    are left as they are in a given ``out``."""
+    what = "grouped_matmul"
+    if W.dim() != 3:
+        raise ValueError(f"{what}: W must be 3-D (experts, n, k)")
+    code = _dtype_code(X)
+    if W.dtype != X.dtype:
+        raise TypeError(f"{what}: X and W must share one storage dtype "
+                        f"(X {X.dtype}, W {W.dtype})")
+    groups, n, k = W.shape
+    wide, narrow = (n, k) if transpose_w else (k, n)
+    if X.dim() != 2 or X.shape[1] != wide:
+        raise ValueError(f"{what}: X must be 2-D with rows of {wide}, got {tuple(X.shape)}")
+    if not W.is_contiguous():
+        raise ValueError(f"{what}: W must be contiguous")
+    rows = X.shape[0]
+    ldx = _pitch(X, "X", what)
+    if out is not None:
+        if out.dim() != 2 or tuple(out.shape) != (rows, narrow) or out.dtype != X.dtype:
+            raise ValueError(f"{what}: out must be {(rows, narrow)} {X.dtype}, "
+                             f"got {tuple(out.shape)} {out.dtype}")
+        ldy = _pitch(out, "out", what)
+        if not _apart(out, X) or not _apart(out, W) or not _apart(out, offsets):
+            raise ValueError(f"{what}: out may not overlap X, W or offsets")
+    dev = _grouped_checks([("X", X)] + ([("out", out)] if out is not None else []), [W], offsets,
+                          groups, what)
+    with _OnStream(dev, stream) as handle:
+        Y = out
+        if Y is None:
+            Y = torch.empty((rows, narrow), dtype=X.dtype, device=dev)
+            ldy = narrow
+        keep, ws, nbytes = _grouped_workspace(0, code, groups, rows, n, k, dev, workspace)
+        check(load().grouped_matmul(X.data_ptr(), ldx, W.data_ptr(), Y.data_ptr(), ldy, code,
+                                    offsets.data_ptr(), groups, rows, n, k,
+                                    1 if transpose_w else 0, 1 if out is None else 0, ws, nbytes,
+                                    handle), what)
+    return Y
+
+
+def grouped_weight_grad(dY: torch.Tensor, X: torch.Tensor, offsets: torch.Tensor, *,
+                        C: torch.Tensor | None = None, beta: float = 1.0,
+                        out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Weight gradients of a layer of experts, G_e = beta C_e + dY_e^T X_e, as a stack
+    (experts, n, k) for dY of width n and X of width k, rows sorted by expert as in
+    grouped_matmul. The output is of ``out``'s dtype, else C's, else ``out_dtype``, else X's;
+    float32 outputs take bfloat16 products unrounded. ``out`` may be C itself: with a float32
+    momentum, ``C=M, beta=mu, out=M`` is M <- mu M + dY^T X."""
+    what = "grouped_weight_grad"
+    code = _dtype_code(X)
+    if dY.dtype != X.dtype:
+        raise TypeError(f"{what}: dY and X must share one storage dtype "
+                        f"(dY {dY.dtype}, X {X.dtype})")
+    if dY.dim() != 2 or X.dim() != 2 or dY.shape[0] != X.shape[0]:
+        raise ValueError(f"{what}: dY and X must be 2-D with the same rows")
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError(f"{what}: offsets must hold at least two entries")
+    rows, n, k, groups = X.shape[0], dY.shape[1], X.shape[1], offsets.shape[0] - 1
+    lddy, ldx = _pitch(dY, "dY", what), _pitch(X, "X", what)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else C.dtype if C is not None else X.dtype
+    for name, t in (("C", C), ("out", out)):
+        if t is None:
+            continue
+        if tuple(t.shape) != (groups, n, k) or t.dtype != out_dtype:
+            raise ValueError(f"{what}: {name} must be {(groups, n, k)} {out_dtype}, "
+                             f"got {tuple(t.shape)} {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be contiguous")
+    if out_dtype not in (X.dtype, torch.float32):
+        raise TypeError(f"{what}: the output must be {X.dtype} or float32, not {out_dtype}")
+    if out is not None:
+        if not _apart(out, dY) or not _apart(out, X) or not _apart(out, offsets):
+            raise ValueError(f"{what}: out may not overlap dY, X or offsets")
+        if C is not None and C.data_ptr() != out.data_ptr() and not _apart(out, C):
+            raise ValueError(f"{what}: out must be C itself or lie apart from it")
+    dev = _grouped_checks([("dY", dY), ("X", X)], [t for t in (C, out) if t is not None], offsets,
+                          groups, what)
+    with _OnStream(dev, stream) as handle:
+        G = torch.empty((groups, n, k), dtype=out_dtype, device=dev) if out is None else out
+        keep, ws, nbytes = _grouped_workspace(1, code, groups, rows, n, k, dev, workspace)
+        check(load().grouped_weight_grad(dY.data_ptr(), lddy, X.data_ptr(), ldx, code,
+                                         offsets.data_ptr(), groups, rows, n, k,
+                                         None if C is None else C.data_ptr(), beta, G.data_ptr(),
+                                         MNS_F32 if out_dtype == torch.float32 else MNS_BF16, ws,
+                                         nbytes, handle), what)
+    return G
 
 
 def profile_begin() -> None:

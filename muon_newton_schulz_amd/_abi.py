@@ -26,6 +26,7 @@ EXPORTS = (
     "mns_ns_workspace_size", "ns_orthogonalize", "gram_ns_orthogonalize",
     "mns_normuon_workspace_size", "normuon_scale", "mns_profile_begin", "mns_profile_end",
     "mns_profile_set_flush", "ns_orthogonalize_noalloc",
+    "mns_grouped_workspace_size", "grouped_matmul", "grouped_weight_grad",
 )
 
 
@@ -120,6 +121,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ns_orthogonalize_noalloc.restype = ctypes.c_int
     lib.ns_orthogonalize_noalloc.argtypes = [vp, vp, ctypes.c_int, i64, i64, i64, ctypes.c_int,
                                              fp, vp]
+    ci, cf, csz = ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    lib.mns_grouped_workspace_size.restype = ci
+    lib.mns_grouped_workspace_size.argtypes = [ci, ci, i64, i64, i64, i64, sz]
+    lib.grouped_matmul.restype = ci
+    lib.grouped_matmul.argtypes = [vp, i64, vp, vp, i64, ci, vp, i64, i64, i64, i64, ci, ci, vp,
+                                   csz, vp]
+    lib.grouped_weight_grad.restype = ci
+    lib.grouped_weight_grad.argtypes = [vp, i64, vp, i64, ci, vp, i64, i64, i64, i64, vp, cf, vp,
+                                        ci, vp, csz, vp]
     lib.mns_profile_set_flush.restype = ctypes.c_int
     lib.mns_profile_set_flush.argtypes = [vp, ctypes.c_size_t]
     _lib = lib

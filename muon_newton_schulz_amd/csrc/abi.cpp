@@ -869,6 +869,119 @@ mns_status normuon_scale(void* O, int dtype, int64_t batch, int64_t rows, int64_
   return MNS_OK;
 }
 
+// ---- products grouped by expert ----------------------------------------------------------------
+
+constexpr int64_t kMaxGroups = 65536;
+constexpr int64_t kMaxPitch = int64_t(1) << 21;
+
+static mns_status check_grouped(int dtype, int64_t groups, int64_t total_rows, int64_t n, int64_t k) {
+  const mns_status st = check_dtype(dtype);
+  if (st != MNS_OK) return st;
+  if (groups < 1 || groups > kMaxGroups || total_rows < 0 || total_rows > kMaxElems)
+    return MNS_ERR_SHAPE;
+  return check_shape(1, n, k);
+}
+
+static Store store_of(int dtype) { return dtype == MNS_BF16 ? Store::BF16 : Store::F32; }
+
+static size_t store_bytes(int dtype) { return dtype == MNS_BF16 ? 2 : 4; }
+
+static mns_status run_grouped(GroupedDesc& d, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  if (grouped_blocks(d) > kMaxElems) return MNS_ERR_SHAPE;
+  const size_t need = grouped_workspace(d);
+  if (need) {
+    const mns_status st = check_ws(workspace, workspace_bytes, need);
+    if (st != MNS_OK) return st;
+    d.workspace = static_cast<float*>(workspace);
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  MNS_HIP(timed(grouped_name(d), 2.0 * d.total_rows * d.n * d.k, 0.0, s, [&] {
+    return grouped(d, s); }));
+  return MNS_OK;
+}
+
+mns_status mns_grouped_workspace_size(int weight_grad, int dtype, int64_t groups,
+                                      int64_t total_rows, int64_t n, int64_t k, size_t* bytes) {
+  if (!bytes) return MNS_ERR_NULL;
+  if (weight_grad != 0 && weight_grad != 1) return MNS_ERR_PARAM;
+  const mns_status st = check_grouped(dtype, groups, total_rows, n, k);
+  if (st != MNS_OK) return st;
+  GroupedDesc d;
+  d.store = store_of(dtype);
+  d.groups = groups;
+  d.total_rows = total_rows;
+  d.n = n;
+  d.k = k;
+  d.weight_grad = weight_grad == 1;
+  *bytes = grouped_workspace(d);
+  return MNS_OK;
+}
+
+mns_status grouped_matmul(const void* X, int64_t ldx, const void* W, void* Y, int64_t ldy,
+                          int dtype, const int64_t* offsets, int64_t groups, int64_t total_rows,
+                          int64_t n, int64_t k, int transpose_w, int fill_rest, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  const mns_status st = check_grouped(dtype, groups, total_rows, n, k);
+  if (st != MNS_OK) return st;
+  if (transpose_w != 0 && transpose_w != 1) return MNS_ERR_PARAM;
+  if (fill_rest != 0 && fill_rest != 1) return MNS_ERR_PARAM;
+  const int64_t in = transpose_w ? n : k, out = transpose_w ? k : n;
+  if (ldx < in || ldx > kMaxPitch || ldy < out || ldy > kMaxPitch) return MNS_ERR_SHAPE;
+  if (!W || !offsets || (total_rows > 0 && (!X || !Y))) return MNS_ERR_NULL;
+  const size_t es = store_bytes(dtype);
+  if (!aligned(X, es) || !aligned(W, es) || !aligned(Y, es) || !aligned(offsets, 8))
+    return MNS_ERR_PARAM;
+  if (total_rows == 0) return MNS_OK;
+  GroupedDesc d;
+  d.store = d.out_store = store_of(dtype);
+  d.A = X; d.lda = ldx;
+  d.B = W;
+  d.C = Y; d.ldc = ldy;
+  d.offsets = offsets;
+  d.groups = groups;
+  d.total_rows = total_rows;
+  d.n = n;
+  d.k = k;
+  d.transpose_w = transpose_w == 1;
+  d.fill_rest = fill_rest == 1;
+  return run_grouped(d, workspace, workspace_bytes, stream);
+}
+
+mns_status grouped_weight_grad(const void* dY, int64_t lddy, const void* X, int64_t ldx,
+                               int dtype, const int64_t* offsets, int64_t groups,
+                               int64_t total_rows, int64_t n, int64_t k, const void* C, float beta,
+                               void* G, int out_dtype, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  mns_status st = check_grouped(dtype, groups, total_rows, n, k);
+  if (st != MNS_OK) return st;
+  st = check_dtype(out_dtype);
+  if (st != MNS_OK) return st;
+  if (out_dtype != dtype && out_dtype != MNS_F32) return MNS_ERR_DTYPE;
+  if (!std::isfinite(beta)) return MNS_ERR_PARAM;
+  if (lddy < n || lddy > kMaxPitch || ldx < k || ldx > kMaxPitch) return MNS_ERR_SHAPE;
+  if (!G || !offsets || (total_rows > 0 && (!dY || !X))) return MNS_ERR_NULL;
+  const size_t es = store_bytes(dtype), os = store_bytes(out_dtype);
+  if (!aligned(dY, es) || !aligned(X, es) || !aligned(G, os) || !aligned(C, os) ||
+      !aligned(offsets, 8))
+    return MNS_ERR_PARAM;
+  GroupedDesc d;
+  d.store = store_of(dtype);
+  d.out_store = store_of(out_dtype);
+  d.A = dY; d.lda = lddy;
+  d.B = X; d.ldb = ldx;
+  d.D = beta != 0.f ? C : nullptr;
+  d.beta = beta;
+  d.C = G;
+  d.offsets = offsets;
+  d.groups = groups;
+  d.total_rows = total_rows;
+  d.n = n;
+  d.k = k;
+  d.weight_grad = true;
+  return run_grouped(d, workspace, workspace_bytes, stream);
+}
+
 mns_status mns_profile_begin(void) {
   std::lock_guard<std::mutex> lk(g_prof_mu);
   for (ProfRec& r : g_prof) {

@@ -82,6 +82,34 @@ const char* gemm_name(const GemmDesc& d);
 bool gemm_kmajor_ok(const GemmDesc& d);
 
 // ---------------------------------------------------------------------------------------
+// Products grouped by expert (grouped.hip). Expert e owns rows [offsets[e], offsets[e + 1]) of
+// the token matrices; W and G hold one n x k matrix per expert.
+//   forward (default)  C = A W_e^T   A: total_rows x k (lda), C: total_rows x n (ldc)
+//   transpose_w        C = A W_e     A: total_rows x n (lda), C: total_rows x k (ldc)
+//   weight_grad        C_e = A_e^T B_e + beta D_e   A: total_rows x n (lda), B: total_rows x k
+//                      (ldb); C, D (may be null): groups x n x k in out_store
+// ---------------------------------------------------------------------------------------
+struct GroupedDesc {
+  Store store = Store::BF16, out_store = Store::BF16;
+  const void* A = nullptr; int64_t lda = 0;
+  const void* B = nullptr; int64_t ldb = 0;   // ldb: weight_grad only (W is contiguous)
+  const void* D = nullptr;
+  void* C = nullptr; int64_t ldc = 0;
+  const int64_t* offsets = nullptr;
+  int64_t groups = 0, total_rows = 0, n = 0, k = 0;
+  float beta = 0.f;
+  bool weight_grad = false, transpose_w = false;
+  float* workspace = nullptr;  // grouped_workspace() bytes
+  bool fill_rest = false;      // rows of no expert are written as zeros (else left as they are)
+};
+hipError_t grouped(const GroupedDesc& d, hipStream_t s);
+// Blocks grouped() launches for these sizes (a launch holds at most 2^31 - 1).
+int64_t grouped_blocks(const GroupedDesc& d);
+// Workspace bytes of grouped() for these sizes.
+size_t grouped_workspace(const GroupedDesc& d);
+const char* grouped_name(const GroupedDesc& d);
+
+// ---------------------------------------------------------------------------------------
 // Elementwise / reduction kernels (elementwise.hip). All are deterministic: fixed
 // reduction orders, no floating-point atomics.
 // ---------------------------------------------------------------------------------------

@@ -1,0 +1,244 @@
+"""Products grouped by expert against float64 on the CPU, element by element with derived bounds
+(grouped_ref), at the sizes where a tile, a chunk or a group ends: no rows, one row, many empty
+experts, odd widths, row pitches, addresses off the 16-byte grid, rows of no expert."""
+import pytest
+import torch
+
+import grouped_ref as ref
+import muon_newton_schulz_amd as mns
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _rand(shape, dtype, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(dtype).cuda()
+
+
+def _offsets(bounds):
+    return torch.tensor(bounds, dtype=torch.int64, device="cuda")
+
+
+def _strided(t, pitch, lead=0):
+    """t's values in rows `pitch` apart, starting `lead` elements into a buffer of 7s."""
+    buf = torch.full((lead + t.shape[0] * pitch + 8,), 7.0, dtype=t.dtype, device=t.device)
+    view = buf[lead:].as_strided(t.shape, (pitch, 1), lead)
+    view.copy_(t)
+    return view, buf
+
+
+# sizes of the experts' row groups, rows before the first and behind the last
+ROUTES = {
+    "one_token": ([0, 0, 1, 0], 0, 0),
+    "one_expert": ([200], 0, 0),
+    "even": ([64] * 4, 0, 0),
+    "ragged": ([1, 0, 129, 127, 0, 33, 256, 2], 0, 5),
+    "front_and_tail": ([7, 140], 3, 150),
+    "all_empty": ([0] * 5, 0, 9),
+    "many": ([(i * 7) % 5 for i in range(150)], 2, 1),
+    "long": ([700, 3, 1100], 0, 0),
+}
+WIDTHS = [(64, 128), (1, 1), (65, 33), (256, 320), (130, 72), (24, 520)]
+
+
+@pytest.mark.parametrize("route", sorted(ROUTES))
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_matmul_both_ways(route, dtype):
+    sizes, front, tail = ROUTES[route]
+    bounds = ref.bounds_of(sizes, front)
+    rows = bounds[-1] + tail
+    for i, (n, k) in enumerate(WIDTHS):
+        W = _rand((len(sizes), n, k), dtype, 100 + i, 0.3)
+        for t in (False, True):
+            print("case", route, dtype, n, k, "transpose_w", t, flush=True)
+            X = _rand((rows, n if t else k), dtype, i)
+            out = mns.grouped_matmul(X, W, _offsets(bounds), transpose_w=t)
+            ref.check(out, *ref.matmul(X, W, bounds, t, torch.zeros_like(out)), (route, n, k, t))
+
+
+@pytest.mark.parametrize("route", sorted(ROUTES))
+@pytest.mark.parametrize("dtype,out_dtype", [(BF, BF), (BF, F32), (F32, F32)],
+                         ids=["bf16", "bf16_f32", "f32"])
+def test_weight_grad(route, dtype, out_dtype):
+    sizes, front, tail = ROUTES[route]
+    bounds = ref.bounds_of(sizes, front)
+    rows = bounds[-1] + tail
+    for i, (n, k) in enumerate(WIDTHS):
+        print("case", route, dtype, out_dtype, n, k, flush=True)
+        dY, X = _rand((rows, n), dtype, i, 0.2), _rand((rows, k), dtype, 50 + i)
+        out = mns.grouped_weight_grad(dY, X, _offsets(bounds), out_dtype=out_dtype)
+        ref.check(out, *ref.weight_grad(dY, X, bounds, None, 0.0, out_dtype), (route, n, k))
+        C = _rand((len(sizes), n, k), out_dtype, 70 + i)
+        want = ref.weight_grad(dY, X, bounds, C, 0.95, out_dtype)
+        got = mns.grouped_weight_grad(dY, X, _offsets(bounds), C=C, beta=0.95, out=C)
+        assert got is C
+        ref.check(C, *want, (route, n, k, "in place"))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_no_rows_at_all(dtype):
+    W = _rand((3, 40, 24), dtype, 1)
+    X = torch.empty(0, 24, dtype=dtype, device="cuda")
+    off = _offsets([0, 0, 0, 0])
+    assert mns.grouped_matmul(X, W, off).shape == (0, 40)
+    G = mns.grouped_weight_grad(torch.empty(0, 40, dtype=dtype, device="cuda"), X, off)
+    assert G.shape == (3, 40, 24) and not G.any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("lead,extra", [(0, 24), (1, 24), (3, 5)])
+def test_row_pitches_and_addresses(dtype, lead, extra):
+    sizes, n, k = [70, 0, 5, 130], 72, 136
+    bounds = ref.bounds_of(sizes, 2)
+    rows = bounds[-1] + 4
+    X0, dY0 = _rand((rows, k), dtype, 1), _rand((rows, n), dtype, 2)
+    X, _ = _strided(X0, k + extra, lead)
+    dY, _ = _strided(dY0, n + extra, lead)
+    Wbuf = torch.empty(4 * n * k + 8, dtype=dtype, device="cuda")
+    W = Wbuf[lead:lead + 4 * n * k].view(4, n, k)
+    W.copy_(_rand((4, n, k), dtype, 3, 0.3))
+    off = _offsets(bounds)
+    for t, src, width in ((False, X, n), (True, dY, k)):
+        out, buf = _strided(torch.full((rows, width), 3.0, dtype=dtype, device="cuda"),
+                            width + extra, lead)
+        before = buf.clone()
+        want, err = ref.matmul(src, W, bounds, t, out)
+        assert mns.grouped_matmul(src, W, off, transpose_w=t, out=out) is out
+        ref.check(out, want, err, ("pitch", lead, extra, t))
+        # rows of no expert and the gaps between rows keep what they held
+        touched = torch.zeros_like(buf, dtype=torch.bool)
+        touched[lead:].as_strided(out.shape, (width + extra, 1), lead)[bounds[0]:bounds[-1]] = True
+        assert torch.equal(buf[~touched], before[~touched])
+    G = mns.grouped_weight_grad(dY, X, off)
+    ref.check(G, *ref.weight_grad(dY, X, bounds, None, 0.0, dtype), ("pitch", lead, extra))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_nothing_leaks_between_experts(dtype):
+    """NaN and infinity in one expert's rows, in the rows of no expert and in one expert's matrix
+    stay there."""
+    sizes, n, k = [20, 31, 0, 40], 48, 104
+    bounds = ref.bounds_of(sizes, 5)
+    rows = bounds[-1] + 6
+    X, dY = _rand((rows, k), dtype, 1), _rand((rows, n), dtype, 2)
+    W = _rand((4, n, k), dtype, 3)
+    off = _offsets(bounds)
+    clean = [mns.grouped_matmul(X, W, off), mns.grouped_matmul(dY, W, off, transpose_w=True),
+             mns.grouped_weight_grad(dY, X, off)]
+    for t in (X, dY):
+        t[:5] = float("nan")
+        t[bounds[1]:bounds[2]] = float("inf")
+        t[bounds[-1]:] = float("nan")
+    W[1] = float("nan")
+    W[2] = float("inf")
+    got = [mns.grouped_matmul(X, W, off), mns.grouped_matmul(dY, W, off, transpose_w=True),
+           mns.grouped_weight_grad(dY, X, off)]
+    keep = torch.ones(rows, dtype=torch.bool)
+    keep[bounds[1]:bounds[2]] = False
+    for c, g in zip(clean[:2], got[:2]):
+        assert torch.equal(g.cpu()[keep], c.cpu()[keep])
+        assert not torch.isfinite(g.cpu()[~keep]).any()
+    assert torch.equal(got[2][[0, 2, 3]], clean[2][[0, 2, 3]])
+    assert not torch.isfinite(got[2][1]).any()
+
+
+def test_beta_zero_reads_no_addend():
+    sizes, n, k = [3, 0, 9], 40, 72
+    bounds = ref.bounds_of(sizes)
+    dY, X = _rand((12, n), BF, 1), _rand((12, k), BF, 2)
+    C = torch.full((3, n, k), float("nan"), device="cuda")
+    G = mns.grouped_weight_grad(dY, X, _offsets(bounds), C=C, beta=0.0)
+    ref.check(G, *ref.weight_grad(dY, X, bounds, None, 0.0, F32))
+
+
+def test_offsets_out_of_range_stay_inside_the_buffers():
+    """Offsets below zero, beyond the rows or decreasing are clamped; the valid experts' rows hold
+    the right values."""
+    n, k, rows = 40, 72, 60
+    X, W = _rand((rows, k), BF, 1), _rand((4, n, k), BF, 2)
+    dY = _rand((rows, n), BF, 3)
+    off = _offsets([-(1 << 40), 20, 30, 1 << 40, -5])
+    want = [0, 20, 30, 60, 60]
+    out = mns.grouped_matmul(X, W, off)
+    ref.check(out[:60], *ref.matmul(X, W, want, False, torch.zeros_like(out)))
+    G = mns.grouped_weight_grad(dY, X, off)
+    ref.check(G[:3], *[t[:3] for t in ref.weight_grad(dY, X, want, None, 0.0, BF)])
+    torch.cuda.synchronize()
+
+
+def _chain(X, W, dY, off, M):
+    Y = mns.grouped_matmul(X, W, off)
+    dX = mns.grouped_matmul(dY, W, off, transpose_w=True)
+    mns.grouped_weight_grad(dY, X, off, C=M, beta=0.5, out=M)
+    return Y, dX
+
+
+def test_captured_and_replayed_with_new_offsets():
+    """A captured call reads the offsets and tokens of each replay."""
+    n, k, rows = 200, 136, 300
+    W = _rand((5, n, k), BF, 1, 0.3)
+    X, dY = _rand((rows, k), BF, 2), _rand((rows, n), BF, 3)
+    off = _offsets([0, 0, 60, 200, 200, 300])
+    M = torch.zeros(5, n, k, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _chain(X, W, dY, off, M)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Y, dX = _chain(X, W, dY, off, M)
+    for i, bounds in enumerate([[0, 10, 10, 250, 300, 300], [0, 300, 300, 300, 300, 300],
+                                [0, 0, 60, 200, 200, 300]]):
+        off.copy_(_offsets(bounds))
+        X.copy_(_rand((rows, k), BF, 20 + i))
+        M.copy_(_rand((5, n, k), F32, 30 + i))
+        M2 = M.clone()
+        Y2, dX2 = _chain(X, W, dY, off, M2)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, Y2) and torch.equal(dX, dX2) and torch.equal(M, M2), bounds
+
+
+def test_two_streams_at_once_and_a_given_stream():
+    n, k, rows = 320, 264, 500
+    W = _rand((4, n, k), BF, 1, 0.3)
+    off = _offsets([0, 100, 100, 420, 500])
+    Xs = [_rand((rows, k), BF, 5 + i) for i in range(2)]
+    alone = [mns.grouped_matmul(x, W, off) for x in Xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in Xs]
+    got = [[mns.grouped_matmul(x, W, off, stream=s) for _ in range(4)]
+           for x, s in zip(Xs, streams)]
+    raw = mns.grouped_matmul(Xs[0], W, off, stream=streams[0].cuda_stream)
+    torch.cuda.synchronize()
+    for a, outs in zip(alone, got):
+        for o in outs:
+            assert torch.equal(o, a)
+    assert torch.equal(raw, alone[0])
+
+
+def test_rows_beyond_32_bits_of_bytes():
+    """Offsets of rows past 2^32 bytes into the token matrices."""
+    k, n, rows = 4096, 64, 600_000
+    X = torch.zeros(rows, k, dtype=BF, device="cuda")          # 4.9 GB
+    W = _rand((2, n, k), BF, 1, 0.1)
+    bounds = [0, rows - 150, rows]
+    X[rows - 200:] = _rand((200, k), BF, 2)
+    X[:3] = _rand((3, k), BF, 3)
+    dY = torch.zeros(rows, n, dtype=BF, device="cuda")
+    dY[rows - 200:] = _rand((200, n), BF, 4)
+    off = _offsets(bounds)
+    pick = torch.cat([torch.arange(3), torch.arange(rows - 200, rows)])
+    small = [0, 53, 203]
+    Y = mns.grouped_matmul(X, W, off)
+    Xp = X[pick.cuda()]
+    ref.check(Y[pick.cuda()], *ref.matmul(Xp, W, small, False, torch.zeros(203, n)))
+    assert not Y[3:rows - 200].any()
+    G = mns.grouped_weight_grad(dY, X, off)
+    # adding the products of the all-zero rows is exact, so the bound is the picked rows'
+    ref.check(G, *ref.weight_grad(dY[pick.cuda()], Xp, small, None, 0.0, BF), "long reduction")
