@@ -172,6 +172,28 @@ mns_status ns_orthogonalize_noalloc(const void* X, void* O, int dtype, int64_t b
                                     int64_t rows, int64_t cols, int T,
                                     const float* abc /* (host) 3*T */, void* stream);
 
+/* Workspace bytes for ns_orthogonalize_backward on `batch` matrices. */
+mns_status mns_ns_backward_workspace_size(int dtype, int64_t batch, int64_t rows, int64_t cols,
+                                          size_t* bytes /* (host) out */);
+
+/* Gradient of ns_orthogonalize (and, in exact arithmetic, of gram_ns_orthogonalize): for each of
+ * `batch` matrices, dX = (d NS_T(X / ||X||_F) / dX)^T dO.
+ *   X   in  dtype [batch][rows][cols], the input of the forward call
+ *   dO  in  the same, the gradient of its output;   dX  out  the same; may not overlap X or dO
+ * The map acts on the singular values only, so its derivative is a symmetric linear map: the
+ * gradient is the derivative in the direction dO, carried along the iteration, and no iterate is
+ * stored. A zero X or a zero dO gives dX = 0.
+ *   Arithmetic: float32 for MNS_F32, and for MNS_BF16 when min(rows, cols) <= 256; else float16
+ *   products with float32 sums, every quantity scaled by a power of two that its bound over the
+ *   iterations keeps in range. MNS_ERR_PARAM when the coefficients amplify a direction more than
+ *   2^20 times (float16; T = 10 with (3.4445, -4.775, 2.0315) still runs) or 10^30 times.
+ *   Sizes: as above, with the iterate counted twice (direction and iterate are stored together),
+ *   else MNS_ERR_SHAPE. */
+mns_status ns_orthogonalize_backward(const void* X, const void* dO, void* dX, int dtype,
+                                     int64_t batch, int64_t rows, int64_t cols, int T,
+                                     const float* abc /* (host) 3*T */, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
 /* Workspace bytes for normuon_scale. */
 mns_status mns_normuon_workspace_size(int64_t batch, int64_t rows, int64_t cols,
                                       size_t* bytes /* (host) out */);

@@ -19,6 +19,7 @@ from ._abi import (MNS_BF16, MNS_F32, MNS_NS_GRAM, MNS_NS_STANDARD, MnsError,  #
 
 __all__ = ["muon_step", "ns_orthogonalize", "ns_orthogonalize_noalloc",
            "gram_ns_orthogonalize", "normuon_scale",
+           "ns_orthogonalize_backward", "ns_backward_workspace_size",
            "grouped_matmul", "grouped_weight_grad",
            "step_workspace_size", "ns_workspace_size", "normuon_workspace_size",
            "restart_mask", "profile_begin", "profile_set_flush", "profile_end", "MnsError",
@@ -495,6 +496,46 @@ def grouped_weight_grad(dY: torch.Tensor, X: torch.Tensor, offsets: torch.Tensor
                                          MNS_F32 if out_dtype == torch.float32 else MNS_BF16, ws,
                                          nbytes, handle), what)
     return G
+
+
+def ns_backward_workspace_size(X: torch.Tensor) -> int:
+    b, r, c = _bshape(X)
+    out = ctypes.c_size_t(0)
+    check(load().mns_ns_backward_workspace_size(_dtype_code(X), b, r, c, ctypes.byref(out)),
+          "mns_ns_backward_workspace_size")
+    return out.value
+
+
+def ns_orthogonalize_backward(X: torch.Tensor, dO: torch.Tensor, coeffs,
+                              out: torch.Tensor | None = None,
+                              workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient dX of ns_orthogonalize(X, coeffs) for the gradient dO of its output (the same for
+    gram_ns_orthogonalize, whose map is the same). X and dO: one matrix or a 3-D batch, of one
+    shape and storage dtype; X is the forward call's input, nothing else is kept from it."""
+    what = "ns_orthogonalize_backward"
+    if dO.shape != X.shape or dO.dtype != X.dtype:
+        raise ValueError(f"{what}: dO must match X in shape and dtype "
+                         f"(X {tuple(X.shape)} {X.dtype}, dO {tuple(dO.shape)} {dO.dtype})")
+    if not dO.is_contiguous():
+        raise ValueError(f"{what}: dO must be contiguous")
+    b, r, c = _bshape(X)
+    code = _dtype_code(X)
+    if not X.is_contiguous():
+        raise ValueError(f"{what}: X must be contiguous")
+    if out is not None:
+        if out.shape != X.shape or out.dtype != X.dtype or not out.is_contiguous():
+            raise ValueError(f"{what}: out must match X in shape and dtype and be contiguous")
+        if not _disjoint(X, out) or not _disjoint(dO, out):
+            raise ValueError(f"{what}: out may not overlap X or dO")
+    dev = _on_one_gpu([X, dO, out], what)
+    abc, T = _coeffs(coeffs)
+    with _OnStream(dev, stream) as handle:
+        dX = torch.empty_like(X) if out is None else out
+        ws = _workspace(ns_backward_workspace_size(X), dev, workspace)
+        check(load().ns_orthogonalize_backward(_ptr(X), _ptr(dO), _ptr(dX), code, b, r, c, T, abc,
+                                               ws.data_ptr(), ws.numel() * ws.element_size(),
+                                               handle), what)
+    return dX
 
 
 def profile_begin() -> None:

@@ -27,6 +27,7 @@ EXPORTS = (
     "mns_normuon_workspace_size", "normuon_scale", "mns_profile_begin", "mns_profile_end",
     "mns_profile_set_flush", "ns_orthogonalize_noalloc",
     "mns_grouped_workspace_size", "grouped_matmul", "grouped_weight_grad",
+    "mns_ns_backward_workspace_size", "ns_orthogonalize_backward",
 )
 
 
@@ -130,6 +131,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.grouped_weight_grad.restype = ci
     lib.grouped_weight_grad.argtypes = [vp, i64, vp, i64, ci, vp, i64, i64, i64, i64, vp, cf, vp,
                                         ci, vp, csz, vp]
+    lib.mns_ns_backward_workspace_size.restype = ci
+    lib.mns_ns_backward_workspace_size.argtypes = [ci, i64, i64, i64, sz]
+    lib.ns_orthogonalize_backward.restype = ci
+    lib.ns_orthogonalize_backward.argtypes = [vp, vp, vp, ci, i64, i64, i64, ci, fp, vp, csz, vp]
     lib.mns_profile_set_flush.restype = ctypes.c_int
     lib.mns_profile_set_flush.argtypes = [vp, ctypes.c_size_t]
     _lib = lib

@@ -982,6 +982,307 @@ mns_status grouped_weight_grad(const void* dY, int64_t lddy, const void* X, int6
   return run_grouped(d, workspace, workspace_bytes, stream);
 }
 
+// ---- gradient of the orthogonalisation ---------------------------------------------------------
+//
+// Per iteration (see ns_backward.hip for the formulas): A = X X^T (symmetric), K = E X^T,
+// S = K + K^T, P = a I + b A + c A^2 (symmetric), K = A S, Q = b S + c (K + K^T), then
+// E <- [P Q] [E; X] as one product of twice the depth, and X <- P X (not after the last
+// iteration). E and X lie one above the other in V (and side by side in V^T), P and Q side by
+// side in PQ, so no product needs its operands gathered.
+//
+// Short sides up to 256 run in float32 whatever the storage: rounding the iterate to float16 is
+// the largest error, it grows along the smallest singular values, and small near-square matrices
+// show it most (float16 against float64, rank 64 plus noise: 4.3e-3 at 64 and 256 square, 2.9e-3
+// at 512; half a bfloat16 step is 3.9e-3). The float32 products there take a few microseconds.
+constexpr int64_t kNsbF32Short = 256;
+// Largest growth of a direction over the iterations that float16 can carry (2^14 of headroom
+// above 1, 2^6 below the smallest value that matters).
+constexpr double kNsbGrowthF16 = 1048576.0, kNsbGrowthF32 = 1e30;
+
+static Geo nsb_geo(int64_t rows, int64_t cols, Store st) {
+  Geo g = make_geo(rows, cols, st);
+  if (g.n <= kNsbF32Short) {
+    g.elem = Elem::F32;
+    g.S = 1.0f;
+  }
+  return g;
+}
+
+struct NsbBuffers {
+  void* V[2] = {};       // [E; X]: 2 n_p x m_p, pitch ld_x
+  void* Vt[2] = {};      // [E^T X^T]: m_p x 2 n_p, pitch ld_t
+  void* A = nullptr;     // n_p x n_p, pitch ld_q
+  void* K = nullptr;
+  void* Ssym = nullptr;
+  void* PQ = nullptr;    // n_p x 2 n_p, pitch ld_t
+  double* px = nullptr;
+  double* pg = nullptr;
+  double* scale = nullptr;
+  double* dot = nullptr;
+  float* gemm_scratch = nullptr;
+  size_t gemm_scratch_bytes = 0;
+  int64_t ld_t = 0, v_stride = 0, vt_stride = 0, q_stride = 0, pq_stride = 0;
+};
+
+static size_t carve_nsb(void* base, const Geo& g, int count, NsbBuffers& b) {
+  Carver cv(base);
+  const size_t es = (size_t)elem_bytes(g.elem);
+  const int nblk = norm_blocks(g.rows * g.cols);
+  b.px = cv.take<double>((size_t)count * nblk);
+  b.pg = cv.take<double>((size_t)count * nblk);
+  b.scale = cv.take<double>((size_t)count * 4);
+  b.dot = cv.take<double>((size_t)count * nsb_dot_blocks(g.rows));
+  b.ld_t = padded_ld(2 * g.n_p);
+  b.v_stride = 2 * g.n_p * g.ld_x;
+  b.vt_stride = g.m_p * b.ld_t;
+  b.q_stride = g.n_p * g.ld_q;
+  b.pq_stride = g.n_p * b.ld_t;
+  for (int i = 0; i < 2; ++i) {
+    b.V[i] = cv.take<char>(es * count * b.v_stride);
+    b.Vt[i] = cv.take<char>(es * count * b.vt_stride);
+  }
+  b.A = cv.take<char>(es * count * b.q_stride);
+  b.K = cv.take<char>(es * count * b.q_stride);
+  b.Ssym = cv.take<char>(es * count * b.q_stride);
+  b.PQ = cv.take<char>(es * count * b.pq_stride);
+  // split-k parts: (output tiles) x (k-tiles / 8), capped as in carve_ns
+  const size_t deep = (size_t)(g.m_p > 2 * g.n_p ? g.m_p : 2 * g.n_p) / 256;
+  size_t scratch = (size_t)count * g.n_p * g.m_p * deep * sizeof(float);
+  if (scratch > kGemmScratchBytes) scratch = kGemmScratchBytes;
+  b.gemm_scratch = cv.take<float>(scratch / sizeof(float));
+  b.gemm_scratch_bytes = scratch;
+  return cv.off + 256;
+}
+
+static double pow2_floor(double x) { return std::ldexp(1.0, std::ilogb(x)); }
+
+// Powers of two that scale the stored quantities of one iteration: E by e, S and A S by kap, P by
+// p, Q by q = p e / S (so that P E and Q X add up), with the bounds below 2^14.
+struct NsbScale {
+  double e, kap, p, q;
+};
+
+// The scales of the T iterations and of the final direction, sc[T].e. A direction of norm 1 grows
+// to at most L_t = max over s in [0, 1] of |f_t'(s)| and |f_t(s) / s| (the factors of the
+// derivative of the composed polynomial f_t), and the singular values to sup |f_t|. False when L
+// leaves the range of the arithmetic.
+static bool nsb_plan(int T, const float* abc, const Geo& g, NsbScale* sc) {
+  const bool f16 = g.elem == Elem::F16;
+  constexpr int kGrid = 2048;
+  double L = 1.0, sup = 1.0;
+  double f[kGrid], d[kGrid];
+  for (int i = 0; i < kGrid; ++i) {
+    f[i] = (i + 1.0) / kGrid;
+    d[i] = 1.0;
+  }
+  double slope0 = 1.0;       // f_t'(0)
+  for (int t = 0; t <= T; ++t) {
+    const double lim = 16384.0;
+    sc[t] = NsbScale{1.0, 1.0, 1.0, 1.0};
+    if (!std::isfinite(L) || !std::isfinite(sup) || L > (f16 ? kNsbGrowthF16 : kNsbGrowthF32))
+      return false;
+    if (f16) sc[t].e = pow2_floor(lim / L);
+    if (t == T) break;
+    const double a = abc[3 * t], b = abc[3 * t + 1], c = abc[3 * t + 2];
+    if (f16) {
+      const double s2 = sup * sup;
+      const double big = s2 > 1.0 ? s2 : 1.0;
+      sc[t].kap = pow2_floor(lim / (2.0 * L * (sup > 1.0 ? sup : 1.0) * big));
+      const double pmax = std::fabs(a) + std::fabs(b) * s2 + std::fabs(c) * s2 * s2;
+      const double qmax = (std::fabs(b) + 2.0 * std::fabs(c) * s2) * 2.0 * L * sup;
+      double p = 256.0;
+      if (p * pmax > lim) p = pow2_floor(lim / pmax);
+      if (p * sc[t].e / g.S * qmax > lim) p = pow2_floor(lim * g.S / (sc[t].e * qmax));
+      sc[t].p = p;
+      sc[t].q = p * sc[t].e / g.S;
+    }
+    slope0 *= a;
+    L = std::fabs(slope0) > 1.0 ? std::fabs(slope0) : 1.0;
+    sup = 0.0;
+    for (int i = 0; i < kGrid; ++i) {
+      const double x = f[i], x2 = x * x;
+      f[i] = x * (a + x2 * (b + x2 * c));
+      d[i] *= a + x2 * (3.0 * b + x2 * 5.0 * c);
+      const double s = (i + 1.0) / kGrid;
+      if (std::fabs(d[i]) > L) L = std::fabs(d[i]);
+      if (std::fabs(f[i]) / s > L) L = std::fabs(f[i]) / s;
+      if (std::fabs(f[i]) > sup) sup = std::fabs(f[i]);
+      if (!std::isfinite(f[i]) || !std::isfinite(d[i])) return false;
+    }
+  }
+  return true;
+}
+
+static mns_status nsb_check(int dtype, int64_t batch, int64_t rows, int64_t cols) {
+  mns_status st = check_dtype(dtype);
+  if (st != MNS_OK) return st;
+  st = check_shape(batch, rows, cols);
+  if (st != MNS_OK) return st;
+  const Store sto = dtype == MNS_BF16 ? Store::BF16 : Store::F32;
+  st = check_iterate(rows, cols, sto);
+  if (st != MNS_OK) return st;
+  // the products address [E; X] and [E^T X^T] with 32-bit byte offsets
+  const Geo g = nsb_geo(rows, cols, sto);
+  const int64_t v = 2 * g.n_p * g.ld_x, vt = g.m_p * padded_ld(2 * g.n_p);
+  return (v > vt ? v : vt) * elem_bytes(g.elem) <= kMaxElems ? MNS_OK : MNS_ERR_SHAPE;
+}
+
+// One chunk of `c` matrices on buffers b: the direction E_T is left in the stored layout.
+static mns_status run_nsb(const Geo& g, int c, const NsbBuffers& b, int T, const float* abc,
+                          const NsbScale* sc, hipStream_t s, void** out) {
+  const size_t es = (size_t)elem_bytes(g.elem);
+  const auto at = [&](void* p, int64_t elems) {
+    return static_cast<void*>(static_cast<char*>(p) + (size_t)elems * es);
+  };
+  const int n = (int)g.n_p, m = (int)g.m_p;
+  const int64_t xoff = g.n_p * g.ld_x;                   // X below E in V
+  const double nn = (double)c * g.n * g.n;
+  GemmDesc base;
+  base.elem = g.elem;
+  base.batch = c;
+  base.partial = b.gemm_scratch;
+  base.partial_bytes = b.gemm_scratch_bytes;
+  const auto square = [&](const void* A, const void* B, int64_t ld, int64_t st, int K, void* C) {
+    GemmDesc d = base;
+    d.A = A; d.lda = ld; d.sA = st;
+    d.B = B; d.ldb = ld; d.sB = st;
+    d.C = C; d.ldc = g.ld_q; d.sC = b.q_stride;
+    d.M = d.N = n;
+    d.K = K;
+    return d;
+  };
+  // [P Q] V[cur] (depth 2 n_p) or P X (depth n_p)
+  const auto update = [&](bool direction, int cur, bool km, bool last) {
+    GemmDesc d = base;
+    d.A = b.PQ; d.lda = b.ld_t; d.sA = b.pq_stride;
+    if (km) {
+      d.B = direction ? b.V[cur] : at(b.V[cur], xoff);
+      d.ldb = g.ld_x; d.sB = b.v_stride;
+      d.b_kmajor = true;
+    } else {
+      d.B = direction ? b.Vt[cur] : at(b.Vt[cur], g.n_p);
+      d.ldb = b.ld_t; d.sB = b.vt_stride;
+    }
+    const bool want_c = !last || !g.tall, want_t = last ? g.tall : !km;
+    if (want_c) {
+      d.C = direction ? b.V[cur ^ 1] : at(b.V[cur ^ 1], xoff);
+      d.ldc = g.ld_x; d.sC = b.v_stride;
+    }
+    if (want_t) {
+      d.Ct = direction ? b.Vt[cur ^ 1] : at(b.Vt[cur ^ 1], g.n_p);
+      d.ldct = b.ld_t; d.sCt = b.vt_stride;
+    }
+    d.M = n; d.N = m; d.K = direction ? 2 * n : n;
+    return d;
+  };
+  GemmDesc probe = update(true, 0, false, false);
+  const bool km = gemm_kmajor_ok(probe);
+  int cur = 0;
+  for (int t = 0; t < T; ++t) {
+    const bool last = t == T - 1;
+    const double a = abc[3 * t], bb = abc[3 * t + 1], cc = abc[3 * t + 2];
+    const void* E = b.V[cur];
+    const void* X = at(b.V[cur], xoff);
+    GemmDesc gram = square(X, X, g.ld_x, b.v_stride, m, b.A);
+    gram.sym = true;
+    gram.alpha = 1.0f / (g.S * g.S);
+    MNS_HIP(timed_gemm(gram, nn * g.m, s));
+    GemmDesc cross = square(E, X, g.ld_x, b.v_stride, m, b.K);
+    cross.alpha = (float)(sc[t].kap / (sc[t].e * g.S));
+    MNS_HIP(timed_gemm(cross, 2.0 * nn * g.m, s));
+    MNS_HIP(timed("symmetrise", 0, nn * 2.0 * es, s, [&] {
+      return symmetrise(b.K, g.ld_q, b.q_stride, nullptr, 0, 0, b.Ssym, g.ld_q, b.q_stride, g.elem,
+                        c, g.n_p, 0.f, 1.f, s); }));
+    GemmDesc poly = square(b.A, b.A, g.ld_q, b.q_stride, n, b.PQ);
+    poly.ldc = b.ld_t; poly.sC = b.pq_stride;
+    poly.sym = true;
+    poly.alpha = (float)(sc[t].p * cc);
+    poly.beta = (float)(sc[t].p * bb);
+    poly.D = b.A; poly.ldd = g.ld_q; poly.sD = b.q_stride;
+    poly.gamma = (float)(sc[t].p * a);
+    poly.diag_limit = (int)g.n;
+    MNS_HIP(timed_gemm(poly, nn * g.n, s));
+    MNS_HIP(timed_gemm(square(b.A, b.Ssym, g.ld_q, b.q_stride, n, b.K), 2.0 * nn * g.n, s));
+    const double qk = sc[t].q / sc[t].kap;
+    MNS_HIP(timed("symmetrise", 0, nn * 3.0 * es, s, [&] {
+      return symmetrise(b.K, g.ld_q, b.q_stride, b.Ssym, g.ld_q, b.q_stride, at(b.PQ, g.n_p),
+                        b.ld_t, b.pq_stride, g.elem, c, g.n_p, (float)(qk * bb), (float)(qk * cc),
+                        s); }));
+    GemmDesc dir = update(true, cur, km, last);
+    dir.alpha = (float)(sc[t + 1].e / (sc[t].p * sc[t].e));
+    MNS_HIP(timed_gemm(dir, 4.0 * nn * g.m, s));
+    if (!last) {
+      GemmDesc upd = update(false, cur, km, false);
+      upd.alpha = (float)(1.0 / sc[t].p);
+      MNS_HIP(timed_gemm(upd, 2.0 * nn * g.m, s));
+    }
+    cur ^= 1;
+  }
+  *out = g.tall ? b.Vt[cur] : b.V[cur];
+  return MNS_OK;
+}
+
+mns_status mns_ns_backward_workspace_size(int dtype, int64_t batch, int64_t rows, int64_t cols,
+                                          size_t* bytes) {
+  if (!bytes) return MNS_ERR_NULL;
+  const mns_status st = nsb_check(dtype, batch, rows, cols);
+  if (st != MNS_OK) return st;
+  NsbBuffers b;
+  *bytes = carve_nsb(nullptr, nsb_geo(rows, cols, store_of(dtype)),
+                     batch < kChunk ? (int)batch : kChunk, b);
+  return MNS_OK;
+}
+
+mns_status ns_orthogonalize_backward(const void* X, const void* dO, void* dX, int dtype,
+                                     int64_t batch, int64_t rows, int64_t cols, int T,
+                                     const float* abc, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  mns_status st = nsb_check(dtype, batch, rows, cols);
+  if (st != MNS_OK) return st;
+  if (!X || !dO || !dX) return MNS_ERR_NULL;
+  st = check_ns(T, abc, MNS_NS_STANDARD, 0u);
+  if (st != MNS_OK) return st;
+  if (!aligned(X, 16) || !aligned(dO, 16) || !aligned(dX, 16)) return MNS_ERR_PARAM;
+  const Store sto = store_of(dtype);
+  const Geo g = nsb_geo(rows, cols, sto);
+  NsbScale sc[kMaxT + 1];
+  if (!nsb_plan(T, abc, g, sc)) return MNS_ERR_PARAM;
+  const int cmax = batch < kChunk ? (int)batch : kChunk;
+  NsbBuffers b;
+  st = check_ws(workspace, workspace_bytes, carve_nsb(nullptr, g, cmax, b));
+  if (st != MNS_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const size_t esz = store_bytes(dtype);
+  const int nblk = norm_blocks(rows * cols);
+  for (int64_t b0 = 0; b0 < batch; b0 += cmax) {
+    const int c = (int)((batch - b0) < cmax ? batch - b0 : cmax);
+    carve_nsb(workspace, g, c, b);
+    const size_t off = (size_t)b0 * rows * cols * esz;
+    const char* x = static_cast<const char*>(X) + off;
+    const char* go = static_cast<const char*>(dO) + off;
+    char* dx = static_cast<char*>(dX) + off;
+    const double all = (double)c * rows * cols, ss = (double)esz, es = elem_bytes(g.elem);
+    MNS_HIP(timed("sumsq", 0, all * ss, s, [&] {
+      return sumsq(x, sto, c, rows * cols, b.px, s); }));
+    MNS_HIP(timed("sumsq", 0, all * ss, s, [&] {
+      return sumsq(go, sto, c, rows * cols, b.pg, s); }));
+    MNS_HIP(timed("nsb_scales", 0, 16.0 * c * nblk, s, [&] {
+      return nsb_scales(b.px, b.pg, nblk, c, g.S, sc[0].e, b.scale, s); }));
+    const NsbDst v{b.V[0], g.ld_x, b.v_stride, g.n_p * g.ld_x};
+    const NsbDst vt{b.Vt[0], b.ld_t, b.vt_stride, g.n_p};
+    MNS_HIP(timed("nsb_load", 0, all * 2.0 * (ss + 2.0 * es), s, [&] {
+      return nsb_load(x, go, sto, c, rows, cols, b.scale, g.elem, g.rows_p, g.cols_p,
+                      g.tall ? vt : v, g.tall ? v : vt, s); }));
+    void* E = nullptr;
+    st = run_nsb(g, c, b, T, abc, sc, s, &E);
+    if (st != MNS_OK) return st;
+    MNS_HIP(timed("nsb_finish", 0, all * (3.0 * ss + 2.0 * es), s, [&] {
+      return nsb_finish(x, sto, E, g.elem, c, rows, cols, g.tall ? b.ld_t : g.ld_x,
+                        g.tall ? b.vt_stride : b.v_stride, b.dot, b.scale, 1.0 / sc[T].e, dx, s); }));
+  }
+  return MNS_OK;
+}
+
 mns_status mns_profile_begin(void) {
   std::lock_guard<std::mutex> lk(g_prof_mu);
   for (ProfRec& r : g_prof) {

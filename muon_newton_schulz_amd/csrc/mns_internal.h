@@ -195,4 +195,31 @@ hipError_t gather_normalize(const PtrPack& M, int count, int64_t k, int64_t cols
                             const int32_t* S, float mu, const float* xscale, Elem e, void* X,
                             void* Xt, int64_t rows_p, int64_t cols_p, hipStream_t s);
 
+// ---------------------------------------------------------------------------------------
+// Newton-Schulz gradient (ns_backward.hip); matrices of count consecutive rows x cols buffers.
+// ---------------------------------------------------------------------------------------
+// scale[4 b ..] = S / ||X_b||, 1 / ||X_b||, e0 / ||dO_b||, ||dO_b|| (zeros for a zero norm) from
+// the sumsq() partials of X and dO.
+hipError_t nsb_scales(const double* px, const double* pg, int nblk, int count, double S, double e0,
+                      double* scale, hipStream_t s);
+// Where nsb_load writes source element (r, c): p[b * stride + which * offset + r * ld + c]
+// (straight) or [... + c * ld + r] (transposed); which = 0 for dO, 1 for X. p null: not written.
+struct NsbDst {
+  void* p = nullptr;
+  int64_t ld = 0, stride = 0, offset = 0;
+};
+hipError_t nsb_load(const void* X, const void* G, Store st, int count, int64_t rows, int64_t cols,
+                    const double* scale, Elem e, int64_t rows_p, int64_t cols_p,
+                    const NsbDst& straight, const NsbDst& transposed, hipStream_t s);
+// C = beta D + gamma (K + K^T) for n_p x n_p matrices (D symmetric, may be null: 0).
+hipError_t symmetrise(const void* K, int64_t ldk, int64_t sK, const void* D, int64_t ldd,
+                      int64_t sD, void* C, int64_t ldc, int64_t sC, Elem e, int count, int64_t n_p,
+                      float beta, float gamma, hipStream_t s);
+// out = (E' - X_0 <X_0, E'>) / ||X|| with E' = E ||dO|| inv_eT, E in the stored layout (row pitch
+// ld, matrix stride sE). part: count * nsb_dot_blocks(rows) doubles.
+int nsb_dot_blocks(int64_t rows);
+hipError_t nsb_finish(const void* X, Store st, const void* E, Elem e, int count, int64_t rows,
+                      int64_t cols, int64_t ld, int64_t sE, double* part, const double* scale,
+                      double inv_eT, void* out, hipStream_t s);
+
 }  // namespace mns

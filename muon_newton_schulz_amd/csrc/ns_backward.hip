@@ -1,0 +1,277 @@
+// Memory-bound kernels of the Newton-Schulz gradient (ns_orthogonalize_backward); its products
+// run on the GEMM of gemm.hip.
+//
+// O = NS_T(X / ||X||_F) acts on the singular values alone, so its derivative at X_0 = X / ||X||
+// is symmetric as a linear map: in the singular basis it scales the symmetric part of a direction
+// by (f_i - f_j) / (s_i - s_j), the skew part by (f_i + f_j) / (s_i + s_j) and the rectangular
+// part by f_i / s_i. The gradient J^T dO therefore equals the derivative J dO in the direction
+// dO, which is carried along the iteration instead of walking back through stored iterates:
+//
+//   A = X X^T,  S = E X^T + X E^T,  P = a I + b A + c A^2,  Q = b S + c (A S + S A),
+//   E <- P E + Q X,  X <- P X              (E_0 = dO)
+//
+// and dX = (E_T - X_0 <X_0, E_T>) / ||X||, the normalisation's (symmetric) derivative.
+#include "mns_internal.h"
+
+namespace mns {
+namespace {
+
+constexpr int kT = 64;      // tile of the transposing kernels
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float widen(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ void narrow(double v, float* o) { *o = (float)v; }
+// float64 -> bfloat16 through float32, to odd: the float32 value is forced to the odd neighbour
+// when inexact, so that the second rounding (to nearest even) sees which side it came from and
+// the result is the one rounding of v.
+__device__ __forceinline__ void narrow(double v, uint16_t* o) {
+  float f = (float)v;
+  uint32_t u = __float_as_uint(f);
+  if (f != f) {
+    *o = 0x7FC0;
+    return;
+  }
+  const double back = (double)f;
+  if (back != v && isfinite(f)) {
+    if (fabs(back) > fabs(v)) --u;     // truncate towards zero ...
+    u |= 1u;                           // ... and make it odd
+  }
+  u += 0x7FFFu + ((u >> 16) & 1u);
+  *o = (uint16_t)(u >> 16);
+}
+
+// scale[4 b ..]: S / ||X||, 1 / ||X||, e0 / ||dO||, ||dO|| of matrix b (zeros for a zero norm),
+// from nblk partial sums of squares of X and, behind them, of dO.
+__global__ __launch_bounds__(kThreads) void k_nsb_scales(const double* px, const double* pg,
+                                                         int nblk, double S, double e0,
+                                                         double* scale) {
+  __shared__ double red[2][kThreads];
+  const int b = blockIdx.x;
+  double sx = 0.0, sg = 0.0;
+  for (int i = threadIdx.x; i < nblk; i += kThreads) {
+    sx += px[(int64_t)b * nblk + i];
+    sg += pg[(int64_t)b * nblk + i];
+  }
+  red[0][threadIdx.x] = sx;
+  red[1][threadIdx.x] = sg;
+  __syncthreads();
+  for (int o = kThreads / 2; o > 0; o >>= 1) {
+    if ((int)threadIdx.x < o) {
+      red[0][threadIdx.x] += red[0][threadIdx.x + o];
+      red[1][threadIdx.x] += red[1][threadIdx.x + o];
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    const double nx = sqrt(red[0][0]), ng = sqrt(red[1][0]);
+    scale[4 * b] = nx == 0.0 ? 0.0 : S / nx;
+    scale[4 * b + 1] = nx == 0.0 ? 0.0 : 1.0 / nx;
+    scale[4 * b + 2] = ng == 0.0 ? 0.0 : e0 / ng;
+    scale[4 * b + 3] = ng;
+  }
+}
+
+// E_0 and X_0 (scaled, zero padded) from dO and X, in either layout or both. Destination
+// elements: straight[b * stride + which * offset + r * ld + c] for source element (r, c), and
+// likewise transposed[... + c * ld + r]; which = 0 for dO (E), 1 for X.
+struct LoadDst {
+  void* p;
+  int64_t ld, stride, offset;
+};
+template <typename TX, typename TO>
+__global__ __launch_bounds__(kThreads) void k_nsb_load(const TX* X, const TX* G, int64_t rows,
+                                                       int64_t cols, int64_t elems,
+                                                       const double* scale, LoadDst st,
+                                                       LoadDst tr) {
+  __shared__ TO tile[kT][kT + 2];
+  const int b = blockIdx.z >> 1, which = blockIdx.z & 1;
+  const int64_t r0 = (int64_t)blockIdx.y * kT, c0 = (int64_t)blockIdx.x * kT;
+  const TX* src = (which ? X : G) + b * elems;
+  const double sc = scale[4 * b + (which ? 0 : 2)];
+  const int lx = threadIdx.x % kT, ly = threadIdx.x / kT;
+#pragma unroll
+  for (int i = 0; i < kT; i += kThreads / kT) {
+    const int64_t r = r0 + ly + i, c = c0 + lx;
+    double v = 0.0;
+    if (r < rows && c < cols) v = (double)widen(src[r * cols + c]) * sc;
+    const TO o = (TO)(float)v;
+    if (st.p) static_cast<TO*>(st.p)[b * st.stride + which * st.offset + r * st.ld + c] = o;
+    tile[ly + i][lx] = o;
+  }
+  if (!tr.p) return;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kT; i += kThreads / kT) {
+    const int64_t r = r0 + lx, c = c0 + ly + i;
+    static_cast<TO*>(tr.p)[b * tr.stride + which * tr.offset + c * tr.ld + r] = tile[lx][ly + i];
+  }
+}
+
+// C = beta D + gamma (K + K^T): tile pairs (i, j) and (j, i), i <= j, one block each pair. D is
+// symmetric and read at (i, j) only; C is exactly symmetric.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_symmetrise(const T* K, int64_t ldk, int64_t sK,
+                                                         const T* D, int64_t ldd, int64_t sD, T* C,
+                                                         int64_t ldc, int64_t sC, float beta,
+                                                         float gamma) {
+  __shared__ float tile[kT][kT + 1];
+  // pair index -> (i, j), i <= j: column j holds j + 1 pairs
+  const int t = blockIdx.x;
+  int j = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+  while ((j + 1) * (j + 2) / 2 <= t) ++j;
+  while (j * (j + 1) / 2 > t) --j;
+  const int i = t - j * (j + 1) / 2;
+  const int b = blockIdx.y;
+  const T* k = K + b * sK;
+  T* c = C + b * sC;
+  const int lx = threadIdx.x % kT, ly = threadIdx.x / kT;
+  float v[kT * kT / kThreads];
+#pragma unroll
+  for (int q = 0; q < kT * kT / kThreads; ++q) {
+    const int r = ly + q * (kThreads / kT);
+    v[q] = (float)k[(int64_t)(i * kT + r) * ldk + j * kT + lx];
+    tile[r][lx] = (float)k[(int64_t)(j * kT + r) * ldk + i * kT + lx];
+  }
+  __syncthreads();
+  float o[kT * kT / kThreads];
+#pragma unroll
+  for (int q = 0; q < kT * kT / kThreads; ++q) {
+    const int r = ly + q * (kThreads / kT);
+    o[q] = gamma * (v[q] + tile[lx][r]);
+    if (D) o[q] += beta * (float)D[b * sD + (int64_t)(i * kT + r) * ldd + j * kT + lx];
+    c[(int64_t)(i * kT + r) * ldc + j * kT + lx] = (T)o[q];
+  }
+  if (i == j) return;
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kT * kT / kThreads; ++q) tile[ly + q * (kThreads / kT)][lx] = o[q];
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kT * kT / kThreads; ++q) {
+    const int r = ly + q * (kThreads / kT);
+    c[(int64_t)(j * kT + r) * ldc + i * kT + lx] = (T)tile[lx][r];
+  }
+}
+
+// Partial sums of <X, E> (E in the stored layout, padded rows), float64: block x of nblk takes
+// rows x, x + nblk, ...
+template <typename TX, typename TE>
+__global__ __launch_bounds__(kThreads) void k_nsb_dot(const TX* X, const TE* E, int64_t rows,
+                                                      int64_t cols, int64_t ld, int64_t sE,
+                                                      double* part) {
+  __shared__ double red[kThreads];
+  const int b = blockIdx.y;
+  double s = 0.0;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const TX* x = X + ((int64_t)b * rows + r) * cols;
+    const TE* e = E + b * sE + r * ld;
+    for (int64_t c = threadIdx.x; c < cols; c += kThreads) s += (double)widen(x[c]) * (double)(float)e[c];
+  }
+  red[threadIdx.x] = s;
+  __syncthreads();
+  for (int o = kThreads / 2; o > 0; o >>= 1) {
+    if ((int)threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) part[(int64_t)b * gridDim.x + blockIdx.x] = red[0];
+}
+
+// dX = (E - X_0 <X_0, E>) / ||X|| with E = E_T ||dO|| / eT: float64 arithmetic (norms of any
+// float32 range, one rounding at the end; the pass is bound by its bytes).
+template <typename TX, typename TE>
+__global__ __launch_bounds__(kThreads) void k_nsb_project(const TX* X, const TE* E, int64_t rows,
+                                                          int64_t cols, int64_t ld, int64_t sE,
+                                                          const double* part, int nblk,
+                                                          const double* scale, double inv_eT,
+                                                          TX* out) {
+  __shared__ double red[kThreads];
+  const int b = blockIdx.y;
+  double s = 0.0;
+  for (int i = threadIdx.x; i < nblk; i += kThreads) s += part[(int64_t)b * nblk + i];
+  red[threadIdx.x] = s;
+  __syncthreads();
+  for (int o = kThreads / 2; o > 0; o >>= 1) {
+    if ((int)threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
+    __syncthreads();
+  }
+  const double ix = scale[4 * b + 1], fe = scale[4 * b + 3] * inv_eT * ix;
+  const double cx = -red[0] * ix * ix * fe;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const TX* x = X + ((int64_t)b * rows + r) * cols;
+    const TE* e = E + b * sE + r * ld;
+    TX* o = out + ((int64_t)b * rows + r) * cols;
+    for (int64_t c = threadIdx.x; c < cols; c += kThreads)
+      narrow((double)(float)e[c] * fe + (double)widen(x[c]) * cx, &o[c]);
+  }
+}
+
+hipError_t last() { return hipGetLastError(); }
+
+}  // namespace
+
+hipError_t nsb_scales(const double* px, const double* pg, int nblk, int count, double S, double e0,
+                      double* scale, hipStream_t s) {
+  hipLaunchKernelGGL(k_nsb_scales, dim3(count), dim3(kThreads), 0, s, px, pg, nblk, S, e0, scale);
+  return last();
+}
+
+hipError_t nsb_load(const void* X, const void* G, Store st, int count, int64_t rows, int64_t cols,
+                    const double* scale, Elem e, int64_t rows_p, int64_t cols_p,
+                    const NsbDst& straight, const NsbDst& transposed, hipStream_t s) {
+  const dim3 grid((unsigned)(cols_p / kT), (unsigned)(rows_p / kT), 2 * count);
+  const LoadDst a{straight.p, straight.ld, straight.stride, straight.offset};
+  const LoadDst t{transposed.p, transposed.ld, transposed.stride, transposed.offset};
+  const int64_t n = rows * cols;
+#define MNS_NSB_LOAD(TX, TO)                                                              \
+  hipLaunchKernelGGL((k_nsb_load<TX, TO>), grid, dim3(kThreads), 0, s,                    \
+                     static_cast<const TX*>(X), static_cast<const TX*>(G), rows, cols, n, \
+                     scale, a, t)
+  if (st == Store::F32) MNS_NSB_LOAD(float, float);
+  else if (e == Elem::F32) MNS_NSB_LOAD(uint16_t, float);
+  else MNS_NSB_LOAD(uint16_t, _Float16);
+#undef MNS_NSB_LOAD
+  return last();
+}
+
+hipError_t symmetrise(const void* K, int64_t ldk, int64_t sK, const void* D, int64_t ldd,
+                      int64_t sD, void* C, int64_t ldc, int64_t sC, Elem e, int count, int64_t n_p,
+                      float beta, float gamma, hipStream_t s) {
+  const int t = (int)(n_p / kT);
+  const dim3 grid(t * (t + 1) / 2, count);
+  if (e == Elem::F16)
+    hipLaunchKernelGGL(k_symmetrise<_Float16>, grid, dim3(kThreads), 0, s,
+                       static_cast<const _Float16*>(K), ldk, sK, static_cast<const _Float16*>(D),
+                       ldd, sD, static_cast<_Float16*>(C), ldc, sC, beta, gamma);
+  else
+    hipLaunchKernelGGL(k_symmetrise<float>, grid, dim3(kThreads), 0, s,
+                       static_cast<const float*>(K), ldk, sK, static_cast<const float*>(D), ldd,
+                       sD, static_cast<float*>(C), ldc, sC, beta, gamma);
+  return last();
+}
+
+int nsb_dot_blocks(int64_t rows) { return (int)(rows < 512 ? rows : 512); }
+
+hipError_t nsb_finish(const void* X, Store st, const void* E, Elem e, int count, int64_t rows,
+                      int64_t cols, int64_t ld, int64_t sE, double* part, const double* scale,
+                      double inv_eT, void* out, hipStream_t s) {
+  const int nblk = nsb_dot_blocks(rows);
+  const dim3 dot(nblk, count), proj((unsigned)(rows < 2048 ? rows : 2048), count);
+#define MNS_NSB_FINISH(TX, TE)                                                                  \
+  do {                                                                                          \
+    hipLaunchKernelGGL((k_nsb_dot<TX, TE>), dot, dim3(kThreads), 0, s, static_cast<const TX*>(X), \
+                       static_cast<const TE*>(E), rows, cols, ld, sE, part);                    \
+    const hipError_t err = last();                                                              \
+    if (err != hipSuccess) return err;                                                          \
+    hipLaunchKernelGGL((k_nsb_project<TX, TE>), proj, dim3(kThreads), 0, s,                     \
+                       static_cast<const TX*>(X), static_cast<const TE*>(E), rows, cols, ld, sE, \
+                       part, nblk, scale, inv_eT, static_cast<TX*>(out));                       \
+  } while (0)
+  if (st == Store::F32) MNS_NSB_FINISH(float, float);
+  else if (e == Elem::F32) MNS_NSB_FINISH(uint16_t, float);
+  else MNS_NSB_FINISH(uint16_t, _Float16);
+#undef MNS_NSB_FINISH
+  return last();
+}
+
+}  // namespace mns
