@@ -254,6 +254,24 @@ mns_status grouped_weight_grad(const void* dY, int64_t lddy, const void* X, int6
                                void* G, int out_dtype, void* workspace, size_t workspace_bytes,
                                void* stream);
 
+/* Workspace bytes muon_step_grouped needs. */
+mns_status mns_grouped_step_workspace_size(int64_t groups, int64_t total_rows, int64_t rows,
+                                           int64_t cols, const mns_hparams* hp,
+                                           size_t* bytes /* (host) out */);
+
+/* muon_step of a stack of experts whose gradients are given as tokens, G_e = dY_e^T X_e, and never
+ * formed: M_e <- mu M_e + dY_e^T X_e in the product's epilogue (float32 sums, not rounded to the
+ * storage dtype in between), then X_0 = M_e / ||M_e||_F, O = NS_T(X_0) and the update of W_e (Muon
+ * or NorMuon) as in muon_step, for every expert, those without rows (G_e = 0) too.
+ *   W  in/out  hp->dtype [groups][rows][cols];  M  in/out  float32, the same shape
+ *   v  in/out  float32 [groups][rows], NorMuon only (else may be NULL)
+ *   dY in  hp->dtype, total_rows x rows, pitch lddy;  X  in  hp->dtype, total_rows x cols, pitch ldx
+ *   offsets, sizes and pitches as for grouped_weight_grad; hp->row_fraction must be 1. */
+mns_status muon_step_grouped(void* W, float* M, float* v, const void* dY, int64_t lddy,
+                             const void* X, int64_t ldx, const int64_t* offsets, int64_t groups,
+                             int64_t total_rows, int64_t rows, int64_t cols, const mns_hparams* hp,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- Instrumentation ---------------------------------------------------------------------
  * Between mns_profile_begin() and mns_profile_end() every kernel launch the library makes is
  * bracketed by a pair of hipEvents recorded on the launch's stream. mns_profile_end() waits

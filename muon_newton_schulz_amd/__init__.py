@@ -20,7 +20,8 @@ from ._abi import (MNS_BF16, MNS_F32, MNS_NS_GRAM, MNS_NS_STANDARD, MnsError,  #
 __all__ = ["muon_step", "ns_orthogonalize", "ns_orthogonalize_noalloc",
            "gram_ns_orthogonalize", "normuon_scale",
            "ns_orthogonalize_backward", "ns_backward_workspace_size",
-           "grouped_matmul", "grouped_weight_grad",
+           "grouped_matmul", "grouped_weight_grad", "muon_step_grouped",
+           "grouped_step_workspace_size",
            "step_workspace_size", "ns_workspace_size", "normuon_workspace_size",
            "restart_mask", "profile_begin", "profile_set_flush", "profile_end", "MnsError",
            "load"]
@@ -496,6 +497,77 @@ def grouped_weight_grad(dY: torch.Tensor, X: torch.Tensor, offsets: torch.Tensor
                                          MNS_F32 if out_dtype == torch.float32 else MNS_BF16, ws,
                                          nbytes, handle), what)
     return G
+
+
+def _grouped_step(W, M, dY, X, offsets, v, normuon, what):
+    """Checks of muon_step_grouped's tensors: device, sizes and row pitches."""
+    if W.dim() != 3 or W.shape != M.shape:
+        raise ValueError(f"{what}: W and M must be 3-D stacks (experts, rows, cols) of one shape")
+    _dtype_code(W)
+    if M.dtype != torch.float32:
+        raise TypeError(f"{what}: momentum must be float32")
+    if dY.dtype != W.dtype or X.dtype != W.dtype:
+        raise TypeError(f"{what}: W, dY and X must share one storage dtype (W {W.dtype}, "
+                        f"dY {dY.dtype}, X {X.dtype})")
+    groups, rows, cols = W.shape
+    if dY.dim() != 2 or X.dim() != 2 or dY.shape[0] != X.shape[0]:
+        raise ValueError(f"{what}: dY and X must be 2-D with the same rows")
+    if dY.shape[1] != rows or X.shape[1] != cols:
+        raise ValueError(f"{what}: dY must have rows of {rows} and X of {cols}")
+    if normuon and v is None:
+        raise ValueError("NorMuon needs v (float32, one entry per expert and row)")
+    if v is not None and (v.dtype != torch.float32 or tuple(v.shape) != (groups, rows)):
+        raise ValueError(f"{what}: v must be float32 of shape ({groups}, {rows})")
+    state = [t for t in (W, M, v) if t is not None]
+    if not all(t.is_contiguous() for t in state):
+        raise ValueError(f"{what}: W, M and v must be contiguous")
+    lddy, ldx = _pitch(dY, "dY", what), _pitch(X, "X", what)
+    for i, a in enumerate(state):
+        for b in state[i + 1:] + [dY, X, offsets]:
+            if not _apart(a, b):
+                raise ValueError(f"{what}: W, M and v may not overlap each other or the inputs")
+    dev = _grouped_checks([("dY", dY), ("X", X)], state, offsets, groups, what)
+    return dev, groups, X.shape[0], rows, cols, lddy, ldx
+
+
+def grouped_step_workspace_size(W, M, dY, X, offsets, v=None, *, mu=0.95, lr=0.02, coeffs,
+                                kind="standard", restart_before=(), normuon=False, beta2=0.95,
+                                eps=1e-8) -> int:
+    what = "grouped_step_workspace_size"
+    hp, _keep = _hparams(_dtype_code(W), mu, lr, coeffs, kind, restart_before, normuon, beta2, eps,
+                         1.0)
+    _dev, groups, total, rows, cols, _a, _b = _grouped_step(W, M, dY, X, offsets, v, normuon, what)
+    out = ctypes.c_size_t(0)
+    check(load().mns_grouped_step_workspace_size(groups, total, rows, cols, ctypes.byref(hp),
+                                                 ctypes.byref(out)),
+          "mns_grouped_step_workspace_size")
+    return out.value
+
+
+def muon_step_grouped(W, M, dY, X, offsets, v=None, *, mu: float, lr: float, coeffs,
+                      kind: str = "standard", restart_before=(), normuon: bool = False,
+                      beta2: float = 0.95, eps: float = 1e-8,
+                      workspace: torch.Tensor | None = None, stream=None) -> None:
+    """One optimizer step, in place on W, M (and v), for a stack of experts (experts, rows, cols)
+    whose gradients dY_e^T X_e are given by their tokens, sorted by expert as in grouped_matmul,
+    and are never formed: the product adds them to the float32 momentum. M is a float32 stack like
+    W, v float32 (experts, rows). Otherwise as muon_step (no row selection)."""
+    what = "muon_step_grouped"
+    hp, _keep = _hparams(_dtype_code(W), mu, lr, coeffs, kind, restart_before, normuon, beta2, eps,
+                         1.0)
+    dev, groups, total, rows, cols, lddy, ldx = _grouped_step(W, M, dY, X, offsets, v, normuon,
+                                                              what)
+    lib = load()
+    need = ctypes.c_size_t(0)
+    check(lib.mns_grouped_step_workspace_size(groups, total, rows, cols, ctypes.byref(hp),
+                                              ctypes.byref(need)),
+          "mns_grouped_step_workspace_size")
+    with _OnStream(dev, stream) as handle:
+        ws = _workspace(need.value, dev, workspace)
+        check(lib.muon_step_grouped(W.data_ptr(), M.data_ptr(), None if v is None else v.data_ptr(),
+                                    dY.data_ptr(), lddy, X.data_ptr(), ldx, offsets.data_ptr(),
+                                    groups, total, rows, cols, ctypes.byref(hp), ws.data_ptr(),
+                                    ws.numel() * ws.element_size(), handle), what)
 
 
 def ns_backward_workspace_size(X: torch.Tensor) -> int:

@@ -27,6 +27,7 @@ EXPORTS = (
     "mns_normuon_workspace_size", "normuon_scale", "mns_profile_begin", "mns_profile_end",
     "mns_profile_set_flush", "ns_orthogonalize_noalloc",
     "mns_grouped_workspace_size", "grouped_matmul", "grouped_weight_grad",
+    "mns_grouped_step_workspace_size", "muon_step_grouped",
     "mns_ns_backward_workspace_size", "ns_orthogonalize_backward",
 )
 
@@ -135,6 +136,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mns_ns_backward_workspace_size.argtypes = [ci, i64, i64, i64, sz]
     lib.ns_orthogonalize_backward.restype = ci
     lib.ns_orthogonalize_backward.argtypes = [vp, vp, vp, ci, i64, i64, i64, ci, fp, vp, csz, vp]
+    hpp = ctypes.POINTER(MnsHparams)
+    lib.mns_grouped_step_workspace_size.restype = ci
+    lib.mns_grouped_step_workspace_size.argtypes = [i64, i64, i64, i64, hpp, sz]
+    lib.muon_step_grouped.restype = ci
+    lib.muon_step_grouped.argtypes = [vp, vp, vp, vp, i64, vp, i64, vp, i64, i64, i64, i64, hpp, vp,
+                                      csz, vp]
     lib.mns_profile_set_flush.restype = ctypes.c_int
     lib.mns_profile_set_flush.argtypes = [vp, ctypes.c_size_t]
     _lib = lib

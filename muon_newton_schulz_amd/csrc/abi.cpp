@@ -524,6 +524,72 @@ size_t step_bytes(const mns_matrix* mats, int count, const mns_hparams* hp) {
   return need;
 }
 
+// One chunk of c matrices of one shape: the momentum and its norm, the Newton-Schulz iterations on
+// g (k x cols) and the weight update. With Gp null the momentum already holds its new values,
+// the c matrices of M consecutive from M_base (never with Dion3's row selection).
+mns_status step_chunk(const Geo& g, int c, int64_t rows, int64_t cols, int64_t k,
+                      const mns_hparams* hp, const PtrPack& Wp, const PtrPack& Mp,
+                      const PtrPack* Gp, const float* M_base, const PtrPack& Vp, void* workspace,
+                      hipStream_t s) {
+  const Store sto = hp->dtype == MNS_BF16 ? Store::BF16 : Store::F32;
+  const bool dion = hp->row_fraction < 1.0;
+  StepWs w;
+  carve_step(workspace, g, c, rows, cols, dion, k, hp->kind, w);
+  const bool km = kmajor_ns(g, c, w.ns);
+
+  const double all = (double)c * rows * cols;      // elements of the chunk's matrices
+  const double sel = (double)c * k * cols;         // elements the NS runs on
+  const double es = elem_bytes(g.elem), ss = sto == Store::BF16 ? 2.0 : 4.0;
+  if (!dion) {
+    if (Gp) {
+      MNS_HIP(timed("momentum", 0, all * (8.0 + ss), s, [&] {
+        return momentum(Mp, *Gp, sto, c, rows * cols, hp->mu, w.partials, s); }));
+    } else {
+      MNS_HIP(timed("sumsq", 0, all * 4.0, s, [&] {
+        return sumsq(M_base, Store::F32, c, rows * cols, w.partials, s); }));
+    }
+    MNS_HIP(timed("finalize_scale", 0, 4.0 * c * w.nblk, s, [&] {
+      return finalize_scale(w.partials, w.nblk, c, g.S, w.xscale, s); }));
+    MNS_HIP(timed("normalize", 0, all * (4.0 + (km ? 1.0 : 2.0) * es), s, [&] {
+      return normalize(&Mp, nullptr, true, sto, c, rows, cols, w.xscale, g.elem,
+                       straight(g, w.ns, km), transposed(g, w.ns, km), g.rows_p,
+                       g.cols_p, s); }));
+  } else {
+    MNS_HIP(timed("momentum_l1", 0, all * (8.0 + ss), s, [&] {
+      return momentum_l1(Mp, *Gp, sto, c, rows, cols, w.l1, w.l2sq, s); }));
+    MNS_HIP(timed("topk", 0, 8.0 * c * rows + 8.0 * c * k, s, [&] {
+      return topk_rows(w.l1, w.l2sq, c, rows, k, g.S, w.S, w.xscale, s); }));
+    MNS_HIP(timed("gather_normalize", 0, sel * (8.0 + (km ? 1.0 : 2.0) * es), s, [&] {
+      return gather_normalize(Mp, c, k, cols, w.S, hp->mu, w.xscale, g.elem,
+                              straight(g, w.ns, km), transposed(g, w.ns, km), g.rows_p,
+                       g.cols_p, s); }));
+  }
+  void* O = nullptr;
+  RowSq rs;
+  rs.part = w.part;
+  rs.rows = (int)k;
+  const mns_status st = run_ns(g, c, w.ns, hp->kind, hp->T, hp->abc, hp->restart_mask, s, &O,
+              hp->normuon ? &rs : nullptr);
+  if (st != MNS_OK) return st;
+  const float inv_s = 1.0f / g.S;
+  if (hp->normuon) {
+    // The row statistics come from the epilogue of the product that wrote the result
+    // (every run ends with one: T >= 1).
+    if (!rs.done) return MNS_ERR_PARAM;
+    MNS_HIP(timed("normuon_finalize", 0, 4.0 * c * k * (w.chunks + 3), s, [&] {
+      return normuon_finalize(w.part, w.chunks, c, k, cols, &Vp, nullptr, 0,
+                              dion ? w.S : nullptr, hp->beta2, hp->eps, inv_s * inv_s, inv_s,
+                              w.rowscale, w.fin, s); }));
+  } else {
+    MNS_HIP(timed("fill", 0, 4.0 * c * k, s, [&] {
+      return fill(w.rowscale, (int64_t)c * k, inv_s, s); }));
+  }
+  MNS_HIP(timed("weight_update", 0, sel * (2.0 * ss + es) + 4.0 * c * k, s, [&] {
+    return weight_update(Wp, sto, c, k, cols, O, g.elem, g.rows_p, g.cols_p, w.rowscale,
+                         dion ? w.S : nullptr, k, hp->lr, s); }));
+  return MNS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -576,55 +642,8 @@ mns_status muon_step(const mns_matrix* mats, int count, const mns_hparams* hp, v
         Gp.p[i] = const_cast<void*>(mm.G);
         Vp.p[i] = mm.v;
       }
-      StepWs w;
-      carve_step(workspace, g, c, rows, cols, dion, k, hp->kind, w);
-      const bool km = kmajor_ns(g, c, w.ns);
-
-      const double all = (double)c * rows * cols;      // elements of the chunk's matrices
-      const double sel = (double)c * k * cols;         // elements the NS runs on
-      const double es = elem_bytes(g.elem), ss = sto == Store::BF16 ? 2.0 : 4.0;
-      if (!dion) {
-        MNS_HIP(timed("momentum", 0, all * (8.0 + ss), s, [&] {
-          return momentum(Mp, Gp, sto, c, rows * cols, hp->mu, w.partials, s); }));
-        MNS_HIP(timed("finalize_scale", 0, 4.0 * c * w.nblk, s, [&] {
-          return finalize_scale(w.partials, w.nblk, c, g.S, w.xscale, s); }));
-        MNS_HIP(timed("normalize", 0, all * (4.0 + (km ? 1.0 : 2.0) * es), s, [&] {
-          return normalize(&Mp, nullptr, true, sto, c, rows, cols, w.xscale, g.elem,
-                           straight(g, w.ns, km), transposed(g, w.ns, km), g.rows_p,
-                           g.cols_p, s); }));
-      } else {
-        MNS_HIP(timed("momentum_l1", 0, all * (8.0 + ss), s, [&] {
-          return momentum_l1(Mp, Gp, sto, c, rows, cols, w.l1, w.l2sq, s); }));
-        MNS_HIP(timed("topk", 0, 8.0 * c * rows + 8.0 * c * k, s, [&] {
-          return topk_rows(w.l1, w.l2sq, c, rows, k, g.S, w.S, w.xscale, s); }));
-        MNS_HIP(timed("gather_normalize", 0, sel * (8.0 + (km ? 1.0 : 2.0) * es), s, [&] {
-          return gather_normalize(Mp, c, k, cols, w.S, hp->mu, w.xscale, g.elem,
-                                  straight(g, w.ns, km), transposed(g, w.ns, km), g.rows_p,
-                           g.cols_p, s); }));
-      }
-      void* O = nullptr;
-      RowSq rs;
-      rs.part = w.part;
-      rs.rows = (int)k;
-      st = run_ns(g, c, w.ns, hp->kind, hp->T, hp->abc, hp->restart_mask, s, &O,
-                  hp->normuon ? &rs : nullptr);
+      st = step_chunk(g, c, rows, cols, k, hp, Wp, Mp, &Gp, nullptr, Vp, workspace, s);
       if (st != MNS_OK) return st;
-      const float inv_s = 1.0f / g.S;
-      if (hp->normuon) {
-        // The row statistics come from the epilogue of the product that wrote the result
-        // (every run ends with one: T >= 1).
-        if (!rs.done) return MNS_ERR_PARAM;
-        MNS_HIP(timed("normuon_finalize", 0, 4.0 * c * k * (w.chunks + 3), s, [&] {
-          return normuon_finalize(w.part, w.chunks, c, k, cols, &Vp, nullptr, 0,
-                                  dion ? w.S : nullptr, hp->beta2, hp->eps, inv_s * inv_s, inv_s,
-                                  w.rowscale, w.fin, s); }));
-      } else {
-        MNS_HIP(timed("fill", 0, 4.0 * c * k, s, [&] {
-          return fill(w.rowscale, (int64_t)c * k, inv_s, s); }));
-      }
-      MNS_HIP(timed("weight_update", 0, sel * (2.0 * ss + es) + 4.0 * c * k, s, [&] {
-        return weight_update(Wp, sto, c, k, cols, O, g.elem, g.rows_p, g.cols_p, w.rowscale,
-                             dion ? w.S : nullptr, k, hp->lr, s); }));
     }
   }
   return MNS_OK;
@@ -1279,6 +1298,90 @@ mns_status ns_orthogonalize_backward(const void* X, const void* dO, void* dX, in
     MNS_HIP(timed("nsb_finish", 0, all * (3.0 * ss + 2.0 * es), s, [&] {
       return nsb_finish(x, sto, E, g.elem, c, rows, cols, g.tall ? b.ld_t : g.ld_x,
                         g.tall ? b.vt_stride : b.v_stride, b.dot, b.scale, 1.0 / sc[T].e, dx, s); }));
+  }
+  return MNS_OK;
+}
+
+// ---- the step of a stack of experts from their tokens ------------------------------------------
+
+static mns_status check_step_grouped(int64_t groups, int64_t total_rows, int64_t rows,
+                                     int64_t cols, const mns_hparams* hp) {
+  if (!hp) return MNS_ERR_NULL;
+  mns_status st = check_grouped(hp->dtype, groups, total_rows, rows, cols);
+  if (st != MNS_OK) return st;
+  mns_matrix one = {};
+  one.rows = rows;
+  one.cols = cols;
+  st = validate_step(&one, 1, hp, false);
+  if (st != MNS_OK) return st;
+  return hp->row_fraction == 1.0 ? MNS_OK : MNS_ERR_PARAM;
+}
+
+static GroupedDesc step_grouped_desc(int64_t groups, int64_t total_rows, int64_t rows, int64_t cols,
+                                     const mns_hparams* hp) {
+  GroupedDesc d;
+  d.store = store_of(hp->dtype);
+  d.out_store = Store::F32;
+  d.groups = groups;
+  d.total_rows = total_rows;
+  d.n = rows;
+  d.k = cols;
+  d.weight_grad = true;
+  return d;
+}
+
+// The product's workspace is free again when the first chunk starts: one region serves both.
+static size_t step_grouped_bytes(int64_t groups, int64_t total_rows, int64_t rows, int64_t cols,
+                                 const mns_hparams* hp) {
+  const size_t prod = grouped_workspace(step_grouped_desc(groups, total_rows, rows, cols, hp));
+  StepWs w;
+  const size_t step = carve_step(nullptr, make_geo(rows, cols, store_of(hp->dtype)),
+                                 groups < kChunk ? (int)groups : kChunk, rows, cols, false, rows,
+                                 hp->kind, w);
+  return prod > step ? prod : step;
+}
+
+mns_status mns_grouped_step_workspace_size(int64_t groups, int64_t total_rows, int64_t rows,
+                                           int64_t cols, const mns_hparams* hp, size_t* bytes) {
+  if (!bytes) return MNS_ERR_NULL;
+  const mns_status st = check_step_grouped(groups, total_rows, rows, cols, hp);
+  if (st != MNS_OK) return st;
+  *bytes = step_grouped_bytes(groups, total_rows, rows, cols, hp);
+  return MNS_OK;
+}
+
+mns_status muon_step_grouped(void* W, float* M, float* v, const void* dY, int64_t lddy,
+                             const void* X, int64_t ldx, const int64_t* offsets, int64_t groups,
+                             int64_t total_rows, int64_t rows, int64_t cols, const mns_hparams* hp,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  mns_status st = check_step_grouped(groups, total_rows, rows, cols, hp);
+  if (st != MNS_OK) return st;
+  if (!W || !M || (hp->normuon && !v)) return MNS_ERR_NULL;
+  if (!aligned(W, 16) || !aligned(M, 16) || !aligned(v, 4)) return MNS_ERR_PARAM;
+  st = check_ws(workspace, workspace_bytes,
+                step_grouped_bytes(groups, total_rows, rows, cols, hp));
+  if (st != MNS_OK) return st;
+  // M <- mu M + dY^T X (its checks of the tokens come before anything is enqueued)
+  const GroupedDesc d = step_grouped_desc(groups, total_rows, rows, cols, hp);
+  st = grouped_weight_grad(dY, lddy, X, ldx, hp->dtype, offsets, groups, total_rows, rows, cols, M,
+                           hp->mu, M, MNS_F32, grouped_workspace(d) ? workspace : nullptr,
+                           workspace_bytes, stream);
+  if (st != MNS_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const Geo g = make_geo(rows, cols, store_of(hp->dtype));
+  const size_t ws = store_bytes(hp->dtype), elems = (size_t)rows * cols;
+  for (int64_t e0 = 0; e0 < groups; e0 += kChunk) {
+    const int c = (int)(groups - e0 < kChunk ? groups - e0 : kChunk);
+    PtrPack Wp = {}, Mp = {}, Vp = {};
+    for (int i = 0; i < c; ++i) {
+      const size_t e = (size_t)(e0 + i);
+      Wp.p[i] = static_cast<char*>(W) + e * elems * ws;
+      Mp.p[i] = M + e * elems;
+      Vp.p[i] = v ? v + e * rows : nullptr;
+    }
+    st = step_chunk(g, c, rows, cols, rows, hp, Wp, Mp, nullptr, M + (size_t)e0 * elems, Vp,
+                    workspace, s);
+    if (st != MNS_OK) return st;
   }
   return MNS_OK;
 }
