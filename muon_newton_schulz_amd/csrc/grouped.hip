@@ -18,6 +18,7 @@ namespace {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 enum Form { NT = 0, NN = 1, TN = 2 };
@@ -27,7 +28,7 @@ struct GroupedArgs {
   int64_t lda, ldb, ldc;        // row pitches, elements (ldc: of C and D)
   int64_t sB, sC;               // per-expert strides of W (NT, NN) and of C, D (TN)
   const int64_t* offsets;
-  int64_t total_rows;
+  int total_rows;
   int groups;
   int N, K;                     // NT, NN: output columns and reduction; TN: output rows, columns
   int tiles_n;
@@ -35,41 +36,48 @@ struct GroupedArgs {
   float beta;                   // TN
 };
 
-__device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) {
-  return v < lo ? lo : v > hi ? hi : v;
+__device__ __forceinline__ int clamp_row(int64_t v, int lo, int hi) {
+  return v < lo ? lo : v > hi ? hi : (int)v;
 }
 
 // Rows [lo, hi) of expert e.
-__device__ __forceinline__ void expert_rows(const GroupedArgs& p, int e, int64_t& lo, int64_t& hi) {
-  lo = clamp64(p.offsets[e], 0, p.total_rows);
-  hi = clamp64(p.offsets[e + 1], lo, p.total_rows);
+__device__ __forceinline__ void expert_rows(const GroupedArgs& p, int e, int& lo, int& hi) {
+  lo = clamp_row(p.offsets[e], 0, p.total_rows);
+  hi = clamp_row(p.offsets[e + 1], lo, p.total_rows);
 }
 
-// Row tile `mt` of the list that walks the experts in order, each cut into tiles of BM rows (with
-// fill_rest, the rows before the first expert and behind the last one come first and last, as
-// expert -1): its expert, first row and the end of the expert's rows. False past the last tile.
-// One wave reads 64 experts' bounds at a time and adds their tile counts by a shuffle scan, so
-// every wave finds its tile by itself, without a launch or a barrier.
-__device__ __forceinline__ bool find_row_tile(const GroupedArgs& p, int BM, int64_t mt, int& expert,
-                                              int64_t& row0, int64_t& row_end) {
+// Where a block of a forward or input-gradient call works: an expert (-1: the rows of no expert,
+// to be filled with zeros), its rows [lo, hi), and the block's place among the expert's tiles.
+struct Place {
+  int expert, lo, hi, inside;
+};
+
+// Position `lin` in the list of tiles that walks the experts in order, each cut into row tiles of
+// BM rows with tiles_n tiles per row tile (with fill_rest, the rows before the first expert and
+// behind the last one come first and last). False past the last tile. Every wave reads 64
+// experts' bounds at a time and adds their tile counts by a shuffle scan, so it finds its place by
+// itself, without a launch or a barrier.
+__device__ __forceinline__ bool find_place(const GroupedArgs& p, int BM, int tiles_n, int64_t lin,
+                                           Place& at) {
   const int lane = threadIdx.x & 63;
   const int front = p.fill_rest ? 1 : 0;
   const int count = p.groups + 2 * front;
   int64_t before = 0;
   for (int g0 = 0; g0 < count; g0 += 64) {
     const int g = g0 + lane, e = g - front;
-    int64_t lo = 0, hi = 0;
+    int lo = 0, hi = 0;
     if (g < count) {
       if (e < 0) {
-        hi = clamp64(p.offsets[0], 0, p.total_rows);
+        hi = clamp_row(p.offsets[0], 0, p.total_rows);
       } else if (e >= p.groups) {
-        lo = clamp64(p.offsets[p.groups], 0, p.total_rows);
+        int first;
+        expert_rows(p, p.groups - 1, first, lo);     // from the last expert's end
         hi = p.total_rows;
       } else {
         expert_rows(p, e, lo, hi);
       }
     }
-    const int64_t tiles = (hi - lo + BM - 1) / BM;
+    const int64_t tiles = (int64_t)((hi - lo + (BM - 1)) / BM) * tiles_n;
     int64_t incl = tiles;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -77,15 +85,13 @@ __device__ __forceinline__ bool find_row_tile(const GroupedArgs& p, int BM, int6
       if (lane >= o) incl += up;
     }
     const int64_t sum = __shfl(incl, 63);
-    if (mt < before + sum) {
-      const unsigned long long over = __ballot(before + incl > mt);
-      const int src = __ffsll(over) - 1;
-      const int64_t first = __shfl(before + incl - tiles, src);
-      const int64_t glo = __shfl(lo, src);
-      row_end = __shfl(hi, src);
-      row0 = glo + (mt - first) * BM;
+    if (lin < before + sum) {
+      const int src = __ffsll((unsigned long long)__ballot(before + incl > lin)) - 1;
+      at.inside = __builtin_amdgcn_readfirstlane((int)(lin - __shfl(before + incl - tiles, src)));
+      at.lo = __builtin_amdgcn_readfirstlane(__shfl(lo, src));
+      at.hi = __builtin_amdgcn_readfirstlane(__shfl(hi, src));
       const int ge = g0 + src - front;
-      expert = ge >= 0 && ge < p.groups ? ge : -1;
+      at.expert = __builtin_amdgcn_readfirstlane(ge >= 0 && ge < p.groups ? ge : -1);
       return true;
     }
     before += sum;
@@ -133,6 +139,59 @@ __device__ __forceinline__ u32x4 load_chunk(const T* p, int valid) {
   return v;
 }
 
+// Writes a wave's FM x FN fragments of 32 x 32 at rows m0, columns n0 of the tile whose first
+// element is `origin`: acc[i][j][4g + e] is row 32 i + (lane & 31), column 32 j + 8 g + 4 (lane >> 5)
+// + e. Four columns go out as one vector; with ADD, beta D is added, its vectors of one fragment
+// row all loaded before the first store.
+template <typename TO, int FM, int FN, bool ADD>
+__device__ __forceinline__ void store_fragments(const GroupedArgs& p, const floatx16 (&acc)[FM][FN],
+                                                int64_t origin, int m0, int n0, int m_valid,
+                                                int n_valid) {
+  const int lane = threadIdx.x & 63;
+  const TO* D = static_cast<const TO*>(p.D);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int m = m0 + 32 * i + (lane & 31);
+    if (m >= m_valid) continue;
+    const int64_t row = origin + m * p.ldc;
+    TO* out = static_cast<TO*>(p.C) + row;
+    float add[FN * 4][4] = {};
+    if (ADD && D) {
+#pragma unroll
+      for (int q = 0; q < FN * 4; ++q) {
+        const int n = n0 + 32 * (q / 4) + 8 * (q % 4) + 4 * (lane >> 5);
+        TO t[4];
+        if (n + 4 <= n_valid) {
+          __builtin_memcpy(t, D + row + n, sizeof(t));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t[e] = n + e < n_valid ? D[row + n + e] : (TO)0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) add[q][e] = (float)t[e];
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < FN * 4; ++q) {
+      const int n = n0 + 32 * (q / 4) + 8 * (q % 4) + 4 * (lane >> 5);
+      TO t[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v = acc[i][q / 4][4 * (q % 4) + e];
+        if (ADD && D) v += p.beta * add[q][e];
+        t[e] = (TO)v;
+      }
+      if (n + 4 <= n_valid) {
+        __builtin_memcpy(out + n, t, sizeof(t));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < n_valid) out[n + e] = t[e];
+      }
+    }
+  }
+}
+
 // Any sizes, pitches and alignment of both types: 128 x 128 tiles, four waves of 64 x 64, k-tiles
 // of 128 bytes a row loaded into registers one tile ahead and stored to LDS as [row][k] (144-byte
 // rows: 16 rows' 16-byte reads cover the 64 banks once), a k-major operand transposed on the way.
@@ -146,54 +205,52 @@ __global__ __launch_bounds__(256) void k_grouped(GroupedArgs p) {
   __shared__ __align__(16) T Bs[BN * PITCH];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int expert = 0;
-  int64_t row0 = 0, row_end = 0;
-  int m_tile = 0, n0;
-  int64_t red;              // length of the reduction
+  int expert, lo, hi, m0, n0;
+  int red;                  // length of the reduction
   const T* A;
   const T* B;
-  int m_valid, n_valid;
+  int m_valid;
   if constexpr (FORM == TN) {
-    const int tm = (p.N + BM - 1) / BM, per = tm * p.tiles_n;
-    expert = blockIdx.x / per;
-    const int t = blockIdx.x % per;
-    m_tile = t / p.tiles_n;
-    n0 = (t % p.tiles_n) * BN;
-    expert_rows(p, expert, row0, row_end);
-    red = row_end - row0;
-    A = static_cast<const T*>(p.A) + row0 * p.lda + m_tile * BM;
-    B = static_cast<const T*>(p.B) + row0 * p.ldb + n0;
-    m_valid = p.N - m_tile * BM;
-    n_valid = p.K - n0;
+    const int per = (p.N + BM - 1) / BM * p.tiles_n, t = (int)(blockIdx.x % per);
+    expert = (int)(blockIdx.x / per);
+    m0 = t / p.tiles_n * BM;
+    n0 = t % p.tiles_n * BN;
+    expert_rows(p, expert, lo, hi);
+    red = hi - lo;
+    A = static_cast<const T*>(p.A) + lo * p.lda + m0;
+    B = static_cast<const T*>(p.B) + lo * p.ldb + n0;
+    m_valid = p.N - m0;
   } else {
-    if (!find_row_tile(p, BM, blockIdx.x / p.tiles_n, expert, row0, row_end)) return;
-    n0 = (int)(blockIdx.x % p.tiles_n) * BN;
+    Place at;
+    if (!find_place(p, BM, p.tiles_n, blockIdx.x, at)) return;
+    expert = at.expert;
+    m0 = at.lo + at.inside / p.tiles_n * BM;
+    n0 = at.inside % p.tiles_n * BN;
     red = expert < 0 ? 0 : p.K;
-    A = static_cast<const T*>(p.A) + row0 * p.lda;
+    A = static_cast<const T*>(p.A) + m0 * p.lda;
     B = static_cast<const T*>(p.B) + (expert < 0 ? 0 : expert) * p.sB +
         (FORM == NT ? n0 * p.ldb : (int64_t)n0);
-    m_valid = (int)(row_end - row0 < BM ? row_end - row0 : BM);
-    n_valid = p.N - n0;
+    m_valid = at.hi - m0;
   }
+  const int n_valid = (FORM == TN ? p.K : p.N) - n0;
 
   // Chunk q of this thread of a k-contiguous operand: row, first k; of a k-major one: k-row,
   // first column (16 k-rows x 4 chunks per wave: 64-byte pieces of a row).
   u32x4 ra[NCH], rb[NCH];
-  auto load = [&](const T* base, int64_t ld, bool kmajor, int valid, int64_t k0, u32x4* r) {
+  auto load = [&](const T* base, int64_t ld, bool kmajor, int valid, int k0, u32x4* r) {
 #pragma unroll
     for (int q = 0; q < NCH; ++q) {
       if (!kmajor) {
         const int c = tid + 256 * q, row = c >> 3, kk = (c & 7) * VEC;
-        const int64_t left = red - k0 - kk;
-        r[q] = load_chunk(base + row * ld + k0 + kk,
-                          row < valid ? (int)(left < VEC ? left : VEC) : 0);
+        const int left = red - k0 - kk;
+        r[q] = load_chunk(base + row * ld + k0 + kk, row < valid ? left : 0);
       } else {
         constexpr int KW = BK / 16;                     // waves' worth of k-rows
         const int u = q * 4 + wave;                     // 16 units of 16 k-rows x 4 chunks
         const int kr = (u % KW) * 16 + (lane & 15);
         const int col = ((u / KW) * 4 + (lane >> 4)) * VEC;
         const int left = valid - col;
-        r[q] = load_chunk(base + (k0 + kr) * ld + col, k0 + kr < red ? (left < VEC ? left : VEC) : 0);
+        r[q] = load_chunk(base + (int64_t)(k0 + kr) * ld + col, k0 + kr < red ? left : 0);
       }
     }
   };
@@ -228,7 +285,7 @@ __global__ __launch_bounds__(256) void k_grouped(GroupedArgs p) {
     load(A, p.lda, FORM == TN, m_valid, 0, ra);
     load(B, p.ldb, FORM != NT, n_valid, 0, rb);
   }
-  for (int64_t k0 = 0; k0 < red; k0 += BK) {
+  for (int k0 = 0; k0 < red; k0 += BK) {
     store(As, FORM == TN, ra);
     store(Bs, FORM != NT, rb);
     __syncthreads();
@@ -254,28 +311,579 @@ __global__ __launch_bounds__(256) void k_grouped(GroupedArgs p) {
     __syncthreads();
   }
 
-  // acc[i][j][4g + e] is row wm*64 + 32i + (lane & 31), column wn*64 + 32j + 8g + 4(lane >> 5) + e.
-  const int64_t crow = FORM == TN ? (int64_t)m_tile * BM : row0;
-  const int64_t cbase = FORM == TN ? expert * p.sC : 0;
+  const int64_t origin = (FORM == TN ? expert * p.sC : 0) + m0 * p.ldc + n0;
+  store_fragments<TO, 2, 2, FORM == TN>(p, acc, origin, wm * 64, wn * 64, m_valid, n_valid);
+}
+
+// Few rows per expert (forward): the product is bound by reading the weights once, so the weights
+// go straight from memory into MFMA operands, 64 bytes of 16 rows per load, with nothing staged
+// and no barrier in the loop; the tokens of the row tile (16 MT rows) are read the same way and
+// come from the caches. A wave owns 16 NT weight rows. WK = 4: the block's four waves split the
+// reduction and add their sums through LDS in wave order (more waves in flight where there are
+// few weight rows); WK = 1: they own 16 NT rows each.
+//
+// A 16-byte chunk per lane holds consecutive k of one row for both operands, so any k order the
+// MFMA uses inside a step is the same on both sides. Loads are D - 1 steps ahead.
+template <typename T>
+struct Small;
+template <>
+struct Small<__bf16> {
+  __device__ static __forceinline__ void mma(floatx4& acc, u32x4 a, u32x4 b) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                  __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
+  }
+};
+template <>
+struct Small<float> {
+  __device__ static __forceinline__ void mma(floatx4& acc, u32x4 a, u32x4 b) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int m = wm * 64 + 32 * i + (lane & 31);
-    if (m >= m_valid) continue;
-    TO* out = static_cast<TO*>(p.C) + cbase + (crow + m) * p.ldc + n0;
-    const TO* add = static_cast<const TO*>(p.D) + cbase + (crow + m) * p.ldc + n0;
+    for (int p = 0; p < 4; ++p)
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[p]), __uint_as_float(b[p]), acc,
+                                                 0, 0, 0);
+  }
+};
+
+template <typename T, int MT, int NTW, int WK>
+__global__ __launch_bounds__(256) void k_grouped_rows(GroupedArgs p) {
+  constexpr int VEC = Frag<T>::VEC, STEP = 4 * VEC;     // k per step: 64 bytes of a row
+  constexpr int BM = 16 * MT, BN = 16 * NTW * (4 / WK);
+  constexpr int D = MT >= 4 ? 3 : 4;                    // operand sets: loads D - 1 steps ahead
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  Place at;
+  if (!find_place(p, BM, p.tiles_n, blockIdx.x, at)) return;
+  const int expert = at.expert;
+  const int row0 = at.lo + at.inside / p.tiles_n * BM;
+  const int n0 = at.inside % p.tiles_n * BN + (WK == 1 ? wave * 16 * NTW : 0);
+  const int m_valid = at.hi - row0 < BM ? at.hi - row0 : BM;
+  const int K = expert < 0 ? 0 : p.K;
+  const int steps = (K + STEP - 1) / STEP;
+  const int s_begin = WK == 1 ? 0 : (int)((int64_t)wave * steps / WK);
+  const int s_end = WK == 1 ? steps : (int)((int64_t)(wave + 1) * steps / WK);
+  const int whole = K / STEP;                           // steps without a tail
+
+  // Rows past the tile's last one (and weight rows past N) read the last one again; their
+  // products are not stored.
+  const int r16 = lane & 15, kc = (lane >> 4) * VEC;
+  const T* xp[MT];
+  const T* wp[NTW];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+  for (int i = 0; i < MT; ++i) {
+    const int m = 16 * i + r16;
+    xp[i] = static_cast<const T*>(p.A) +
+            (int64_t)(row0 + (m < m_valid ? m : m_valid - 1)) * p.lda + kc;
+  }
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int n = wn * 64 + 32 * j + 8 * g + 4 * (lane >> 5);
+  for (int j = 0; j < NTW; ++j) {
+    const int n = n0 + 16 * j + r16;
+    wp[j] = static_cast<const T*>(p.B) + (expert < 0 ? 0 : expert) * p.sB +
+            (int64_t)(n < p.N ? n : p.N - 1) * p.ldb + kc;
+  }
+  floatx4 acc[MT][NTW];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (n + e >= n_valid) continue;
-          float v = acc[i][j][4 * g + e];
-          if (FORM == TN && p.D) v += p.beta * (float)add[n + e];
-          out[n + e] = (TO)v;
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NTW; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+  u32x4 xa[D][MT], wa[D][NTW];
+  auto load = [&](int s, int d) {
+    const int64_t o = (int64_t)s * STEP;
+#pragma unroll
+    for (int j = 0; j < NTW; ++j) __builtin_memcpy(&wa[d][j], wp[j] + o, 16);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) __builtin_memcpy(&xa[d][i], xp[i] + o, 16);
+  };
+  auto mul = [&](int d) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NTW; ++j) Small<T>::mma(acc[i][j], wa[d][j], xa[d][i]);
+  };
+  // Whole steps s_begin .. w_end - 1, step s in set (s - s_begin) % D. A load past the last one
+  // reads the last step again (its set is not used), so the loop has no tests between loads.
+  const int w_end = s_end < whole ? s_end : whole;
+  if (w_end > s_begin) {
+    const int last = w_end - 1;
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) load(s_begin + d < last ? s_begin + d : last, d);
+    int s = s_begin;
+    for (; s + D <= w_end; s += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        const int ahead = s + d + D - 1;
+        load(ahead < last ? ahead : last, (d + D - 1) % D);
+        mul(d);
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d)
+      if (s + d < w_end) mul(d);
+  }
+  for (int s = w_end > s_begin ? w_end : s_begin; s < s_end; ++s) {     // the step with the tail
+    const int64_t o = (int64_t)s * STEP;
+    const int left = K - s * STEP - kc;
+    u32x4 w[NTW], x[MT];
+#pragma unroll
+    for (int j = 0; j < NTW; ++j) w[j] = load_chunk(wp[j] + o, left);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) x[i] = load_chunk(xp[i] + o, left);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NTW; ++j) Small<T>::mma(acc[i][j], w[j], x[i]);
+  }
+
+  // acc[i][j][e]: token 16 i + (lane & 15), weight row n0 + 16 j + 4 (lane >> 4) + e.
+  auto put = [&](int i, int j, const floatx4& v) {
+    const int m = 16 * i + r16, n = n0 + 16 * j + 4 * (lane >> 4);
+    if (m >= m_valid) return;
+    T* out = static_cast<T*>(p.C) + (int64_t)(row0 + m) * p.ldc + n;
+    T t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] = (T)v[e];
+    if (n + 4 <= p.N) {
+      __builtin_memcpy(out, t, sizeof(t));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < p.N) out[e] = t[e];
+    }
+  };
+  if constexpr (WK == 1) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NTW; ++j) put(i, j, acc[i][j]);
+  } else {
+    __shared__ floatx4 ex[WK][MT * NTW][64];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NTW; ++j) ex[wave][i * NTW + j][lane] = acc[i][j];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NTW; ++j) {
+        const int t = i * NTW + j;
+        if (t % WK != wave) continue;
+        floatx4 v = ex[0][t][lane];
+#pragma unroll
+        for (int w = 1; w < WK; ++w) v += ex[w][t][lane];
+        put(i, j, v);
+      }
+  }
+}
+
+// ---- large products, bfloat16 --------------------------------------------------------------
+//
+// 256 x 256 tiles, eight waves of 128 x 64 (2 x 4), k-tiles of 64 moved to LDS by DMA, double
+// buffered: the main loop of the Newton-Schulz product (gemm.hip), for ragged rows and for both
+// operands in either order. An operand whose rows run along the reduction lies in LDS as
+// [row][k] in 16-byte chunks, chunk c of row r at c ^ ((r ^ (r >> 3 & 3)) & 7); one whose rows run
+// along the output (W in dX = dY W, both in dY^T X) lies as [k][256 columns], chunk c of k-row r
+// at c ^ 4 (r & 3), and is read through the transposing LDS load.
+//
+// Nothing is masked in the loop: an operand row past the end of its matrix lies past the buffer
+// resource's end and reads as zero, and a row of the next expert only feeds output rows that are
+// not stored. For the weight gradient the reduction ends inside a k-tile: the resources end at
+// the expert's last row, so the rest of the tile is zeros for both operands; they start at the
+// k-tile (not at the expert), so offsets stay below 2 GiB however many rows an expert has.
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kChunks = 8;                  // 16-byte chunks of a 128-byte LDS row
+constexpr int kBufferFlags = 0x00020000;    // buffer resource word 3: raw loads
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
+  const int n = bytes > 0x7FFFFFFFLL ? 0x7FFFFFFF : bytes < 0 ? 0 : (int)bytes;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, n, kBufferFlags);
+}
+
+// 16 bytes per lane, global -> LDS: lane l's land at dst + 16 l (dst wave-uniform).
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, u32x4* dst, int voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, voff, soff, 0, 0);
+}
+
+__device__ __forceinline__ int swz(int row, int chunk) {
+  return row * kChunks + (chunk ^ ((row ^ ((row >> 3) & 3)) & 7));
+}
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(lds_void*)p;
+}
+
+// This wave's DMA and LDS accesses are done, then the workgroup meets.
+__device__ __forceinline__ void block_sync() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);       // vmcnt(0) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Tile (tm, tn) of place `t` among tiles_m x tiles_n: groups of 4 row tiles, column by column inside a
+// group, so that tiles in flight together share operand rows.
+__device__ __forceinline__ void tile_order(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int per = 4 * tiles_n, g = t / per, l = t % per;
+  const int rest = tiles_m - 4 * g, size = rest < 4 ? rest : 4;
+  tm = 4 * g + l % size;
+  tn = l / size;
+}
+
+// Blocks go round the 8 XCDs (L2 domains) one by one. Each window of 256 blocks (one per CU) is
+// dealt to them in runs of 32 consecutive tiles, so the 32 CUs of an XCD work side by side, and an
+// expert with many rows is spread over the XCDs.
+__device__ __forceinline__ int64_t xcd_order(int64_t b) {
+  const int64_t w = b & ~(int64_t)255;
+  const int r = (int)(b & 255);
+  return w + (r & 7) * 32 + (r >> 3);
+}
+
+template <typename TO, int FORM>
+__global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
+  constexpr int BM = 256, BN = 256, BK = 64, FM = 4, FN = 2, INST = 4;   // DMA per wave and operand
+  constexpr int STAGE = (BM + BN) * kChunks;
+  constexpr bool AK = FORM == TN, BKM = FORM != NT;     // operand stored along the output
+  constexpr int KROW = 512;                             // bytes of a [k][256] LDS row
+  __shared__ u32x4 lds[2 * STAGE];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+
+  int expert, m0, n0, red, m_valid;
+  const char* Abase;
+  const char* Bbase;
+  int64_t a_bytes, b_bytes;       // of the whole operand block (not TN)
+  const int64_t lin = xcd_order(blockIdx.x);
+  if constexpr (FORM == TN) {
+    const int tiles_m = (p.N + BM - 1) / BM, per = tiles_m * p.tiles_n;
+    expert = (int)(lin / per);
+    if (expert >= p.groups) return;
+    int tm, tn, lo, hi;
+    tile_order((int)(lin % per), tiles_m, p.tiles_n, tm, tn);
+    expert_rows(p, expert, lo, hi);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    m0 = tm * BM;
+    n0 = tn * BN;
+    red = hi - lo;
+    m_valid = p.N - m0;
+    Abase = static_cast<const char*>(p.A) + (lo * p.lda + m0) * 2;
+    Bbase = static_cast<const char*>(p.B) + (lo * p.ldb + n0) * 2;
+    a_bytes = b_bytes = 0;
+  } else {
+    Place at;
+    if (!find_place(p, BM, p.tiles_n, lin, at)) return;
+    expert = at.expert;
+    int tm, tn;
+    tile_order(at.inside, (at.hi - at.lo + BM - 1) / BM, p.tiles_n, tm, tn);
+    m0 = at.lo + tm * BM;
+    n0 = tn * BN;
+    red = expert < 0 ? 0 : p.K;
+    m_valid = at.hi - m0;
+    Abase = static_cast<const char*>(p.A) + m0 * p.lda * 2;
+    a_bytes = ((int64_t)(m_valid - 1) * p.lda + p.K) * 2;
+    Bbase = static_cast<const char*>(p.B) + ((expert < 0 ? 0 : expert) * p.sB +
+                                             (BKM ? (int64_t)n0 : n0 * p.ldb)) * 2;
+    b_bytes = (BKM ? (int64_t)p.K * p.ldb - n0 : (int64_t)(p.N - n0) * p.ldb) * 2;
+  }
+  const int n_valid = (FORM == TN ? p.K : p.N) - n0;
+  const int KL = (red + BK - 1) / BK;
+  const __amdgpu_buffer_rsrc_t rA0 = make_rsrc(Abase, a_bytes), rB0 = make_rsrc(Bbase, b_bytes);
+  // Resource of k-tile kt: the block's (offset by kt), or, for the weight gradient, one that starts
+  // at the k-tile and ends with the expert's last row.
+  auto res = [&](int kt, bool b) {
+    if constexpr (FORM == TN) {
+      const int64_t ld = b ? p.ldb : p.lda;
+      const int64_t left = ((int64_t)(red - kt * BK - 1) * ld + (b ? n_valid : m_valid)) * 2;
+      return make_rsrc((b ? Bbase : Abase) + kt * BK * ld * 2, left);
+    } else {
+      return b ? rB0 : rA0;
+    }
+  };
+  auto koff = [&](int kt, bool b) {
+    if constexpr (FORM == TN) return 0;
+    else return b && BKM ? kt * BK * (int)p.ldb * 2 : kt * BK * 2;
+  };
+
+  // Per-lane byte offsets of this wave's DMA instructions (see the layouts above).
+  int offA[INST], offB[INST];
+  auto lane_offset = [&](int i, bool kmajor, int64_t ld) {
+    if (kmajor) {
+      const int kr = 2 * (wave * INST + i) + (lane >> 5);
+      return (kr * (int)ld + 8 * ((lane & 31) ^ (4 * (kr & 3)))) * 2;
+    }
+    const int row = (wave * INST + i) * 8 + (lane >> 3);
+    return (row * (int)ld + 8 * ((lane & 7) ^ ((row ^ ((row >> 3) & 3)) & 7))) * 2;
+  };
+#pragma unroll
+  for (int i = 0; i < INST; ++i) {
+    offA[i] = lane_offset(i, AK, p.lda);
+    offB[i] = lane_offset(i, BKM, p.ldb);
+  }
+
+  floatx16 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+
+  const int arow = wm * 128 + (lane & 31), brow = BM + wn * 64 + (lane & 31);
+  u32x4 af[2][FM], bf[2][FN];
+  // Transposing reads: in each 16-lane group G = lane / 16, lane 4s + a points at 8 bytes of k-row
+  // 8 (G / 2) + s (+ 4 for the second read), columns c .. c + 3, c = first + 16 (G % 2) + 4 a, and
+  // lane 4a + b receives the four k of column c + b: each lane ends with 8 consecutive k of its
+  // row of the fragment, as the MFMA expects.
+  uint32_t a_addr[FM], b_addr[FN];
+  {
+    const int G = lane >> 4, sq = (lane & 15) >> 2, a4 = lane & 3, kb = 8 * (G >> 1) + sq;
+    const uint32_t base = lds_address(lds);
+    auto address = [&](int first) {
+      const int c = first + 16 * (G & 1) + 4 * a4;
+      return (uint32_t)(kb * KROW + ((c >> 3) ^ (4 * (kb & 3))) * 16 + (c & 7) * 2);
+    };
+#pragma unroll
+    for (int i = 0; i < FM; ++i) a_addr[i] = base + address(wm * 128 + 32 * i);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) b_addr[j] = base + BM * 128 + address(wn * 64 + 32 * j);
+  }
+  auto load_frags = [&](int buf, int ks, int slot) {
+    const int ch = 2 * ks + (lane >> 5);
+    if constexpr (!AK) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) af[slot][i] = lds[buf * STAGE + swz(arow + 32 * i, ch)];
+    }
+    if constexpr (!BKM) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) bf[slot][j] = lds[buf * STAGE + swz(brow + 32 * j, ch)];
+    }
+  };
+  // The transposing loads wait for themselves (the compiler would wait for every outstanding DMA
+  // first); outputs are early-clobber, and the fragments that the MFMAs before them read are
+  // inputs, so none of those registers is written while an MFMA may still read it.
+  auto load_tr = [&](int buf, int ks, int slot) {
+    const uint32_t o = (uint32_t)(buf * STAGE * 16 + ks * 16 * KROW);
+    const int ps = slot ^ 1;
+    if constexpr (BKM) {
+      u32x2 t0, t1, t2, t3;
+      asm volatile(
+          "ds_read_b64_tr_b16 %0, %4\n\t"
+          "ds_read_b64_tr_b16 %1, %4 offset:2048\n\t"
+          "ds_read_b64_tr_b16 %2, %5\n\t"
+          "ds_read_b64_tr_b16 %3, %5 offset:2048\n\t"
+          "s_waitcnt lgkmcnt(0)"
+          : "=&v"(t0), "=&v"(t1), "=&v"(t2), "=&v"(t3)
+          : "v"(b_addr[0] + o), "v"(b_addr[1] + o), "v"(af[ps][0]), "v"(af[ps][1]),
+            "v"(af[ps][2]), "v"(af[ps][3]), "v"(bf[ps][0]), "v"(bf[ps][1]));
+      bf[slot][0] = u32x4{t0.x, t0.y, t1.x, t1.y};
+      bf[slot][1] = u32x4{t2.x, t2.y, t3.x, t3.y};
+    }
+    if constexpr (AK) {
+      u32x2 t0, t1, t2, t3, t4, t5, t6, t7;
+      asm volatile(
+          "ds_read_b64_tr_b16 %0, %8\n\t"
+          "ds_read_b64_tr_b16 %1, %8 offset:2048\n\t"
+          "ds_read_b64_tr_b16 %2, %9\n\t"
+          "ds_read_b64_tr_b16 %3, %9 offset:2048\n\t"
+          "ds_read_b64_tr_b16 %4, %10\n\t"
+          "ds_read_b64_tr_b16 %5, %10 offset:2048\n\t"
+          "ds_read_b64_tr_b16 %6, %11\n\t"
+          "ds_read_b64_tr_b16 %7, %11 offset:2048\n\t"
+          "s_waitcnt lgkmcnt(0)"
+          : "=&v"(t0), "=&v"(t1), "=&v"(t2), "=&v"(t3), "=&v"(t4), "=&v"(t5), "=&v"(t6),
+            "=&v"(t7)
+          : "v"(a_addr[0] + o), "v"(a_addr[1] + o), "v"(a_addr[2] + o), "v"(a_addr[3] + o),
+            "v"(af[ps][0]), "v"(af[ps][1]), "v"(af[ps][2]), "v"(af[ps][3]), "v"(bf[ps][0]),
+            "v"(bf[ps][1]));
+      af[slot][0] = u32x4{t0.x, t0.y, t1.x, t1.y};
+      af[slot][1] = u32x4{t2.x, t2.y, t3.x, t3.y};
+      af[slot][2] = u32x4{t4.x, t4.y, t5.x, t5.y};
+      af[slot][3] = u32x4{t6.x, t6.y, t7.x, t7.y};
+    }
+  };
+  // DMA instruction q of k-tile kt into buffer buf (q < INST: A, else B).
+  auto dma_one = [&](__amdgpu_buffer_rsrc_t rA, __amdgpu_buffer_rsrc_t rB, int kt, int buf, int q) {
+    if (q < INST)
+      dma16(rA, &lds[buf * STAGE + (wave * INST + q) * 64], offA[q], koff(kt, false));
+    else
+      dma16(rB, &lds[buf * STAGE + BM * kChunks + (wave * INST + q - INST) * 64], offB[q - INST],
+            koff(kt, true));
+  };
+  // The MFMAs of fragment slot s, with DMA instructions q0 .. q0 + 3 of k-tile kt between the first
+  // of them when NQ = 4.
+  auto kstep = [&](int s, int kt, int buf, int q0, auto nq) {
+    constexpr int NQ = decltype(nq)::value;
+    __amdgpu_buffer_rsrc_t rA = rA0, rB = rB0;
+    if constexpr (NQ > 0) {
+      if (q0 < INST) rA = res(kt, false);
+      else rB = res(kt, true);
+    }
+#pragma unroll
+    for (int m = 0; m < FM * FN; ++m) {
+      Frag<__bf16>::mma(acc[m / FN][m % FN], bf[s][m % FN], af[s][m / FN]);
+      if (m < NQ) dma_one(rA, rB, kt, buf, q0 + m);
+    }
+    if constexpr (NQ > 0) {
+#pragma unroll
+      for (int m = 0; m < FM * FN; ++m) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (m < NQ) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      }
+    }
+  };
+  using N0 = std::integral_constant<int, 0>;
+  using N4 = std::integral_constant<int, 4>;
+  // k-tile kl from buffer kl % 2. Of k-tile kl + 1 the A half went out in the previous k-tile's last
+  // k-step and the B half goes out in k-step 0; the barrier before k-step 3 (whose fragments are
+  // in registers by then) waits for it and frees this buffer for k-tile kl + 2.
+  auto body = [&](int kl, auto has1, auto has2) {
+    const int b = kl & 1;
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    load_frags(b, 1, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (decltype(has1)::value) kstep(0, kl + 1, b ^ 1, INST, N4{});
+    else kstep(0, 0, 0, 0, N0{});
+    __builtin_amdgcn_sched_barrier(0);
+    load_tr(b, 1, 1);
+    load_frags(b, 2, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    kstep(1, 0, 0, 0, N0{});
+    __builtin_amdgcn_sched_barrier(0);
+    load_tr(b, 2, 0);
+    load_frags(b, 3, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    kstep(0, 0, 0, 0, N0{});
+    __builtin_amdgcn_sched_barrier(0);
+    load_tr(b, 3, 1);
+    block_sync();
+    load_frags(b ^ 1, 0, 0);     // behind the last k-tile: an idle buffer, the values unused
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (decltype(has2)::value) kstep(1, kl + 2, b, 0, N4{});
+    else kstep(1, 0, 0, 0, N0{});
+    __builtin_amdgcn_sched_barrier(0);
+    load_tr(b ^ 1, 0, 0);
+  };
+  if (KL > 0) {
+#pragma unroll
+    for (int q = 0; q < 2 * INST; ++q) dma_one(res(0, false), res(0, true), 0, 0, q);
+    if (KL > 1) {
+#pragma unroll
+      for (int q = 0; q < INST; ++q) dma_one(res(1, false), res(1, true), 1, 1, q);
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) af[1][i] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < FN; ++j) bf[1][j] = u32x4{0u, 0u, 0u, 0u};
+    block_sync();
+    load_frags(0, 0, 0);
+    load_tr(0, 0, 0);
+    using T1 = std::true_type;
+    using F1 = std::false_type;
+    int kl = 0;
+    for (; kl + 2 < KL; ++kl) body(kl, T1{}, T1{});
+    if (kl + 1 < KL) body(kl++, T1{}, F1{});
+    body(kl, F1{}, F1{});
+  }
+  block_sync();
+
+  // Epilogue: the tile goes through the idle LDS so that whole rows leave, 16 bytes a lane. Forward
+  // and input gradient: once, as bfloat16. Weight gradient: float32, 128 rows at a time, and beta C
+  // is added to the float32 sum on the way out (one rounding).
+  const int64_t origin = (FORM == TN ? expert * p.sC : 0) + m0 * p.ldc + n0;
+  if constexpr (FORM != TN) {
+    __bf16* tile = reinterpret_cast<__bf16*>(lds);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int m = wm * 128 + 32 * i + (lane & 31);
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int n = wn * 64 + 32 * j + 8 * g + 4 * (lane >> 5);
+          __bf16* dst = tile + m * BN + ((n >> 3) ^ (m & 31)) * 8 + (n & 7);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dst[e] = (__bf16)acc[i][j][4 * g + e];
+        }
+    }
+    __syncthreads();
+    __bf16* out = static_cast<__bf16*>(p.C) + origin;
+    const int c = tid & 31, n = c * 8;
+    const int rows = m_valid < BM ? m_valid : BM;
+    for (int m = tid >> 5; m < rows; m += 16) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(tile + m * BN + (c ^ (m & 31)) * 8);
+      if (n + 8 <= n_valid) {
+        __builtin_memcpy(out + m * p.ldc + n, &v, 16);
+      } else {
+        __bf16 t[8];
+        __builtin_memcpy(t, &v, 16);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (n + e < n_valid) out[m * p.ldc + n + e] = t[e];
+      }
+    }
+  } else {
+    floatx4* tile = reinterpret_cast<floatx4*>(lds);
+    TO* out = static_cast<TO*>(p.C) + origin;
+    const TO* D = p.D ? static_cast<const TO*>(p.D) + origin : nullptr;
+    const int c = tid & 63, n = c * 4;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (half) __syncthreads();
+      if (wm == half) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          const int m = 32 * i + (lane & 31);
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const int ch = wn * 16 + 8 * j + 2 * g + (lane >> 5);
+              floatx4 v;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g + e];
+              tile[m * 64 + (ch ^ (m & 63))] = v;
+            }
         }
       }
+      __syncthreads();
+      const int rows = m_valid - 128 * half < 128 ? m_valid - 128 * half : 128;
+      constexpr int RB = 4;           // rows of a thread whose loads of C go out together
+      for (int mb = tid >> 6; mb < rows; mb += 8 * RB) {
+        TO add[RB][4];
+        if (D) {
+#pragma unroll
+          for (int r = 0; r < RB; ++r) {
+            const int m = mb + 8 * r;
+            const TO* src = D + (128 * half + (m < rows ? m : mb)) * p.ldc + n;
+            if (n + 4 <= n_valid) {
+              __builtin_memcpy(add[r], src, sizeof(add[r]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) add[r][e] = n + e < n_valid ? src[e] : (TO)0.f;
+            }
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+          const int m = mb + 8 * r;
+          if (m >= rows) break;
+          const floatx4 v = tile[m * 64 + (c ^ (m & 63))];
+          TO t[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t[e] = (TO)(D ? v[e] + p.beta * (float)add[r][e] : v[e]);
+          TO* dst = out + (128 * half + m) * p.ldc + n;
+          if (n + 4 <= n_valid) {
+            __builtin_memcpy(dst, t, sizeof(t));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (n + e < n_valid) dst[e] = t[e];
+          }
+        }
+      }
+    }
   }
 }
 
@@ -285,16 +893,100 @@ hipError_t launch_grouped(const GroupedArgs& a, int64_t blocks, hipStream_t s) {
   return hipGetLastError();
 }
 
-constexpr int kTile = 128;
 int64_t tiles_up(int64_t x, int64_t t) { return (x + t - 1) / t; }
+
+int cu_count() {
+  static const int n = [] {
+    int dev = 0, v = 0;
+    if (hipGetDevice(&dev) == hipSuccess &&
+        hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && v > 0)
+      return v;
+    return 256;
+  }();
+  return n;
+}
+
+// Tile and kernel of a call, from its sizes alone.
+enum class Kernel { Tile128, Rows, Big };
+struct Plan {
+  Kernel kernel;
+  int bm, bn;           // output tile
+  int mt, ntw, wk;      // Rows
+};
+
+bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// What k_grouped_big's DMA assumes: bfloat16, 16-byte aligned operands and row pitches, a whole
+// number of k-tiles (the weight gradient's reduction may end anywhere), and for W read along the
+// output one expert's matrix below 2 GiB.
+bool big_ok(const GroupedDesc& d) {
+  if (d.store != Store::BF16 || !on16(d.A) || !on16(d.B) || d.lda % 8) return false;
+  if (d.weight_grad) return d.ldb % 8 == 0 && d.total_rows >= 128 * d.groups;
+  const int64_t red = d.transpose_w ? d.n : d.k;
+  if (red % 64 || d.k % 8 || (d.n * d.k) % 8 || d.n * d.k >= (int64_t(1) << 30)) return false;
+  return d.total_rows >= 128 * d.groups;
+}
+
+Plan plan_of(const GroupedDesc& d) {
+  Plan p{Kernel::Tile128, 128, 128, 0, 0, 0};
+  if (big_ok(d)) {
+    p.kernel = Kernel::Big;
+    p.bm = p.bn = 256;
+    return p;
+  }
+  if (d.weight_grad || d.transpose_w) return p;
+  // Forward with at most 96 rows per expert on average: the weights' bytes bound it.
+  const int64_t used = d.groups < d.total_rows ? d.groups : d.total_rows;   // experts with rows
+  if (d.total_rows <= 96 * d.groups) {
+    p.kernel = Kernel::Rows;
+    const int64_t avg = tiles_up(d.total_rows, used > 0 ? used : 1);
+    p.mt = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
+    // Eight waves per CU: 256 weight rows per block, else 64, else 16 with the reduction split.
+    const int64_t row_tiles = used + d.total_rows / (16 * p.mt) / 2;
+    const int64_t want = 2 * cu_count();                     // blocks of four waves
+    if (row_tiles * tiles_up(d.n, 256) >= want) p.ntw = 4, p.wk = 1;
+    else if (row_tiles * tiles_up(d.n, 64) >= want) p.ntw = 4, p.wk = 4;
+    else p.ntw = 1, p.wk = 4;
+    p.bm = 16 * p.mt;
+    p.bn = 16 * p.ntw * (4 / p.wk);
+  }
+  return p;
+}
+
+template <typename T, int MT>
+hipError_t launch_rows(const GroupedArgs& a, const Plan& p, int64_t blocks, hipStream_t s) {
+  const dim3 grid((unsigned)blocks), block(256);
+  if (p.ntw == 4 && p.wk == 1)
+    hipLaunchKernelGGL((k_grouped_rows<T, MT, 4, 1>), grid, block, 0, s, a);
+  else if (p.ntw == 4)
+    hipLaunchKernelGGL((k_grouped_rows<T, MT, 4, 4>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((k_grouped_rows<T, MT, 1, 4>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_rows(const GroupedArgs& a, const Plan& p, int64_t blocks, hipStream_t s) {
+  if (p.mt == 1) return launch_rows<T, 1>(a, p, blocks, s);
+  if (p.mt == 2) return launch_rows<T, 2>(a, p, blocks, s);
+  return launch_rows<T, 4>(a, p, blocks, s);
+}
 
 }  // namespace
 
 int64_t grouped_blocks(const GroupedDesc& d) {
-  if (d.weight_grad) return d.groups * tiles_up(d.n, kTile) * tiles_up(d.k, kTile);
+  const Plan p = plan_of(d);
+  if (d.weight_grad) return d.groups * tiles_up(d.n, p.bm) * tiles_up(d.k, p.bn);
   // every expert can end in a part tile, and so can the rows of no expert
-  return (tiles_up(d.total_rows, kTile) + d.groups + 2) *
-         tiles_up(d.transpose_w ? d.k : d.n, kTile);
+  return (tiles_up(d.total_rows, p.bm) + d.groups + 2) *
+         tiles_up(d.transpose_w ? d.k : d.n, p.bn);
+}
+
+template <typename TO, int FORM>
+static hipError_t launch_big(const GroupedArgs& a, int64_t blocks, hipStream_t s) {
+  hipLaunchKernelGGL((k_grouped_big<TO, FORM>), dim3((unsigned)((blocks + 255) / 256 * 256)), dim3(512),
+                     0, s, a);
+  return hipGetLastError();
 }
 
 size_t grouped_workspace(const GroupedDesc&) { return 0; }
@@ -303,17 +995,19 @@ const char* grouped_name(const GroupedDesc& d) {
   const bool f = d.store == Store::F32;
   if (d.weight_grad) return f ? "grouped_wgrad_f32" : "grouped_wgrad_bf16";
   if (d.transpose_w) return f ? "grouped_nn_f32" : "grouped_nn_bf16";
+  if (plan_of(d).kernel == Kernel::Rows) return f ? "grouped_rows_f32" : "grouped_rows_bf16";
   return f ? "grouped_nt_f32" : "grouped_nt_bf16";
 }
 
 hipError_t grouped(const GroupedDesc& d, hipStream_t s) {
+  const Plan pl = plan_of(d);
   const int64_t blocks = grouped_blocks(d);
   if (blocks < 1 || blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   GroupedArgs a;
   a.A = d.A; a.B = d.B; a.D = d.D; a.C = d.C;
   a.lda = d.lda;
   a.offsets = d.offsets;
-  a.total_rows = d.total_rows;
+  a.total_rows = (int)d.total_rows;
   a.groups = (int)d.groups;
   a.fill_rest = d.fill_rest ? 1 : 0;
   a.beta = d.beta;
@@ -323,7 +1017,10 @@ hipError_t grouped(const GroupedDesc& d, hipStream_t s) {
     a.ldc = d.k;
     a.N = (int)d.n;
     a.K = (int)d.k;
-    a.tiles_n = (int)tiles_up(d.k, kTile);
+    a.tiles_n = (int)tiles_up(d.k, pl.bn);
+    if (pl.kernel == Kernel::Big)
+      return d.out_store == Store::F32 ? launch_big<float, TN>(a, blocks, s)
+                                       : launch_big<__bf16, TN>(a, blocks, s);
     if (d.store == Store::F32) return launch_grouped<float, float, TN>(a, blocks, s);
     if (d.out_store == Store::F32) return launch_grouped<__bf16, float, TN>(a, blocks, s);
     return launch_grouped<__bf16, __bf16, TN>(a, blocks, s);
@@ -332,7 +1029,12 @@ hipError_t grouped(const GroupedDesc& d, hipStream_t s) {
   a.ldc = d.ldc;
   a.N = (int)(d.transpose_w ? d.k : d.n);
   a.K = (int)(d.transpose_w ? d.n : d.k);
-  a.tiles_n = (int)tiles_up(a.N, kTile);
+  a.tiles_n = (int)tiles_up(a.N, pl.bn);
+  if (pl.kernel == Kernel::Rows)
+    return d.store == Store::F32 ? launch_rows<float>(a, pl, blocks, s)
+                                 : launch_rows<__bf16>(a, pl, blocks, s);
+  if (pl.kernel == Kernel::Big)
+    return d.transpose_w ? launch_big<__bf16, NN>(a, blocks, s) : launch_big<__bf16, NT>(a, blocks, s);
   if (d.store == Store::F32)
     return d.transpose_w ? launch_grouped<float, float, NN>(a, blocks, s)
                          : launch_grouped<float, float, NT>(a, blocks, s);

@@ -77,6 +77,28 @@ def test_weight_grad(route, dtype, out_dtype):
         ref.check(C, *want, (route, n, k, "in place"))
 
 
+# more than one tile in every direction, on both sides of whole ones, groups that end inside a
+# row tile, rows enough for the large tiles (and, f32, the same shapes on the others)
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("n,k", [(512, 576), (520, 320), (192, 1000), (640, 64), (257, 448)])
+def test_many_tiles(dtype, n, k):
+    for sizes, front, tail in (([1500, 0, 257, 63], 3, 300), ([256, 512], 0, 0)):
+        bounds = ref.bounds_of(sizes, front)
+        rows, e = bounds[-1] + tail, len(sizes)
+        W, off = _rand((e, n, k), dtype, 1, 0.3), _offsets(bounds)
+        X, dY = _rand((rows, k), dtype, 2), _rand((rows, n), dtype, 3)
+        print("case", dtype, n, k, sizes, flush=True)
+        Y = mns.grouped_matmul(X, W, off)
+        ref.check(Y, *ref.matmul(X, W, bounds, False, torch.zeros_like(Y)), "forward")
+        dX = mns.grouped_matmul(dY, W, off, transpose_w=True)
+        ref.check(dX, *ref.matmul(dY, W, bounds, True, torch.zeros_like(dX)), "input gradient")
+        for out_dtype in {dtype, F32}:
+            C = _rand((e, n, k), out_dtype, 4)
+            for c, beta in ((None, 0.0), (C, -0.7)):
+                G = mns.grouped_weight_grad(dY, X, off, C=c, beta=beta, out_dtype=out_dtype)
+                ref.check(G, *ref.weight_grad(dY, X, bounds, c, beta, out_dtype), "weight gradient")
+
+
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 def test_no_rows_at_all(dtype):
     W = _rand((3, 40, 24), dtype, 1)
