@@ -934,6 +934,11 @@ mns_status mns_grouped_workspace_size(int weight_grad, int dtype, int64_t groups
   d.k = k;
   d.weight_grad = weight_grad == 1;
   *bytes = grouped_workspace(d);
+  if (!weight_grad) {                 // for either direction
+    d.transpose_w = true;
+    const size_t other = grouped_workspace(d);
+    if (other > *bytes) *bytes = other;
+  }
   return MNS_OK;
 }
 

@@ -34,6 +34,8 @@ struct GroupedArgs {
   int tiles_n;
   int fill_rest;                // NT, NN: rows of no expert are written as zeros
   float beta;                   // TN
+  int split_cap;                // most parts of a tile of the last round (k_grouped_big)
+  float* partial;               // their sums, 256 KB a part
 };
 
 __device__ __forceinline__ int clamp_row(int64_t v, int lo, int hi) {
@@ -52,51 +54,85 @@ struct Place {
   int expert, lo, hi, inside;
 };
 
-// Position `lin` in the list of tiles that walks the experts in order, each cut into row tiles of
-// BM rows with tiles_n tiles per row tile (with fill_rest, the rows before the first expert and
-// behind the last one come first and last). False past the last tile. Every wave reads 64
-// experts' bounds at a time and adds their tile counts by a shuffle scan, so it finds its place by
-// itself, without a launch or a barrier.
-__device__ __forceinline__ bool find_place(const GroupedArgs& p, int BM, int tiles_n, int64_t lin,
-                                           Place& at) {
+// The list of tiles that walks the experts in order, each cut into row tiles of BM rows with
+// tiles_n tiles per row tile (with `rest`, the rows before the first expert and behind the last
+// one come first and last). Every wave reads 64 experts' bounds at a time, one per lane, and adds
+// their tile counts by a shuffle scan, so it finds its place by itself, without a launch or a
+// barrier; up to 64 entries stay in registers for the next lookups.
+struct Walk {
+  int lo, hi;            // this lane's expert
+  int64_t incl;          // tiles up to and with it, from the start of its 64
+  int64_t total;         // tiles of all experts
+};
+
+__device__ __forceinline__ int64_t read_lane(int64_t v, int lane) {
+  const unsigned lo = __builtin_amdgcn_readlane((int)(unsigned)v, lane);
+  const int hi = __builtin_amdgcn_readlane((int)(v >> 32), lane);
+  return (int64_t)((uint64_t)(unsigned)hi << 32 | lo);
+}
+
+__device__ __forceinline__ void walk_batch(const GroupedArgs& p, int BM, int tiles_n, int rest,
+                                           int g0, Walk& w) {
   const int lane = threadIdx.x & 63;
-  const int front = p.fill_rest ? 1 : 0;
-  const int count = p.groups + 2 * front;
-  int64_t before = 0;
-  for (int g0 = 0; g0 < count; g0 += 64) {
-    const int g = g0 + lane, e = g - front;
-    int lo = 0, hi = 0;
-    if (g < count) {
-      if (e < 0) {
-        hi = clamp_row(p.offsets[0], 0, p.total_rows);
-      } else if (e >= p.groups) {
-        int first;
-        expert_rows(p, p.groups - 1, first, lo);     // from the last expert's end
-        hi = p.total_rows;
-      } else {
-        expert_rows(p, e, lo, hi);
-      }
+  const int g = g0 + lane, e = g - rest;
+  w.lo = w.hi = 0;
+  if (g < p.groups + 2 * rest) {
+    if (e < 0) {
+      w.hi = clamp_row(p.offsets[0], 0, p.total_rows);
+    } else if (e >= p.groups) {
+      int first;
+      expert_rows(p, p.groups - 1, first, w.lo);     // from the last expert's end
+      w.hi = p.total_rows;
+    } else {
+      expert_rows(p, e, w.lo, w.hi);
     }
-    const int64_t tiles = (int64_t)((hi - lo + (BM - 1)) / BM) * tiles_n;
-    int64_t incl = tiles;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t up = __shfl_up(incl, o);
-      if (lane >= o) incl += up;
-    }
-    const int64_t sum = __shfl(incl, 63);
-    if (lin < before + sum) {
-      const int src = __ffsll((unsigned long long)__ballot(before + incl > lin)) - 1;
-      at.inside = __builtin_amdgcn_readfirstlane((int)(lin - __shfl(before + incl - tiles, src)));
-      at.lo = __builtin_amdgcn_readfirstlane(__shfl(lo, src));
-      at.hi = __builtin_amdgcn_readfirstlane(__shfl(hi, src));
-      const int ge = g0 + src - front;
-      at.expert = __builtin_amdgcn_readfirstlane(ge >= 0 && ge < p.groups ? ge : -1);
-      return true;
-    }
-    before += sum;
   }
-  return false;
+  w.incl = (int64_t)((w.hi - w.lo + (BM - 1)) / BM) * tiles_n;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t up = __shfl_up(w.incl, o);
+    if (lane >= o) w.incl += up;
+  }
+}
+
+// The first batch, and the total over all of them.
+__device__ __forceinline__ Walk walk_start(const GroupedArgs& p, int BM, int tiles_n, int rest) {
+  Walk w;
+  const int count = p.groups + 2 * rest;
+  int64_t total = 0;
+  for (int g0 = (count - 1) / 64 * 64; g0 >= 0; g0 -= 64) {
+    walk_batch(p, BM, tiles_n, rest, g0, w);
+    total += read_lane(w.incl, 63);
+  }
+  w.total = total;
+  return w;
+}
+
+// The place of position `lin` (false past the last tile). Everything found is read from one lane
+// into scalar registers: a buffer resource computed from vector registers would make each load a
+// loop over its values.
+__device__ __forceinline__ bool find_place(const GroupedArgs& p, int BM, int tiles_n, int rest,
+                                           Walk w, int64_t lin, Place& at) {
+  if (lin >= w.total) return false;
+  const int count = p.groups + 2 * rest;
+  int g0 = 0;
+  if (count > 64) {
+    for (; g0 < count; g0 += 64) {
+      walk_batch(p, BM, tiles_n, rest, g0, w);
+      const int64_t sum = read_lane(w.incl, 63);
+      if (lin < sum) break;
+      lin -= sum;
+    }
+  }
+  const unsigned long long over = __ballot(w.incl > lin);
+  const int src = over ? __ffsll(over) - 1 : 63;
+  const int64_t before = src ? read_lane(w.incl, src - 1) : 0;
+  at.inside = (int)(lin - before);
+  at.lo = __builtin_amdgcn_readlane(w.lo, src);
+  at.hi = __builtin_amdgcn_readlane(w.hi, src);
+  const int ge = g0 + src - rest;
+  at.expert = ge >= 0 && ge < p.groups ? ge : -1;
+  return true;
 }
 
 template <typename T>
@@ -147,13 +183,14 @@ template <typename TO, int FM, int FN, bool ADD>
 __device__ __forceinline__ void store_fragments(const GroupedArgs& p, const floatx16 (&acc)[FM][FN],
                                                 int64_t origin, int m0, int n0, int m_valid,
                                                 int n_valid) {
-  const int lane = threadIdx.x & 63;
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));     // addresses computed here, not kept across a caller's loop
   const TO* D = static_cast<const TO*>(p.D);
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int m = m0 + 32 * i + (lane & 31);
     if (m >= m_valid) continue;
-    const int64_t row = origin + m * p.ldc;
+    const int64_t row = origin + m * (int)p.ldc;
     TO* out = static_cast<TO*>(p.C) + row;
     float add[FN * 4][4] = {};
     if (ADD && D) {
@@ -222,7 +259,9 @@ __global__ __launch_bounds__(256) void k_grouped(GroupedArgs p) {
     m_valid = p.N - m0;
   } else {
     Place at;
-    if (!find_place(p, BM, p.tiles_n, blockIdx.x, at)) return;
+    if (!find_place(p, BM, p.tiles_n, p.fill_rest, walk_start(p, BM, p.tiles_n, p.fill_rest),
+                    blockIdx.x, at))
+      return;
     expert = at.expert;
     m0 = at.lo + at.inside / p.tiles_n * BM;
     n0 = at.inside % p.tiles_n * BN;
@@ -350,7 +389,9 @@ __global__ __launch_bounds__(256) void k_grouped_rows(GroupedArgs p) {
   constexpr int D = MT >= 4 ? 3 : 4;                    // operand sets: loads D - 1 steps ahead
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   Place at;
-  if (!find_place(p, BM, p.tiles_n, blockIdx.x, at)) return;
+  if (!find_place(p, BM, p.tiles_n, p.fill_rest, walk_start(p, BM, p.tiles_n, p.fill_rest),
+                    blockIdx.x, at))
+      return;
   const int expert = at.expert;
   const int row0 = at.lo + at.inside / p.tiles_n * BM;
   const int n0 = at.inside % p.tiles_n * BN + (WK == 1 ? wave * 16 * NTW : 0);
@@ -530,75 +571,161 @@ __device__ __forceinline__ void tile_order(int t, int tiles_m, int tiles_n, int&
   tn = l / size;
 }
 
-// Blocks go round the 8 XCDs (L2 domains) one by one. Each window of 256 blocks (one per CU) is
-// dealt to them in runs of 32 consecutive tiles, so the 32 CUs of an XCD work side by side, and an
-// expert with many rows is spread over the XCDs.
-__device__ __forceinline__ int64_t xcd_order(int64_t b) {
-  const int64_t w = b & ~(int64_t)255;
-  const int r = (int)(b & 255);
-  return w + (r & 7) * 32 + (r >> 3);
+// Blocks go round the 8 XCDs (L2 domains) one by one: block b of a window of 256 takes the window's
+// tile xcd_order(b), so the 32 CUs of an XCD work on 32 consecutive tiles, and an expert with many
+// rows is spread over the XCDs.
+__device__ __forceinline__ int xcd_order(int b) { return (b & 7) * 32 + (b >> 3); }
+
+// How the tiles of a call are dealt to the 256 blocks: whole rounds first; a last round that would
+// be at most half full is cut along the reduction into `split` parts a tile, whose float32 sums
+// k_grouped_join adds in part order.
+struct Deal {
+  int64_t total, rounds;
+  int tail, split;
+};
+__device__ __forceinline__ Deal deal(int64_t total, int cap) {
+  Deal d;
+  d.total = total;
+  d.rounds = total / 256;
+  d.tail = (int)(total % 256);
+  int s = d.tail > 0 ? 256 / d.tail : 1;
+  if (s > cap) s = cap;
+  d.split = s < 1 ? 1 : s;
+  return d;
 }
 
+// Weight gradients with at most 64 experts: experts with the most rows first (ties: in order), so
+// that the blocks' last tiles are short ones. This lane's expert's rank.
+__device__ __forceinline__ int rows_rank(const GroupedArgs& p) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = 0;
+  if (lane < p.groups) expert_rows(p, lane, lo, hi);
+  const int mine = hi - lo;
+  int rank = 0;
+  for (int l = 0; l < p.groups; ++l) {
+    const int other = __builtin_amdgcn_readlane(mine, l);
+    rank += other > mine || (other == mine && l < lane);
+  }
+  return lane < p.groups ? rank : -1;
+}
+
+// One tile (or a part of its reduction) in scalar registers: where its operands start and how many
+// bytes behind that exist, its k-tiles, its output.
+struct Unit {
+  const char* A;
+  const char* B;
+  int64_t a_bytes, b_bytes;     // forward, input gradient
+  int rows;                     // weight gradient: rows of the reduction
+  int KL;
+  int m_valid, n_valid;
+  int64_t origin;
+  int slot;                     // of the part's sums; -1: the whole tile
+};
+
+// The tile of position lin: expert, rows of the expert, tile coordinates in the output.
+template <int FORM>
+__device__ __forceinline__ bool tile_at(const GroupedArgs& p, const Walk& w, int rank, int64_t lin,
+                                        int& expert, int& lo, int& hi, int& m0, int& n0) {
+  int tm, tn;
+  if constexpr (FORM == TN) {
+    const int tiles_m = (p.N + 255) / 256, per = tiles_m * p.tiles_n;
+    if (lin >= (int64_t)per * p.groups) return false;
+    expert = (int)(lin / per);
+    if (p.groups <= 64) expert = __ffsll((unsigned long long)__ballot(rank == expert)) - 1;
+    tile_order((int)(lin % per), tiles_m, p.tiles_n, tm, tn);
+    expert_rows(p, expert, lo, hi);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    m0 = tm * 256;
+  } else {
+    Place at;
+    if (!find_place(p, 256, p.tiles_n, 0, w, lin, at)) return false;
+    expert = at.expert;
+    lo = at.lo;
+    hi = at.hi;
+    tile_order(at.inside, (hi - lo + 255) / 256, p.tiles_n, tm, tn);
+    m0 = lo + tm * 256;
+  }
+  n0 = tn * 256;
+  return true;
+}
+
+// A block works through its units (every 256th tile, then at most one of the last round) without
+// a break between them: the DMA runs two k-tiles ahead across the end of a tile, so the next
+// tile's first k-tiles land while this one's last products and its epilogue run. The epilogue has
+// the 32 KB of LDS that the two stages leave.
 template <typename TO, int FORM>
 __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
   constexpr int BM = 256, BN = 256, BK = 64, FM = 4, FN = 2, INST = 4;   // DMA per wave and operand
   constexpr int STAGE = (BM + BN) * kChunks;
   constexpr bool AK = FORM == TN, BKM = FORM != NT;     // operand stored along the output
   constexpr int KROW = 512;                             // bytes of a [k][256] LDS row
-  __shared__ u32x4 lds[2 * STAGE];
+  __shared__ u32x4 lds[2 * STAGE + 2048];               // 160 KB
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
+  const int block = xcd_order(blockIdx.x);
 
-  int expert, m0, n0, red, m_valid;
-  const char* Abase;
-  const char* Bbase;
-  int64_t a_bytes, b_bytes;       // of the whole operand block (not TN)
-  const int64_t lin = xcd_order(blockIdx.x);
+  Walk walk = {};
+  int rank = -1;
   if constexpr (FORM == TN) {
-    const int tiles_m = (p.N + BM - 1) / BM, per = tiles_m * p.tiles_n;
-    expert = (int)(lin / per);
-    if (expert >= p.groups) return;
-    int tm, tn, lo, hi;
-    tile_order((int)(lin % per), tiles_m, p.tiles_n, tm, tn);
-    expert_rows(p, expert, lo, hi);
-    lo = __builtin_amdgcn_readfirstlane(lo);
-    hi = __builtin_amdgcn_readfirstlane(hi);
-    m0 = tm * BM;
-    n0 = tn * BN;
-    red = hi - lo;
-    m_valid = p.N - m0;
-    Abase = static_cast<const char*>(p.A) + (lo * p.lda + m0) * 2;
-    Bbase = static_cast<const char*>(p.B) + (lo * p.ldb + n0) * 2;
-    a_bytes = b_bytes = 0;
+    if (p.groups <= 64) rank = rows_rank(p);
+    walk.total = (int64_t)((p.N + BM - 1) / BM) * p.tiles_n * p.groups;
   } else {
-    Place at;
-    if (!find_place(p, BM, p.tiles_n, lin, at)) return;
-    expert = at.expert;
-    int tm, tn;
-    tile_order(at.inside, (at.hi - at.lo + BM - 1) / BM, p.tiles_n, tm, tn);
-    m0 = at.lo + tm * BM;
-    n0 = tn * BN;
-    red = expert < 0 ? 0 : p.K;
-    m_valid = at.hi - m0;
-    Abase = static_cast<const char*>(p.A) + m0 * p.lda * 2;
-    a_bytes = ((int64_t)(m_valid - 1) * p.lda + p.K) * 2;
-    Bbase = static_cast<const char*>(p.B) + ((expert < 0 ? 0 : expert) * p.sB +
-                                             (BKM ? (int64_t)n0 : n0 * p.ldb)) * 2;
-    b_bytes = (BKM ? (int64_t)p.K * p.ldb - n0 : (int64_t)(p.N - n0) * p.ldb) * 2;
+    walk = walk_start(p, BM, p.tiles_n, 0);
   }
-  const int n_valid = (FORM == TN ? p.K : p.N) - n0;
-  const int KL = (red + BK - 1) / BK;
-  const __amdgpu_buffer_rsrc_t rA0 = make_rsrc(Abase, a_bytes), rB0 = make_rsrc(Bbase, b_bytes);
-  // Resource of k-tile kt: the block's (offset by kt), or, for the weight gradient, one that starts
-  // at the k-tile and ends with the expert's last row.
-  auto res = [&](int kt, bool b) {
+  const Deal dl = deal(walk.total, p.split_cap);
+
+  auto unit = [&](int64_t i, Unit& u) {
+    int part = 0, parts = 1;
+    int64_t lin = i * 256 + block;
+    u.slot = -1;
+    if (i > dl.rounds) return false;
+    if (i == dl.rounds) {                   // the last round, spread evenly over the XCDs
+      const int units = dl.tail * dl.split, share = (units + 7) / 8;
+      const int at = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
+      if ((int)(blockIdx.x >> 3) >= share || at >= units) return false;
+      part = at / dl.tail;
+      parts = dl.split;
+      if (parts > 1) u.slot = at;
+      lin = i * 256 + at % dl.tail;
+    }
+    int expert, lo, hi, m0, n0;
+    if (!tile_at<FORM>(p, walk, rank, lin, expert, lo, hi, m0, n0)) return false;
+    const int red = FORM == TN ? hi - lo : p.K, tiles = (red + BK - 1) / BK;
+    const int k0 = (int)((int64_t)part * tiles / parts), k1 = (int)((int64_t)(part + 1) * tiles / parts);
+    u.KL = k1 - k0 < 2 ? 2 : k1 - k0;                   // the DMA looks two k-tiles ahead
+    u.n_valid = (FORM == TN ? p.K : p.N) - n0;
+    if constexpr (FORM == TN) {
+      const int left = red - k0 * BK, most = (k1 - k0) * BK;
+      u.rows = left < most ? left : most;
+      u.m_valid = p.N - m0;
+      u.A = static_cast<const char*>(p.A) + ((lo + (int64_t)k0 * BK) * p.lda + m0) * 2;
+      u.B = static_cast<const char*>(p.B) + ((lo + (int64_t)k0 * BK) * p.ldb + n0) * 2;
+      u.a_bytes = u.b_bytes = 0;
+      u.origin = expert * p.sC + m0 * p.ldc + n0;
+    } else {
+      u.rows = 0;
+      u.m_valid = hi - m0;
+      u.A = static_cast<const char*>(p.A) + (m0 * p.lda + k0 * BK) * 2;
+      u.a_bytes = ((int64_t)(u.m_valid - 1) * p.lda + p.K - k0 * BK) * 2;
+      const char* W = static_cast<const char*>(p.B) + expert * p.sB * 2;
+      u.B = W + (BKM ? (int64_t)k0 * BK * p.ldb + n0 : n0 * p.ldb + k0 * BK) * 2;
+      u.b_bytes = (BKM ? (int64_t)(p.K - k0 * BK) * p.ldb - n0
+                       : (int64_t)(p.N - n0) * p.ldb - k0 * BK) * 2;
+      u.origin = m0 * p.ldc + n0;
+    }
+    return true;
+  };
+  // Resource of k-tile kt of a unit: the unit's (k-tiles by offset), or, for the weight gradient, one
+  // that starts at the k-tile and ends with the unit's last row.
+  auto res = [&](const Unit& u, int kt, bool b) {
     if constexpr (FORM == TN) {
       const int64_t ld = b ? p.ldb : p.lda;
-      const int64_t left = ((int64_t)(red - kt * BK - 1) * ld + (b ? n_valid : m_valid)) * 2;
-      return make_rsrc((b ? Bbase : Abase) + kt * BK * ld * 2, left);
+      const int64_t left = ((int64_t)(u.rows - kt * BK - 1) * ld + (b ? u.n_valid : u.m_valid)) * 2;
+      return make_rsrc((b ? u.B : u.A) + kt * BK * ld * 2, u.rows > kt * BK ? left : 0);
     } else {
-      return b ? rB0 : rA0;
+      return b ? make_rsrc(u.B, u.b_bytes) : make_rsrc(u.A, u.a_bytes);
     }
   };
   auto koff = [&](int kt, bool b) {
@@ -623,12 +750,14 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
   }
 
   floatx16 acc[FM][FN];
+  auto clear = [&] {
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
+      for (int j = 0; j < FN; ++j)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+  };
 
   const int arow = wm * 128 + (lane & 31), brow = BM + wn * 64 + (lane & 31);
   u32x4 af[2][FM], bf[2][FN];
@@ -703,75 +832,130 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
       af[slot][3] = u32x4{t6.x, t6.y, t7.x, t7.y};
     }
   };
-  // DMA instruction q of k-tile kt into buffer buf (q < INST: A, else B).
-  auto dma_one = [&](__amdgpu_buffer_rsrc_t rA, __amdgpu_buffer_rsrc_t rB, int kt, int buf, int q) {
+  Unit cur, nxt;
+  int frags = FM;
+  // DMA instruction q (q < INST: A, else B) of k-tile kt into buffer buf.
+  auto dma_one = [&](__amdgpu_buffer_rsrc_t r, int kt, int buf, int q) {
     if (q < INST)
-      dma16(rA, &lds[buf * STAGE + (wave * INST + q) * 64], offA[q], koff(kt, false));
+      dma16(r, &lds[buf * STAGE + (wave * INST + q) * 64], offA[q], koff(kt, false));
     else
-      dma16(rB, &lds[buf * STAGE + BM * kChunks + (wave * INST + q - INST) * 64], offB[q - INST],
+      dma16(r, &lds[buf * STAGE + BM * kChunks + (wave * INST + q - INST) * 64], offB[q - INST],
             koff(kt, true));
   };
-  // The MFMAs of fragment slot s, with DMA instructions q0 .. q0 + 3 of k-tile kt between the first
-  // of them when NQ = 4.
-  auto kstep = [&](int s, int kt, int buf, int q0, auto nq) {
-    constexpr int NQ = decltype(nq)::value;
-    __amdgpu_buffer_rsrc_t rA = rA0, rB = rB0;
-    if constexpr (NQ > 0) {
-      if (q0 < INST) rA = res(kt, false);
-      else rB = res(kt, true);
-    }
+  // The MFMAs of fragment slot s; with half >= 0 the four DMA instructions of one operand (0: A, 1: B)
+  // of the unit's k-tile kt (past its last one: the next unit's) go out between the first of them.
+  // PART: the row tile ends inside the block's tile, and the MFMAs of fragments of 32 rows without
+  // a row to store are skipped (each SIMD holds a wave of the upper and one of the lower half).
+  auto kstep = [&](int s, int kt, int buf, auto half, auto part) {
+    constexpr int H = decltype(half)::value;
+    constexpr bool PART = decltype(part)::value;
+    const bool over = kt >= cur.KL;
+    const int k = over ? kt - cur.KL : kt;
+    const __amdgpu_buffer_rsrc_t r = res(over ? nxt : cur, k, H == 1);
 #pragma unroll
     for (int m = 0; m < FM * FN; ++m) {
-      Frag<__bf16>::mma(acc[m / FN][m % FN], bf[s][m % FN], af[s][m / FN]);
-      if (m < NQ) dma_one(rA, rB, kt, buf, q0 + m);
+      if (!PART || m / FN < frags)
+        Frag<__bf16>::mma(acc[m / FN][m % FN], bf[s][m % FN], af[s][m / FN]);
+      if (H >= 0 && m < INST) dma_one(r, k, buf, H * INST + m);
     }
-    if constexpr (NQ > 0) {
+    if constexpr (H >= 0 && !PART) {
 #pragma unroll
       for (int m = 0; m < FM * FN; ++m) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if (m < NQ) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        if (m < INST) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
       }
     }
   };
-  using N0 = std::integral_constant<int, 0>;
-  using N4 = std::integral_constant<int, 4>;
-  // k-tile kl from buffer kl % 2. Of k-tile kl + 1 the A half went out in the previous k-tile's last
-  // k-step and the B half goes out in k-step 0; the barrier before k-step 3 (whose fragments are
-  // in registers by then) waits for it and frees this buffer for k-tile kl + 2.
-  auto body = [&](int kl, auto has1, auto has2) {
-    const int b = kl & 1;
+  using HN = std::integral_constant<int, -1>;
+  using HA = std::integral_constant<int, 0>;
+  using HB = std::integral_constant<int, 1>;
+  // k-tile kl of the unit from buffer b. Of k-tile kl + 1 the A half went out in the previous
+  // k-tile's last k-step and the B half goes out in k-step 0; the barrier before k-step 3 (whose
+  // fragments are in registers by then) waits for it and frees this buffer for k-tile kl + 2.
+  auto body = [&](int kl, int b, auto part) {
     __builtin_amdgcn_s_waitcnt(0xC07F);
     load_frags(b, 1, 1);
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (decltype(has1)::value) kstep(0, kl + 1, b ^ 1, INST, N4{});
-    else kstep(0, 0, 0, 0, N0{});
+    kstep(0, kl + 1, b ^ 1, HB{}, part);
     __builtin_amdgcn_sched_barrier(0);
     load_tr(b, 1, 1);
     load_frags(b, 2, 0);
     __builtin_amdgcn_sched_barrier(0);
-    kstep(1, 0, 0, 0, N0{});
+    kstep(1, 0, 0, HN{}, part);
     __builtin_amdgcn_sched_barrier(0);
     load_tr(b, 2, 0);
     load_frags(b, 3, 1);
     __builtin_amdgcn_sched_barrier(0);
-    kstep(0, 0, 0, 0, N0{});
+    kstep(0, 0, 0, HN{}, part);
     __builtin_amdgcn_sched_barrier(0);
     load_tr(b, 3, 1);
     block_sync();
-    load_frags(b ^ 1, 0, 0);     // behind the last k-tile: an idle buffer, the values unused
+    load_frags(b ^ 1, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (decltype(has2)::value) kstep(1, kl + 2, b, 0, N4{});
-    else kstep(1, 0, 0, 0, N0{});
+    kstep(1, kl + 2, b, HA{}, part);
     __builtin_amdgcn_sched_barrier(0);
     load_tr(b ^ 1, 0, 0);
   };
-  if (KL > 0) {
+  // Rows of the tile through 32 KB of LDS, so that whole rows leave, 16 bytes a lane: 32 rows of
+  // each half at a time, as bfloat16.
+  __bf16* const stage = reinterpret_cast<__bf16*>(lds + 2 * STAGE);
+  auto lds_sync = [] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);       // lgkmcnt(0): the DMA in flight is not waited for
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  auto store_rows = [&] {
+    __bf16* out = static_cast<__bf16*>(p.C) + cur.origin;
+    // Opaque here, so that the addresses below are computed now and not kept across the main loop
+    // (they would be spilled, and reloading them waits for every store and DMA in flight).
+    int t = tid;
+    asm volatile("" : "+v"(t));
+    const int ln = t & 63, c = t & 31, n = c * 8;
 #pragma unroll
-    for (int q = 0; q < 2 * INST; ++q) dma_one(res(0, false), res(0, true), 0, 0, q);
-    if (KL > 1) {
+    for (int i = 0; i < FM; ++i) {
+      if (i) lds_sync();
+      const int rr = wm * 32 + (ln & 31);
 #pragma unroll
-      for (int q = 0; q < INST; ++q) dma_one(res(1, false), res(1, true), 1, 1, q);
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int col = wn * 64 + 32 * j + 8 * g + 4 * (ln >> 5);
+          __bf16* dst = stage + rr * BN + ((col >> 3) ^ (rr & 31)) * 8 + (col & 7);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dst[e] = (__bf16)acc[i][j][4 * g + e];
+        }
+      lds_sync();
+      u32x4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = (t >> 5) + 16 * q;
+        v[q] = *reinterpret_cast<const u32x4*>(stage + r * BN + (c ^ (r & 31)) * 8);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = (t >> 5) + 16 * q, m = (r >> 5) * 128 + 32 * i + (r & 31);
+        if (m >= cur.m_valid) continue;
+        __bf16* dst = out + m * (int)p.ldc + n;
+        if (n + 8 <= cur.n_valid) {
+          __builtin_memcpy(dst, &v[q], 16);
+        } else {
+          __bf16 x[8];
+          __builtin_memcpy(x, &v[q], 16);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < cur.n_valid) dst[e] = x[e];
+        }
+      }
     }
+  };
+
+  clear();
+  if (unit(0, cur)) {
+#pragma unroll
+    for (int q = 0; q < 2 * INST; ++q) dma_one(res(cur, 0, q >= INST), 0, 0, q);
+#pragma unroll
+    for (int q = 0; q < INST; ++q) dma_one(res(cur, 1, false), 1, 1, q);
 #pragma unroll
     for (int i = 0; i < FM; ++i) af[1][i] = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
@@ -779,112 +963,105 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
     block_sync();
     load_frags(0, 0, 0);
     load_tr(0, 0, 0);
-    using T1 = std::true_type;
-    using F1 = std::false_type;
-    int kl = 0;
-    for (; kl + 2 < KL; ++kl) body(kl, T1{}, T1{});
-    if (kl + 1 < KL) body(kl++, T1{}, F1{});
-    body(kl, F1{}, F1{});
-  }
-  block_sync();
-
-  // Epilogue: the tile goes through the idle LDS so that whole rows leave, 16 bytes a lane. Forward
-  // and input gradient: once, as bfloat16. Weight gradient: float32, 128 rows at a time, and beta C
-  // is added to the float32 sum on the way out (one rounding).
-  const int64_t origin = (FORM == TN ? expert * p.sC : 0) + m0 * p.ldc + n0;
-  if constexpr (FORM != TN) {
-    __bf16* tile = reinterpret_cast<__bf16*>(lds);
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int m = wm * 128 + 32 * i + (lane & 31);
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int n = wn * 64 + 32 * j + 8 * g + 4 * (lane >> 5);
-          __bf16* dst = tile + m * BN + ((n >> 3) ^ (m & 31)) * 8 + (n & 7);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dst[e] = (__bf16)acc[i][j][4 * g + e];
-        }
-    }
-    __syncthreads();
-    __bf16* out = static_cast<__bf16*>(p.C) + origin;
-    const int c = tid & 31, n = c * 8;
-    const int rows = m_valid < BM ? m_valid : BM;
-    for (int m = tid >> 5; m < rows; m += 16) {
-      const u32x4 v = *reinterpret_cast<const u32x4*>(tile + m * BN + (c ^ (m & 31)) * 8);
-      if (n + 8 <= n_valid) {
-        __builtin_memcpy(out + m * p.ldc + n, &v, 16);
+    int b = 0;
+    bool more = true;
+    for (int64_t i = 1; more; ++i) {
+      more = unit(i, nxt);
+      if (!more) {                // nothing follows: the DMA past the end reads no bytes
+        nxt = cur;
+        nxt.a_bytes = nxt.b_bytes = 0;
+        nxt.rows = 0;
+      }
+      const int below = cur.m_valid - 128 * wm;
+      frags = below <= 0 ? 0 : below >= 128 ? FM : (below + 31) / 32;
+      if (cur.m_valid >= BM) {
+        for (int kl = 0; kl < cur.KL; ++kl, b ^= 1) body(kl, b, std::false_type{});
       } else {
-        __bf16 t[8];
-        __builtin_memcpy(t, &v, 16);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (n + e < n_valid) out[m * p.ldc + n + e] = t[e];
+        for (int kl = 0; kl < cur.KL; ++kl, b ^= 1) body(kl, b, std::true_type{});
       }
+      if (cur.slot >= 0) {
+        floatx4* P = reinterpret_cast<floatx4*>(p.partial) + (int64_t)cur.slot * (BM * BN / 4);
+#pragma unroll
+        for (int m = 0; m < FM * FN; ++m)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            floatx4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = acc[m / FN][m % FN][4 * g + e];
+            P[(m * 4 + g) * 512 + tid] = v;
+          }
+      } else if (FORM != TN || (sizeof(TO) == 2 && !p.D)) {
+        store_rows();
+      } else {
+        store_fragments<TO, FM, FN, true>(p, acc, cur.origin, wm * 128, wn * 64, cur.m_valid,
+                                          cur.n_valid);
+      }
+      clear();
+      cur = nxt;
     }
-  } else {
-    floatx4* tile = reinterpret_cast<floatx4*>(lds);
-    TO* out = static_cast<TO*>(p.C) + origin;
-    const TO* D = p.D ? static_cast<const TO*>(p.D) + origin : nullptr;
-    const int c = tid & 63, n = c * 4;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (half) __syncthreads();
-      if (wm == half) {
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-          const int m = 32 * i + (lane & 31);
-#pragma unroll
-          for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const int ch = wn * 16 + 8 * j + 2 * g + (lane >> 5);
-              floatx4 v;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g + e];
-              tile[m * 64 + (ch ^ (m & 63))] = v;
-            }
-        }
-      }
-      __syncthreads();
-      const int rows = m_valid - 128 * half < 128 ? m_valid - 128 * half : 128;
-      constexpr int RB = 4;           // rows of a thread whose loads of C go out together
-      for (int mb = tid >> 6; mb < rows; mb += 8 * RB) {
-        TO add[RB][4];
-        if (D) {
-#pragma unroll
-          for (int r = 0; r < RB; ++r) {
-            const int m = mb + 8 * r;
-            const TO* src = D + (128 * half + (m < rows ? m : mb)) * p.ldc + n;
-            if (n + 4 <= n_valid) {
-              __builtin_memcpy(add[r], src, sizeof(add[r]));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) add[r][e] = n + e < n_valid ? src[e] : (TO)0.f;
-            }
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          const int m = mb + 8 * r;
-          if (m >= rows) break;
-          const floatx4 v = tile[m * 64 + (c ^ (m & 63))];
-          TO t[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) t[e] = (TO)(D ? v[e] + p.beta * (float)add[r][e] : v[e]);
-          TO* dst = out + (128 * half + m) * p.ldc + n;
-          if (n + 4 <= n_valid) {
-            __builtin_memcpy(dst, t, sizeof(t));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (n + e < n_valid) dst[e] = t[e];
-          }
+    block_sync();                 // no DMA is in flight when the block ends
+  }
+  // The rows of no expert: before the first one's begin and from the last one's end.
+  if (FORM != TN && p.fill_rest) {
+    int first, last, x;
+    expert_rows(p, 0, first, x);
+    expert_rows(p, p.groups - 1, x, last);
+    const int rest = first + (p.total_rows - last);
+    __bf16* out = static_cast<__bf16*>(p.C);
+    for (int r = blockIdx.x; r < rest; r += gridDim.x) {
+      const int64_t row = r < first ? r : last + (r - first);
+      for (int n = tid * 8; n < p.N; n += 512 * 8) {
+        if (n + 8 <= p.N) {
+          const u32x4 z = {0u, 0u, 0u, 0u};
+          __builtin_memcpy(out + row * p.ldc + n, &z, 16);
+        } else {
+          for (int e = n; e < p.N; ++e) out[row * p.ldc + e] = (__bf16)0.f;
         }
       }
     }
   }
+}
+
+// Adds the parts of the last round's split tiles in part order and stores them: one block per
+// 64 x 64 piece of a tile (the product kernel's fragment order: float4 (m * 4 + g) * 512 + thread).
+template <typename TO, int FORM>
+__global__ __launch_bounds__(256) void k_grouped_join(GroupedArgs p) {
+  Walk walk = {};
+  int rank = -1;
+  if constexpr (FORM == TN) {
+    if (p.groups <= 64) rank = rows_rank(p);
+    walk.total = (int64_t)((p.N + 255) / 256) * p.tiles_n * p.groups;
+  } else {
+    walk = walk_start(p, 256, p.tiles_n, 0);
+  }
+  const Deal dl = deal(walk.total, p.split_cap);
+  const int t = blockIdx.x >> 4, piece = blockIdx.x & 15;
+  if (dl.split < 2 || t >= dl.tail) return;
+  int expert, lo, hi, m0, n0;
+  if (!tile_at<FORM>(p, walk, rank, dl.rounds * 256 + t, expert, lo, hi, m0, n0)) return;
+  const int m_valid = FORM == TN ? p.N - m0 : hi - m0;
+  const int n_valid = (FORM == TN ? p.K : p.N) - n0;
+  // this piece's fragments: rows 64 (piece / 4) .., columns 64 (piece % 4) ..
+  const int wm = piece >> 3, wn = piece & 3, i0 = ((piece >> 2) & 1) * 2;
+  const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;       // wave q: fragment (i0 + q / 2, q % 2)
+  const floatx4* P = reinterpret_cast<const floatx4*>(p.partial) +
+                     (((i0 + q / 2) * 2 + q % 2) * 4) * 512 + (wm * 4 + wn) * 64 + lane;
+  floatx16 acc[1][1];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[0][0][e] = 0.f;
+  for (int part = 0; part < dl.split; ++part) {
+    const floatx4* src = P + (int64_t)(part * dl.tail + t) * (256 * 256 / 4);
+    floatx4 v[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) v[g] = src[g * 512];
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[0][0][4 * g + e] += v[g][e];
+  }
+  store_fragments<TO, 1, 1, FORM == TN>(p, acc, (FORM == TN ? expert * p.sC : 0) + m0 * p.ldc + n0,
+                                        wm * 128 + 32 * (i0 + q / 2), wn * 64 + 32 * (q % 2), m_valid,
+                                        n_valid);
 }
 
 template <typename T, typename TO, int FORM>
@@ -923,7 +1100,7 @@ bool big_ok(const GroupedDesc& d) {
   if (d.store != Store::BF16 || !on16(d.A) || !on16(d.B) || d.lda % 8) return false;
   if (d.weight_grad) return d.ldb % 8 == 0 && d.total_rows >= 128 * d.groups;
   const int64_t red = d.transpose_w ? d.n : d.k;
-  if (red % 64 || d.k % 8 || (d.n * d.k) % 8 || d.n * d.k >= (int64_t(1) << 30)) return false;
+  if (red % 64 || red < 128 || d.k % 8 || (d.n * d.k) % 8 || d.n * d.k >= (int64_t(1) << 30)) return false;
   return d.total_rows >= 128 * d.groups;
 }
 
@@ -983,13 +1160,29 @@ int64_t grouped_blocks(const GroupedDesc& d) {
 }
 
 template <typename TO, int FORM>
-static hipError_t launch_big(const GroupedArgs& a, int64_t blocks, hipStream_t s) {
-  hipLaunchKernelGGL((k_grouped_big<TO, FORM>), dim3((unsigned)((blocks + 255) / 256 * 256)), dim3(512),
-                     0, s, a);
+static hipError_t launch_big(const GroupedArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((k_grouped_big<TO, FORM>), dim3(256), dim3(512), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.split_cap < 2) return e;
+  // a split last round has at most 128 tiles
+  hipLaunchKernelGGL((k_grouped_join<TO, FORM>), dim3(128 * 16), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
-size_t grouped_workspace(const GroupedDesc&) { return 0; }
+// Parts a tile of the last round may be cut into: at least 8 k-tiles each (on the average expert,
+// for the weight gradient), and only where a call has few rounds, so that filling the last one
+// pays for the second launch.
+static int split_cap(const GroupedDesc& d) {
+  const Plan p = plan_of(d);
+  if (p.kernel != Kernel::Big || grouped_blocks(d) > 6 * 256) return 1;
+  const int64_t red = d.weight_grad ? d.total_rows / d.groups : d.transpose_w ? d.n : d.k;
+  const int64_t cap = red / 64 / 8;
+  return cap < 1 ? 1 : cap > 16 ? 16 : (int)cap;
+}
+
+size_t grouped_workspace(const GroupedDesc& d) {
+  return split_cap(d) > 1 ? size_t(256) * 256 * 256 * sizeof(float) : 0;
+}
 
 const char* grouped_name(const GroupedDesc& d) {
   const bool f = d.store == Store::F32;
@@ -1012,6 +1205,8 @@ hipError_t grouped(const GroupedDesc& d, hipStream_t s) {
   a.fill_rest = d.fill_rest ? 1 : 0;
   a.beta = d.beta;
   a.sB = a.sC = d.n * d.k;
+  a.split_cap = split_cap(d);
+  a.partial = d.workspace;
   if (d.weight_grad) {
     a.ldb = d.ldb;
     a.ldc = d.k;
@@ -1019,8 +1214,7 @@ hipError_t grouped(const GroupedDesc& d, hipStream_t s) {
     a.K = (int)d.k;
     a.tiles_n = (int)tiles_up(d.k, pl.bn);
     if (pl.kernel == Kernel::Big)
-      return d.out_store == Store::F32 ? launch_big<float, TN>(a, blocks, s)
-                                       : launch_big<__bf16, TN>(a, blocks, s);
+      return d.out_store == Store::F32 ? launch_big<float, TN>(a, s) : launch_big<__bf16, TN>(a, s);
     if (d.store == Store::F32) return launch_grouped<float, float, TN>(a, blocks, s);
     if (d.out_store == Store::F32) return launch_grouped<__bf16, float, TN>(a, blocks, s);
     return launch_grouped<__bf16, __bf16, TN>(a, blocks, s);
@@ -1034,7 +1228,7 @@ hipError_t grouped(const GroupedDesc& d, hipStream_t s) {
     return d.store == Store::F32 ? launch_rows<float>(a, pl, blocks, s)
                                  : launch_rows<__bf16>(a, pl, blocks, s);
   if (pl.kernel == Kernel::Big)
-    return d.transpose_w ? launch_big<__bf16, NN>(a, blocks, s) : launch_big<__bf16, NT>(a, blocks, s);
+    return d.transpose_w ? launch_big<__bf16, NN>(a, s) : launch_big<__bf16, NT>(a, s);
   if (d.store == Store::F32)
     return d.transpose_w ? launch_grouped<float, float, NN>(a, blocks, s)
                          : launch_grouped<float, float, NT>(a, blocks, s);
