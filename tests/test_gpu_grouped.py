@@ -99,6 +99,44 @@ def test_many_tiles(dtype, n, k):
                 ref.check(G, *ref.weight_grad(dY, X, bounds, c, beta, out_dtype), "weight gradient")
 
 
+@pytest.mark.parametrize("sizes", [[600, 150, 0, 400], [3000], [1100, 1500]])
+def test_long_reductions_in_parts(sizes):
+    """Few tiles and a long reduction: the tiles are computed in parts and joined."""
+    n, k = 384, 2048
+    bounds = ref.bounds_of(sizes, 1)
+    rows, e = bounds[-1] + 2, len(sizes)
+    off = _offsets(bounds)
+    W, X = _rand((e, n, k), BF, 1, 0.3), _rand((rows, k), BF, 2)
+    Y = mns.grouped_matmul(X, W, off)
+    ref.check(Y, *ref.matmul(X, W, bounds, False, torch.zeros_like(Y)), "forward")
+    W, dY = _rand((e, k, n), BF, 3, 0.3), _rand((rows, k), BF, 4)
+    dX = mns.grouped_matmul(dY, W, off, transpose_w=True)
+    ref.check(dX, *ref.matmul(dY, W, bounds, True, torch.zeros_like(dX)), "input gradient")
+    dY = _rand((rows, n), BF, 5)
+    for out_dtype in (BF, F32):
+        C = _rand((e, n, k), out_dtype, 6)
+        G = mns.grouped_weight_grad(dY, X, off, C=C, beta=0.5)
+        ref.check(G, *ref.weight_grad(dY, X, bounds, C, 0.5, out_dtype), "weight gradient")
+    again = mns.grouped_weight_grad(dY, X, off, C=C, beta=0.5)
+    assert torch.equal(again, G)
+
+
+def test_more_experts_than_lanes_with_many_rows():
+    sizes = [(i * 37) % 300 + (i % 3 == 0) * 90 for i in range(70)]
+    n, k = 136, 192
+    bounds = ref.bounds_of(sizes, 5)
+    rows, off = bounds[-1] + 7, _offsets(bounds)
+    assert rows >= 128 * len(sizes)
+    W, X, dY = _rand((70, n, k), BF, 1, 0.3), _rand((rows, k), BF, 2), _rand((rows, n), BF, 3)
+    Y = mns.grouped_matmul(X, W, off)
+    ref.check(Y, *ref.matmul(X, W, bounds, False, torch.zeros_like(Y)), "forward")
+    G = mns.grouped_weight_grad(dY, X, off)
+    ref.check(G, *ref.weight_grad(dY, X, bounds, None, 0.0, BF), "weight gradient")
+    W, dY = _rand((70, k, n), BF, 4, 0.3), _rand((rows, k), BF, 5)
+    dX = mns.grouped_matmul(dY, W, off, transpose_w=True)
+    ref.check(dX, *ref.matmul(dY, W, bounds, True, torch.zeros_like(dX)), "input gradient")
+
+
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 def test_no_rows_at_all(dtype):
     W = _rand((3, 40, 24), dtype, 1)
