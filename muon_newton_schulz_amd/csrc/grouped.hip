@@ -652,15 +652,14 @@ __device__ __forceinline__ bool tile_at(const GroupedArgs& p, const Walk& w, int
 
 // A block works through its units (every 256th tile, then at most one of the last round) without
 // a break between them: the DMA runs two k-tiles ahead across the end of a tile, so the next
-// tile's first k-tiles land while this one's last products and its epilogue run. The epilogue has
-// the 32 KB of LDS that the two stages leave.
+// tile's first k-tiles land while this one's last products and its epilogue run.
 template <typename TO, int FORM>
 __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
   constexpr int BM = 256, BN = 256, BK = 64, FM = 4, FN = 2, INST = 4;   // DMA per wave and operand
-  constexpr int STAGE = (BM + BN) * kChunks;
+  constexpr int SLOT = 256 * kChunks;                   // u32x4 of one operand's k-tile (32 KB)
   constexpr bool AK = FORM == TN, BKM = FORM != NT;     // operand stored along the output
   constexpr int KROW = 512;                             // bytes of a [k][256] LDS row
-  __shared__ u32x4 lds[2 * STAGE + 2048];               // 160 KB
+  __shared__ u32x4 lds[5 * SLOT];                       // A: slots 0, 1; B: slots 2, 3, 4
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
@@ -759,7 +758,7 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
   };
 
-  const int arow = wm * 128 + (lane & 31), brow = BM + wn * 64 + (lane & 31);
+  const int arow = wm * 128 + (lane & 31), brow = wn * 64 + (lane & 31);
   u32x4 af[2][FM], bf[2][FN];
   // Transposing reads: in each 16-lane group G = lane / 16, lane 4s + a points at 8 bytes of k-row
   // 8 (G / 2) + s (+ 4 for the second read), columns c .. c + 3, c = first + 16 (G % 2) + 4 a, and
@@ -776,27 +775,52 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
 #pragma unroll
     for (int i = 0; i < FM; ++i) a_addr[i] = base + address(wm * 128 + 32 * i);
 #pragma unroll
-    for (int j = 0; j < FN; ++j) b_addr[j] = base + BM * 128 + address(wn * 64 + 32 * j);
+    for (int j = 0; j < FN; ++j) b_addr[j] = base + 2 * SLOT * 16 + address(wn * 64 + 32 * j);
   }
-  auto load_frags = [&](int buf, int ks, int slot) {
+  auto load_frags = [&](int a, int b, int ks, int slot) {
     const int ch = 2 * ks + (lane >> 5);
     if constexpr (!AK) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i) af[slot][i] = lds[buf * STAGE + swz(arow + 32 * i, ch)];
+      for (int i = 0; i < FM; ++i) af[slot][i] = lds[a * SLOT + swz(arow + 32 * i, ch)];
     }
     if constexpr (!BKM) {
 #pragma unroll
-      for (int j = 0; j < FN; ++j) bf[slot][j] = lds[buf * STAGE + swz(brow + 32 * j, ch)];
+      for (int j = 0; j < FN; ++j) bf[slot][j] = lds[(2 + b) * SLOT + swz(brow + 32 * j, ch)];
     }
   };
   // The transposing loads wait for themselves (the compiler would wait for every outstanding DMA
   // first); outputs are early-clobber, and the fragments that the MFMAs before them read are
   // inputs, so none of those registers is written while an MFMA may still read it.
-  auto load_tr = [&](int buf, int ks, int slot) {
-    const uint32_t o = (uint32_t)(buf * STAGE * 16 + ks * 16 * KROW);
+  auto load_tr = [&](int a, int b, int ks, int slot) {
+    const uint32_t oa = (uint32_t)(a * SLOT * 16 + ks * 16 * KROW);
+    const uint32_t ob = (uint32_t)(b * SLOT * 16 + ks * 16 * KROW);
     const int ps = slot ^ 1;
-    if constexpr (BKM) {
-      u32x2 t0, t1, t2, t3;
+    u32x2 t0, t1, t2, t3, s0, s1, s2, s3, s4, s5, s6, s7;
+    if constexpr (AK) {
+      asm volatile(
+          "ds_read_b64_tr_b16 %0, %12\n\t"
+          "ds_read_b64_tr_b16 %1, %12 offset:2048\n\t"
+          "ds_read_b64_tr_b16 %2, %13\n\t"
+          "ds_read_b64_tr_b16 %3, %13 offset:2048\n\t"
+          "ds_read_b64_tr_b16 %4, %14\n\t"
+          "ds_read_b64_tr_b16 %5, %14 offset:2048\n\t"
+          "ds_read_b64_tr_b16 %6, %15\n\t"
+          "ds_read_b64_tr_b16 %7, %15 offset:2048\n\t"
+          "ds_read_b64_tr_b16 %8, %16\n\t"
+          "ds_read_b64_tr_b16 %9, %16 offset:2048\n\t"
+          "ds_read_b64_tr_b16 %10, %17\n\t"
+          "ds_read_b64_tr_b16 %11, %17 offset:2048\n\t"
+          "s_waitcnt lgkmcnt(0)"
+          : "=&v"(t0), "=&v"(t1), "=&v"(t2), "=&v"(t3), "=&v"(s0), "=&v"(s1), "=&v"(s2),
+            "=&v"(s3), "=&v"(s4), "=&v"(s5), "=&v"(s6), "=&v"(s7)
+          : "v"(b_addr[0] + ob), "v"(b_addr[1] + ob), "v"(a_addr[0] + oa), "v"(a_addr[1] + oa),
+            "v"(a_addr[2] + oa), "v"(a_addr[3] + oa), "v"(af[ps][0]), "v"(af[ps][1]),
+            "v"(af[ps][2]), "v"(af[ps][3]), "v"(bf[ps][0]), "v"(bf[ps][1]));
+      af[slot][0] = u32x4{s0.x, s0.y, s1.x, s1.y};
+      af[slot][1] = u32x4{s2.x, s2.y, s3.x, s3.y};
+      af[slot][2] = u32x4{s4.x, s4.y, s5.x, s5.y};
+      af[slot][3] = u32x4{s6.x, s6.y, s7.x, s7.y};
+    } else if constexpr (BKM) {
       asm volatile(
           "ds_read_b64_tr_b16 %0, %4\n\t"
           "ds_read_b64_tr_b16 %1, %4 offset:2048\n\t"
@@ -804,49 +828,26 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
           "ds_read_b64_tr_b16 %3, %5 offset:2048\n\t"
           "s_waitcnt lgkmcnt(0)"
           : "=&v"(t0), "=&v"(t1), "=&v"(t2), "=&v"(t3)
-          : "v"(b_addr[0] + o), "v"(b_addr[1] + o), "v"(af[ps][0]), "v"(af[ps][1]),
+          : "v"(b_addr[0] + ob), "v"(b_addr[1] + ob), "v"(af[ps][0]), "v"(af[ps][1]),
             "v"(af[ps][2]), "v"(af[ps][3]), "v"(bf[ps][0]), "v"(bf[ps][1]));
+    }
+    if constexpr (BKM) {
       bf[slot][0] = u32x4{t0.x, t0.y, t1.x, t1.y};
       bf[slot][1] = u32x4{t2.x, t2.y, t3.x, t3.y};
-    }
-    if constexpr (AK) {
-      u32x2 t0, t1, t2, t3, t4, t5, t6, t7;
-      asm volatile(
-          "ds_read_b64_tr_b16 %0, %8\n\t"
-          "ds_read_b64_tr_b16 %1, %8 offset:2048\n\t"
-          "ds_read_b64_tr_b16 %2, %9\n\t"
-          "ds_read_b64_tr_b16 %3, %9 offset:2048\n\t"
-          "ds_read_b64_tr_b16 %4, %10\n\t"
-          "ds_read_b64_tr_b16 %5, %10 offset:2048\n\t"
-          "ds_read_b64_tr_b16 %6, %11\n\t"
-          "ds_read_b64_tr_b16 %7, %11 offset:2048\n\t"
-          "s_waitcnt lgkmcnt(0)"
-          : "=&v"(t0), "=&v"(t1), "=&v"(t2), "=&v"(t3), "=&v"(t4), "=&v"(t5), "=&v"(t6),
-            "=&v"(t7)
-          : "v"(a_addr[0] + o), "v"(a_addr[1] + o), "v"(a_addr[2] + o), "v"(a_addr[3] + o),
-            "v"(af[ps][0]), "v"(af[ps][1]), "v"(af[ps][2]), "v"(af[ps][3]), "v"(bf[ps][0]),
-            "v"(bf[ps][1]));
-      af[slot][0] = u32x4{t0.x, t0.y, t1.x, t1.y};
-      af[slot][1] = u32x4{t2.x, t2.y, t3.x, t3.y};
-      af[slot][2] = u32x4{t4.x, t4.y, t5.x, t5.y};
-      af[slot][3] = u32x4{t6.x, t6.y, t7.x, t7.y};
     }
   };
   Unit cur, nxt;
   int frags = FM;
-  // DMA instruction q (q < INST: A, else B) of k-tile kt into buffer buf.
-  auto dma_one = [&](__amdgpu_buffer_rsrc_t r, int kt, int buf, int q) {
-    if (q < INST)
-      dma16(r, &lds[buf * STAGE + (wave * INST + q) * 64], offA[q], koff(kt, false));
-    else
-      dma16(r, &lds[buf * STAGE + BM * kChunks + (wave * INST + q - INST) * 64], offB[q - INST],
-            koff(kt, true));
+  // DMA instruction q of the A (B) half of k-tile kt into A (B) slot `slot`.
+  auto dma_one = [&](__amdgpu_buffer_rsrc_t r, int kt, int slot, bool b, int q) {
+    dma16(r, &lds[((b ? 2 : 0) + slot) * SLOT + (wave * INST + q) * 64], b ? offB[q] : offA[q],
+          koff(kt, b));
   };
   // The MFMAs of fragment slot s; with half >= 0 the four DMA instructions of one operand (0: A, 1: B)
   // of the unit's k-tile kt (past its last one: the next unit's) go out between the first of them.
   // PART: the row tile ends inside the block's tile, and the MFMAs of fragments of 32 rows without
   // a row to store are skipped (each SIMD holds a wave of the upper and one of the lower half).
-  auto kstep = [&](int s, int kt, int buf, auto half, auto part) {
+  auto kstep = [&](int s, int kt, int slot, auto half, auto part) {
     constexpr int H = decltype(half)::value;
     constexpr bool PART = decltype(part)::value;
     const bool over = kt >= cur.KL;
@@ -856,7 +857,7 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
     for (int m = 0; m < FM * FN; ++m) {
       if (!PART || m / FN < frags)
         Frag<__bf16>::mma(acc[m / FN][m % FN], bf[s][m % FN], af[s][m / FN]);
-      if (H >= 0 && m < INST) dma_one(r, k, buf, H * INST + m);
+      if (H >= 0 && m < INST) dma_one(r, k, slot, H == 1, m);
     }
     if constexpr (H >= 0 && !PART) {
 #pragma unroll
@@ -869,72 +870,72 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
   using HN = std::integral_constant<int, -1>;
   using HA = std::integral_constant<int, 0>;
   using HB = std::integral_constant<int, 1>;
-  // k-tile kl of the unit from buffer b. Of k-tile kl + 1 the A half went out in the previous
-  // k-tile's last k-step and the B half goes out in k-step 0; the barrier before k-step 3 (whose
-  // fragments are in registers by then) waits for it and frees this buffer for k-tile kl + 2.
-  auto body = [&](int kl, int b, auto part) {
+  // k-tile kl of the unit from A slot a, B slot b. The DMA runs ahead: the B half of k-tile kl + 2 goes
+  // out in k-step 0, the A half in k-step 3, behind the barrier that frees this k-tile's slots (its
+  // last fragments are in registers by then). That barrier waits for k-tile kl + 1 but not for the
+  // four newest loads, the B half of kl + 2: B is the weights, read by few tiles and mostly from
+  // HBM, and has 1.75 k-tiles to land; A is shared by more tiles, mostly comes from L2, and has one.
+  auto body = [&](int kl, int a, int b, auto part) {
+    const int b1 = b == 2 ? 0 : b + 1, b2 = b == 0 ? 2 : b - 1;
     __builtin_amdgcn_s_waitcnt(0xC07F);
-    load_frags(b, 1, 1);
+    load_frags(a, b, 1, 1);
     __builtin_amdgcn_sched_barrier(0);
-    kstep(0, kl + 1, b ^ 1, HB{}, part);
+    kstep(0, kl + 2, b2, HB{}, part);
     __builtin_amdgcn_sched_barrier(0);
-    load_tr(b, 1, 1);
-    load_frags(b, 2, 0);
+    load_tr(a, b, 1, 1);
+    load_frags(a, b, 2, 0);
     __builtin_amdgcn_sched_barrier(0);
     kstep(1, 0, 0, HN{}, part);
     __builtin_amdgcn_sched_barrier(0);
-    load_tr(b, 2, 0);
-    load_frags(b, 3, 1);
+    load_tr(a, b, 2, 0);
+    load_frags(a, b, 3, 1);
     __builtin_amdgcn_sched_barrier(0);
     kstep(0, 0, 0, HN{}, part);
     __builtin_amdgcn_sched_barrier(0);
-    load_tr(b, 3, 1);
-    block_sync();
-    load_frags(b ^ 1, 0, 0);
-    __builtin_amdgcn_sched_barrier(0);
-    kstep(1, kl + 2, b, HA{}, part);
-    __builtin_amdgcn_sched_barrier(0);
-    load_tr(b ^ 1, 0, 0);
-  };
-  // Rows of the tile through 32 KB of LDS, so that whole rows leave, 16 bytes a lane: 32 rows of
-  // each half at a time, as bfloat16.
-  __bf16* const stage = reinterpret_cast<__bf16*>(lds + 2 * STAGE);
-  auto lds_sync = [] {
+    load_tr(a, b, 3, 1);
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0xC07F);       // lgkmcnt(0): the DMA in flight is not waited for
+    __builtin_amdgcn_s_waitcnt(0x0074);       // vmcnt(4) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+    load_frags(a ^ 1, b1, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    kstep(1, kl + 2, a, HA{}, part);
+    __builtin_amdgcn_sched_barrier(0);
+    load_tr(a ^ 1, b1, 0, 0);
   };
-  auto store_rows = [&] {
+  // The tile through LDS, so that whole 128-byte lines leave, 16 bytes a lane. The B slot of the k-tile
+  // just finished (the third: the next two hold or receive the next unit's) is free until this
+  // wave's own DMA fills its 4 KB of it again, so each wave stages 32 rows x 64 columns there by
+  // itself, without a barrier.
+  auto store_rows = [&](int b) {
     __bf16* out = static_cast<__bf16*>(p.C) + cur.origin;
     // Opaque here, so that the addresses below are computed now and not kept across the main loop
     // (they would be spilled, and reloading them waits for every store and DMA in flight).
-    int t = tid;
-    asm volatile("" : "+v"(t));
-    const int ln = t & 63, c = t & 31, n = c * 8;
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    __bf16* const stage = reinterpret_cast<__bf16*>(lds + (2 + b) * SLOT + wave * 256);
+    const int c = ln & 7, n = wn * 64 + c * 8;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      if (i) lds_sync();
-      const int rr = wm * 32 + (ln & 31);
+      const int rr = ln & 31;
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int col = wn * 64 + 32 * j + 8 * g + 4 * (ln >> 5);
-          __bf16* dst = stage + rr * BN + ((col >> 3) ^ (rr & 31)) * 8 + (col & 7);
+          const int col = 32 * j + 8 * g + 4 * (ln >> 5);
+          __bf16* dst = stage + rr * 64 + ((col >> 3) ^ (rr & 7)) * 8 + (col & 7);
 #pragma unroll
           for (int e = 0; e < 4; ++e) dst[e] = (__bf16)acc[i][j][4 * g + e];
         }
-      lds_sync();
       u32x4 v[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int r = (t >> 5) + 16 * q;
-        v[q] = *reinterpret_cast<const u32x4*>(stage + r * BN + (c ^ (r & 31)) * 8);
+        const int r = (ln >> 3) + 8 * q;
+        v[q] = *reinterpret_cast<const u32x4*>(stage + r * 64 + (c ^ (r & 7)) * 8);
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int r = (t >> 5) + 16 * q, m = (r >> 5) * 128 + 32 * i + (r & 31);
+        const int m = wm * 128 + 32 * i + (ln >> 3) + 8 * q;
         if (m >= cur.m_valid) continue;
         __bf16* dst = out + m * (int)p.ldc + n;
         if (n + 8 <= cur.n_valid) {
@@ -953,17 +954,22 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
   clear();
   if (unit(0, cur)) {
 #pragma unroll
-    for (int q = 0; q < 2 * INST; ++q) dma_one(res(cur, 0, q >= INST), 0, 0, q);
+    for (int h = 0; h < 4; ++h) {               // B 0, A 0, B 1, A 1
+      const __amdgpu_buffer_rsrc_t r = res(cur, h >> 1, !(h & 1));
 #pragma unroll
-    for (int q = 0; q < INST; ++q) dma_one(res(cur, 1, false), 1, 1, q);
+      for (int q = 0; q < INST; ++q) dma_one(r, h >> 1, h >> 1, !(h & 1), q);
+    }
 #pragma unroll
     for (int i = 0; i < FM; ++i) af[1][i] = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
     for (int j = 0; j < FN; ++j) bf[1][j] = u32x4{0u, 0u, 0u, 0u};
-    block_sync();
-    load_frags(0, 0, 0);
-    load_tr(0, 0, 0);
-    int b = 0;
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0078);         // vmcnt(8): k-tile 0 has landed
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    load_frags(0, 0, 0, 0);
+    load_tr(0, 0, 0, 0);
+    int a = 0, b = 0;
     bool more = true;
     for (int64_t i = 1; more; ++i) {
       more = unit(i, nxt);
@@ -974,11 +980,15 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
       }
       const int below = cur.m_valid - 128 * wm;
       frags = below <= 0 ? 0 : below >= 128 ? FM : (below + 31) / 32;
-      if (cur.m_valid >= BM) {
-        for (int kl = 0; kl < cur.KL; ++kl, b ^= 1) body(kl, b, std::false_type{});
-      } else {
-        for (int kl = 0; kl < cur.KL; ++kl, b ^= 1) body(kl, b, std::true_type{});
-      }
+      auto run = [&](auto part) {
+        for (int kl = 0; kl < cur.KL; ++kl) {
+          body(kl, a, b, part);
+          a ^= 1;
+          b = b == 2 ? 0 : b + 1;
+        }
+      };
+      if (cur.m_valid >= BM) run(std::false_type{});
+      else run(std::true_type{});
       if (cur.slot >= 0) {
         floatx4* P = reinterpret_cast<floatx4*>(p.partial) + (int64_t)cur.slot * (BM * BN / 4);
 #pragma unroll
@@ -991,7 +1001,7 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
             P[(m * 4 + g) * 512 + tid] = v;
           }
       } else if (FORM != TN || (sizeof(TO) == 2 && !p.D)) {
-        store_rows();
+        store_rows(b == 0 ? 2 : b - 1);
       } else {
         store_fragments<TO, FM, FN, true>(p, acc, cur.origin, wm * 128, wn * 64, cur.m_valid,
                                           cur.n_valid);
