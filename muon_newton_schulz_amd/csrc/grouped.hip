@@ -229,6 +229,62 @@ __device__ __forceinline__ void store_fragments(const GroupedArgs& p, const floa
   }
 }
 
+// The other orientation (A feeds the MFMA's A input): element e of a lane is row m0 + 8 (e / 4)
+// + 4 (lane >> 5) + e % 4, column n0 + (lane & 31). 32 lanes hold 32 neighbouring columns, so a
+// float32 output and its addend move as whole 128-byte lines, straight from registers; bfloat16
+// neighbours are paired (the even lane takes row e, the odd one row e + 1), 64 bytes of four rows
+// a store. One fragment's addends, and its store:
+template <typename TO>
+__device__ __forceinline__ void load_addend(const GroupedArgs& p, int64_t origin, int m0, int n0,
+                                            int m_valid, int n_valid, float (&add)[16]) {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));     // addresses computed here, not kept across a caller's loop
+  const TO* D = static_cast<const TO*>(p.D) + origin;
+  const int n = n0 + (lane & 31);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int m = m0 + 8 * (e / 4) + 4 * (lane >> 5) + e % 4;
+    // past the end: the tile's first element, in bounds and not used
+    add[e] = (float)D[m < m_valid && n < n_valid ? m * (int)p.ldc + n : 0];
+  }
+}
+template <typename TO>
+__device__ __forceinline__ void store_lanes(const GroupedArgs& p, const floatx16& acc,
+                                            int64_t origin, int m0, int n0, int m_valid,
+                                            int n_valid, const float (&add)[16]) {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  TO* C = static_cast<TO*>(p.C) + origin;
+  const int n = n0 + (lane & 31);
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) {
+    const int m = m0 + 8 * (e / 4) + 4 * (lane >> 5) + e % 4;
+    float v[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      v[r] = acc[e + r];
+      if (p.D) v[r] += p.beta * add[e + r];
+    }
+    if constexpr (sizeof(TO) == 4) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        if (m + r < m_valid && n < n_valid) C[(m + r) * (int)p.ldc + n] = v[r];
+    } else {
+      const bool odd = lane & 1;
+      const unsigned give = __builtin_bit_cast(unsigned, odd ? v[0] : v[1]);
+      // quad_perm [1, 0, 3, 2]: the neighbour's value of the row this lane stores
+      const float got = __builtin_bit_cast(
+          float, __builtin_amdgcn_update_dpp(0u, give, 0xB1, 0xF, 0xF, true));
+      const TO pair[2] = {(TO)(odd ? got : v[0]), (TO)(odd ? v[1] : got)};
+      const int mm = m + odd, nn = n - odd;
+      if (mm >= m_valid) continue;
+      TO* dst = C + mm * (int)p.ldc + nn;
+      if (nn + 1 < n_valid) __builtin_memcpy(dst, pair, sizeof(pair));
+      else if (nn < n_valid) dst[0] = pair[0];
+    }
+  }
+}
+
 // Any sizes, pitches and alignment of both types: 128 x 128 tiles, four waves of 64 x 64, k-tiles
 // of 128 bytes a row loaded into registers one tile ahead and stored to LDS as [row][k] (144-byte
 // rows: 16 rows' 16-byte reads cover the 64 banks once), a k-major operand transposed on the way.
@@ -272,6 +328,17 @@ __global__ __launch_bounds__(256) void k_grouped(GroupedArgs p) {
     m_valid = at.hi - m0;
   }
   const int n_valid = (FORM == TN ? p.K : p.N) - n0;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int64_t origin = (FORM == TN ? expert * p.sC : 0) + m0 * p.ldc + n0;
+  // The addend first: with few rows its bytes and the output's are what the call takes.
+  float add[2][2][16];
+  if (FORM == TN && p.D) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        load_addend<TO>(p, origin, wm * 64 + 32 * i, wn * 64 + 32 * j, m_valid, n_valid, add[i][j]);
+  }
 
   // Chunk q of this thread of a k-contiguous operand: row, first k; of a k-major one: k-row,
   // first column (16 k-rows x 4 chunks per wave: 64-byte pieces of a row).
@@ -319,7 +386,6 @@ __global__ __launch_bounds__(256) void k_grouped(GroupedArgs p) {
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-  const int wm = wave >> 1, wn = wave & 1;
   if (red > 0) {
     load(A, p.lda, FORM == TN, m_valid, 0, ra);
     load(B, p.ldb, FORM != NT, n_valid, 0, rb);
@@ -341,17 +407,29 @@ __global__ __launch_bounds__(256) void k_grouped(GroupedArgs p) {
         a[i] = *reinterpret_cast<const u32x4*>(As + (wm * 64 + 32 * i + (lane & 31)) * PITCH + kk);
         b[i] = *reinterpret_cast<const u32x4*>(Bs + (wn * 64 + 32 * i + (lane & 31)) * PITCH + kk);
       }
-      // the B tile feeds the MFMA's A input: each lane holds 4 consecutive columns of one row
+      // B as the MFMA's A input: each lane holds 4 consecutive columns of one row; the other way
+      // round, for the weight gradient: one column of 16 rows
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) F::mma(acc[i][j], b[j], a[i]);
+        for (int j = 0; j < 2; ++j) {
+          if constexpr (FORM == TN) F::mma(acc[i][j], a[i], b[j]);
+          else F::mma(acc[i][j], b[j], a[i]);
+        }
     }
     __syncthreads();
   }
 
-  const int64_t origin = (FORM == TN ? expert * p.sC : 0) + m0 * p.ldc + n0;
-  store_fragments<TO, 2, 2, FORM == TN>(p, acc, origin, wm * 64, wn * 64, m_valid, n_valid);
+  if constexpr (FORM == TN) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        store_lanes<TO>(p, acc[i][j], origin, wm * 64 + 32 * i, wn * 64 + 32 * j, m_valid, n_valid,
+                        add[i][j]);
+  } else {
+    store_fragments<TO, 2, 2, false>(p, acc, origin, wm * 64, wn * 64, m_valid, n_valid);
+  }
 }
 
 // Few rows per expert (forward): the product is bound by reading the weights once, so the weights
@@ -653,7 +731,7 @@ __device__ __forceinline__ bool tile_at(const GroupedArgs& p, const Walk& w, int
 // A block works through its units (every 256th tile, then at most one of the last round) without
 // a break between them: the DMA runs two k-tiles ahead across the end of a tile, so the next
 // tile's first k-tiles land while this one's last products and its epilogue run.
-template <typename TO, int FORM>
+template <typename TO, int FORM, bool ADD>
 __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
   constexpr int BM = 256, BN = 256, BK = 64, FM = 4, FN = 2, INST = 4;   // DMA per wave and operand
   constexpr int SLOT = 256 * kChunks;                   // u32x4 of one operand's k-tile (32 KB)
@@ -951,6 +1029,59 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
     }
   };
 
+  // The same with beta C, added to the float32 sum (one rounding): a fragment of 32 x 32 at a time,
+  // whose addend is loaded while it goes through LDS. (A float32 output without an addend is
+  // stored from registers, two lanes a 32-byte piece: 470 against 479 us on 32 experts of
+  // 8192 x 1024; with one, pieces took 640 us and whole lines take 593.)
+  auto store_sums = [&](int b) {
+    TO* out = static_cast<TO*>(p.C) + cur.origin;
+    const TO* D = static_cast<const TO*>(p.D) + cur.origin;
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    floatx4* const stage = reinterpret_cast<floatx4*>(lds + (2 + b) * SLOT + wave * 256);
+    const int c = ln & 7, r0 = ln >> 3;
+#pragma unroll
+    for (int f = 0; f < FM * FN; ++f) {
+      const int n = wn * 64 + 32 * (f % FN) + 4 * c, m0 = wm * 128 + 32 * (f / FN) + r0;
+      TO add[4][4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        // past the last row: the tile's first, in bounds and not used
+        const TO* src = D + (m0 + 8 * q < cur.m_valid ? (m0 + 8 * q) * (int)p.ldc : 0) + n;
+        if (n + 4 <= cur.n_valid) {
+          __builtin_memcpy(add[q], src, sizeof(add[q]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) add[q][e] = n + e < cur.n_valid ? src[e] : (TO)0.f;
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        floatx4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = acc[f / FN][f % FN][4 * g + e];
+        stage[(ln & 31) * 8 + ((2 * g + (ln >> 5)) ^ (ln & 7))] = v;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = r0 + 8 * q;
+        const floatx4 v = stage[r * 8 + (c ^ (r & 7))];
+        if (m0 + 8 * q >= cur.m_valid) continue;
+        TO t[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = (TO)(v[e] + p.beta * (float)add[q][e]);
+        TO* dst = out + (m0 + 8 * q) * (int)p.ldc + n;
+        if (n + 4 <= cur.n_valid) {
+          __builtin_memcpy(dst, t, sizeof(t));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < cur.n_valid) dst[e] = t[e];
+        }
+      }
+    }
+  };
+
   clear();
   if (unit(0, cur)) {
 #pragma unroll
@@ -1000,11 +1131,13 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
             for (int e = 0; e < 4; ++e) v[e] = acc[m / FN][m % FN][4 * g + e];
             P[(m * 4 + g) * 512 + tid] = v;
           }
-      } else if (FORM != TN || (sizeof(TO) == 2 && !p.D)) {
+      } else if constexpr (ADD) {
+        store_sums(b == 0 ? 2 : b - 1);
+      } else if constexpr (sizeof(TO) == 2) {
         store_rows(b == 0 ? 2 : b - 1);
       } else {
-        store_fragments<TO, FM, FN, true>(p, acc, cur.origin, wm * 128, wn * 64, cur.m_valid,
-                                          cur.n_valid);
+        store_fragments<TO, FM, FN, false>(p, acc, cur.origin, wm * 128, wn * 64, cur.m_valid,
+                                           cur.n_valid);
       }
       clear();
       cur = nxt;
@@ -1171,7 +1304,10 @@ int64_t grouped_blocks(const GroupedDesc& d) {
 
 template <typename TO, int FORM>
 static hipError_t launch_big(const GroupedArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_grouped_big<TO, FORM>), dim3(256), dim3(512), 0, s, a);
+  if (FORM == TN && a.D)
+    hipLaunchKernelGGL((k_grouped_big<TO, FORM, FORM == TN>), dim3(256), dim3(512), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_grouped_big<TO, FORM, false>), dim3(256), dim3(512), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.split_cap < 2) return e;
   // a split last round has at most 128 tiles
