@@ -61,15 +61,9 @@ struct Place {
 // barrier; up to 64 entries stay in registers for the next lookups.
 struct Walk {
   int lo, hi;            // this lane's expert
-  int64_t incl;          // tiles up to and with it, from the start of its 64
-  int64_t total;         // tiles of all experts
+  int incl;              // tiles up to and with it, from the start of its 64
+  int total;             // tiles of all experts
 };
-
-__device__ __forceinline__ int64_t read_lane(int64_t v, int lane) {
-  const unsigned lo = __builtin_amdgcn_readlane((int)(unsigned)v, lane);
-  const int hi = __builtin_amdgcn_readlane((int)(v >> 32), lane);
-  return (int64_t)((uint64_t)(unsigned)hi << 32 | lo);
-}
 
 __device__ __forceinline__ void walk_batch(const GroupedArgs& p, int BM, int tiles_n, int rest,
                                            int g0, Walk& w) {
@@ -87,10 +81,12 @@ __device__ __forceinline__ void walk_batch(const GroupedArgs& p, int BM, int til
       expert_rows(p, e, w.lo, w.hi);
     }
   }
-  w.incl = (int64_t)((w.hi - w.lo + (BM - 1)) / BM) * tiles_n;
+  // The host refuses calls of 2^31 tiles; only offsets that overlap can add up to more (find_place
+  // then checks what it finds).
+  w.incl = (w.hi - w.lo + (BM - 1)) / BM * tiles_n;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const int64_t up = __shfl_up(w.incl, o);
+    const int up = __shfl_up(w.incl, o);
     if (lane >= o) w.incl += up;
   }
 }
@@ -99,10 +95,10 @@ __device__ __forceinline__ void walk_batch(const GroupedArgs& p, int BM, int til
 __device__ __forceinline__ Walk walk_start(const GroupedArgs& p, int BM, int tiles_n, int rest) {
   Walk w;
   const int count = p.groups + 2 * rest;
-  int64_t total = 0;
+  int total = 0;
   for (int g0 = (count - 1) / 64 * 64; g0 >= 0; g0 -= 64) {
     walk_batch(p, BM, tiles_n, rest, g0, w);
-    total += read_lane(w.incl, 63);
+    total += __builtin_amdgcn_readlane(w.incl, 63);
   }
   w.total = total;
   return w;
@@ -112,27 +108,26 @@ __device__ __forceinline__ Walk walk_start(const GroupedArgs& p, int BM, int til
 // into scalar registers: a buffer resource computed from vector registers would make each load a
 // loop over its values.
 __device__ __forceinline__ bool find_place(const GroupedArgs& p, int BM, int tiles_n, int rest,
-                                           Walk w, int64_t lin, Place& at) {
+                                           Walk w, int lin, Place& at) {
   if (lin >= w.total) return false;
   const int count = p.groups + 2 * rest;
   int g0 = 0;
   if (count > 64) {
     for (; g0 < count; g0 += 64) {
       walk_batch(p, BM, tiles_n, rest, g0, w);
-      const int64_t sum = read_lane(w.incl, 63);
+      const int sum = __builtin_amdgcn_readlane(w.incl, 63);
       if (lin < sum) break;
       lin -= sum;
     }
   }
   const unsigned long long over = __ballot(w.incl > lin);
   const int src = over ? __ffsll(over) - 1 : 63;
-  const int64_t before = src ? read_lane(w.incl, src - 1) : 0;
-  at.inside = (int)(lin - before);
+  at.inside = lin - (src ? __builtin_amdgcn_readlane(w.incl, src - 1) : 0);
   at.lo = __builtin_amdgcn_readlane(w.lo, src);
   at.hi = __builtin_amdgcn_readlane(w.hi, src);
   const int ge = g0 + src - rest;
   at.expert = ge >= 0 && ge < p.groups ? ge : -1;
-  return true;
+  return at.inside >= 0 && at.inside < (at.hi - at.lo + (BM - 1)) / BM * tiles_n;
 }
 
 template <typename T>
@@ -316,7 +311,7 @@ __global__ __launch_bounds__(256) void k_grouped(GroupedArgs p) {
   } else {
     Place at;
     if (!find_place(p, BM, p.tiles_n, p.fill_rest, walk_start(p, BM, p.tiles_n, p.fill_rest),
-                    blockIdx.x, at))
+                    (int)blockIdx.x, at))
       return;
     expert = at.expert;
     m0 = at.lo + at.inside / p.tiles_n * BM;
@@ -468,7 +463,7 @@ __global__ __launch_bounds__(256) void k_grouped_rows(GroupedArgs p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   Place at;
   if (!find_place(p, BM, p.tiles_n, p.fill_rest, walk_start(p, BM, p.tiles_n, p.fill_rest),
-                    blockIdx.x, at))
+                    (int)blockIdx.x, at))
       return;
   const int expert = at.expert;
   const int row0 = at.lo + at.inside / p.tiles_n * BM;
@@ -658,14 +653,12 @@ __device__ __forceinline__ int xcd_order(int b) { return (b & 7) * 32 + (b >> 3)
 // be at most half full is cut along the reduction into `split` parts a tile, whose float32 sums
 // k_grouped_join adds in part order.
 struct Deal {
-  int64_t total, rounds;
-  int tail, split;
+  int rounds, tail, split;
 };
-__device__ __forceinline__ Deal deal(int64_t total, int cap) {
+__device__ __forceinline__ Deal deal(int total, int cap) {
   Deal d;
-  d.total = total;
-  d.rounds = total / 256;
-  d.tail = (int)(total % 256);
+  d.rounds = total >> 8;
+  d.tail = total & 255;
   int s = d.tail > 0 ? 256 / d.tail : 1;
   if (s > cap) s = cap;
   d.split = s < 1 ? 1 : s;
@@ -702,15 +695,15 @@ struct Unit {
 
 // The tile of position lin: expert, rows of the expert, tile coordinates in the output.
 template <int FORM>
-__device__ __forceinline__ bool tile_at(const GroupedArgs& p, const Walk& w, int rank, int64_t lin,
+__device__ __forceinline__ bool tile_at(const GroupedArgs& p, const Walk& w, int rank, int lin,
                                         int& expert, int& lo, int& hi, int& m0, int& n0) {
   int tm, tn;
   if constexpr (FORM == TN) {
     const int tiles_m = (p.N + 255) / 256, per = tiles_m * p.tiles_n;
-    if (lin >= (int64_t)per * p.groups) return false;
-    expert = (int)(lin / per);
+    if (lin >= w.total) return false;
+    expert = lin / per;
     if (p.groups <= 64) expert = __ffsll((unsigned long long)__ballot(rank == expert)) - 1;
-    tile_order((int)(lin % per), tiles_m, p.tiles_n, tm, tn);
+    tile_order(lin % per, tiles_m, p.tiles_n, tm, tn);
     expert_rows(p, expert, lo, hi);
     lo = __builtin_amdgcn_readfirstlane(lo);
     hi = __builtin_amdgcn_readfirstlane(hi);
@@ -747,15 +740,15 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
   int rank = -1;
   if constexpr (FORM == TN) {
     if (p.groups <= 64) rank = rows_rank(p);
-    walk.total = (int64_t)((p.N + BM - 1) / BM) * p.tiles_n * p.groups;
+    walk.total = (p.N + BM - 1) / BM * p.tiles_n * p.groups;
   } else {
     walk = walk_start(p, BM, p.tiles_n, 0);
   }
   const Deal dl = deal(walk.total, p.split_cap);
 
-  auto unit = [&](int64_t i, Unit& u) {
+  auto unit = [&](int i, Unit& u) {
     int part = 0, parts = 1;
-    int64_t lin = i * 256 + block;
+    int lin = i * 256 + block;
     u.slot = -1;
     if (i > dl.rounds) return false;
     if (i == dl.rounds) {                   // the last round, spread evenly over the XCDs
@@ -770,7 +763,8 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
     int expert, lo, hi, m0, n0;
     if (!tile_at<FORM>(p, walk, rank, lin, expert, lo, hi, m0, n0)) return false;
     const int red = FORM == TN ? hi - lo : p.K, tiles = (red + BK - 1) / BK;
-    const int k0 = (int)((int64_t)part * tiles / parts), k1 = (int)((int64_t)(part + 1) * tiles / parts);
+    const int k0 = parts > 1 ? part * tiles / parts : 0;      // parts <= 16, tiles < 2^26
+    const int k1 = parts > 1 ? (part + 1) * tiles / parts : tiles;
     u.KL = k1 - k0 < 2 ? 2 : k1 - k0;                   // the DMA looks two k-tiles ahead
     u.n_valid = (FORM == TN ? p.K : p.N) - n0;
     if constexpr (FORM == TN) {
@@ -953,6 +947,12 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
   // last fragments are in registers by then). That barrier waits for k-tile kl + 1 but not for the
   // four newest loads, the B half of kl + 2: B is the weights, read by few tiles and mostly from
   // HBM, and has 1.75 k-tiles to land; A is shared by more tiles, mostly comes from L2, and has one.
+  // After a whole tile's epilogue its stores (one instruction per 16 bytes of a lane: kStores) lie
+  // between those loads and k-tile kl + 1, and the first barrier leaves them in flight too.
+  constexpr int kStores = ADD ? 0 : sizeof(TO) == 2 ? FM * FN * 2 : FM * FN * 4;
+  constexpr int kVm = 4 + kStores, kLate = (kVm & 15) | (kVm >> 4) << 14 | 0x70;
+  static_assert(kVm < 64, "vmcnt has six bits");
+  bool late = false;
   auto body = [&](int kl, int a, int b, auto part) {
     const int b1 = b == 2 ? 0 : b + 1, b2 = b == 0 ? 2 : b - 1;
     __builtin_amdgcn_s_waitcnt(0xC07F);
@@ -972,7 +972,9 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
     __builtin_amdgcn_sched_barrier(0);
     load_tr(a, b, 3, 1);
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0074);       // vmcnt(4) lgkmcnt(0)
+    if (late) __builtin_amdgcn_s_waitcnt(kLate);
+    else __builtin_amdgcn_s_waitcnt(0x0074);  // vmcnt(4) lgkmcnt(0)
+    late = false;
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     load_frags(a ^ 1, b1, 0, 0);
@@ -984,7 +986,8 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
   // The tile through LDS, so that whole 128-byte lines leave, 16 bytes a lane. The B slot of the k-tile
   // just finished (the third: the next two hold or receive the next unit's) is free until this
   // wave's own DMA fills its 4 KB of it again, so each wave stages 32 rows x 64 columns there by
-  // itself, without a barrier.
+  // itself, without a barrier. Chunk c of row r lies at c ^ (r >> 1 & 7), its two halves swapped in
+  // rows 16 to 31: the 32 rows a half-wave writes then cover all 64 banks once.
   auto store_rows = [&](int b) {
     __bf16* out = static_cast<__bf16*>(p.C) + cur.origin;
     // Opaque here, so that the addresses below are computed now and not kept across the main loop
@@ -1001,7 +1004,8 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int col = 32 * j + 8 * g + 4 * (ln >> 5);
-          __bf16* dst = stage + rr * 64 + ((col >> 3) ^ (rr & 7)) * 8 + (col & 7);
+          __bf16* dst = stage + rr * 64 + ((col >> 3) ^ ((rr >> 1) & 7)) * 8 +
+                        ((col & 4) ^ ((rr >> 2) & 4));
 #pragma unroll
           for (int e = 0; e < 4; ++e) dst[e] = (__bf16)acc[i][j][4 * g + e];
         }
@@ -1009,7 +1013,8 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int r = (ln >> 3) + 8 * q;
-        v[q] = *reinterpret_cast<const u32x4*>(stage + r * 64 + (c ^ (r & 7)) * 8);
+        v[q] = *reinterpret_cast<const u32x4*>(stage + r * 64 + (c ^ ((r >> 1) & 7)) * 8);
+        if (q >= 2) v[q] = u32x4{v[q].z, v[q].w, v[q].x, v[q].y};
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -1060,12 +1065,12 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
         floatx4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = acc[f / FN][f % FN][4 * g + e];
-        stage[(ln & 31) * 8 + ((2 * g + (ln >> 5)) ^ (ln & 7))] = v;
+        stage[(ln & 31) * 8 + ((2 * g + (ln >> 5)) ^ ((ln >> 1) & 7))] = v;
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int r = r0 + 8 * q;
-        const floatx4 v = stage[r * 8 + (c ^ (r & 7))];
+        const floatx4 v = stage[r * 8 + (c ^ ((r >> 1) & 7))];
         if (m0 + 8 * q >= cur.m_valid) continue;
         TO t[4];
 #pragma unroll
@@ -1102,7 +1107,7 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
     load_tr(0, 0, 0, 0);
     int a = 0, b = 0;
     bool more = true;
-    for (int64_t i = 1; more; ++i) {
+    for (int i = 1; more; ++i) {
       more = unit(i, nxt);
       if (!more) {                // nothing follows: the DMA past the end reads no bytes
         nxt = cur;
@@ -1139,6 +1144,7 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
         store_fragments<TO, FM, FN, false>(p, acc, cur.origin, wm * 128, wn * 64, cur.m_valid,
                                            cur.n_valid);
       }
+      late = !ADD && cur.slot < 0 && cur.m_valid >= BM && cur.n_valid >= BN;
       clear();
       cur = nxt;
     }
@@ -1173,7 +1179,7 @@ __global__ __launch_bounds__(256) void k_grouped_join(GroupedArgs p) {
   int rank = -1;
   if constexpr (FORM == TN) {
     if (p.groups <= 64) rank = rows_rank(p);
-    walk.total = (int64_t)((p.N + 255) / 256) * p.tiles_n * p.groups;
+    walk.total = (p.N + 255) / 256 * p.tiles_n * p.groups;
   } else {
     walk = walk_start(p, 256, p.tiles_n, 0);
   }
