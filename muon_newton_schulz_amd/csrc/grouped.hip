@@ -1213,6 +1213,160 @@ __global__ __launch_bounds__(256) void k_grouped_join(GroupedArgs p) {
                                         n_valid);
 }
 
+// ---- a middling number of rows, bfloat16 ------------------------------------------------------
+//
+// Up to some hundred rows per expert the weights' bytes still bound a forward or input gradient,
+// and the rows fit one or two tiles of 128: a block takes 128 rows x BN columns, so most weights
+// are read once. What counts is bytes in flight: a ring of NS k-tiles in LDS (160 KB a CU), all but
+// one of them loading, one barrier per k-tile. Fragments of 32 rows without a row are skipped;
+// operand layouts as in k_grouped_big (a [k][BN] operand with BN = 64 has chunk c of k-row r at
+// c ^ 4 (r >> 1 & 1)).
+template <int FORM, int BN>
+__global__ __launch_bounds__(256) void k_grouped_ring(GroupedArgs p) {
+  constexpr int BM = 128, BK = 64, FM = 2, FN = BN / 64, AI = 4, BI = BN / 32;
+  constexpr bool BKM = FORM == NN;
+  constexpr int NS = BN == 128 ? 5 : 6;
+  constexpr int STAGE = (BM + BN) * kChunks;
+  constexpr int KCH = BN / 8, KROW = BN * 2;            // chunks and bytes of a [k][BN] row
+  __shared__ u32x4 lds[NS * STAGE];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+
+  Place at;
+  if (!find_place(p, BM, p.tiles_n, p.fill_rest, walk_start(p, BM, p.tiles_n, p.fill_rest),
+                  (int)blockIdx.x, at))
+    return;
+  const int m0 = at.lo + at.inside / p.tiles_n * BM, n0 = at.inside % p.tiles_n * BN;
+  const int m_valid = at.hi - m0, n_valid = p.N - n0;
+  const int KL = at.expert < 0 ? 0 : p.K / BK;
+
+  floatx16 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+
+  if (KL > 0) {
+    const __amdgpu_buffer_rsrc_t rA =
+        make_rsrc(static_cast<const char*>(p.A) + m0 * p.lda * 2,
+                  ((int64_t)((m_valid < BM ? m_valid : BM) - 1) * p.lda + p.K) * 2);
+    const __amdgpu_buffer_rsrc_t rB = make_rsrc(
+        static_cast<const char*>(p.B) + (at.expert * p.sB + (BKM ? (int64_t)n0 : n0 * p.ldb)) * 2,
+        (BKM ? (int64_t)p.K * p.ldb - n0 : (int64_t)n_valid * p.ldb) * 2);
+    const __amdgpu_buffer_rsrc_t none = make_rsrc(p.A, 0);     // reads zeros from nowhere
+    int offA[AI], offB[BI];
+#pragma unroll
+    for (int i = 0; i < AI; ++i) {
+      const int row = (wave * AI + i) * 8 + (lane >> 3);
+      offA[i] = (row * (int)p.lda + 8 * ((lane & 7) ^ ((row ^ ((row >> 3) & 3)) & 7))) * 2;
+    }
+#pragma unroll
+    for (int i = 0; i < BI; ++i) {
+      if constexpr (BKM) {
+        const int kr = (64 / KCH) * (wave * BI + i) + lane / KCH;
+        const int x = BN == 128 ? 4 * (kr & 3) : 4 * ((kr >> 1) & 1);
+        offB[i] = (kr * (int)p.ldb + 8 * ((lane % KCH) ^ x)) * 2;
+      } else {
+        const int row = (wave * BI + i) * 8 + (lane >> 3);
+        offB[i] = (row * (int)p.ldb + 8 * ((lane & 7) ^ ((row ^ ((row >> 3) & 3)) & 7))) * 2;
+      }
+    }
+    auto issue = [&](int kt, int st) {
+      const bool real = kt < KL;
+      const __amdgpu_buffer_rsrc_t a = real ? rA : none, b = real ? rB : none;
+      const int ka = real ? kt * BK * 2 : 0, kb = !real ? 0 : BKM ? kt * BK * (int)p.ldb * 2 : ka;
+#pragma unroll
+      for (int i = 0; i < BI; ++i)
+        dma16(b, &lds[st * STAGE + BM * kChunks + (wave * BI + i) * 64], offB[i], kb);
+#pragma unroll
+      for (int i = 0; i < AI; ++i)
+        dma16(a, &lds[st * STAGE + (wave * AI + i) * 64], offA[i], ka);
+    };
+    const int below = m_valid - 64 * wm;
+    const int frags = below <= 0 ? 0 : below > 32 ? 2 : 1;
+    uint32_t b_addr[FN] = {};
+    if constexpr (BKM) {
+      const int G = lane >> 4, sq = (lane & 15) >> 2, a4 = lane & 3, kb = 8 * (G >> 1) + sq;
+      const int x = BN == 128 ? 4 * (kb & 3) : 4 * ((kb >> 1) & 1);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int c = wn * (BN / 2) + 32 * j + 16 * (G & 1) + 4 * a4;
+        b_addr[j] = lds_address(lds) + BM * 128 + kb * KROW + ((c >> 3) ^ x) * 16 + (c & 7) * 2;
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) issue(s, s);
+    int st = 0, fill = NS - 1;
+    for (int kt = 0; kt < KL; ++kt) {
+      // k-tile kt has landed (NS - 2 newer ones may be on their way), for every wave behind the
+      // barrier, where the stage of k-tile kt - 1 is free too
+      constexpr int kVm = (NS - 2) * (AI + BI);
+      static_assert(kVm < 64, "vmcnt has six bits");
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt((kVm & 15) | (kVm >> 4) << 14 | 0x70);
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      issue(kt + NS - 1, fill);
+      const u32x4* A = lds + st * STAGE;
+      const u32x4* B = A + BM * kChunks;
+      u32x4 a[4][FM], b[4][FN];
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const int ch = 2 * ks + (lane >> 5);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) a[ks][i] = A[swz(wm * 64 + 32 * i + (lane & 31), ch)];
+        if constexpr (!BKM) {
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            b[ks][j] = B[swz(wn * (BN / 2) + 32 * j + (lane & 31), ch)];
+        }
+      }
+      if constexpr (BKM) {
+        // one k-tile's transposing reads of a fragment column, waited for in the same block (the
+        // compiler would wait for every outstanding DMA)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          const uint32_t at0 = b_addr[j] + (uint32_t)(st * STAGE * 16);
+          u32x2 t[8];
+          asm volatile(
+              "ds_read_b64_tr_b16 %0, %8\n\t"
+              "ds_read_b64_tr_b16 %1, %8 offset:%c9\n\t"
+              "ds_read_b64_tr_b16 %2, %8 offset:%c10\n\t"
+              "ds_read_b64_tr_b16 %3, %8 offset:%c11\n\t"
+              "ds_read_b64_tr_b16 %4, %8 offset:%c12\n\t"
+              "ds_read_b64_tr_b16 %5, %8 offset:%c13\n\t"
+              "ds_read_b64_tr_b16 %6, %8 offset:%c14\n\t"
+              "ds_read_b64_tr_b16 %7, %8 offset:%c15\n\t"
+              "s_waitcnt lgkmcnt(0)"
+              : "=&v"(t[0]), "=&v"(t[1]), "=&v"(t[2]), "=&v"(t[3]), "=&v"(t[4]), "=&v"(t[5]),
+                "=&v"(t[6]), "=&v"(t[7])
+              : "v"(at0), "i"(4 * KROW), "i"(16 * KROW), "i"(20 * KROW), "i"(32 * KROW),
+                "i"(36 * KROW), "i"(48 * KROW), "i"(52 * KROW));
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            b[ks][j] = u32x4{t[2 * ks].x, t[2 * ks].y, t[2 * ks + 1].x, t[2 * ks + 1].y};
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        if (i < frags) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) Frag<__bf16>::mma(acc[i][j], b[ks][j], a[ks][i]);
+        }
+      st = st + 1 == NS ? 0 : st + 1;
+      fill = fill + 1 == NS ? 0 : fill + 1;
+    }
+    block_sync();                 // no DMA is in flight when the block ends
+  }
+  store_fragments<__bf16, FM, FN, false>(p, acc, m0 * p.ldc + n0, wm * 64, wn * (BN / 2), m_valid,
+                                         n_valid);
+}
+
 template <typename T, typename TO, int FORM>
 hipError_t launch_grouped(const GroupedArgs& a, int64_t blocks, hipStream_t s) {
   hipLaunchKernelGGL((k_grouped<T, TO, FORM>), dim3((unsigned)blocks), dim3(256), 0, s, a);
@@ -1233,7 +1387,7 @@ int cu_count() {
 }
 
 // Tile and kernel of a call, from its sizes alone.
-enum class Kernel { Tile128, Rows, Big };
+enum class Kernel { Tile128, Rows, Ring, Big };
 struct Plan {
   Kernel kernel;
   int bm, bn;           // output tile
@@ -1242,34 +1396,74 @@ struct Plan {
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// What k_grouped_big's DMA assumes: bfloat16, 16-byte aligned operands and row pitches, a whole
-// number of k-tiles (the weight gradient's reduction may end anywhere), and for W read along the
-// output one expert's matrix below 2 GiB.
-bool big_ok(const GroupedDesc& d) {
+// What the DMA kernels assume: bfloat16, 16-byte aligned operands and row pitches, a whole number of
+// k-tiles (the weight gradient's reduction may end anywhere), and for W read along the output one
+// expert's matrix below 2 GiB.
+bool dma_ok(const GroupedDesc& d) {
   if (d.store != Store::BF16 || !on16(d.A) || !on16(d.B) || d.lda % 8) return false;
-  if (d.weight_grad) return d.ldb % 8 == 0 && d.total_rows >= 128 * d.groups;
+  if (d.weight_grad) return d.ldb % 8 == 0;
   const int64_t red = d.transpose_w ? d.n : d.k;
-  if (red % 64 || red < 128 || d.k % 8 || (d.n * d.k) % 8 || d.n * d.k >= (int64_t(1) << 30)) return false;
-  return d.total_rows >= 128 * d.groups;
+  return red % 64 == 0 && red >= 128 && d.k % 8 == 0 && (d.n * d.k) % 8 == 0 &&
+         d.n * d.k < (int64_t(1) << 30);
 }
 
+// The kernel of a call, by sizes, types and alignment. Times in us of random rows per expert
+// ("4096x2048 x 8": 8 experts of n = 4096, k = 2048; weights not in a cache):
+//
+//   Weight gradient without an addend: k_grouped_big whenever its DMA applies (against k_grouped, 24
+//   rows each: 121 / 212 on 8192x1024 x 32, 41 / 52 on 4096x2048 x 8, 20 / 20 on 1024x4096 x 4).
+//   With one the addend and the output are what is moved, and many small tiles keep more of it in
+//   flight: k_grouped up to 128 rows each (24 rows: 401 / 473 of k_grouped_big, 107 / 126,
+//   34 / 38; 128 rows: 461 / 490, 127 / 127, 39 / 37; 512 rows: 919 / 615, 225 / 164, 62 / 47).
+//   Forward, input gradient: k_grouped_big from 448 tiles of 256 x 256 on, whatever the rows: its
+//   blocks run from tile to tile without a break, so the weights stream at the HBM rate (8192x1024
+//   x 32, forward: 12 rows 103 against 118 of k_grouped_ring and 133 of k_grouped_rows, 100 rows
+//   125 / 160 / 248; input gradient, 128 tiles, so not by this rule: 12 rows 122 / 97).
+//   Fewer tiles leave CUs without work for too long; then, forward with at most 24 rows each,
+//   k_grouped_rows (4096x2048 x 8, 12 rows: 35 against 38 of k_grouped_ring and 48 of
+//   k_grouped_big; 1024x4096 x 4: 16 / 30 / 26; 40 rows: 41 / 40 / 51 and 20 / 35 / 27), else
+//   k_grouped_ring up to 256 rows each (4096x2048 x 8, 100 rows: 41 / 52 of k_grouped_big; input
+//   gradient 12 rows 43 / 52, 100 rows 57 / 55) if it has a block for every other CU or the
+//   reduction is too short for k_grouped_big to split, k_grouped_big beyond (300 rows: 54 / 92 of
+//   k_grouped_ring, input gradient 74 / 113).
+//   What the DMA cannot take: k_grouped_rows up to 96 rows each (forward), else k_grouped.
 Plan plan_of(const GroupedDesc& d) {
   Plan p{Kernel::Tile128, 128, 128, 0, 0, 0};
-  if (big_ok(d)) {
-    p.kernel = Kernel::Big;
-    p.bm = p.bn = 256;
+  const bool dma = dma_ok(d);
+  const int64_t cus = cu_count();
+  const int64_t used = d.groups < d.total_rows ? d.groups : d.total_rows;   // experts with rows
+  if (d.weight_grad) {
+    if (dma && (!d.D || d.total_rows > 128 * d.groups)) {
+      p.kernel = Kernel::Big;
+      p.bm = p.bn = 256;
+    }
     return p;
   }
-  if (d.weight_grad || d.transpose_w) return p;
-  // Forward with at most 96 rows per expert on average: the weights' bytes bound it.
-  const int64_t used = d.groups < d.total_rows ? d.groups : d.total_rows;   // experts with rows
-  if (d.total_rows <= 96 * d.groups) {
+  const int64_t out = d.transpose_w ? d.k : d.n, red = d.transpose_w ? d.n : d.k;
+  if (dma) {
+    const int64_t big_tiles = (used + d.total_rows / 256) * tiles_up(out, 256);
+    const int64_t bn = tiles_up(out, 128) * used >= cus / 2 ? 128 : 64;
+    const int64_t ring_tiles = (used + d.total_rows / 128) * tiles_up(out, bn);
+    const bool few = !d.transpose_w && d.total_rows <= 24 * used;
+    if (4 * big_tiles >= 7 * cus || d.total_rows > 256 * d.groups ||
+        (!few && 2 * ring_tiles < cus && red >= 1024)) {
+      p.kernel = Kernel::Big;
+      p.bm = p.bn = 256;
+      return p;
+    }
+    if (!few) {
+      p.kernel = Kernel::Ring;
+      p.bn = (int)bn;
+      return p;
+    }
+  }
+  if (!d.transpose_w && d.total_rows <= 96 * d.groups) {
     p.kernel = Kernel::Rows;
     const int64_t avg = tiles_up(d.total_rows, used > 0 ? used : 1);
     p.mt = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
     // Eight waves per CU: 256 weight rows per block, else 64, else 16 with the reduction split.
     const int64_t row_tiles = used + d.total_rows / (16 * p.mt) / 2;
-    const int64_t want = 2 * cu_count();                     // blocks of four waves
+    const int64_t want = 2 * cus;                            // blocks of four waves
     if (row_tiles * tiles_up(d.n, 256) >= want) p.ntw = 4, p.wk = 1;
     else if (row_tiles * tiles_up(d.n, 64) >= want) p.ntw = 4, p.wk = 4;
     else p.ntw = 1, p.wk = 4;
@@ -1338,10 +1532,16 @@ size_t grouped_workspace(const GroupedDesc& d) {
 
 const char* grouped_name(const GroupedDesc& d) {
   const bool f = d.store == Store::F32;
-  if (d.weight_grad) return f ? "grouped_wgrad_f32" : "grouped_wgrad_bf16";
-  if (d.transpose_w) return f ? "grouped_nn_f32" : "grouped_nn_bf16";
-  if (plan_of(d).kernel == Kernel::Rows) return f ? "grouped_rows_f32" : "grouped_rows_bf16";
-  return f ? "grouped_nt_f32" : "grouped_nt_bf16";
+  switch (plan_of(d).kernel) {
+    case Kernel::Rows: return f ? "grouped_rows_f32" : "grouped_rows_bf16";
+    case Kernel::Ring: return d.transpose_w ? "grouped_ring_nn" : "grouped_ring_nt";
+    case Kernel::Big:
+      return d.weight_grad ? "grouped_256_tn" : d.transpose_w ? "grouped_256_nn" : "grouped_256_nt";
+    default:
+      if (d.weight_grad) return f ? "grouped_128_tn_f32" : "grouped_128_tn_bf16";
+      if (d.transpose_w) return f ? "grouped_128_nn_f32" : "grouped_128_nn_bf16";
+      return f ? "grouped_128_nt_f32" : "grouped_128_nt_bf16";
+  }
 }
 
 hipError_t grouped(const GroupedDesc& d, hipStream_t s) {
@@ -1379,6 +1579,14 @@ hipError_t grouped(const GroupedDesc& d, hipStream_t s) {
   if (pl.kernel == Kernel::Rows)
     return d.store == Store::F32 ? launch_rows<float>(a, pl, blocks, s)
                                  : launch_rows<__bf16>(a, pl, blocks, s);
+  if (pl.kernel == Kernel::Ring) {
+    const dim3 grid((unsigned)blocks), block(256);
+    if (d.transpose_w && pl.bn == 128) hipLaunchKernelGGL((k_grouped_ring<NN, 128>), grid, block, 0, s, a);
+    else if (d.transpose_w) hipLaunchKernelGGL((k_grouped_ring<NN, 64>), grid, block, 0, s, a);
+    else if (pl.bn == 128) hipLaunchKernelGGL((k_grouped_ring<NT, 128>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_grouped_ring<NT, 64>), grid, block, 0, s, a);
+    return hipGetLastError();
+  }
   if (pl.kernel == Kernel::Big)
     return d.transpose_w ? launch_big<__bf16, NN>(a, s) : launch_big<__bf16, NT>(a, s);
   if (d.store == Store::F32)

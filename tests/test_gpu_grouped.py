@@ -302,3 +302,19 @@ def test_rows_beyond_32_bits_of_bytes():
     G = mns.grouped_weight_grad(dY, X, off)
     # adding the products of the all-zero rows is exact, so the bound is the picked rows'
     ref.check(G, *ref.weight_grad(dY[pick.cuda()], Xp, small, None, 0.0, BF), "long reduction")
+
+
+@pytest.mark.parametrize("sizes", [[40, 0, 100, 61], [129, 3, 90], [33] * 9, [128, 127]])
+@pytest.mark.parametrize("n,k", [(192, 512), (520, 128), (64, 1024)])
+def test_some_dozens_of_rows(sizes, n, k):
+    """Row counts around one tile of 128, reductions of a few k-tiles up to more than the ring holds."""
+    bounds = ref.bounds_of(sizes, 2)
+    rows, e = bounds[-1] + 3, len(sizes)
+    off = _offsets(bounds)
+    print("case", sizes, n, k, flush=True)
+    W, X = _rand((e, n, k), BF, 1, 0.3), _rand((rows, k), BF, 2)
+    Y = mns.grouped_matmul(X, W, off)
+    ref.check(Y, *ref.matmul(X, W, bounds, False, torch.zeros_like(Y)), "forward")
+    W, dY = _rand((e, k, n), BF, 3, 0.3), _rand((rows, k), BF, 4)
+    dX = mns.grouped_matmul(dY, W, off, transpose_w=True)
+    ref.check(dX, *ref.matmul(dY, W, bounds, True, torch.zeros_like(dX)), "input gradient")
