@@ -328,7 +328,9 @@ class _OnStream:
         if stream is None:
             if device.index != torch.cuda.current_device():
                 self._ctx = torch.cuda.device(device)
-            self.handle = torch.cuda.current_stream(device).cuda_stream
+            # the current stream's handle, without building a stream object around it (3.5 us of a
+            # small call's 12)
+            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
             return
         if not hasattr(stream, "cuda_stream"):
             handle = int(stream)

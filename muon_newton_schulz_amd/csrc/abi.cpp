@@ -1151,6 +1151,19 @@ static mns_status nsb_check(int dtype, int64_t batch, int64_t rows, int64_t cols
   return (v > vt ? v : vt) * elem_bytes(g.elem) <= kMaxElems ? MNS_OK : MNS_ERR_SHAPE;
 }
 
+// Whether the products [P Q] [E; X] and P X read [E; X] as it is stored (gemm_kmajor_ok goes by the
+// output's tiles, the same for both).
+static bool nsb_kmajor(const Geo& g, int c, const NsbBuffers& b) {
+  GemmDesc d;
+  d.elem = g.elem;
+  d.C = b.V[1];
+  d.M = (int)g.n_p;
+  d.N = (int)g.m_p;
+  d.K = (int)g.n_p;
+  d.batch = c;
+  return gemm_kmajor_ok(d);
+}
+
 // One chunk of `c` matrices on buffers b: the direction E_T is left in the stored layout.
 static mns_status run_nsb(const Geo& g, int c, const NsbBuffers& b, int T, const float* abc,
                           const NsbScale* sc, hipStream_t s, void** out) {
@@ -1199,8 +1212,7 @@ static mns_status run_nsb(const Geo& g, int c, const NsbBuffers& b, int T, const
     d.M = n; d.N = m; d.K = direction ? 2 * n : n;
     return d;
   };
-  GemmDesc probe = update(true, 0, false, false);
-  const bool km = gemm_kmajor_ok(probe);
+  const bool km = nsb_kmajor(g, c, b);
   int cur = 0;
   for (int t = 0; t < T; ++t) {
     const bool last = t == T - 1;
@@ -1293,7 +1305,8 @@ mns_status ns_orthogonalize_backward(const void* X, const void* dO, void* dX, in
     MNS_HIP(timed("nsb_scales", 0, 16.0 * c * nblk, s, [&] {
       return nsb_scales(b.px, b.pg, nblk, c, g.S, sc[0].e, b.scale, s); }));
     const NsbDst v{b.V[0], g.ld_x, b.v_stride, g.n_p * g.ld_x};
-    const NsbDst vt{b.Vt[0], b.ld_t, b.vt_stride, g.n_p};
+    // [E^T X^T] only where the products read it
+    const NsbDst vt{nsb_kmajor(g, c, b) ? nullptr : b.Vt[0], b.ld_t, b.vt_stride, g.n_p};
     MNS_HIP(timed("nsb_load", 0, all * 2.0 * (ss + 2.0 * es), s, [&] {
       return nsb_load(x, go, sto, c, rows, cols, b.scale, g.elem, g.rows_p, g.cols_p,
                       g.tall ? vt : v, g.tall ? v : vt, s); }));
