@@ -1045,8 +1045,20 @@ struct NsbBuffers {
   double* dot = nullptr;
   float* gemm_scratch = nullptr;
   size_t gemm_scratch_bytes = 0;
+  void* C2 = nullptr;    // few launches (nsb_fused): 2 n_p square, pitch ld_t; PQ too is then
   int64_t ld_t = 0, v_stride = 0, vt_stride = 0, q_stride = 0, pq_stride = 0;
 };
+
+// Small problems, bound by their launches: the n x n side of an iteration as one kernel, A and K in one
+// symmetric product [E; X] [E; X]^T and the update in one product of [P Q; 0 P]. Three launches an
+// iteration instead of eight, for a third to a half more arithmetic. In us, eight launches against
+// three: float32 256x1024 402 / 235, 4 x 64x2048 589 / 517, 16 x 256x1024 861 / 953, 512x2048
+// 639 / 535, 4 x 512x512 721 / 780; float16 333x1111 303 / 207, 512x8192 465 / 351, 4 x 512x2048
+// 456 / 466, 16 x 512x512 522 / 933, 1024x1024 460 / 526.
+static bool nsb_fused(const Geo& g, int count) {
+  const double work = (double)count * g.n_p * g.n_p * (g.m_p + g.n_p);
+  return g.n_p <= 512 && work <= (g.elem == Elem::F16 ? 2.4e9 : 8e8);
+}
 
 static size_t carve_nsb(void* base, const Geo& g, int count, NsbBuffers& b) {
   Carver cv(base);
@@ -1065,13 +1077,18 @@ static size_t carve_nsb(void* base, const Geo& g, int count, NsbBuffers& b) {
     b.V[i] = cv.take<char>(es * count * b.v_stride);
     b.Vt[i] = cv.take<char>(es * count * b.vt_stride);
   }
-  b.A = cv.take<char>(es * count * b.q_stride);
-  b.K = cv.take<char>(es * count * b.q_stride);
-  b.Ssym = cv.take<char>(es * count * b.q_stride);
+  if (nsb_fused(g, count)) {
+    b.pq_stride *= 2;
+    b.C2 = cv.take<char>(es * count * b.pq_stride);
+  } else {
+    b.A = cv.take<char>(es * count * b.q_stride);
+    b.K = cv.take<char>(es * count * b.q_stride);
+    b.Ssym = cv.take<char>(es * count * b.q_stride);
+  }
   b.PQ = cv.take<char>(es * count * b.pq_stride);
   // split-k parts: (output tiles) x (k-tiles / 8), capped as in carve_ns
   const size_t deep = (size_t)(g.m_p > 2 * g.n_p ? g.m_p : 2 * g.n_p) / 256;
-  size_t scratch = (size_t)count * g.n_p * g.m_p * deep * sizeof(float);
+  size_t scratch = (size_t)count * 4 * g.n_p * g.m_p * deep * sizeof(float);
   if (scratch > kGemmScratchBytes) scratch = kGemmScratchBytes;
   b.gemm_scratch = cv.take<float>(scratch / sizeof(float));
   b.gemm_scratch_bytes = scratch;
@@ -1162,6 +1179,60 @@ static bool nsb_kmajor(const Geo& g, int c, const NsbBuffers& b) {
   d.K = (int)g.n_p;
   d.batch = c;
   return gemm_kmajor_ok(d);
+}
+
+// The fused form of run_nsb for small problems (nsb_fused): [E; X] [E; X]^T, the n x n side, the
+// update.
+static mns_status run_nsb_fused(const Geo& g, int c, const NsbBuffers& b, int T, const float* abc,
+                                const NsbScale* sc, hipStream_t s, void** out) {
+  const int n = (int)g.n_p, m = (int)g.m_p;
+  const double nn = (double)c * g.n * g.n;
+  GemmDesc base;
+  base.elem = g.elem;
+  base.batch = c;
+  base.partial = b.gemm_scratch;
+  base.partial_bytes = b.gemm_scratch_bytes;
+  // (more rows never turn a product away from its k-major operand)
+  const bool km = nsb_kmajor(g, c, b);
+  int cur = 0;
+  for (int t = 0; t < T; ++t) {
+    const bool last = t == T - 1;
+    // C2 = [E; X] [E; X]^T / S^2: A as it is, K times e / S
+    GemmDesc gram = base;
+    gram.A = gram.B = b.V[cur];
+    gram.lda = gram.ldb = g.ld_x;
+    gram.sA = gram.sB = b.v_stride;
+    gram.C = b.C2; gram.ldc = b.ld_t; gram.sC = b.pq_stride;
+    gram.M = gram.N = 2 * n;
+    gram.K = m;
+    gram.sym = true;
+    gram.alpha = 1.0f / (g.S * g.S);
+    MNS_HIP(timed_gemm(gram, 3.0 * nn * g.m, s));
+    // E' times sc[t + 1].e; Q X comes with e / S (of K) times S (of X): e, as P E does
+    const float r = (float)(sc[t + 1].e / sc[t].e);
+    MNS_HIP(timed("nsb_square", 3.0 * nn * g.n, 0.0, s, [&] {
+      return nsb_square(b.C2, b.PQ, b.ld_t, b.pq_stride, g.elem, c, (int)g.n, n, abc[3 * t],
+                        abc[3 * t + 1], abc[3 * t + 2], r, r, s); }));
+    GemmDesc up = base;
+    up.A = b.PQ; up.lda = b.ld_t; up.sA = b.pq_stride;
+    if (km) {
+      up.B = b.V[cur]; up.ldb = g.ld_x; up.sB = b.v_stride;
+      up.b_kmajor = true;
+    } else {
+      up.B = b.Vt[cur]; up.ldb = b.ld_t; up.sB = b.vt_stride;
+    }
+    if (!last || !g.tall) {
+      up.C = b.V[cur ^ 1]; up.ldc = g.ld_x; up.sC = b.v_stride;
+    }
+    if (last ? g.tall : !km) {
+      up.Ct = b.Vt[cur ^ 1]; up.ldct = b.ld_t; up.sCt = b.vt_stride;
+    }
+    up.M = last ? n : 2 * n; up.N = m; up.K = 2 * n;
+    MNS_HIP(timed_gemm(up, (last ? 4.0 : 6.0) * nn * g.m, s));
+    cur ^= 1;
+  }
+  *out = g.tall ? b.Vt[cur] : b.V[cur];
+  return MNS_OK;
 }
 
 // One chunk of `c` matrices on buffers b: the direction E_T is left in the stored layout.
@@ -1311,7 +1382,8 @@ mns_status ns_orthogonalize_backward(const void* X, const void* dO, void* dX, in
       return nsb_load(x, go, sto, c, rows, cols, b.scale, g.elem, g.rows_p, g.cols_p,
                       g.tall ? vt : v, g.tall ? v : vt, s); }));
     void* E = nullptr;
-    st = run_nsb(g, c, b, T, abc, sc, s, &E);
+    st = nsb_fused(g, c) ? run_nsb_fused(g, c, b, T, abc, sc, s, &E)
+                         : run_nsb(g, c, b, T, abc, sc, s, &E);
     if (st != MNS_OK) return st;
     MNS_HIP(timed("nsb_finish", 0, all * (3.0 * ss + 2.0 * es), s, [&] {
       return nsb_finish(x, sto, E, g.elem, c, rows, cols, g.tall ? b.ld_t : g.ld_x,

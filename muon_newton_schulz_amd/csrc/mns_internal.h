@@ -215,6 +215,11 @@ hipError_t nsb_load(const void* X, const void* G, Store st, int count, int64_t r
 hipError_t symmetrise(const void* K, int64_t ldk, int64_t sK, const void* D, int64_t ldd,
                       int64_t sD, void* C, int64_t ldc, int64_t sC, Elem e, int count, int64_t n_p,
                       float beta, float gamma, hipStream_t s);
+// The n x n side of an iteration at once: from C2 = [E; X] [E; X]^T (2 n_p square, pitch ld, matrix
+// stride `stride`) to PQ = [r P, q Q; 0, P], P = a I + b A + c A^2 (I on the first n), Q = b S + c (A S
+// + S A), A and S = K + K^T the blocks of C2.
+hipError_t nsb_square(const void* C2, void* PQ, int64_t ld, int64_t stride, Elem e, int count, int n,
+                      int n_p, float a, float b, float c, float r, float q, hipStream_t s);
 // out = (E' - X_0 <X_0, E'>) / ||X|| with E' = E ||dO|| inv_eT, E in the stored layout (row pitch
 // ld, matrix stride sE). part: count * nsb_dot_blocks(rows) doubles.
 int nsb_dot_blocks(int64_t rows);

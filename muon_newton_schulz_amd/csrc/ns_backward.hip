@@ -237,6 +237,98 @@ __global__ __launch_bounds__(kThreads) void k_symmetrise(const T* K, int64_t ldk
   }
 }
 
+// The n x n side of an iteration in one launch, for matrices whose launches count more than their
+// arithmetic. C2 = alpha [E; X] [E; X]^T (2 n_p square) holds A = X X^T in its last quarter, K = E X^T
+// in its second and K^T in its third. A block makes one 32 x 32 tile of P and of Q,
+//   P_ij = a I + b A_ij + c A_i A_j^T,   Q_ij = b S_ij + c (A_i S_j^T + S_i A_j^T),
+// from the row blocks A_i, A_j, S_i = K_i + K^T_i, S_j (A and S are symmetric), its four waves each
+// a quarter of the products' depth, and writes them as the operand of the update,
+//   [E'; X'] = [ r P  r Q ; 0  P ] [E; X].
+// Twice the arithmetic of the separate symmetric products, but no intermediate leaves the chip.
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+__device__ __forceinline__ void mma32(floatx16& acc, u32x4 a, u32x4 b, _Float16) {
+  typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+  acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a),
+                                               __builtin_bit_cast(half8, b), acc, 0, 0, 0);
+}
+__device__ __forceinline__ void mma32(floatx16& acc, u32x4 a, u32x4 b, float) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[p]), __uint_as_float(b[p]), acc, 0,
+                                               0, 0);
+}
+
+struct SquareArgs {
+  const void* C2;
+  void* PQ;
+  int64_t ld, stride;        // of both (elements)
+  int n, n_p;
+  float a, b, c, r, q;       // q: scale of Q against r P's
+};
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_nsb_square(SquareArgs g) {
+  constexpr int VEC = 16 / (int)sizeof(T), STEP = 2 * VEC;      // k per step: two chunks
+  typedef T vec __attribute__((ext_vector_type(VEC)));
+  __shared__ float part[4][2][16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int tiles = g.n_p / 32;
+  const int i0 = (int)(blockIdx.x / tiles) * 32, j0 = (int)(blockIdx.x % tiles) * 32;
+  const T* C2 = static_cast<const T*>(g.C2) + blockIdx.y * g.stride;
+  T* PQ = static_cast<T*>(g.PQ) + blockIdx.y * g.stride;
+  const int row = lane & 31, kc = (lane >> 5) * VEC;
+  const T* K = C2 + g.n_p;                         // [E X^T]
+  const T* KT = C2 + g.n_p * g.ld;                 // [X E^T]
+  const T* A = KT + g.n_p;
+  const int64_t oi = (i0 + row) * g.ld + kc, oj = (j0 + row) * g.ld + kc;
+  floatx16 pa, qa;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) pa[e] = qa[e] = 0.f;
+  const int quarter = g.n_p / 4;
+#pragma unroll 4
+  for (int k = wave * quarter; k < (wave + 1) * quarter; k += STEP) {
+    auto at = [&](const T* base, int64_t o) { return *reinterpret_cast<const vec*>(base + o + k); };
+    const u32x4 ai = __builtin_bit_cast(u32x4, at(A, oi)), aj = __builtin_bit_cast(u32x4, at(A, oj));
+    const u32x4 si = __builtin_bit_cast(u32x4, at(K, oi) + at(KT, oi));
+    const u32x4 sj = __builtin_bit_cast(u32x4, at(K, oj) + at(KT, oj));
+    mma32(pa, aj, ai, T{});              // a lane's registers: 4 neighbouring columns of row i
+    mma32(qa, sj, ai, T{});
+    mma32(qa, aj, si, T{});
+  }
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    part[wave][0][e][lane] = pa[e];
+    part[wave][1][e][lane] = qa[e];
+  }
+  __syncthreads();
+  // wave w finishes register groups w: columns 8 w + 4 (lane >> 5) .. + 3 of row lane & 31
+  typedef T t4 __attribute__((ext_vector_type(4)));
+  const int i = i0 + row, j = j0 + 8 * wave + 4 * (lane >> 5);
+  const t4 av = *reinterpret_cast<const t4*>(A + i * g.ld + j);
+  const t4 kv = *reinterpret_cast<const t4*>(K + i * g.ld + j);
+  const t4 kt = *reinterpret_cast<const t4*>(KT + i * g.ld + j);
+  t4 p1, p2, q, z;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int x = 4 * wave + e;
+    const float ps = part[0][0][x][lane] + part[1][0][x][lane] + part[2][0][x][lane] + part[3][0][x][lane];
+    const float qs = part[0][1][x][lane] + part[1][1][x][lane] + part[2][1][x][lane] + part[3][1][x][lane];
+    float p = g.b * (float)av[e] + g.c * ps;
+    if (i == j + e && i < g.n) p += g.a;
+    p1[e] = (T)(g.r * p);
+    p2[e] = (T)p;
+    q[e] = (T)(g.q * (g.b * (float)(kv[e] + kt[e]) + g.c * qs));
+    z[e] = (T)0.f;
+  }
+  T* top = PQ + i * g.ld + j;
+  T* low = top + g.n_p * g.ld;
+  *reinterpret_cast<t4*>(top) = p1;
+  *reinterpret_cast<t4*>(top + g.n_p) = q;
+  *reinterpret_cast<t4*>(low) = z;
+  *reinterpret_cast<t4*>(low + g.n_p) = p2;
+}
+
 // Partial sums of <X, E> (E in the stored layout, padded rows), float64: block x of nblk takes
 // rows x, x + nblk, ...
 template <typename TX, typename TE>
@@ -363,6 +455,15 @@ hipError_t symmetrise(const void* K, int64_t ldk, int64_t sK, const void* D, int
     hipLaunchKernelGGL(k_symmetrise<float>, grid, dim3(kThreads), 0, s,
                        static_cast<const float*>(K), ldk, sK, static_cast<const float*>(D), ldd,
                        sD, static_cast<float*>(C), ldc, sC, beta, gamma);
+  return last();
+}
+
+hipError_t nsb_square(const void* C2, void* PQ, int64_t ld, int64_t stride, Elem e, int count, int n,
+                      int n_p, float a, float b, float c, float r, float q, hipStream_t s) {
+  const SquareArgs g{C2, PQ, ld, stride, n, n_p, a, b, c, r, q};
+  const dim3 grid((n_p / 32) * (n_p / 32), count);
+  if (e == Elem::F16) hipLaunchKernelGGL(k_nsb_square<_Float16>, grid, dim3(256), 0, s, g);
+  else hipLaunchKernelGGL(k_nsb_square<float>, grid, dim3(256), 0, s, g);
   return last();
 }
 
