@@ -427,6 +427,113 @@ __global__ __launch_bounds__(256) void k_grouped(GroupedArgs p) {
   }
 }
 
+// The same for forwards and input gradients whose grid would leave CUs without work: 64 x 64 tiles, whose four waves split the
+// reduction (wave w takes k-tiles w, w + 4, ...), each with its own LDS and no barrier in the loop; the
+// four sums are added in wave order through LDS. A fourth of the steps of memory latency one after
+// the other, and four times the blocks.
+template <typename T, int FORM>
+__global__ __launch_bounds__(256) void k_grouped_split(GroupedArgs p) {
+  using F = Frag<T>;
+  constexpr int BM = 64, BN = 64, VEC = F::VEC, BK = F::BK, PITCH = BK + VEC;
+  constexpr int NCH = 8;                                 // chunks per lane and operand
+  constexpr int WAVE = (BM + BN) * PITCH;                // elements of one wave's LDS
+  __shared__ __align__(16) T lds[4 * WAVE];
+  static_assert(sizeof(lds) >= 4 * 4 * 16 * 64 * sizeof(float), "the waves' sums fit");
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  Place at;
+  if (!find_place(p, BM, p.tiles_n, p.fill_rest, walk_start(p, BM, p.tiles_n, p.fill_rest),
+                  (int)blockIdx.x, at))
+    return;
+  const int m0 = at.lo + at.inside / p.tiles_n * BM, n0 = at.inside % p.tiles_n * BN;
+  const int m_valid = at.hi - m0, n_valid = p.N - n0;
+  const int red = at.expert < 0 ? 0 : p.K;
+  const T* A = static_cast<const T*>(p.A) + m0 * p.lda;
+  const T* B = static_cast<const T*>(p.B) + (at.expert < 0 ? 0 : at.expert) * p.sB +
+               (FORM == NT ? n0 * p.ldb : (int64_t)n0);
+
+  auto load = [&](const T* base, int64_t ld, bool kmajor, int valid, int k0, u32x4* r) {
+#pragma unroll
+    for (int q = 0; q < NCH; ++q) {
+      if (!kmajor) {
+        const int c = lane + 64 * q, row = c >> 3, kk = (c & 7) * VEC;
+        r[q] = load_chunk(base + row * ld + k0 + kk, row < valid ? red - k0 - kk : 0);
+      } else {
+        constexpr int KW = BK / 16;
+        const int kr = (q % KW) * 16 + (lane & 15), col = ((q / KW) * 4 + (lane >> 4)) * VEC;
+        r[q] = load_chunk(base + (int64_t)(k0 + kr) * ld + col, k0 + kr < red ? valid - col : 0);
+      }
+    }
+  };
+  auto store = [&](T* dst, bool kmajor, const u32x4* r) {
+#pragma unroll
+    for (int q = 0; q < NCH; ++q) {
+      if (!kmajor) {
+        const int c = lane + 64 * q, row = c >> 3, kk = (c & 7) * VEC;
+        *reinterpret_cast<u32x4*>(dst + row * PITCH + kk) = r[q];
+      } else {
+        constexpr int KW = BK / 16;
+        const int kr = (q % KW) * 16 + (lane & 15), col = ((q / KW) * 4 + (lane >> 4)) * VEC;
+        T e[VEC];
+        __builtin_memcpy(e, &r[q], 16);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) dst[(col + i) * PITCH + kr] = e[i];
+      }
+    }
+  };
+  floatx16 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+  T* As = lds + wave * WAVE;
+  T* Bs = As + BM * PITCH;
+  u32x4 ra[NCH], rb[NCH];
+  int k0 = wave * BK;
+  if (k0 < red) {
+    load(A, p.lda, false, m_valid, k0, ra);
+    load(B, p.ldb, FORM != NT, n_valid, k0, rb);
+  }
+  for (; k0 < red; k0 += 4 * BK) {
+    store(As, false, ra);
+    store(Bs, FORM != NT, rb);
+    if (k0 + 4 * BK < red) {
+      load(A, p.lda, false, m_valid, k0 + 4 * BK, ra);
+      load(B, p.ldb, FORM != NT, n_valid, k0 + 4 * BK, rb);
+    }
+#pragma unroll
+    for (int s = 0; s < BK / (2 * VEC); ++s) {
+      u32x4 a[2], b[2];
+      const int kk = (2 * s + (lane >> 5)) * VEC;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        a[i] = *reinterpret_cast<const u32x4*>(As + (32 * i + (lane & 31)) * PITCH + kk);
+        b[i] = *reinterpret_cast<const u32x4*>(Bs + (32 * i + (lane & 31)) * PITCH + kk);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) F::mma(acc[i][j], b[j], a[i]);
+    }
+  }
+  // wave w finishes fragment (w / 2, w % 2)
+  const int mi = 32 * (wave >> 1), nj = 32 * (wave & 1);
+  __syncthreads();
+  float(*part)[4][16][64] = reinterpret_cast<float(*)[4][16][64]>(lds);     // [wave][fragment]
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) part[wave][f][e][lane] = acc[f >> 1][f & 1][e];
+  __syncthreads();
+  floatx16 sum[1][1];
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    sum[0][0][e] = part[0][wave][e][lane] + part[1][wave][e][lane] + part[2][wave][e][lane] +
+                   part[3][wave][e][lane];
+  store_fragments<T, 1, 1, false>(p, sum, m0 * p.ldc + n0, mi, nj, m_valid, n_valid);
+}
+
 // Few rows per expert (forward): the product is bound by reading the weights once, so the weights
 // go straight from memory into MFMA operands, 64 bytes of 16 rows per load, with nothing staged
 // and no barrier in the loop; the tokens of the row tile (16 MT rows) are read the same way and
@@ -1373,6 +1480,14 @@ hipError_t launch_grouped(const GroupedArgs& a, int64_t blocks, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename T>
+hipError_t launch_split(const GroupedArgs& a, bool transpose_w, int64_t blocks, hipStream_t s) {
+  const dim3 grid((unsigned)blocks), block(256);
+  if (transpose_w) hipLaunchKernelGGL((k_grouped_split<T, NN>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_grouped_split<T, NT>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
 int64_t tiles_up(int64_t x, int64_t t) { return (x + t - 1) / t; }
 
 int cu_count() {
@@ -1387,7 +1502,7 @@ int cu_count() {
 }
 
 // Tile and kernel of a call, from its sizes alone.
-enum class Kernel { Tile128, Rows, Ring, Big };
+enum class Kernel { Tile128, Split64, Rows, Ring, Big };
 struct Plan {
   Kernel kernel;
   int bm, bn;           // output tile
@@ -1426,7 +1541,10 @@ bool dma_ok(const GroupedDesc& d) {
 //   gradient 12 rows 43 / 52, 100 rows 57 / 55) if it has a block for every other CU or the
 //   reduction is too short for k_grouped_big to split, k_grouped_big beyond (300 rows: 54 / 92 of
 //   k_grouped_ring, input gradient 74 / 113).
-//   What the DMA cannot take: k_grouped_rows up to 96 rows each (forward), else k_grouped.
+//   What the DMA cannot take: k_grouped_rows up to 96 rows each (forward); k_grouped_split up to 160
+//   tiles of 128 x 128 (float32, 1021 rows over 5 experts of 513x1277: forward 36 against 103,
+//   input gradient 37 / 47; bfloat16 45 / 62 and 26 / 26; 200 tiles: 142 / 124, 51 / 38), else
+//   k_grouped.
 Plan plan_of(const GroupedDesc& d) {
   Plan p{Kernel::Tile128, 128, 128, 0, 0, 0};
   const bool dma = dma_ok(d);
@@ -1469,6 +1587,9 @@ Plan plan_of(const GroupedDesc& d) {
     else p.ntw = 1, p.wk = 4;
     p.bm = 16 * p.mt;
     p.bn = 16 * p.ntw * (4 / p.wk);
+  } else if ((used + d.total_rows / 128) * tiles_up(out, 128) <= 5 * cus / 8) {
+    p.kernel = Kernel::Split64;
+    p.bm = p.bn = 64;
   }
   return p;
 }
@@ -1537,6 +1658,9 @@ const char* grouped_name(const GroupedDesc& d) {
     case Kernel::Ring: return d.transpose_w ? "grouped_ring_nn" : "grouped_ring_nt";
     case Kernel::Big:
       return d.weight_grad ? "grouped_256_tn" : d.transpose_w ? "grouped_256_nn" : "grouped_256_nt";
+    case Kernel::Split64:
+      if (d.transpose_w) return f ? "grouped_64_nn_f32" : "grouped_64_nn_bf16";
+      return f ? "grouped_64_nt_f32" : "grouped_64_nt_bf16";
     default:
       if (d.weight_grad) return f ? "grouped_128_tn_f32" : "grouped_128_tn_bf16";
       if (d.transpose_w) return f ? "grouped_128_nn_f32" : "grouped_128_nn_bf16";
@@ -1579,6 +1703,9 @@ hipError_t grouped(const GroupedDesc& d, hipStream_t s) {
   if (pl.kernel == Kernel::Rows)
     return d.store == Store::F32 ? launch_rows<float>(a, pl, blocks, s)
                                  : launch_rows<__bf16>(a, pl, blocks, s);
+  if (pl.kernel == Kernel::Split64)
+    return d.store == Store::F32 ? launch_split<float>(a, d.transpose_w, blocks, s)
+                                 : launch_split<__bf16>(a, d.transpose_w, blocks, s);
   if (pl.kernel == Kernel::Ring) {
     const dim3 grid((unsigned)blocks), block(256);
     if (d.transpose_w && pl.bn == 128) hipLaunchKernelGGL((k_grouped_ring<NN, 128>), grid, block, 0, s, a);
