@@ -1097,6 +1097,45 @@ static size_t carve_nsb(void* base, const Geo& g, int count, NsbBuffers& b) {
 
 static double pow2_floor(double x) { return std::ldexp(1.0, std::ilogb(x)); }
 
+// Short sides up to 64 (kNsbSmall). Blocks per matrix: a block reads 32 KB of partial sums for each
+// (about 0.3 us) and takes about 5 us for 64 columns, so sqrt(m / 4) of them balance the two; no more
+// than two per CU over the whole chunk.
+static NsbSmall nsb_small_plan(const Geo& g, int count) {
+  NsbSmall d;
+  d.n = g.n;
+  d.m = g.m;
+  d.ld = (g.m + 63) / 64 * 64;
+  d.count = count;
+  d.tall = g.tall;
+  const int64_t tiles = d.ld / 64;
+  int64_t blocks = std::llround(std::sqrt((double)g.m / 4.0));
+  if (blocks * count > 512) blocks = 512 / count;
+  if (blocks > tiles) blocks = tiles;
+  if (blocks < 1) blocks = 1;
+  const int64_t per = (tiles + blocks - 1) / blocks;
+  d.cols_per = (int)(per * 64);
+  d.blocks = (int)((tiles + per - 1) / per);
+  return d;
+}
+
+static size_t carve_nsb_small(void* base, const Geo& g, int count, NsbBuffers& b, NsbSmall& d) {
+  Carver cv(base);
+  const int nblk = norm_blocks(g.rows * g.cols);
+  d = nsb_small_plan(g, count);
+  b.px = cv.take<double>((size_t)count * nblk);
+  b.pg = cv.take<double>((size_t)count * nblk);
+  b.scale = cv.take<double>((size_t)count * 4);
+  b.dot = cv.take<double>((size_t)count * nsb_dot_blocks(g.rows));
+  d.V = cv.take<float>((size_t)count * 2 * 64 * d.ld);
+  for (float*& p : d.part) p = cv.take<float>((size_t)count * d.blocks * 2 * 64 * 64);
+  if (g.tall) d.Et = cv.take<float>((size_t)count * g.m * 64);
+  return cv.off + 256;
+}
+
+static size_t nsb_bytes(void* base, const Geo& g, int count, NsbBuffers& b, NsbSmall& d) {
+  return g.n <= kNsbSmall ? carve_nsb_small(base, g, count, b, d) : carve_nsb(base, g, count, b);
+}
+
 // Powers of two that scale the stored quantities of one iteration: E by e, S and A S by kap, P by
 // p, Q by q = p e / S (so that P E and Q X add up), with the bounds below 2^14.
 struct NsbScale {
@@ -1335,8 +1374,9 @@ mns_status mns_ns_backward_workspace_size(int dtype, int64_t batch, int64_t rows
   const mns_status st = nsb_check(dtype, batch, rows, cols);
   if (st != MNS_OK) return st;
   NsbBuffers b;
-  *bytes = carve_nsb(nullptr, nsb_geo(rows, cols, store_of(dtype)),
-                     batch < kChunk ? (int)batch : kChunk, b);
+  NsbSmall small;
+  *bytes = nsb_bytes(nullptr, nsb_geo(rows, cols, store_of(dtype)),
+                     batch < kChunk ? (int)batch : kChunk, b, small);
   return MNS_OK;
 }
 
@@ -1356,14 +1396,15 @@ mns_status ns_orthogonalize_backward(const void* X, const void* dO, void* dX, in
   if (!nsb_plan(T, abc, g, sc)) return MNS_ERR_PARAM;
   const int cmax = batch < kChunk ? (int)batch : kChunk;
   NsbBuffers b;
-  st = check_ws(workspace, workspace_bytes, carve_nsb(nullptr, g, cmax, b));
+  NsbSmall small;
+  st = check_ws(workspace, workspace_bytes, nsb_bytes(nullptr, g, cmax, b, small));
   if (st != MNS_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const size_t esz = store_bytes(dtype);
   const int nblk = norm_blocks(rows * cols);
   for (int64_t b0 = 0; b0 < batch; b0 += cmax) {
     const int c = (int)((batch - b0) < cmax ? batch - b0 : cmax);
-    carve_nsb(workspace, g, c, b);
+    nsb_bytes(workspace, g, c, b, small);
     const size_t off = (size_t)b0 * rows * cols * esz;
     const char* x = static_cast<const char*>(X) + off;
     const char* go = static_cast<const char*>(dO) + off;
@@ -1375,6 +1416,20 @@ mns_status ns_orthogonalize_backward(const void* X, const void* dO, void* dX, in
       return sumsq(go, sto, c, rows * cols, b.pg, s); }));
     MNS_HIP(timed("nsb_scales", 0, 16.0 * c * nblk, s, [&] {
       return nsb_scales(b.px, b.pg, nblk, c, g.S, sc[0].e, b.scale, s); }));
+    if (g.n <= kNsbSmall) {
+      MNS_HIP(timed("nsb_small_load", 0, all * 2.0 * (ss + es), s, [&] {
+        return nsb_small_load(small, x, go, sto, b.scale, s); }));
+      const double nn = (double)c * g.n * g.n;
+      for (int t = 0; t < T; ++t)
+        MNS_HIP(timed("nsb_small_step", nn * (9.0 * g.m + 3.0 * g.n), 0, s, [&] {
+          return nsb_small_step(small, t, t == T - 1, abc[3 * t], abc[3 * t + 1], abc[3 * t + 2],
+                                s); }));
+      MNS_HIP(timed("nsb_finish", 0, all * (3.0 * ss + 2.0 * es), s, [&] {
+        return nsb_finish(x, sto, g.tall ? small.Et : small.V, Elem::F32, c, rows, cols,
+                          g.tall ? 64 : small.ld, g.tall ? g.m * 64 : 128 * small.ld, b.dot,
+                          b.scale, 1.0, dx, s); }));
+      continue;
+    }
     const NsbDst v{b.V[0], g.ld_x, b.v_stride, g.n_p * g.ld_x};
     // [E^T X^T] only where the products read it
     const NsbDst vt{nsb_kmajor(g, c, b) ? nullptr : b.Vt[0], b.ld_t, b.vt_stride, g.n_p};

@@ -220,6 +220,22 @@ hipError_t symmetrise(const void* K, int64_t ldk, int64_t sK, const void* D, int
 // + S A), A and S = K + K^T the blocks of C2.
 hipError_t nsb_square(const void* C2, void* PQ, int64_t ld, int64_t stride, Elem e, int count, int n,
                       int n_p, float a, float b, float c, float r, float q, hipStream_t s);
+// Matrices whose short side is at most 64 (kNsbSmall): one launch per iteration. V: [E; X], 128 x ld
+// floats per matrix, ld = m rounded up to 64; part: two buffers of blocks * 2 * 64 * 64 floats per
+// matrix; Et (tall): m x 64 floats per matrix, E_T as the tall matrix is stored.
+constexpr int kNsbSmall = 64;
+struct NsbSmall {
+  float* V = nullptr;
+  float* part[2] = {};
+  float* Et = nullptr;
+  int64_t n = 0, m = 0, ld = 0;
+  int blocks = 0, cols_per = 0, count = 0;      // cols_per: a multiple of 64
+  bool tall = false;
+};
+hipError_t nsb_small_load(const NsbSmall& d, const void* X, const void* G, Store st,
+                          const double* scale, hipStream_t s);
+hipError_t nsb_small_step(const NsbSmall& d, int t, bool last_step, float a, float b, float c,
+                          hipStream_t s);
 // out = (E' - X_0 <X_0, E'>) / ||X|| with E' = E ||dO|| inv_eT, E in the stored layout (row pitch
 // ld, matrix stride sE). part: count * nsb_dot_blocks(rows) doubles.
 int nsb_dot_blocks(int64_t rows);

@@ -329,6 +329,204 @@ __global__ __launch_bounds__(256) void k_nsb_square(SquareArgs g) {
   *reinterpret_cast<t4*>(low + g.n_p) = p2;
 }
 
+// ---- short sides up to 64 -------------------------------------------------------------------
+//
+// The n x n side of such a matrix fits one block, so an iteration is one launch: every block of a
+// matrix adds the partial Gram matrices A and K that all its blocks left, forms P and Q from them
+// by itself, updates its own columns of E and X (64 at a time, in place) and leaves the next
+// partial sums from the new values while it has them. float32 throughout; matrices padded to 64
+// rows, not 256. The four waves own the quadrants of every 64 x 64 product.
+constexpr int kN = 64, kNP = kN + 1;          // LDS row pitch: 32 rows of one column on 32 banks
+
+// acc (quadrant qi, qj) += sum over k < 64 of L[i ls + k lk] R[j rs + k rk]
+__device__ __forceinline__ void quad64(floatx16& acc, const float* L, int ls, int lk, const float* R,
+                                       int rs, int rk, int qi, int qj) {
+  const int lane = threadIdx.x & 63, k1 = lane >> 5;
+  const float* l = L + (32 * qi + (lane & 31)) * ls + k1 * lk;
+  const float* r = R + (32 * qj + (lane & 31)) * rs + k1 * rk;
+#pragma unroll 8
+  for (int k = 0; k < kN; k += 2)
+    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(l[k * lk], r[k * rk], acc, 0, 0, 0);
+}
+// element e of a lane: row, column within the 64 x 64 result
+__device__ __forceinline__ int quad_row(int e, int qi) {
+  return 32 * qi + 8 * (e / 4) + 4 * ((threadIdx.x & 63) >> 5) + e % 4;
+}
+__device__ __forceinline__ int quad_col(int qj) { return 32 * qj + (threadIdx.x & 31); }
+__device__ __forceinline__ floatx16 zero16() {
+  floatx16 z;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) z[e] = 0.f;
+  return z;
+}
+
+struct SmallArgs {
+  float* V;                // [E; X] per matrix: 128 rows, pitch ld
+  float* part[2];          // [matrix][block][A, K][64 x 64], read and written in turn
+  float* Et;               // last step of a tall matrix: E^T, m x 64
+  int64_t ld, v_stride, et_stride;
+  int n, cols_per, blocks;   // columns and blocks per matrix
+  int64_t m;
+};
+
+__device__ __forceinline__ float* part_of(const SmallArgs& g, int parity, int b, int blk) {
+  return g.part[parity] + ((int64_t)b * g.blocks + blk) * (2 * kN * kN);
+}
+
+__device__ __forceinline__ void leave_parts(const SmallArgs& g, int parity, const floatx16& aa,
+                                            const floatx16& kk, int qi, int qj) {
+  float* out = part_of(g, parity, blockIdx.y, blockIdx.x);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int o = quad_row(e, qi) * kN + quad_col(qj);
+    out[o] = aa[e];
+    out[kN * kN + o] = kk[e];
+  }
+}
+
+// E_0, X_0 from dO and X (rows x cols as stored; tall: the transposed tile), and their partial sums.
+template <typename TX>
+__global__ __launch_bounds__(256) void k_nsb_small_load(const TX* X, const TX* G, bool tall,
+                                                        const double* scale, SmallArgs g) {
+  __shared__ float tile[2][kN * kNP];
+  const int b = blockIdx.y, wave = threadIdx.x >> 6, qi = wave >> 1, qj = wave & 1;
+  const int64_t c_begin = (int64_t)blockIdx.x * g.cols_per;
+  const int64_t c_end = c_begin + g.cols_per < g.ld ? c_begin + g.cols_per : g.ld;
+  floatx16 aa = zero16(), kk = zero16();
+  for (int64_t c0 = c_begin; c0 < c_end; c0 += kN) {
+    for (int which = 0; which < 2; ++which) {
+      const TX* src = (which ? X : G) + (int64_t)b * g.n * g.m;
+      const double sc = scale[4 * b + (which ? 0 : 2)];
+      for (int q = threadIdx.x; q < kN * kN; q += 256) {
+        // lanes run along the stored rows
+        const int i = tall ? q % kN : q / kN, c = tall ? q / kN : q % kN;
+        float v = 0.f;
+        if (i < g.n && c0 + c < g.m) {
+          const int64_t o = tall ? (c0 + c) * g.n + i : i * g.m + c0 + c;
+          v = (float)((double)widen(src[o]) * sc);
+        }
+        tile[which][i * kNP + c] = v;
+      }
+    }
+    __syncthreads();
+    float* V = g.V + b * g.v_stride + c0;
+    for (int q = threadIdx.x; q < 2 * kN * kN; q += 256) {
+      const int r = q / kN, c = q % kN;
+      V[r * g.ld + c] = tile[r / kN][(r % kN) * kNP + c];
+    }
+    quad64(aa, tile[1], kNP, 1, tile[1], kNP, 1, qi, qj);
+    quad64(kk, tile[0], kNP, 1, tile[1], kNP, 1, qi, qj);
+    __syncthreads();
+  }
+  leave_parts(g, 0, aa, kk, qi, qj);
+}
+
+__global__ __launch_bounds__(256) void k_nsb_small_step(SmallArgs g, float a, float bb, float c,
+                                                        int parity, bool last) {
+  __shared__ float P[kN * kNP], Q[kN * kNP], E[kN * kNP], X[kN * kNP];
+  const int b = blockIdx.y, tid = threadIdx.x, wave = tid >> 6, qi = wave >> 1, qj = wave & 1;
+  {
+    // A and K: the blocks' partial sums, in block order
+    float4 s[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s[q] = float4{0.f, 0.f, 0.f, 0.f};
+    const float4* src = reinterpret_cast<const float4*>(part_of(g, parity, b, 0)) + tid;
+#pragma unroll 2
+    for (int blk = 0; blk < g.blocks; ++blk, src += 2 * kN * kN / 4) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float4 v = src[256 * q];
+        s[q].x += v.x;
+        s[q].y += v.y;
+        s[q].z += v.z;
+        s[q].w += v.w;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int o = (tid + 256 * (q & 3)) * 4;
+      float* dst = (q < 4 ? P : Q) + (o / kN) * kNP + o % kN;
+      dst[0] = s[q].x;
+      dst[1] = s[q].y;
+      dst[2] = s[q].z;
+      dst[3] = s[q].w;
+    }
+  }
+  __syncthreads();
+  // S = K + K^T, in Q
+  float sv[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int i = quad_row(e, qi), j = quad_col(qj);
+    sv[e] = Q[i * kNP + j] + Q[j * kNP + i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 16; ++e) Q[quad_row(e, qi) * kNP + quad_col(qj)] = sv[e];
+  __syncthreads();
+  floatx16 a2 = zero16(), as = zero16();
+  quad64(a2, P, kNP, 1, P, kNP, 1, qi, qj);
+  quad64(as, P, kNP, 1, Q, kNP, 1, qi, qj);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) E[quad_row(e, qi) * kNP + quad_col(qj)] = as[e];
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int i = quad_row(e, qi), j = quad_col(qj);
+    a2[e] = c * a2[e] + bb * P[i * kNP + j] + (i == j && i < g.n ? a : 0.f);
+    as[e] = bb * sv[e] + c * (as[e] + E[j * kNP + i]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int o = quad_row(e, qi) * kNP + quad_col(qj);
+    P[o] = a2[e];
+    Q[o] = as[e];
+  }
+  floatx16 aa = zero16(), kk = zero16();
+  const int64_t c_begin = (int64_t)blockIdx.x * g.cols_per;
+  const int64_t c_end = c_begin + g.cols_per < g.ld ? c_begin + g.cols_per : g.ld;
+  for (int64_t c0 = c_begin; c0 < c_end; c0 += kN) {
+    float* V = g.V + b * g.v_stride + c0;
+    for (int q = tid; q < 2 * kN * kN / 4; q += 256) {
+      const int r = q / (kN / 4), x = q % (kN / 4) * 4;
+      const float4 v = *reinterpret_cast<const float4*>(V + r * g.ld + x);
+      float* dst = (r < kN ? E : X) + (r % kN) * kNP + x;
+      dst[0] = v.x;
+      dst[1] = v.y;
+      dst[2] = v.z;
+      dst[3] = v.w;
+    }
+    __syncthreads();
+    floatx16 en = zero16(), xn = zero16();
+    quad64(en, P, kNP, 1, E, 1, kNP, qi, qj);
+    quad64(en, Q, kNP, 1, X, 1, kNP, qi, qj);
+    if (!last) quad64(xn, P, kNP, 1, X, 1, kNP, qi, qj);
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int i = quad_row(e, qi), j = quad_col(qj);
+      E[i * kNP + j] = en[e];
+      X[i * kNP + j] = xn[e];
+      if (!last || !g.Et) V[i * g.ld + j] = en[e];
+      if (!last) V[(kN + i) * g.ld + j] = xn[e];
+    }
+    __syncthreads();
+    if (!last) {
+      quad64(aa, X, kNP, 1, X, kNP, 1, qi, qj);
+      quad64(kk, E, kNP, 1, X, kNP, 1, qi, qj);
+    } else if (g.Et) {
+      float* Et = g.Et + b * g.et_stride + c0 * kN;
+      for (int q = tid; q < kN * kN; q += 256) {
+        const int col = q / kN, i = q % kN;
+        if (c0 + col < g.m) Et[q] = E[i * kNP + col];
+      }
+    }
+    __syncthreads();
+  }
+  if (!last) leave_parts(g, parity ^ 1, aa, kk, qi, qj);
+}
+
 // Partial sums of <X, E> (E in the stored layout, padded rows), float64: block x of nblk takes
 // rows x, x + nblk, ...
 template <typename TX, typename TE>
@@ -464,6 +662,42 @@ hipError_t nsb_square(const void* C2, void* PQ, int64_t ld, int64_t stride, Elem
   const dim3 grid((n_p / 32) * (n_p / 32), count);
   if (e == Elem::F16) hipLaunchKernelGGL(k_nsb_square<_Float16>, grid, dim3(256), 0, s, g);
   else hipLaunchKernelGGL(k_nsb_square<float>, grid, dim3(256), 0, s, g);
+  return last();
+}
+
+static SmallArgs small_args(const NsbSmall& d) {
+  SmallArgs g;
+  g.V = d.V;
+  g.part[0] = d.part[0];
+  g.part[1] = d.part[1];
+  g.Et = d.tall ? d.Et : nullptr;
+  g.ld = d.ld;
+  g.v_stride = 2 * kN * d.ld;
+  g.et_stride = d.m * kN;
+  g.n = (int)d.n;
+  g.cols_per = d.cols_per;
+  g.blocks = d.blocks;
+  g.m = d.m;
+  return g;
+}
+
+hipError_t nsb_small_load(const NsbSmall& d, const void* X, const void* G, Store st,
+                          const double* scale, hipStream_t s) {
+  const dim3 grid(d.blocks, d.count);
+  if (st == Store::F32)
+    hipLaunchKernelGGL(k_nsb_small_load<float>, grid, dim3(256), 0, s, static_cast<const float*>(X),
+                       static_cast<const float*>(G), d.tall, scale, small_args(d));
+  else
+    hipLaunchKernelGGL(k_nsb_small_load<uint16_t>, grid, dim3(256), 0, s,
+                       static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(G), d.tall,
+                       scale, small_args(d));
+  return last();
+}
+
+hipError_t nsb_small_step(const NsbSmall& d, int t, bool last_step, float a, float b, float c,
+                          hipStream_t s) {
+  hipLaunchKernelGGL(k_nsb_small_step, dim3(d.blocks, d.count), dim3(256), 0, s, small_args(d), a, b,
+                     c, t & 1, last_step);
   return last();
 }
 

@@ -36,6 +36,9 @@ CASES = [
     ("bf16", "normal", 2, 1, 1), ("bf16", "normal", 5, 17, 23), ("bf16", "lowrank", 2, 64, 64),
     ("bf16", "lowrank", 1, 256, 256), ("bf16", "lowrank", 2, 257, 300), ("bf16", "student_t", 3, 1111, 333),
     ("bf16", "normal", 1, 512, 2048), ("bf16", "lowrank", 1, 700, 700), ("bf16", "normal", 40, 24, 130),
+    ("f32", "normal", 3, 64, 64), ("f32", "student_t", 2, 64, 65), ("f32", "normal", 2, 3000, 33),
+    ("bf16", "normal", 1, 63, 5000), ("bf16", "student_t", 33, 40, 96), ("bf16", "normal", 2, 129, 64),
+    ("f32", "normal", 1, 65, 64), ("f32", "normal", 1, 65, 66),
     ("bf16", "student_t", 2, 1100, 2300), ("bf16", "normal", 1, 2300, 1100), ("f32", "normal", 35, 30, 20),
 ]
 
