@@ -891,12 +891,13 @@ mns_status normuon_scale(void* O, int dtype, int64_t batch, int64_t rows, int64_
 // ---- products grouped by expert ----------------------------------------------------------------
 
 constexpr int64_t kMaxGroups = 65536;
+constexpr int64_t kMaxRows = int64_t(1) << 30;      // row arithmetic in the kernels is 32-bit
 constexpr int64_t kMaxPitch = int64_t(1) << 21;
 
 static mns_status check_grouped(int dtype, int64_t groups, int64_t total_rows, int64_t n, int64_t k) {
   const mns_status st = check_dtype(dtype);
   if (st != MNS_OK) return st;
-  if (groups < 1 || groups > kMaxGroups || total_rows < 0 || total_rows > kMaxElems)
+  if (groups < 1 || groups > kMaxGroups || total_rows < 0 || total_rows > kMaxRows)
     return MNS_ERR_SHAPE;
   return check_shape(1, n, k);
 }

@@ -1564,7 +1564,7 @@ Plan plan_of(const GroupedDesc& d) {
     const int64_t ring_tiles = (used + d.total_rows / 128) * tiles_up(out, bn);
     const bool few = !d.transpose_w && d.total_rows <= 24 * used;
     if (4 * big_tiles >= 7 * cus || d.total_rows > 256 * d.groups ||
-        (!few && 2 * ring_tiles < cus && red >= 1024)) {
+        (!few && 2 * ring_tiles < cus && red >= 1536)) {
       p.kernel = Kernel::Big;
       p.bm = p.bn = 256;
       return p;
@@ -1637,14 +1637,14 @@ static hipError_t launch_big(const GroupedArgs& a, hipStream_t s) {
 }
 
 // Parts a tile of the last round may be cut into: at least 8 k-tiles each (on the average expert,
-// for the weight gradient), and only where a call has few rounds, so that filling the last one
-// pays for the second launch.
+// for the weight gradient), and only where a call has few rounds and three parts are possible, so
+// that filling the last one pays for the second launch (4 to 14 us).
 static int split_cap(const GroupedDesc& d) {
   const Plan p = plan_of(d);
   if (p.kernel != Kernel::Big || grouped_blocks(d) > 6 * 256) return 1;
   const int64_t red = d.weight_grad ? d.total_rows / d.groups : d.transpose_w ? d.n : d.k;
   const int64_t cap = red / 64 / 8;
-  return cap < 1 ? 1 : cap > 16 ? 16 : (int)cap;
+  return cap < 3 ? 1 : cap > 16 ? 16 : (int)cap;
 }
 
 size_t grouped_workspace(const GroupedDesc& d) {

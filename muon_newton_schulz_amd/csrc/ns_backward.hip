@@ -241,9 +241,11 @@ __global__ __launch_bounds__(kThreads) void k_symmetrise(const T* K, int64_t ldk
 // arithmetic. C2 = alpha [E; X] [E; X]^T (2 n_p square) holds A = X X^T in its last quarter, K = E X^T
 // in its second and K^T in its third. A block makes one 32 x 32 tile of P and of Q,
 //   P_ij = a I + b A_ij + c A_i A_j^T,   Q_ij = b S_ij + c (A_i S_j^T + S_i A_j^T),
-// from the row blocks A_i, A_j, S_i = K_i + K^T_i, S_j (A and S are symmetric), its four waves each
-// a quarter of the products' depth, and writes them as the operand of the update,
+// from the row blocks A_i, A_j, S_i = K_i + K^T_i, S_j (A and S are symmetric), and writes them as
+// the operand of the update,
 //   [E'; X'] = [ r P  r Q ; 0  P ] [E; X].
+// The row blocks go through LDS, whole 128-byte lines at a time, and each wave takes a fourth of
+// every line (fragments straight from memory touch 32 lines a load: 27 against 16 us on 3 x 512^2).
 // Twice the arithmetic of the separate symmetric products, but no intermediate leaves the chip.
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
@@ -269,32 +271,48 @@ struct SquareArgs {
 
 template <typename T>
 __global__ __launch_bounds__(256) void k_nsb_square(SquareArgs g) {
-  constexpr int VEC = 16 / (int)sizeof(T), STEP = 2 * VEC;      // k per step: two chunks
+  constexpr int VEC = 16 / (int)sizeof(T), BK = 8 * VEC, PITCH = 9;      // 16-byte chunks
   typedef T vec __attribute__((ext_vector_type(VEC)));
   __shared__ float part[4][2][16][64];
+  __shared__ u32x4 rows[4][32 * PITCH];              // A_i, A_j, S_i, S_j: 128 bytes of 32 rows
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int tiles = g.n_p / 32;
   const int i0 = (int)(blockIdx.x / tiles) * 32, j0 = (int)(blockIdx.x % tiles) * 32;
   const T* C2 = static_cast<const T*>(g.C2) + blockIdx.y * g.stride;
   T* PQ = static_cast<T*>(g.PQ) + blockIdx.y * g.stride;
-  const int row = lane & 31, kc = (lane >> 5) * VEC;
+  const int row = lane & 31;
   const T* K = C2 + g.n_p;                         // [E X^T]
   const T* KT = C2 + g.n_p * g.ld;                 // [X E^T]
   const T* A = KT + g.n_p;
-  const int64_t oi = (i0 + row) * g.ld + kc, oj = (j0 + row) * g.ld + kc;
   floatx16 pa, qa;
 #pragma unroll
   for (int e = 0; e < 16; ++e) pa[e] = qa[e] = 0.f;
-  const int quarter = g.n_p / 4;
-#pragma unroll 4
-  for (int k = wave * quarter; k < (wave + 1) * quarter; k += STEP) {
-    auto at = [&](const T* base, int64_t o) { return *reinterpret_cast<const vec*>(base + o + k); };
-    const u32x4 ai = __builtin_bit_cast(u32x4, at(A, oi)), aj = __builtin_bit_cast(u32x4, at(A, oj));
-    const u32x4 si = __builtin_bit_cast(u32x4, at(K, oi) + at(KT, oi));
-    const u32x4 sj = __builtin_bit_cast(u32x4, at(K, oj) + at(KT, oj));
-    mma32(pa, aj, ai, T{});              // a lane's registers: 4 neighbouring columns of row i
-    mma32(qa, sj, ai, T{});
-    mma32(qa, aj, si, T{});
+  const int lr = threadIdx.x >> 3, lc = threadIdx.x & 7;         // this thread's chunk of a block
+  const int64_t oi = (i0 + lr) * g.ld + lc * VEC, oj = (j0 + lr) * g.ld + lc * VEC;
+  auto at = [&](const T* base, int64_t o) { return *reinterpret_cast<const vec*>(base + o); };
+  vec ai = at(A, oi), aj = at(A, oj), ki = at(K, oi), kj = at(K, oj), ti = at(KT, oi), tj = at(KT, oj);
+  for (int k = 0; k < g.n_p; k += BK) {
+    const int o = lr * PITCH + lc;
+    rows[0][o] = __builtin_bit_cast(u32x4, ai);
+    rows[1][o] = __builtin_bit_cast(u32x4, aj);
+    rows[2][o] = __builtin_bit_cast(u32x4, ki + ti);
+    rows[3][o] = __builtin_bit_cast(u32x4, kj + tj);
+    __syncthreads();
+    if (k + BK < g.n_p) {
+      const int x = k + BK;
+      ai = at(A, oi + x);
+      aj = at(A, oj + x);
+      ki = at(K, oi + x);
+      kj = at(K, oj + x);
+      ti = at(KT, oi + x);
+      tj = at(KT, oj + x);
+    }
+    const int f = row * PITCH + 2 * wave + (lane >> 5);
+    const u32x4 fai = rows[0][f], faj = rows[1][f], fsi = rows[2][f], fsj = rows[3][f];
+    mma32(pa, faj, fai, T{});            // a lane's registers: 4 neighbouring columns of row i
+    mma32(qa, fsj, fai, T{});
+    mma32(qa, faj, fsi, T{});
+    __syncthreads();
   }
 #pragma unroll
   for (int e = 0; e < 16; ++e) {

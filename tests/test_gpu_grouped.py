@@ -318,3 +318,65 @@ def test_some_dozens_of_rows(sizes, n, k):
     W, dY = _rand((e, k, n), BF, 3, 0.3), _rand((rows, k), BF, 4)
     dX = mns.grouped_matmul(dY, W, off, transpose_w=True)
     ref.check(dX, *ref.matmul(dY, W, bounds, True, torch.zeros_like(dX)), "input gradient")
+
+
+@pytest.mark.parametrize("sizes", [[300, 0, 150, 260], [40, 0, 100, 61], [9, 0, 3, 16]])
+def test_row_pitches_on_aligned_sizes(sizes):
+    """Pitches of whole 16 bytes and widths of whole k-tiles, in groups of many, some dozens and few
+    rows: rows of no expert and the gaps between rows keep what they held."""
+    n, k, extra = 320, 192, 72
+    bounds = ref.bounds_of(sizes, 3)
+    rows = bounds[-1] + 5
+    X, _ = _strided(_rand((rows, k), BF, 1), k + extra)
+    dY, _ = _strided(_rand((rows, n), BF, 2), n + extra)
+    W, off = _rand((4, n, k), BF, 3, 0.3), _offsets(bounds)
+    for t, src, width in ((False, X, n), (True, dY, k)):
+        out, buf = _strided(torch.full((rows, width), 3.0, dtype=BF, device="cuda"), width + extra)
+        before = buf.clone()
+        want, err = ref.matmul(src, W, bounds, t, out)
+        mns.grouped_matmul(src, W, off, transpose_w=t, out=out)
+        ref.check(out, want, err, ("pitch", sizes, t))
+        touched = torch.zeros_like(buf, dtype=torch.bool)
+        touched.as_strided(out.shape, (width + extra, 1))[bounds[0]:bounds[-1]] = True
+        assert torch.equal(buf[~touched], before[~touched])
+    for out_dtype in (BF, F32):
+        G = mns.grouped_weight_grad(dY, X, off, out_dtype=out_dtype)
+        ref.check(G, *ref.weight_grad(dY, X, bounds, None, 0.0, out_dtype), ("pitch", sizes))
+
+
+def test_short_reductions_over_many_tiles():
+    """More tiles than blocks, two k-tiles each: a block goes from tile to tile at once."""
+    n, k, sizes = 4096, 128, [2600, 5, 1300, 1200]
+    bounds = ref.bounds_of(sizes)
+    off = _offsets(bounds)
+    W, X = _rand((4, n, k), BF, 1, 0.3), _rand((bounds[-1], k), BF, 2)
+    Y = mns.grouped_matmul(X, W, off)
+    ref.check(Y, *ref.matmul(X, W, bounds, False, torch.zeros_like(Y)), "forward")
+    W, dY = _rand((4, k, n), BF, 3, 0.3), _rand((bounds[-1], k), BF, 4)
+    dX = mns.grouped_matmul(dY, W, off, transpose_w=True)
+    ref.check(dX, *ref.matmul(dY, W, bounds, True, torch.zeros_like(dX)), "input gradient")
+
+
+@pytest.mark.parametrize("out_dtype", [BF, F32], ids=["bf16", "f32"])
+def test_weight_gradients_of_few_rows_over_many_tiles(out_dtype):
+    """Experts with no row, one row, one k-tile and a little more, over more tiles than blocks."""
+    n, k, sizes = 2048, 2000, [0, 1, 64, 65, 130, 3]
+    bounds = ref.bounds_of(sizes, 2)
+    off = _offsets(bounds)
+    rows = bounds[-1] + 2
+    dY, X = _rand((rows, n), BF, 1), _rand((rows, k), BF, 2)
+    C = _rand((6, n, k), out_dtype, 3)
+    for c, beta in ((None, 0.0), (C, 0.9)):
+        G = mns.grouped_weight_grad(dY, X, off, C=c, beta=beta, out_dtype=out_dtype)
+        ref.check(G, *ref.weight_grad(dY, X, bounds, c, beta, out_dtype), (out_dtype, beta))
+
+
+def test_no_rows_but_a_workspace():
+    """A batch without rows through the kernel that takes weight gradients of aligned sizes."""
+    off = _offsets([0, 0, 0])
+    empty = torch.empty(0, 256, dtype=BF, device="cuda")
+    G = mns.grouped_weight_grad(empty, empty, off)
+    assert G.shape == (2, 256, 256) and not G.any()
+    C = _rand((2, 256, 256), F32, 1)
+    G = mns.grouped_weight_grad(empty, empty, off, C=C, beta=2.0)
+    assert torch.equal(G, 2.0 * C)

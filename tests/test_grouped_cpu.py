@@ -91,6 +91,7 @@ def _call(lib, **kw):
     (dict(groups=65537), _abi.MNS_ERR_SHAPE),
     (dict(rows=-1), _abi.MNS_ERR_SHAPE),
     (dict(rows=1 << 31), _abi.MNS_ERR_SHAPE),
+    (dict(rows=(1 << 30) + 1), _abi.MNS_ERR_SHAPE),
     (dict(n=0), _abi.MNS_ERR_SHAPE),
     (dict(k=65537, ldx=65537), _abi.MNS_ERR_SHAPE),
     (dict(ldx=23), _abi.MNS_ERR_SHAPE),
