@@ -222,7 +222,7 @@ mns_status normuon_scale(void* O, int dtype, int64_t batch, int64_t rows, int64_
  *   and pitches of whole 16 bytes run faster.
  *   Sizes: 1 <= groups <= 65536; 0 <= total_rows <= 2^30 (the token pointers may be NULL when it is
  *   0); 1 <= n, k <= 65536, n*k <= 2^31 - 1; pitches <= 2^21; at most 2^31 - 1 output tiles
- *   of 16 x 64; else MNS_ERR_SHAPE.
+ *   of 16 x 16; else MNS_ERR_SHAPE.
  *   workspace (may be NULL when the size query returns 0, which goes by the sizes alone and covers
  *   every alignment and addend) must be 256-byte aligned.
  *   Rounding: the order of a sum's float32 additions depends on the sizes and the number of CUs
