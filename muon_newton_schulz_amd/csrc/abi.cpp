@@ -1051,14 +1051,14 @@ struct NsbBuffers {
 };
 
 // Small problems, bound by their launches: the n x n side of an iteration as one kernel, A and K in one
-// symmetric product [E; X] [E; X]^T and the update in one product of [P Q; 0 P]. Three launches an
-// iteration instead of eight, for a third to a half more arithmetic. In us, eight launches against
-// three: float32 256x1024 402 / 235, 4 x 64x2048 589 / 517, 16 x 256x1024 861 / 953, 512x2048
-// 639 / 535, 4 x 512x512 721 / 780; float16 333x1111 303 / 207, 512x8192 465 / 351, 4 x 512x2048
-// 456 / 466, 16 x 512x512 522 / 933, 1024x1024 460 / 526.
+// symmetric product [E; X] [E; X]^T and the update in one launch. Three launches an iteration instead of
+// eight, for a third to a half more arithmetic; in float16 also a third less error (k_nsb_square). In
+// us, eight launches against three: float32 256x1024 402 / 235, 4 x 64x2048 589 / 517, 16 x 256x1024
+// 861 / 953, 512x2048 639 / 535, 4 x 512x512 721 / 780; float16 333x1111 303 / 182, 512x8192 465 / 390,
+// 2 x 512x4096 443 / 396, 4 x 512x2048 447 / 440, 3 x 512x4096 445 / 524, 16 x 512x512 509 / 663.
 static bool nsb_fused(const Geo& g, int count) {
   const double work = (double)count * g.n_p * g.n_p * (g.m_p + g.n_p);
-  return g.n_p <= 512 && work <= (g.elem == Elem::F16 ? 2.4e9 : 8e8);
+  return g.n_p <= 512 && work <= (g.elem == Elem::F16 ? 2.8e9 : 8e8);
 }
 
 static size_t carve_nsb(void* base, const Geo& g, int count, NsbBuffers& b) {
@@ -1079,7 +1079,7 @@ static size_t carve_nsb(void* base, const Geo& g, int count, NsbBuffers& b) {
     b.Vt[i] = cv.take<char>(es * count * b.vt_stride);
   }
   if (nsb_fused(g, count)) {
-    b.pq_stride *= 2;
+    b.pq_stride *= g.elem == Elem::F16 ? 3 : 2;
     b.C2 = cv.take<char>(es * count * b.pq_stride);
   } else {
     b.A = cv.take<char>(es * count * b.q_stride);
@@ -1139,8 +1139,9 @@ static size_t nsb_bytes(void* base, const Geo& g, int count, NsbBuffers& b, NsbS
 
 // Powers of two that scale the stored quantities of one iteration: E by e, S and A S by kap, P by
 // p, Q by q = p e / S (so that P E and Q X add up), with the bounds below 2^14.
+// gram (run_nsb_fused): of A, and of K on top of e / S, so that float16 holds A's small entries.
 struct NsbScale {
-  double e, kap, p, q;
+  double e, kap, p, q, gram;
 };
 
 // The scales of the T iterations and of the final direction, sc[T].e. A direction of norm 1 grows
@@ -1159,7 +1160,7 @@ static bool nsb_plan(int T, const float* abc, const Geo& g, NsbScale* sc) {
   double slope0 = 1.0;       // f_t'(0)
   for (int t = 0; t <= T; ++t) {
     const double lim = 16384.0;
-    sc[t] = NsbScale{1.0, 1.0, 1.0, 1.0};
+    sc[t] = NsbScale{1.0, 1.0, 1.0, 1.0, 1.0};
     if (!std::isfinite(L) || !std::isfinite(sup) || L > (f16 ? kNsbGrowthF16 : kNsbGrowthF32))
       return false;
     if (f16) sc[t].e = pow2_floor(lim / L);
@@ -1176,6 +1177,8 @@ static bool nsb_plan(int T, const float* abc, const Geo& g, NsbScale* sc) {
       if (p * sc[t].e / g.S * qmax > lim) p = pow2_floor(lim * g.S / (sc[t].e * qmax));
       sc[t].p = p;
       sc[t].q = p * sc[t].e / g.S;
+      // K <= e L sup gram / S <= 2^14, A <= sup S
+      sc[t].gram = pow2_floor(g.S / (sup > 1.0 ? sup : 1.0));
     }
     slope0 *= a;
     L = std::fabs(slope0) > 1.0 ? std::fabs(slope0) : 1.0;
@@ -1233,11 +1236,11 @@ static mns_status run_nsb_fused(const Geo& g, int c, const NsbBuffers& b, int T,
   base.partial = b.gemm_scratch;
   base.partial_bytes = b.gemm_scratch_bytes;
   // (more rows never turn a product away from its k-major operand)
-  const bool km = nsb_kmajor(g, c, b);
+  const bool km = nsb_kmajor(g, c, b), f16 = g.elem == Elem::F16;
   int cur = 0;
   for (int t = 0; t < T; ++t) {
     const bool last = t == T - 1;
-    // C2 = [E; X] [E; X]^T / S^2: A as it is, K times e / S
+    // C2 = [E; X] [E; X]^T gram / S^2: A times gram, K times gram e / S
     GemmDesc gram = base;
     gram.A = gram.B = b.V[cur];
     gram.lda = gram.ldb = g.ld_x;
@@ -1246,13 +1249,24 @@ static mns_status run_nsb_fused(const Geo& g, int c, const NsbBuffers& b, int T,
     gram.M = gram.N = 2 * n;
     gram.K = m;
     gram.sym = true;
-    gram.alpha = 1.0f / (g.S * g.S);
+    gram.alpha = (float)sc[t].gram / (g.S * g.S);
     MNS_HIP(timed_gemm(gram, 3.0 * nn * g.m, s));
     // E' times sc[t + 1].e; Q X comes with e / S (of K) times S (of X): e, as P E does
     const float r = (float)(sc[t + 1].e / sc[t].e);
+    const double gr = sc[t].gram;
     MNS_HIP(timed("nsb_square", 3.0 * nn * g.n, 0.0, s, [&] {
       return nsb_square(b.C2, b.PQ, b.ld_t, b.pq_stride, g.elem, c, (int)g.n, n, abc[3 * t],
-                        abc[3 * t + 1], abc[3 * t + 2], r, r, s); }));
+                        (float)(abc[3 * t + 1] / gr), (float)(abc[3 * t + 2] / (gr * gr)), r,
+                        t == 0 && f16 ? b.scale : nullptr, g.S, s); }));
+    if (f16) {
+      const bool flip = last && g.tall;
+      MNS_HIP(timed("nsb_update", (last ? 4.0 : 6.0) * nn * g.m, 0.0, s, [&] {
+        return nsb_update(b.PQ, b.ld_t, b.pq_stride, b.V[cur], g.ld_x, b.v_stride,
+                          flip ? b.Vt[cur ^ 1] : b.V[cur ^ 1], flip ? b.ld_t : g.ld_x,
+                          flip ? b.vt_stride : b.v_stride, c, (int)g.n, n, g.m, m, last, flip, s); }));
+      cur ^= 1;
+      continue;
+    }
     GemmDesc up = base;
     up.A = b.PQ; up.lda = b.ld_t; up.sA = b.pq_stride;
     if (km) {
@@ -1405,6 +1419,7 @@ mns_status ns_orthogonalize_backward(const void* X, const void* dO, void* dX, in
   const int nblk = norm_blocks(rows * cols);
   for (int64_t b0 = 0; b0 < batch; b0 += cmax) {
     const int c = (int)((batch - b0) < cmax ? batch - b0 : cmax);
+    const bool own = g.elem == Elem::F16 && nsb_fused(g, c);       // nsb_update, V alone
     nsb_bytes(workspace, g, c, b, small);
     const size_t off = (size_t)b0 * rows * cols * esz;
     const char* x = static_cast<const char*>(X) + off;
@@ -1416,7 +1431,7 @@ mns_status ns_orthogonalize_backward(const void* X, const void* dO, void* dX, in
     MNS_HIP(timed("sumsq", 0, all * ss, s, [&] {
       return sumsq(go, sto, c, rows * cols, b.pg, s); }));
     MNS_HIP(timed("nsb_scales", 0, 16.0 * c * nblk, s, [&] {
-      return nsb_scales(b.px, b.pg, nblk, c, g.S, sc[0].e, b.scale, s); }));
+      return nsb_scales(b.px, b.pg, nblk, c, g.S, sc[0].e, own, b.scale, s); }));
     if (g.n <= kNsbSmall) {
       MNS_HIP(timed("nsb_small_load", 0, all * 2.0 * (ss + es), s, [&] {
         return nsb_small_load(small, x, go, sto, b.scale, s); }));
@@ -1433,7 +1448,7 @@ mns_status ns_orthogonalize_backward(const void* X, const void* dO, void* dX, in
     }
     const NsbDst v{b.V[0], g.ld_x, b.v_stride, g.n_p * g.ld_x};
     // [E^T X^T] only where the products read it
-    const NsbDst vt{nsb_kmajor(g, c, b) ? nullptr : b.Vt[0], b.ld_t, b.vt_stride, g.n_p};
+    const NsbDst vt{own || nsb_kmajor(g, c, b) ? nullptr : b.Vt[0], b.ld_t, b.vt_stride, g.n_p};
     MNS_HIP(timed("nsb_load", 0, all * 2.0 * (ss + 2.0 * es), s, [&] {
       return nsb_load(x, go, sto, c, rows, cols, b.scale, g.elem, g.rows_p, g.cols_p,
                       g.tall ? vt : v, g.tall ? v : vt, s); }));

@@ -9,6 +9,7 @@
 // the kernels only: no host copy, no synchronisation, so the calls can be captured. Every offset
 // is clamped to [0, total_rows] and an end before its begin is an empty group, so wrong offsets
 // give wrong results but never an access outside the buffers.
+#include "lds_dma.h"
 #include "mns_internal.h"
 
 #include <type_traits>
@@ -16,7 +17,6 @@
 namespace mns {
 namespace {
 
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
@@ -709,38 +709,6 @@ __global__ __launch_bounds__(256) void k_grouped_rows(GroupedArgs p) {
 // not stored. For the weight gradient the reduction ends inside a k-tile: the resources end at
 // the expert's last row, so the rest of the tile is zeros for both operands; they start at the
 // k-tile (not at the expert), so offsets stay below 2 GiB however many rows an expert has.
-
-typedef __attribute__((address_space(3))) void lds_void;
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-
-constexpr int kChunks = 8;                  // 16-byte chunks of a 128-byte LDS row
-constexpr int kBufferFlags = 0x00020000;    // buffer resource word 3: raw loads
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
-  const int n = bytes > 0x7FFFFFFFLL ? 0x7FFFFFFF : bytes < 0 ? 0 : (int)bytes;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, n, kBufferFlags);
-}
-
-// 16 bytes per lane, global -> LDS: lane l's land at dst + 16 l (dst wave-uniform).
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, u32x4* dst, int voff, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, voff, soff, 0, 0);
-}
-
-__device__ __forceinline__ int swz(int row, int chunk) {
-  return row * kChunks + (chunk ^ ((row ^ ((row >> 3) & 3)) & 7));
-}
-
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-  return (uint32_t)(uintptr_t)(lds_void*)p;
-}
-
-// This wave's DMA and LDS accesses are done, then the workgroup meets.
-__device__ __forceinline__ void block_sync() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070);       // vmcnt(0) lgkmcnt(0)
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
 
 // Tile (tm, tn) of place `t` among tiles_m x tiles_n: groups of 4 row tiles, column by column inside a
 // group, so that tiles in flight together share operand rows.

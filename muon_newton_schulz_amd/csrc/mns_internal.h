@@ -199,9 +199,10 @@ hipError_t gather_normalize(const PtrPack& M, int count, int64_t k, int64_t cols
 // Newton-Schulz gradient (ns_backward.hip); matrices of count consecutive rows x cols buffers.
 // ---------------------------------------------------------------------------------------
 // scale[4 b ..] = S / ||X_b||, 1 / ||X_b||, e0 / ||dO_b||, ||dO_b|| (zeros for a zero norm) from
-// the sumsq() partials of X and dO.
+// the sumsq() partials of X and dO; exact: the first and third as powers of two (rounded down), the
+// fourth e0 / the third.
 hipError_t nsb_scales(const double* px, const double* pg, int nblk, int count, double S, double e0,
-                      double* scale, hipStream_t s);
+                      bool exact, double* scale, hipStream_t s);
 // Where nsb_load writes source element (r, c): p[b * stride + which * offset + r * ld + c]
 // (straight) or [... + c * ld + r] (transposed); which = 0 for dO, 1 for X. p null: not written.
 struct NsbDst {
@@ -216,10 +217,17 @@ hipError_t symmetrise(const void* K, int64_t ldk, int64_t sK, const void* D, int
                       int64_t sD, void* C, int64_t ldc, int64_t sC, Elem e, int count, int64_t n_p,
                       float beta, float gamma, hipStream_t s);
 // The n x n side of an iteration at once: from C2 = [E; X] [E; X]^T (2 n_p square, pitch ld, matrix
-// stride `stride`) to PQ = [r P, q Q; 0, P], P = a I + b A + c A^2 (I on the first n), Q = b S + c (A S
-// + S A), A and S = K + K^T the blocks of C2.
+// stride `stride`) to PQ: float32 [r P, r Q; 0, P], float16 [r P, r Q; P, dP; r dP, -] with dP = 2^11 (P
+// less its float16 value). P = a I + b A + c A^2 (I on the first n), Q = b S + c (A S + S A), A and S =
+// K + K^T the blocks of C2. scale: nsb_scales' with exact, in the first iteration, else null.
 hipError_t nsb_square(const void* C2, void* PQ, int64_t ld, int64_t stride, Elem e, int count, int n,
-                      int n_p, float a, float b, float c, float r, float q, hipStream_t s);
+                      int n_p, float a, float b, float c, float r, const double* scale, double S,
+                      hipStream_t s);
+// float16: [E'; X'] (out; only_e: E', transposed if trans) from that PQ and V = [E; X], both with X n_p
+// rows behind E, n x m in them; padding (to n_p, m_p: multiples of 128) is written as zeros.
+hipError_t nsb_update(const void* PQ, int64_t ld, int64_t stride, const void* V, int64_t ldv,
+                      int64_t sV, void* out, int64_t ldo, int64_t sO, int count, int n, int n_p,
+                      int64_t m, int64_t m_p, bool only_e, bool trans, hipStream_t s);
 // Matrices whose short side is at most 64 (kNsbSmall): one launch per iteration. V: [E; X], 128 x ld
 // floats per matrix, ld = m rounded up to 64; part: two buffers of blocks * 2 * 64 * 64 floats per
 // matrix; Et (tall): m x 64 floats per matrix, E_T as the tall matrix is stored.

@@ -11,6 +11,7 @@
 //   E <- P E + Q X,  X <- P X              (E_0 = dO)
 //
 // and dX = (E_T - X_0 <X_0, E_T>) / ||X||, the normalisation's (symmetric) derivative.
+#include "lds_dma.h"
 #include "mns_internal.h"
 
 namespace mns {
@@ -77,10 +78,12 @@ __device__ __forceinline__ void store8(T* p, const T* v) {
 }
 
 // scale[4 b ..]: S / ||X||, 1 / ||X||, e0 / ||dO||, ||dO|| of matrix b (zeros for a zero norm),
-// from nblk partial sums of squares of X and, behind them, of dO.
+// from nblk partial sums of squares of X and, behind them, of dO. exact: the first and third rounded
+// down to powers of two, so that a bfloat16 matrix keeps every bit in float16; k_nsb_square makes up
+// for X's in the first iteration, and the fourth is e0 / (third).
 __global__ __launch_bounds__(kThreads) void k_nsb_scales(const double* px, const double* pg,
                                                          int nblk, double S, double e0,
-                                                         double* scale) {
+                                                         bool exact, double* scale) {
   __shared__ double red[2][kThreads];
   const int b = blockIdx.x;
   double sx = 0.0, sg = 0.0;
@@ -100,10 +103,12 @@ __global__ __launch_bounds__(kThreads) void k_nsb_scales(const double* px, const
   }
   if (threadIdx.x == 0) {
     const double nx = sqrt(red[0][0]), ng = sqrt(red[1][0]);
-    scale[4 * b] = nx == 0.0 ? 0.0 : S / nx;
+    const double sx = nx == 0.0 ? 0.0 : S / nx, sg = ng == 0.0 ? 0.0 : e0 / ng;
+    const bool px2 = exact && nx > 0.0 && nx < 1e300, pg2 = exact && ng > 0.0 && ng < 1e300;
+    scale[4 * b] = px2 ? ldexp(1.0, ilogb(sx)) : sx;
     scale[4 * b + 1] = nx == 0.0 ? 0.0 : 1.0 / nx;
-    scale[4 * b + 2] = ng == 0.0 ? 0.0 : e0 / ng;
-    scale[4 * b + 3] = ng;
+    scale[4 * b + 2] = pg2 ? ldexp(1.0, ilogb(sg)) : sg;
+    scale[4 * b + 3] = pg2 ? e0 / ldexp(1.0, ilogb(sg)) : ng;
   }
 }
 
@@ -242,12 +247,17 @@ __global__ __launch_bounds__(kThreads) void k_symmetrise(const T* K, int64_t ldk
 // in its second and K^T in its third. A block makes one 32 x 32 tile of P and of Q,
 //   P_ij = a I + b A_ij + c A_i A_j^T,   Q_ij = b S_ij + c (A_i S_j^T + S_i A_j^T),
 // from the row blocks A_i, A_j, S_i = K_i + K^T_i, S_j (A and S are symmetric), and writes them as
-// the operand of the update,
-//   [E'; X'] = [ r P  r Q ; 0  P ] [E; X].
+// the operand of the update: float32
+//   [ r P  r Q ; 0  P ],
+// float16, for k_nsb_update,
+//   [ r P  r Q ; P  dP ; r dP ],   dP = 2^11 (P - its float16 value).
+// In P E + Q X the two terms cancel, which makes P's rounding the largest of an iteration (relative
+// error of the gradient at 3 x 1111x333, 1.7e-3 of it the output's own rounding: 2.6e-3 without dP).
+// Where X_0 was scaled by a power of two, the first iteration's X is short of the normalised one by
+// a factor s in [1, 2): A by s^2 and S by s, and P and Q take s more for the X they multiply.
 // The row blocks go through LDS, whole 128-byte lines at a time, and each wave takes a fourth of
 // every line (fragments straight from memory touch 32 lines a load: 27 against 16 us on 3 x 512^2).
 // Twice the arithmetic of the separate symmetric products, but no intermediate leaves the chip.
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ void mma32(floatx16& acc, u32x4 a, u32x4 b, _Float16) {
   typedef _Float16 half8 __attribute__((ext_vector_type(8)));
@@ -266,7 +276,9 @@ struct SquareArgs {
   void* PQ;
   int64_t ld, stride;        // of both (elements)
   int n, n_p;
-  float a, b, c, r, q;       // q: scale of Q against r P's
+  float a, b, c, r;
+  const double* scale;       // k_nsb_scales' (exact), in the first iteration
+  double S;
 };
 
 template <typename T>
@@ -322,29 +334,204 @@ __global__ __launch_bounds__(256) void k_nsb_square(SquareArgs g) {
   __syncthreads();
   // wave w finishes register groups w: columns 8 w + 4 (lane >> 5) .. + 3 of row lane & 31
   typedef T t4 __attribute__((ext_vector_type(4)));
+  float b = g.b, c = g.c, s = 1.f;
+  if (g.scale) {
+    const double* sc = g.scale + 4 * blockIdx.y;
+    if (sc[0] > 0.0) s = (float)(sc[1] * g.S / sc[0]);
+    b *= s * s;
+    c *= s * s * s * s;
+  }
   const int i = i0 + row, j = j0 + 8 * wave + 4 * (lane >> 5);
   const t4 av = *reinterpret_cast<const t4*>(A + i * g.ld + j);
   const t4 kv = *reinterpret_cast<const t4*>(K + i * g.ld + j);
   const t4 kt = *reinterpret_cast<const t4*>(KT + i * g.ld + j);
-  t4 p1, p2, q, z;
+  t4 p1, p2, q, lo, rlo;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int x = 4 * wave + e;
     const float ps = part[0][0][x][lane] + part[1][0][x][lane] + part[2][0][x][lane] + part[3][0][x][lane];
     const float qs = part[0][1][x][lane] + part[1][1][x][lane] + part[2][1][x][lane] + part[3][1][x][lane];
-    float p = g.b * (float)av[e] + g.c * ps;
+    float p = b * (float)av[e] + c * ps;
     if (i == j + e && i < g.n) p += g.a;
-    p1[e] = (T)(g.r * p);
-    p2[e] = (T)p;
-    q[e] = (T)(g.q * (g.b * (float)(kv[e] + kt[e]) + g.c * qs));
-    z[e] = (T)0.f;
+    const float rp = g.r * p, sp = s * p;
+    p1[e] = (T)rp;
+    p2[e] = (T)sp;
+    rlo[e] = (T)(2048.f * (rp - (float)p1[e]));
+    lo[e] = (T)(2048.f * (sp - (float)p2[e]));
+    q[e] = (T)(g.r * (b * (float)(kv[e] + kt[e]) + c * qs));
   }
   T* top = PQ + i * g.ld + j;
   T* low = top + g.n_p * g.ld;
   *reinterpret_cast<t4*>(top) = p1;
   *reinterpret_cast<t4*>(top + g.n_p) = q;
-  *reinterpret_cast<t4*>(low) = z;
-  *reinterpret_cast<t4*>(low + g.n_p) = p2;
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<t4*>(low) = p2;
+    *reinterpret_cast<t4*>(low + g.n_p) = lo;
+    *reinterpret_cast<t4*>(low + g.n_p * g.ld) = rlo;
+  } else {
+    *reinterpret_cast<t4*>(low) = t4{};
+    *reinterpret_cast<t4*>(low + g.n_p) = p2;
+  }
+}
+
+// The update of that form, float16:
+//   E' = r P E + r Q X,   X' = P X,   P as two float16 numbers.
+// Tiles of BT x BT (128: eight waves of 32 x 64; 64, where there are few tiles: four of 32 x 32),
+// k-tiles of 64 in a ring of four LDS stages that DMA fills, one barrier each; operands as in
+// grouped.hip's ring kernel (V is read along the output, through the transposing LDS load). The
+// small part of P comes first and is scaled down before the rest is added. Tiles of the padding are
+// zeros, without a product, and the k-tiles stop at n. TRANS (the last iteration of tall matrices): E'
+// alone, transposed. 17 us on 3 x 1111x333 (18 dependent k-tiles of about 0.7 us; the padded
+// product on the general GEMM, one part of P, 14 us and 7 for joining its parts).
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+struct UpdateArgs {
+  const _Float16* PQ;        // of k_nsb_square, 3 n_p rows
+  int64_t ld, stride;
+  const _Float16* V;         // [E; X]
+  int64_t ldv, sV;
+  _Float16* out;             // [E'; X'], or E'^T
+  int64_t ldo, sO;
+  int n, n_p;
+  int64_t m;
+  int row_tiles, col_tiles, columns;   // row tiles of E' and X'; columns of tiles of all matrices
+};
+
+template <int BT, bool TRANS>
+__global__ __launch_bounds__(4 * BT) void k_nsb_update(UpdateArgs g) {
+  constexpr int NS = 4, STAGE = 2 * BT * kChunks, KROW = 2 * BT, FN = BT / 64, KCH = BT / 8;
+  __shared__ u32x4 lds[NS * STAGE];                  // 128 or 64 KB
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  // Blocks go round the 8 XCDs one by one: all row tiles of a column of tiles on one of them, which
+  // then reads that part of V alone.
+  const int row_tiles = g.n_p / BT, all = g.row_tiles, place = (int)blockIdx.x >> 3;
+  const int column = ((int)blockIdx.x & 7) + 8 * (place / all), down = place % all;
+  if (column >= g.columns) return;
+  const bool x_rows = down >= row_tiles;
+  const int i0 = (down - (x_rows ? row_tiles : 0)) * BT, j0 = column % g.col_tiles * BT;
+  const int64_t b = column / g.col_tiles;
+  const int per = (g.n + 63) / 64;                   // k-tiles of a product of depth n
+  const int KL = i0 >= g.n || j0 >= g.m ? 0 : x_rows ? 2 * per : 3 * per;
+  const int ld = (int)g.ld, ldv = (int)g.ldv;
+
+  floatx16 acc[FN];
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[j][e] = 0.f;
+  if (KL > 0) {
+    const __amdgpu_buffer_rsrc_t rA =
+        make_rsrc(g.PQ + b * g.stride, (int64_t)3 * g.n_p * g.ld * 2);
+    const __amdgpu_buffer_rsrc_t rB = make_rsrc(g.V + b * g.sV, (int64_t)2 * g.n_p * g.ldv * 2);
+    const __amdgpu_buffer_rsrc_t none = make_rsrc(g.PQ, 0);    // reads zeros from nowhere
+    int offA[2], offB[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = (wave * 2 + i) * 8 + (lane >> 3);
+      offA[i] = (row * ld + 8 * ((lane & 7) ^ ((row ^ ((row >> 3) & 3)) & 7))) * 2;
+      const int kr = (wave * 2 + i) * (64 / KCH) + lane / KCH;
+      const int x = BT == 128 ? 4 * (kr & 3) : 4 * ((kr >> 1) & 1);
+      offB[i] = (kr * ldv + 8 * ((lane % KCH) ^ x)) * 2;
+    }
+    auto issue = [&](int kt, int st) {
+      const bool real = kt < KL;
+      const __amdgpu_buffer_rsrc_t a = real ? rA : none, v = real ? rB : none;
+      // E': r dP E, r P E, r Q X; X': dP X, P X
+      const int seg = kt >= 2 * per ? 2 : kt >= per ? 1 : 0;
+      const int k = (kt - seg * per) * 64;
+      const int ar = x_rows ? g.n_p : seg == 0 ? 2 * g.n_p : 0;
+      const int ac = x_rows ? (seg == 0 ? g.n_p : 0) : seg == 2 ? g.n_p : 0;
+      const int vr = x_rows || seg == 2 ? g.n_p : 0;
+      const int oa = real ? ((ar + i0) * ld + ac + k) * 2 : 0;
+      const int ov = real ? ((vr + k) * ldv + j0) * 2 : 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        dma16(v, &lds[st * STAGE + BT * kChunks + (wave * 2 + i) * 64], offB[i], ov);
+        dma16(a, &lds[st * STAGE + (wave * 2 + i) * 64], offA[i], oa);
+      }
+    };
+    const int G = lane >> 4, kb = 8 * (G >> 1) + ((lane & 15) >> 2);
+    const int x = BT == 128 ? 4 * (kb & 3) : 4 * ((kb >> 1) & 1);
+    uint32_t b_addr[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int col = wn * (BT / 2) + 32 * j + 16 * (G & 1) + 4 * (lane & 3);
+      b_addr[j] = lds_address(lds) + BT * 128 + kb * KROW + ((col >> 3) ^ x) * 16 +
+                  (col & 7) * 2;
+    }
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) issue(s, s);
+    int st = 0, fill = NS - 1;
+    for (int kt = 0; kt < KL; ++kt) {
+      // k-tile kt has landed (two newer ones, eight DMAs, may be on their way), for every wave
+      // behind the barrier, where the stage of k-tile kt - 1 is free too
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0x0070 | (NS - 2) * 4);
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      issue(kt + NS - 1, fill);
+      const u32x4* A = lds + st * STAGE;
+      u32x4 a[4], v[4][FN];
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) a[ks] = A[swz(wm * 32 + (lane & 31), 2 * ks + (lane >> 5))];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        // waited for in the same block (the compiler would wait for every outstanding DMA)
+        u32x2 t[8];
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %8\n\t"
+            "ds_read_b64_tr_b16 %1, %8 offset:%c9\n\t"
+            "ds_read_b64_tr_b16 %2, %8 offset:%c10\n\t"
+            "ds_read_b64_tr_b16 %3, %8 offset:%c11\n\t"
+            "ds_read_b64_tr_b16 %4, %8 offset:%c12\n\t"
+            "ds_read_b64_tr_b16 %5, %8 offset:%c13\n\t"
+            "ds_read_b64_tr_b16 %6, %8 offset:%c14\n\t"
+            "ds_read_b64_tr_b16 %7, %8 offset:%c15\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(t[0]), "=&v"(t[1]), "=&v"(t[2]), "=&v"(t[3]), "=&v"(t[4]), "=&v"(t[5]),
+              "=&v"(t[6]), "=&v"(t[7])
+            : "v"(b_addr[j] + (uint32_t)(st * STAGE * 16)), "i"(4 * KROW), "i"(16 * KROW),
+              "i"(20 * KROW), "i"(32 * KROW), "i"(36 * KROW), "i"(48 * KROW), "i"(52 * KROW));
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          v[ks][j] = u32x4{t[2 * ks].x, t[2 * ks].y, t[2 * ks + 1].x, t[2 * ks + 1].y};
+      }
+      if (kt == per) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[j][e] *= 0x1p-11f;
+      }
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          if constexpr (TRANS) mma32(acc[j], a[ks], v[ks][j], _Float16{});
+          else mma32(acc[j], v[ks][j], a[ks], _Float16{});
+        }
+      st = st + 1 == NS ? 0 : st + 1;
+      fill = fill + 1 == NS ? 0 : fill + 1;
+    }
+    block_sync();                 // no DMA is in flight when the block ends
+  }
+  // a lane's registers: 4 neighbouring columns of one row (TRANS: rows of one column) in 4 groups
+  typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+  const int one = lane & 31, four = 4 * (lane >> 5);
+  _Float16* out = g.out + b * g.sO;
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int r = i0 + wm * 32, c = j0 + wn * (BT / 2) + 32 * j;
+    _Float16* o = out + (TRANS ? (c + one) * g.ldo + r + four
+                               : ((x_rows ? g.n_p : 0) + r + one) * g.ldo + c + four);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      half4 h;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = (_Float16)acc[j][4 * q + e];
+      *reinterpret_cast<half4*>(o + 8 * q) = h;
+    }
+  }
 }
 
 // ---- short sides up to 64 -------------------------------------------------------------------
@@ -625,8 +812,9 @@ hipError_t last() { return hipGetLastError(); }
 }  // namespace
 
 hipError_t nsb_scales(const double* px, const double* pg, int nblk, int count, double S, double e0,
-                      double* scale, hipStream_t s) {
-  hipLaunchKernelGGL(k_nsb_scales, dim3(count), dim3(kThreads), 0, s, px, pg, nblk, S, e0, scale);
+                      bool exact, double* scale, hipStream_t s) {
+  hipLaunchKernelGGL(k_nsb_scales, dim3(count), dim3(kThreads), 0, s, px, pg, nblk, S, e0, exact,
+                     scale);
   return last();
 }
 
@@ -675,11 +863,34 @@ hipError_t symmetrise(const void* K, int64_t ldk, int64_t sK, const void* D, int
 }
 
 hipError_t nsb_square(const void* C2, void* PQ, int64_t ld, int64_t stride, Elem e, int count, int n,
-                      int n_p, float a, float b, float c, float r, float q, hipStream_t s) {
-  const SquareArgs g{C2, PQ, ld, stride, n, n_p, a, b, c, r, q};
+                      int n_p, float a, float b, float c, float r, const double* scale, double S,
+                      hipStream_t s) {
+  const SquareArgs g{C2, PQ, ld, stride, n, n_p, a, b, c, r, scale, S};
   const dim3 grid((n_p / 32) * (n_p / 32), count);
   if (e == Elem::F16) hipLaunchKernelGGL(k_nsb_square<_Float16>, grid, dim3(256), 0, s, g);
   else hipLaunchKernelGGL(k_nsb_square<float>, grid, dim3(256), 0, s, g);
+  return last();
+}
+
+hipError_t nsb_update(const void* PQ, int64_t ld, int64_t stride, const void* V, int64_t ldv,
+                      int64_t sV, void* out, int64_t ldo, int64_t sO, int count, int n, int n_p,
+                      int64_t m, int64_t m_p, bool only_e, bool trans, hipStream_t s) {
+  // 64 x 64 where the products fill at most 100 tiles of 128 x 128 (all five iterations, us, 64 / 128:
+  // 512x512 173 / 208, three of them 234 / 246, 333x1111 184 / 199; two of those, 108 tiles, 244 / 238, 2 x 512x2048
+  // 315 / 283)
+  const int64_t live = (int64_t)((n + 127) / 128) * ((m + 127) / 128) * 2 * count;
+  const int bt = live <= 100 ? 64 : 128;
+  const int rt = n_p / bt * (only_e ? 1 : 2), ct = (int)(m_p / bt);
+  const UpdateArgs g{static_cast<const _Float16*>(PQ), ld, stride, static_cast<const _Float16*>(V),
+                     ldv, sV, static_cast<_Float16*>(out), ldo, sO, n, n_p, m, rt, ct, ct * count};
+  const dim3 grid((unsigned)((ct * count + 7) / 8 * 8 * rt)), block(4 * bt);
+  if (bt == 64) {
+    if (trans) hipLaunchKernelGGL((k_nsb_update<64, true>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((k_nsb_update<64, false>), grid, block, 0, s, g);
+  } else {
+    if (trans) hipLaunchKernelGGL((k_nsb_update<128, true>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((k_nsb_update<128, false>), grid, block, 0, s, g);
+  }
   return last();
 }
 

@@ -168,3 +168,21 @@ def test_two_streams_at_once():
     for a, outs in zip(alone, got):
         for o in outs:
             assert torch.equal(o, a)
+
+
+@pytest.mark.parametrize("dist", ["normal", "lowrank"])
+@pytest.mark.parametrize("batch,rows,cols", [(1, 257, 300), (1, 300, 257), (3, 1111, 333),
+                                             (2, 512, 512), (4, 512, 1030), (1, 400, 6000)])
+def test_small_bfloat16_within_half_a_step(batch, rows, cols, dist):
+    """The arithmetic's error together with the output's rounding stays below the largest rounding
+    of a bfloat16 output alone (2^-8 of a value; its mean over a matrix is below half of that), for
+    near-square and low-rank matrices too, where float16 shows most. Nothing is read from a
+    workspace before it is written (filled with NaN), the padding among it."""
+    _say("case", dist, batch, rows, cols)
+    X, G, xs, gs = _batch(dist, batch, rows, cols, "bf16", 57)
+    ws = torch.full((mns.ns_backward_workspace_size(X),), 0xFF, dtype=torch.uint8, device="cuda")
+    dX = mns.ns_orthogonalize_backward(X, G, C5, workspace=ws)
+    for i in range(batch):
+        err = rel(to_f64(dX[i]), ref.gradient(xs[i], gs[i], C5))
+        _say("  matrix", i, "error", f"{err:.2e}")
+        assert err <= 2.0 ** -8
