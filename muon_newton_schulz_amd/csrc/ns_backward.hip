@@ -149,7 +149,8 @@ __global__ __launch_bounds__(kThreads) void k_nsb_load(const TX* X, const TX* G,
 }
 
 // The straight layout alone (a wide matrix whose products read the iterate as it is stored): rows of
-// 8-element vectors, bound by its bytes. blockIdx.y: padded row; blockIdx.z as above.
+// 8-element vectors, bound by its bytes (4096 x 16384: 152 us, 3.5 TB/s). blockIdx.y: padded row;
+// blockIdx.z as above.
 template <typename TX, typename TO>
 __global__ __launch_bounds__(kThreads) void k_nsb_load_rows(const TX* X, const TX* G, int64_t rows,
                                                             int64_t cols, int64_t cols_p,
@@ -180,7 +181,8 @@ __global__ __launch_bounds__(kThreads) void k_nsb_load_rows(const TX* X, const T
 }
 
 // C = beta D + gamma (K + K^T): tile pairs (i, j) and (j, i), i <= j, one block each pair. D is
-// symmetric and read at (i, j) only; C is exactly symmetric.
+// symmetric and read at (i, j) only; C is exactly symmetric. Bound by its bytes (n = 4096: 12 us, 5.6
+// TB/s from the caches).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_symmetrise(const T* K, int64_t ldk, int64_t sK,
                                                          const T* D, int64_t ldd, int64_t sD, T* C,
@@ -257,7 +259,8 @@ __global__ __launch_bounds__(kThreads) void k_symmetrise(const T* K, int64_t ldk
 // a factor s in [1, 2): A by s^2 and S by s, and P and Q take s more for the X they multiply.
 // The row blocks go through LDS, whole 128-byte lines at a time, and each wave takes a fourth of
 // every line (fragments straight from memory touch 32 lines a load: 27 against 16 us on 3 x 512^2).
-// Twice the arithmetic of the separate symmetric products, but no intermediate leaves the chip.
+// Twice the arithmetic of the separate symmetric products, but no intermediate leaves the chip. 14 us
+// on 3 x 333^2, 9 on 256^2 in float32: a launch, and k-tiles of LDS fills one after the other.
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ void mma32(floatx16& acc, u32x4 a, u32x4 b, _Float16) {
   typedef _Float16 half8 __attribute__((ext_vector_type(8)));
@@ -540,7 +543,9 @@ __global__ __launch_bounds__(4 * BT) void k_nsb_update(UpdateArgs g) {
 // matrix adds the partial Gram matrices A and K that all its blocks left, forms P and Q from them
 // by itself, updates its own columns of E and X (64 at a time, in place) and leaves the next
 // partial sums from the new values while it has them. float32 throughout; matrices padded to 64
-// rows, not 256. The four waves own the quadrants of every 64 x 64 product.
+// rows, not 256. Bound by the latency of its few dependent products; with T = 5, against the form of
+// three launches: 64x256 104 / 194 us, 24 x 64x1024 234 / 1255, 24 x 64x12288 971 / 7481. The four
+// waves own the quadrants of every 64 x 64 product.
 constexpr int kN = 64, kNP = kN + 1;          // LDS row pitch: 32 rows of one column on 32 banks
 
 // acc (quadrant qi, qj) += sum over k < 64 of L[i ls + k lk] R[j rs + k rk]
@@ -733,7 +738,7 @@ __global__ __launch_bounds__(256) void k_nsb_small_step(SmallArgs g, float a, fl
 }
 
 // Partial sums of <X, E> (E in the stored layout, padded rows), float64: block x of nblk takes
-// rows x, x + nblk, ...
+// rows x, x + nblk, ... Bound by its bytes (8 x 1024x8192: 51 us, 5.3 TB/s).
 template <typename TX, typename TE>
 __global__ __launch_bounds__(kThreads) void k_nsb_dot(const TX* X, const TE* E, int64_t rows,
                                                       int64_t cols, int64_t ld, int64_t sE,
@@ -767,7 +772,8 @@ __global__ __launch_bounds__(kThreads) void k_nsb_dot(const TX* X, const TE* E, 
 }
 
 // dX = (E - X_0 <X_0, E>) / ||X|| with E = E_T ||dO|| / eT: float64 arithmetic (norms of any
-// float32 range, one rounding at the end; the pass is bound by its bytes).
+// float32 range, one rounding at the end; the pass is bound by its bytes: 8 x 1024x8192 66 us, 6.1
+// TB/s).
 template <typename TX, typename TE>
 __global__ __launch_bounds__(kThreads) void k_nsb_project(const TX* X, const TE* E, int64_t rows,
                                                           int64_t cols, int64_t ld, int64_t sE,
@@ -875,9 +881,9 @@ hipError_t nsb_square(const void* C2, void* PQ, int64_t ld, int64_t stride, Elem
 hipError_t nsb_update(const void* PQ, int64_t ld, int64_t stride, const void* V, int64_t ldv,
                       int64_t sV, void* out, int64_t ldo, int64_t sO, int count, int n, int n_p,
                       int64_t m, int64_t m_p, bool only_e, bool trans, hipStream_t s) {
-  // 64 x 64 where the products fill at most 100 tiles of 128 x 128 (all five iterations, us, 64 / 128:
-  // 512x512 173 / 208, three of them 234 / 246, 333x1111 184 / 199; two of those, 108 tiles, 244 / 238, 2 x 512x2048
-  // 315 / 283)
+  // 64 x 64 where the products fill at most 100 tiles of 128 x 128 (the whole call, T = 5, us, 64 / 128:
+  // 512x512 173 / 208, three of them 234 / 246, 333x1111 184 / 199; two of those, 108 tiles, 244 / 238,
+  // 2 x 512x2048 315 / 283)
   const int64_t live = (int64_t)((n + 127) / 128) * ((m + 127) / 128) * 2 * count;
   const int bt = live <= 100 ? 64 : 128;
   const int rt = n_p / bt * (only_e ? 1 : 2), ct = (int)(m_p / bt);
