@@ -149,7 +149,7 @@ __global__ __launch_bounds__(kThreads) void k_nsb_load(const TX* X, const TX* G,
 }
 
 // The straight layout alone (a wide matrix whose products read the iterate as it is stored): rows of
-// 8-element vectors, bound by its bytes (4096 x 16384: 152 us, 3.5 TB/s). blockIdx.y: padded row;
+// 8-element vectors, bound by its bytes (4096 x 16384: 81 us, 6.6 TB/s). blockIdx.y: padded row;
 // blockIdx.z as above.
 template <typename TX, typename TO>
 __global__ __launch_bounds__(kThreads) void k_nsb_load_rows(const TX* X, const TX* G, int64_t rows,
@@ -162,20 +162,26 @@ __global__ __launch_bounds__(kThreads) void k_nsb_load_rows(const TX* X, const T
   TO* dst = static_cast<TO*>(st.p) + b * st.stride + which * st.offset + r * st.ld;
   const double sc = scale[4 * b + (which ? 0 : 2)];
   const bool vec = cols % 8 == 0;
-  for (int64_t c = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8; c < cols_p;
-       c += (int64_t)gridDim.x * kThreads * 8) {
-    float v[8] = {};
-    if (r < rows && c < cols) {
-      if (vec) {
-        load8(src + c, v);
-      } else {
+  // four vectors of a thread in flight together
+  const int64_t c0 = ((int64_t)blockIdx.x * 4 * kThreads + threadIdx.x) * 8;
+  float v[4][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? widen(src[c + e]) : 0.f;
-      }
+  for (int u = 0; u < 4; ++u) {
+    const int64_t c = c0 + u * kThreads * 8;
+    if (r < rows && c < cols && vec) {
+      load8(src + c, v[u]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[u][e] = r < rows && c + e < cols ? widen(src[c + e]) : 0.f;
     }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int64_t c = c0 + u * kThreads * 8;
+    if (c >= cols_p) break;
     TO o[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = (TO)(float)((double)v[e] * sc);
+    for (int e = 0; e < 8; ++e) o[e] = (TO)(float)((double)v[u][e] * sc);
     store8(dst + c, o);
   }
 }
@@ -832,8 +838,9 @@ hipError_t nsb_load(const void* X, const void* G, Store st, int count, int64_t r
   const LoadDst t{transposed.p, transposed.ld, transposed.stride, transposed.offset};
   const int64_t n = rows * cols;
   // a transposed layout goes through LDS tiles; the straight one alone is a row pass (134 M elements
-  // of 4096 x 16384: 284 against 152 us)
-  const dim3 flat((unsigned)((cols_p / 8 + kThreads - 1) / kThreads), (unsigned)rows_p, 2 * count);
+  // of 4096 x 16384: 284 against 81 us)
+  const dim3 flat((unsigned)((cols_p / 8 + 4 * kThreads - 1) / (4 * kThreads)), (unsigned)rows_p,
+                  2 * count);
 #define MNS_NSB_LOAD(TX, TO)                                                                \
   do {                                                                                      \
     if (t.p)                                                                                \
