@@ -285,6 +285,7 @@ struct SquareArgs {
   void* PQ;
   int64_t ld, stride;        // of both (elements)
   int n, n_p;
+  int tiles;                 // of 32 rows: up to n_p; float16: as far as k_nsb_update reads
   float a, b, c, r;
   const double* scale;       // k_nsb_scales' (exact), in the first iteration
   double S;
@@ -297,7 +298,7 @@ __global__ __launch_bounds__(256) void k_nsb_square(SquareArgs g) {
   __shared__ float part[4][2][16][64];
   __shared__ u32x4 rows[4][32 * PITCH];              // A_i, A_j, S_i, S_j: 128 bytes of 32 rows
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int tiles = g.n_p / 32;
+  const int tiles = g.tiles;
   const int i0 = (int)(blockIdx.x / tiles) * 32, j0 = (int)(blockIdx.x % tiles) * 32;
   const T* C2 = static_cast<const T*>(g.C2) + blockIdx.y * g.stride;
   T* PQ = static_cast<T*>(g.PQ) + blockIdx.y * g.stride;
@@ -312,14 +313,16 @@ __global__ __launch_bounds__(256) void k_nsb_square(SquareArgs g) {
   const int64_t oi = (i0 + lr) * g.ld + lc * VEC, oj = (j0 + lr) * g.ld + lc * VEC;
   auto at = [&](const T* base, int64_t o) { return *reinterpret_cast<const vec*>(base + o); };
   vec ai = at(A, oi), aj = at(A, oj), ki = at(K, oi), kj = at(K, oj), ti = at(KT, oi), tj = at(KT, oj);
-  for (int k = 0; k < g.n_p; k += BK) {
+  // behind n everything is zero: k stops there, and tiles there are written without a product
+  const int depth = i0 >= g.n || j0 >= g.n ? 0 : g.n;
+  for (int k = 0; k < depth; k += BK) {
     const int o = lr * PITCH + lc;
     rows[0][o] = __builtin_bit_cast(u32x4, ai);
     rows[1][o] = __builtin_bit_cast(u32x4, aj);
     rows[2][o] = __builtin_bit_cast(u32x4, ki + ti);
     rows[3][o] = __builtin_bit_cast(u32x4, kj + tj);
     __syncthreads();
-    if (k + BK < g.n_p) {
+    if (k + BK < depth) {
       const int x = k + BK;
       ai = at(A, oi + x);
       aj = at(A, oj + x);
@@ -878,8 +881,9 @@ hipError_t symmetrise(const void* K, int64_t ldk, int64_t sK, const void* D, int
 hipError_t nsb_square(const void* C2, void* PQ, int64_t ld, int64_t stride, Elem e, int count, int n,
                       int n_p, float a, float b, float c, float r, const double* scale, double S,
                       hipStream_t s) {
-  const SquareArgs g{C2, PQ, ld, stride, n, n_p, a, b, c, r, scale, S};
-  const dim3 grid((n_p / 32) * (n_p / 32), count);
+  const int tiles = (e == Elem::F16 ? (n + 127) / 128 * 128 : n_p) / 32;
+  const SquareArgs g{C2, PQ, ld, stride, n, n_p, tiles, a, b, c, r, scale, S};
+  const dim3 grid(tiles * tiles, count);
   if (e == Elem::F16) hipLaunchKernelGGL(k_nsb_square<_Float16>, grid, dim3(256), 0, s, g);
   else hipLaunchKernelGGL(k_nsb_square<float>, grid, dim3(256), 0, s, g);
   return last();
