@@ -1050,15 +1050,18 @@ struct NsbBuffers {
   int64_t ld_t = 0, v_stride = 0, vt_stride = 0, q_stride = 0, pq_stride = 0;
 };
 
-// Small problems, bound by their launches: the n x n side of an iteration as one kernel, A and K in one
-// symmetric product [E; X] [E; X]^T and the update in one launch. Three launches an iteration instead of
-// eight, for a third to a half more arithmetic; in float16 also a third less error (k_nsb_square). In
-// us, eight launches against three: float32 256x1024 402 / 235, 4 x 64x2048 589 / 517, 16 x 256x1024
-// 861 / 953, 512x2048 639 / 535, 4 x 512x512 721 / 780; float16 333x1111 303 / 182, 512x8192 465 / 390,
-// 2 x 512x4096 443 / 396, 4 x 512x2048 447 / 440, 3 x 512x4096 445 / 524, 16 x 512x512 509 / 663.
+// Small problems, bound by their launches: an iteration as three launches instead of eight (A, K and K^T;
+// the n x n side; the update), for a third to a half more arithmetic. In us, eight launches against
+// three, float32 (the first and last on the general product, padded to 256): 256x1024 402 / 235,
+// 4 x 64x2048 589 / 517, 16 x 256x1024 861 / 953, 512x2048 639 / 535, 4 x 512x512 721 / 780. float16
+// (kernels of its own that stop at n, so that a small n counts for more; a third less error too,
+// k_nsb_square): 333x1111 303 / 161, 16 of them 761 / 709, 8 x 300x3000 759 / 607, 512x8192 465 / 397,
+// 4 x 512x2048 447 / 425, 8 x 512x1024 536 / 534, 3 x 512x4096 451 / 556, 16 x 512x512 522 / 712.
 static bool nsb_fused(const Geo& g, int count) {
-  const double work = (double)count * g.n_p * g.n_p * (g.m_p + g.n_p);
-  return g.n_p <= 512 && work <= (g.elem == Elem::F16 ? 2.8e9 : 8e8);
+  if (g.n_p > 512) return false;
+  if (g.elem != Elem::F16) return (double)count * g.n_p * g.n_p * (g.m_p + g.n_p) <= 8e8;
+  const double n = (double)((g.n + 127) / 128 * 128);
+  return count * n * n * n * (g.m + n) <= 1.7e12;
 }
 
 static size_t carve_nsb(void* base, const Geo& g, int count, NsbBuffers& b) {
@@ -1135,6 +1138,17 @@ static size_t carve_nsb_small(void* base, const Geo& g, int count, NsbBuffers& b
 
 static size_t nsb_bytes(void* base, const Geo& g, int count, NsbBuffers& b, NsbSmall& d) {
   return g.n <= kNsbSmall ? carve_nsb_small(base, g, count, b, d) : carve_nsb(base, g, count, b);
+}
+
+// A call's: of its full chunks, or of the last one where that takes the form of nsb_fused and more.
+static size_t nsb_need(const Geo& g, int64_t batch) {
+  NsbBuffers b;
+  NsbSmall d;
+  if (batch <= kChunk) return nsb_bytes(nullptr, g, (int)batch, b, d);
+  const size_t full = nsb_bytes(nullptr, g, kChunk, b, d);
+  const int rest = (int)(batch % kChunk);
+  const size_t last = rest ? nsb_bytes(nullptr, g, rest, b, d) : 0;
+  return full > last ? full : last;
 }
 
 // Powers of two that scale the stored quantities of one iteration: E by e, S and A S by kap, P by
@@ -1241,16 +1255,23 @@ static mns_status run_nsb_fused(const Geo& g, int c, const NsbBuffers& b, int T,
   for (int t = 0; t < T; ++t) {
     const bool last = t == T - 1;
     // C2 = [E; X] [E; X]^T gram / S^2: A times gram, K times gram e / S
-    GemmDesc gram = base;
-    gram.A = gram.B = b.V[cur];
-    gram.lda = gram.ldb = g.ld_x;
-    gram.sA = gram.sB = b.v_stride;
-    gram.C = b.C2; gram.ldc = b.ld_t; gram.sC = b.pq_stride;
-    gram.M = gram.N = 2 * n;
-    gram.K = m;
-    gram.sym = true;
-    gram.alpha = (float)sc[t].gram / (g.S * g.S);
-    MNS_HIP(timed_gemm(gram, 3.0 * nn * g.m, s));
+    const float alpha = (float)sc[t].gram / (g.S * g.S);
+    if (f16) {
+      MNS_HIP(timed("nsb_gram", 3.0 * nn * g.m, 0.0, s, [&] {
+        return nsb_gram(b.V[cur], g.ld_x, b.v_stride, b.C2, b.ld_t, b.pq_stride, c, (int)g.n, n,
+                        g.m, alpha, s); }));
+    } else {
+      GemmDesc gram = base;
+      gram.A = gram.B = b.V[cur];
+      gram.lda = gram.ldb = g.ld_x;
+      gram.sA = gram.sB = b.v_stride;
+      gram.C = b.C2; gram.ldc = b.ld_t; gram.sC = b.pq_stride;
+      gram.M = gram.N = 2 * n;
+      gram.K = m;
+      gram.sym = true;
+      gram.alpha = alpha;
+      MNS_HIP(timed_gemm(gram, 3.0 * nn * g.m, s));
+    }
     // E' times sc[t + 1].e; Q X comes with e / S (of K) times S (of X): e, as P E does
     const float r = (float)(sc[t + 1].e / sc[t].e);
     const double gr = sc[t].gram;
@@ -1388,10 +1409,7 @@ mns_status mns_ns_backward_workspace_size(int dtype, int64_t batch, int64_t rows
   if (!bytes) return MNS_ERR_NULL;
   const mns_status st = nsb_check(dtype, batch, rows, cols);
   if (st != MNS_OK) return st;
-  NsbBuffers b;
-  NsbSmall small;
-  *bytes = nsb_bytes(nullptr, nsb_geo(rows, cols, store_of(dtype)),
-                     batch < kChunk ? (int)batch : kChunk, b, small);
+  *bytes = nsb_need(nsb_geo(rows, cols, store_of(dtype)), batch);
   return MNS_OK;
 }
 
@@ -1412,7 +1430,7 @@ mns_status ns_orthogonalize_backward(const void* X, const void* dO, void* dX, in
   const int cmax = batch < kChunk ? (int)batch : kChunk;
   NsbBuffers b;
   NsbSmall small;
-  st = check_ws(workspace, workspace_bytes, nsb_bytes(nullptr, g, cmax, b, small));
+  st = check_ws(workspace, workspace_bytes, nsb_need(g, batch));
   if (st != MNS_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const size_t esz = store_bytes(dtype);

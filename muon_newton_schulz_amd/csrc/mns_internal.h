@@ -223,6 +223,10 @@ hipError_t symmetrise(const void* K, int64_t ldk, int64_t sK, const void* D, int
 hipError_t nsb_square(const void* C2, void* PQ, int64_t ld, int64_t stride, Elem e, int count, int n,
                       int n_p, float a, float b, float c, float r, const double* scale, double S,
                       hipStream_t s);
+// float16, C2 for nsb_square from V = [E; X] (X n_p rows behind E) times alpha: A, K and K^T, as far as it
+// reads.
+hipError_t nsb_gram(const void* V, int64_t ldv, int64_t sV, void* C2, int64_t ld, int64_t stride,
+                    int count, int n, int n_p, int64_t m, float alpha, hipStream_t s);
 // float16: [E'; X'] (out; only_e: E', transposed if trans) from that PQ and V = [E; X], both with X n_p
 // rows behind E, n x m in them; padding (to n_p, m_p: multiples of 128) is written as zeros.
 hipError_t nsb_update(const void* PQ, int64_t ld, int64_t stride, const void* V, int64_t ldv,

@@ -266,7 +266,8 @@ __global__ __launch_bounds__(kThreads) void k_symmetrise(const T* K, int64_t ldk
 // The row blocks go through LDS, whole 128-byte lines at a time, and each wave takes a fourth of
 // every line (fragments straight from memory touch 32 lines a load: 27 against 16 us on 3 x 512^2).
 // Twice the arithmetic of the separate symmetric products, but no intermediate leaves the chip. 14 us
-// on 3 x 333^2, 9 on 256^2 in float32: a launch, and k-tiles of LDS fills one after the other.
+// on 3 x 512^2 (9 on 3 x 333^2, stopping at n), 9 on 256^2 in float32: a launch, and k-tiles of LDS
+// fills one after the other.
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ void mma32(floatx16& acc, u32x4 a, u32x4 b, _Float16) {
   typedef _Float16 half8 __attribute__((ext_vector_type(8)));
@@ -384,6 +385,131 @@ __global__ __launch_bounds__(256) void k_nsb_square(SquareArgs g) {
     *reinterpret_cast<t4*>(low) = t4{};
     *reinterpret_cast<t4*>(low + g.n_p) = p2;
   }
+}
+
+// C2's blocks A, K and K^T for short reductions, float16: 64 x 64 tiles of E X^T and of half of X X^T,
+// each stored in both places; as far as k_nsb_square reads (n to the next 128; zeros behind n). Eight
+// waves in two groups of four, 32 x 32 a wave, the groups taking k-tiles of 64 in turn: half as many
+// steps one after the other, which are what bounds it; their sums are added through LDS. Each group
+// has a ring of four LDS stages that DMA fills. 9 us on 3 x 1111x333, 18 on the general product and its
+// tail (the whole call, T = 5: 201 / 246; 2 x 257x300 142 / 170, 512x8192 398 / 394, 8 x 512x512 410 / 386).
+struct GramArgs {
+  const _Float16* V;         // [E; X]
+  int64_t ldv, sV;
+  _Float16* C2;
+  int64_t ld, stride;
+  int n, n_p, row_tiles;     // row_tiles: of 64, up to n rounded up to 128
+  int64_t m;
+  float alpha;
+};
+
+__global__ __launch_bounds__(512) void k_nsb_gram(GramArgs g) {
+  constexpr int NS = 4, TILE = 64 * kChunks, STAGE = 2 * TILE, GROUP = NS * STAGE, TP = 72;
+  __shared__ u32x4 lds[2 * GROUP];                   // 128 KB
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave8 = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int group = wave8 >> 2, wave = wave8 & 3, wm = wave >> 1, wn = wave & 1;
+  const int rt = g.row_tiles, unit = (int)blockIdx.x;
+  const bool cross = unit < rt * rt;
+  int ti, tj;
+  if (cross) {
+    ti = unit / rt;
+    tj = unit % rt;
+  } else {                                           // row by row of the upper half
+    int left = unit - rt * rt;
+    ti = 0;
+    while (left >= rt - ti) left -= rt - ti++;
+    tj = ti + left;
+  }
+  const int i0 = (cross ? 0 : g.n_p) + ti * 64, j0 = g.n_p + tj * 64;      // rows of V
+  const int KL = ti * 64 >= g.n || tj * 64 >= g.n ? 0 : ((int)g.m + 63) / 64;
+  const int ldv = (int)g.ldv;
+  const int64_t b = blockIdx.y;
+
+  floatx16 acc;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+  if (KL > 0) {
+    const __amdgpu_buffer_rsrc_t rV = make_rsrc(g.V + b * g.sV, (int64_t)2 * g.n_p * g.ldv * 2);
+    const __amdgpu_buffer_rsrc_t none = make_rsrc(g.V, 0);     // reads zeros from nowhere
+    u32x4* ring = lds + group * GROUP;
+    int off[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = (wave * 2 + i) * 8 + (lane >> 3);
+      off[i] = (row * ldv + 8 * ((lane & 7) ^ ((row ^ ((row >> 3) & 3)) & 7))) * 2;
+    }
+    auto issue = [&](int step, int st) {
+      const int kt = 2 * step + group;
+      const bool real = kt < KL;
+      const __amdgpu_buffer_rsrc_t r = real ? rV : none;
+      const int oa = real ? (i0 * ldv + kt * 64) * 2 : 0, ob = real ? (j0 * ldv + kt * 64) * 2 : 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        dma16(r, &ring[st * STAGE + (wave * 2 + i) * 64], off[i], oa);
+        dma16(r, &ring[st * STAGE + TILE + (wave * 2 + i) * 64], off[i], ob);
+      }
+    };
+    const int steps = (KL + 1) / 2;
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) issue(s, s);
+    int st = 0, fill = NS - 1;
+    for (int step = 0; step < steps; ++step) {
+      // as in k_nsb_update: this step's k-tiles have landed, the stage before is free
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0x0070 | (NS - 2) * 4);
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      issue(step + NS - 1, fill);
+      const u32x4* A = ring + st * STAGE;
+      const u32x4* B = A + TILE;
+      u32x4 a[4], v[4];
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const int ch = 2 * ks + (lane >> 5);
+        a[ks] = A[swz(wm * 32 + (lane & 31), ch)];
+        v[ks] = B[swz(wn * 32 + (lane & 31), ch)];
+      }
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) mma32(acc, v[ks], a[ks], _Float16{});
+      st = st + 1 == NS ? 0 : st + 1;
+      fill = fill + 1 == NS ? 0 : fill + 1;
+    }
+    block_sync();                 // no DMA is in flight
+    float(*sums)[16][64] = reinterpret_cast<float(*)[16][64]>(lds);
+    if (group == 1) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sums[wave][e][lane] = acc[e];
+    }
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[e] = (acc[e] + sums[wave][e][lane]) * g.alpha;
+    }
+    __syncthreads();
+  }
+  // a lane's registers: 4 neighbouring columns of one row, in 4 groups; transposed through LDS
+  typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+  _Float16* C2 = g.C2 + b * g.stride;
+  _Float16* T = reinterpret_cast<_Float16*>(lds);
+  if (group == 0) {
+    const int r = wm * 32 + (lane & 31), c = wn * 32 + 4 * (lane >> 5);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      half4 h;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        h[e] = (_Float16)acc[4 * q + e];
+        T[(c + 8 * q + e) * TP + r] = h[e];
+      }
+      *reinterpret_cast<half4*>(C2 + (i0 + r) * g.ld + j0 + c + 8 * q) = h;
+    }
+  }
+  __syncthreads();
+  if (!cross && ti == tj) return;
+  const int row = tid >> 3, ch = tid & 7;
+  *reinterpret_cast<u32x4*>(C2 + (j0 + row) * g.ld + i0 + 8 * ch) =
+      *reinterpret_cast<const u32x4*>(T + row * TP + 8 * ch);
 }
 
 // The update of that form, float16:
@@ -886,6 +1012,15 @@ hipError_t nsb_square(const void* C2, void* PQ, int64_t ld, int64_t stride, Elem
   const dim3 grid(tiles * tiles, count);
   if (e == Elem::F16) hipLaunchKernelGGL(k_nsb_square<_Float16>, grid, dim3(256), 0, s, g);
   else hipLaunchKernelGGL(k_nsb_square<float>, grid, dim3(256), 0, s, g);
+  return last();
+}
+
+hipError_t nsb_gram(const void* V, int64_t ldv, int64_t sV, void* C2, int64_t ld, int64_t stride,
+                    int count, int n, int n_p, int64_t m, float alpha, hipStream_t s) {
+  const int rt = (n + 127) / 128 * 2;
+  const GramArgs g{static_cast<const _Float16*>(V), ldv, sV, static_cast<_Float16*>(C2), ld, stride, n,
+                   n_p, rt, m, alpha};
+  hipLaunchKernelGGL(k_nsb_gram, dim3(rt * rt + rt * (rt + 1) / 2, count), dim3(512), 0, s, g);
   return last();
 }
 

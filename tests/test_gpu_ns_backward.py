@@ -186,3 +186,23 @@ def test_small_bfloat16_within_half_a_step(batch, rows, cols, dist):
         err = rel(to_f64(dX[i]), ref.gradient(xs[i], gs[i], C5))
         _say("  matrix", i, "error", f"{err:.2e}")
         assert err <= 2.0 ** -8
+
+
+def test_last_chunk_of_another_form():
+    """63 matrices: 32, then 31 in the form of small problems, on the workspace of the size asked
+    for, against the same matrices in calls of their own chunk."""
+    _say("case 63 x 300 x 570")
+    g = torch.Generator().manual_seed(5)
+    X = torch.randn(63, 300, 570, generator=g).bfloat16().cuda()
+    G = torch.randn(63, 300, 570, generator=g).bfloat16().cuda()
+    guard = 4096
+    need = mns.ns_backward_workspace_size(X)
+    room = torch.full((need + guard,), 0xFF, dtype=torch.uint8, device="cuda")
+    dX = mns.ns_orthogonalize_backward(X, G, C5, workspace=room[:need])
+    assert (room[need:] == 0xFF).all()
+    assert torch.equal(dX[:32], mns.ns_orthogonalize_backward(X[:32], G[:32], C5))
+    assert torch.equal(dX[32:], mns.ns_orthogonalize_backward(X[32:].clone(), G[32:].clone(), C5))
+    for i in (0, 31, 32, 62):
+        err = rel(to_f64(dX[i]), ref.gradient(X[i].double().cpu().numpy(), G[i].double().cpu().numpy(), C5))
+        _say("  matrix", i, "error", f"{err:.2e}")
+        assert err <= 2.0 ** -8

@@ -128,3 +128,18 @@ def test_binding_refusals():
         mns.ns_orthogonalize_backward(X, X.clone(), C5, out=X)
     with pytest.raises(ValueError):
         mns.ns_orthogonalize_backward(X[0], X[0], C5)
+
+
+@pytest.mark.parametrize("rows,cols", [(300, 570), (570, 300), (257, 560), (64, 4096), (16, 12288),
+                                       (256, 256), (100, 700), (512, 512), (1024, 1024)])
+def test_workspace_of_a_batch_covers_its_last_chunk(rows, cols):
+    """Batches run in chunks of 32; a shorter last one may take another form, with buffers of
+    other sizes, on the same workspace."""
+    lib = mns.load()
+    out = ctypes.c_size_t()
+    for dtype in (_abi.MNS_F32, _abi.MNS_BF16):
+        def size(batch):
+            assert lib.mns_ns_backward_workspace_size(dtype, batch, rows, cols, ctypes.byref(out)) == 0
+            return out.value
+        for rest in range(1, 32):
+            assert size(32 + rest) >= max(size(32), size(rest))
