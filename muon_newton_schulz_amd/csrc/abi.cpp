@@ -1054,9 +1054,10 @@ struct NsbBuffers {
 // the n x n side; the update), for a third to a half more arithmetic. In us, eight launches against
 // three, float32 (the first and last on the general product, padded to 256): 256x1024 402 / 235,
 // 4 x 64x2048 589 / 517, 16 x 256x1024 861 / 953, 512x2048 639 / 535, 4 x 512x512 721 / 780. float16
-// (kernels of its own that stop at n, so that a small n counts for more; a third less error too,
-// k_nsb_square): 333x1111 303 / 161, 16 of them 761 / 709, 8 x 300x3000 759 / 607, 512x8192 465 / 397,
-// 4 x 512x2048 447 / 425, 8 x 512x1024 536 / 534, 3 x 512x4096 451 / 556, 16 x 512x512 522 / 712.
+// (kernels of its own that stop at n, so that a small n counts for more, and a third to a half of the
+// error, k_nsb_square and k_nsb_update, for which a few per cent of time are given up at the limit):
+// 333x1111 303 / 170, 16 of them 761 / 771, 8 x 300x3000 759 / 680, 512x8192 465 / 422, 4 x 512x2048
+// 447 / 451, 8 x 512x1024 536 / 563, 3 x 512x4096 451 / 556 and more, 16 x 512x512 522 / 712 and more.
 static bool nsb_fused(const Geo& g, int count) {
   if (g.n_p > 512) return false;
   if (g.elem != Elem::F16) return (double)count * g.n_p * g.n_p * (g.m_p + g.n_p) <= 8e8;
@@ -1073,7 +1074,8 @@ static size_t carve_nsb(void* base, const Geo& g, int count, NsbBuffers& b) {
   b.scale = cv.take<double>((size_t)count * 4);
   b.dot = cv.take<double>((size_t)count * nsb_dot_blocks(g.rows));
   b.ld_t = padded_ld(2 * g.n_p);
-  b.v_stride = 2 * g.n_p * g.ld_x;
+  const bool own = g.elem == Elem::F16 && nsb_fused(g, count);    // nsb_update: [E; X; dX]
+  b.v_stride = (own ? 3 : 2) * g.n_p * g.ld_x;
   b.vt_stride = g.m_p * b.ld_t;
   b.q_stride = g.n_p * g.ld_q;
   b.pq_stride = g.n_p * b.ld_t;
@@ -1082,7 +1084,7 @@ static size_t carve_nsb(void* base, const Geo& g, int count, NsbBuffers& b) {
     b.Vt[i] = cv.take<char>(es * count * b.vt_stride);
   }
   if (nsb_fused(g, count)) {
-    b.pq_stride *= g.elem == Elem::F16 ? 3 : 2;
+    b.pq_stride *= own ? 3 : 2;
     b.C2 = cv.take<char>(es * count * b.pq_stride);
   } else {
     b.A = cv.take<char>(es * count * b.q_stride);
@@ -1284,7 +1286,8 @@ static mns_status run_nsb_fused(const Geo& g, int c, const NsbBuffers& b, int T,
       MNS_HIP(timed("nsb_update", (last ? 4.0 : 6.0) * nn * g.m, 0.0, s, [&] {
         return nsb_update(b.PQ, b.ld_t, b.pq_stride, b.V[cur], g.ld_x, b.v_stride,
                           flip ? b.Vt[cur ^ 1] : b.V[cur ^ 1], flip ? b.ld_t : g.ld_x,
-                          flip ? b.vt_stride : b.v_stride, c, (int)g.n, n, g.m, m, last, flip, s); }));
+                          flip ? b.vt_stride : b.v_stride, c, (int)g.n, n, g.m, m, t == 0, last, flip,
+                          s); }));
       cur ^= 1;
       continue;
     }

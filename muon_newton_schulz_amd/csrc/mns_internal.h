@@ -227,11 +227,11 @@ hipError_t nsb_square(const void* C2, void* PQ, int64_t ld, int64_t stride, Elem
 // reads.
 hipError_t nsb_gram(const void* V, int64_t ldv, int64_t sV, void* C2, int64_t ld, int64_t stride,
                     int count, int n, int n_p, int64_t m, float alpha, hipStream_t s);
-// float16: [E'; X'] (out; only_e: E', transposed if trans) from that PQ and V = [E; X], both with X n_p
-// rows behind E, n x m in them; padding (to n_p, m_p: multiples of 128) is written as zeros.
+// float16: [E'; X'; dX'] (out; only_e: E', transposed if trans) from that PQ and V = [E; X; dX] (first:
+// [E; X]), n_p rows from block to block, n x m in them, dX = 2^11 (X less its float16 value); padding (to n_p, m_p: multiples of 128) is written as zeros.
 hipError_t nsb_update(const void* PQ, int64_t ld, int64_t stride, const void* V, int64_t ldv,
                       int64_t sV, void* out, int64_t ldo, int64_t sO, int count, int n, int n_p,
-                      int64_t m, int64_t m_p, bool only_e, bool trans, hipStream_t s);
+                      int64_t m, int64_t m_p, bool first, bool only_e, bool trans, hipStream_t s);
 // Matrices whose short side is at most 64 (kNsbSmall): one launch per iteration. V: [E; X], 128 x ld
 // floats per matrix, ld = m rounded up to 64; part: two buffers of blocks * 2 * 64 * 64 floats per
 // matrix; Et (tall): m x 64 floats per matrix, E_T as the tall matrix is stored.

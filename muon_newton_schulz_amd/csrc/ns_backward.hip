@@ -260,7 +260,8 @@ __global__ __launch_bounds__(kThreads) void k_symmetrise(const T* K, int64_t ldk
 // float16, for k_nsb_update,
 //   [ r P  r Q ; P  dP ; r dP ],   dP = 2^11 (P - its float16 value).
 // In P E + Q X the two terms cancel, which makes P's rounding the largest of an iteration (relative
-// error of the gradient at 3 x 1111x333, 1.7e-3 of it the output's own rounding: 2.6e-3 without dP).
+// error of the gradient at 3 x 1111x333, 1.7e-3 of it the output's own rounding: 2.6e-3 without dP, 2.1e-3
+// with it).
 // Where X_0 was scaled by a power of two, the first iteration's X is short of the normalised one by
 // a factor s in [1, 2): A by s^2 and S by s, and P and Q take s more for the X they multiply.
 // The row blocks go through LDS, whole 128-byte lines at a time, and each wave takes a fourth of
@@ -392,7 +393,7 @@ __global__ __launch_bounds__(256) void k_nsb_square(SquareArgs g) {
 // waves in two groups of four, 32 x 32 a wave, the groups taking k-tiles of 64 in turn: half as many
 // steps one after the other, which are what bounds it; their sums are added through LDS. Each group
 // has a ring of four LDS stages that DMA fills. 9 us on 3 x 1111x333, 18 on the general product and its
-// tail (the whole call, T = 5: 201 / 246; 2 x 257x300 142 / 170, 512x8192 398 / 394, 8 x 512x512 410 / 386).
+// tail (the whole call, T = 5, without dX: 201 / 246; 2 x 257x300 142 / 170, 512x8192 398 / 394, 8 x 512x512 410 / 386).
 struct GramArgs {
   const _Float16* V;         // [E; X]
   int64_t ldv, sV;
@@ -513,11 +514,14 @@ __global__ __launch_bounds__(512) void k_nsb_gram(GramArgs g) {
 }
 
 // The update of that form, float16:
-//   E' = r P E + r Q X,   X' = P X,   P as two float16 numbers.
+//   E' = r P E + r Q X,   X' = P X,   P, and X within its own update, as two float16 numbers (dX = 2^11 (X
+// less its float16 value), a third block of V; none in the first iteration): X's rounding, carried
+// from one iteration to the next, is what low-rank matrices amplify (2 x 284x1083, rank 64 plus noise:
+// 2.8e-3 with one, 1.8e-3 with two, 1.7e-3 of it the output's own).
 // Tiles of BT x BT (128: eight waves of 32 x 64; 64, where there are few tiles: four of 32 x 32),
 // k-tiles of 64 in a ring of four LDS stages that DMA fills, one barrier each; operands as in
 // grouped.hip's ring kernel (V is read along the output, through the transposing LDS load). The
-// small part of P comes first and is scaled down before the rest is added. Tiles of the padding are
+// small parts come first and are scaled down before the rest is added. Tiles of the padding are
 // zeros, without a product, and the k-tiles stop at n. TRANS (the last iteration of tall matrices): E'
 // alone, transposed. 17 us on 3 x 1111x333 (18 dependent k-tiles of about 0.7 us; the padded
 // product on the general GEMM, one part of P, 14 us and 7 for joining its parts).
@@ -525,13 +529,14 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 struct UpdateArgs {
   const _Float16* PQ;        // of k_nsb_square, 3 n_p rows
   int64_t ld, stride;
-  const _Float16* V;         // [E; X]
+  const _Float16* V;         // [E; X; dX]
   int64_t ldv, sV;
-  _Float16* out;             // [E'; X'], or E'^T
+  _Float16* out;             // [E'; X'; dX'], or E'^T
   int64_t ldo, sO;
   int n, n_p;
   int64_t m;
   int row_tiles, col_tiles, columns;   // row tiles of E' and X'; columns of tiles of all matrices
+  int first;                 // no dX
 };
 
 template <int BT, bool TRANS>
@@ -550,7 +555,8 @@ __global__ __launch_bounds__(4 * BT) void k_nsb_update(UpdateArgs g) {
   const int i0 = (down - (x_rows ? row_tiles : 0)) * BT, j0 = column % g.col_tiles * BT;
   const int64_t b = column / g.col_tiles;
   const int per = (g.n + 63) / 64;                   // k-tiles of a product of depth n
-  const int KL = i0 >= g.n || j0 >= g.m ? 0 : x_rows ? 2 * per : 3 * per;
+  const int KL = i0 >= g.n || j0 >= g.m ? 0 : x_rows && g.first ? 2 * per : 3 * per;
+  const int small = x_rows && !g.first ? 2 * per : per;        // k-tiles of the small parts
   const int ld = (int)g.ld, ldv = (int)g.ldv;
 
   floatx16 acc[FN];
@@ -561,7 +567,7 @@ __global__ __launch_bounds__(4 * BT) void k_nsb_update(UpdateArgs g) {
   if (KL > 0) {
     const __amdgpu_buffer_rsrc_t rA =
         make_rsrc(g.PQ + b * g.stride, (int64_t)3 * g.n_p * g.ld * 2);
-    const __amdgpu_buffer_rsrc_t rB = make_rsrc(g.V + b * g.sV, (int64_t)2 * g.n_p * g.ldv * 2);
+    const __amdgpu_buffer_rsrc_t rB = make_rsrc(g.V + b * g.sV, (int64_t)3 * g.n_p * g.ldv * 2);
     const __amdgpu_buffer_rsrc_t none = make_rsrc(g.PQ, 0);    // reads zeros from nowhere
     int offA[2], offB[2];
 #pragma unroll
@@ -575,12 +581,12 @@ __global__ __launch_bounds__(4 * BT) void k_nsb_update(UpdateArgs g) {
     auto issue = [&](int kt, int st) {
       const bool real = kt < KL;
       const __amdgpu_buffer_rsrc_t a = real ? rA : none, v = real ? rB : none;
-      // E': r dP E, r P E, r Q X; X': dP X, P X
+      // E': r dP E, r P E, r Q X; X': dP X, P dX (not in the first iteration), P X
       const int seg = kt >= 2 * per ? 2 : kt >= per ? 1 : 0;
       const int k = (kt - seg * per) * 64;
       const int ar = x_rows ? g.n_p : seg == 0 ? 2 * g.n_p : 0;
       const int ac = x_rows ? (seg == 0 ? g.n_p : 0) : seg == 2 ? g.n_p : 0;
-      const int vr = x_rows || seg == 2 ? g.n_p : 0;
+      const int vr = x_rows ? (seg == 1 && !g.first ? 2 * g.n_p : g.n_p) : seg == 2 ? g.n_p : 0;
       const int oa = real ? ((ar + i0) * ld + ac + k) * 2 : 0;
       const int ov = real ? ((vr + k) * ldv + j0) * 2 : 0;
 #pragma unroll
@@ -635,7 +641,7 @@ __global__ __launch_bounds__(4 * BT) void k_nsb_update(UpdateArgs g) {
         for (int ks = 0; ks < 4; ++ks)
           v[ks][j] = u32x4{t[2 * ks].x, t[2 * ks].y, t[2 * ks + 1].x, t[2 * ks + 1].y};
       }
-      if (kt == per) {
+      if (kt == small) {
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
@@ -664,10 +670,14 @@ __global__ __launch_bounds__(4 * BT) void k_nsb_update(UpdateArgs g) {
                                : ((x_rows ? g.n_p : 0) + r + one) * g.ldo + c + four);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      half4 h;
+      half4 h, d;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = (_Float16)acc[j][4 * q + e];
+      for (int e = 0; e < 4; ++e) {
+        h[e] = (_Float16)acc[j][4 * q + e];
+        d[e] = (_Float16)(2048.f * (acc[j][4 * q + e] - (float)h[e]));
+      }
       *reinterpret_cast<half4*>(o + 8 * q) = h;
+      if (x_rows) *reinterpret_cast<half4*>(o + g.n_p * g.ldo + 8 * q) = d;
     }
   }
 }
@@ -1026,15 +1036,17 @@ hipError_t nsb_gram(const void* V, int64_t ldv, int64_t sV, void* C2, int64_t ld
 
 hipError_t nsb_update(const void* PQ, int64_t ld, int64_t stride, const void* V, int64_t ldv,
                       int64_t sV, void* out, int64_t ldo, int64_t sO, int count, int n, int n_p,
-                      int64_t m, int64_t m_p, bool only_e, bool trans, hipStream_t s) {
-  // 64 x 64 where the products fill at most 100 tiles of 128 x 128 (the whole call, T = 5, us, 64 / 128:
+                      int64_t m, int64_t m_p, bool first, bool only_e, bool trans, hipStream_t s) {
+  // 64 x 64 where the products fill at most 100 tiles of 128 x 128 (the whole call, T = 5, before dX and
+  // k_nsb_gram, us, 64 / 128:
   // 512x512 173 / 208, three of them 234 / 246, 333x1111 184 / 199; two of those, 108 tiles, 244 / 238,
   // 2 x 512x2048 315 / 283)
   const int64_t live = (int64_t)((n + 127) / 128) * ((m + 127) / 128) * 2 * count;
   const int bt = live <= 100 ? 64 : 128;
   const int rt = n_p / bt * (only_e ? 1 : 2), ct = (int)(m_p / bt);
   const UpdateArgs g{static_cast<const _Float16*>(PQ), ld, stride, static_cast<const _Float16*>(V),
-                     ldv, sV, static_cast<_Float16*>(out), ldo, sO, n, n_p, m, rt, ct, ct * count};
+                     ldv, sV, static_cast<_Float16*>(out), ldo, sO, n, n_p, m, rt, ct, ct * count,
+                     first};
   const dim3 grid((unsigned)((ct * count + 7) / 8 * 8 * rt)), block(4 * bt);
   if (bt == 64) {
     if (trans) hipLaunchKernelGGL((k_nsb_update<64, true>), grid, block, 0, s, g);
