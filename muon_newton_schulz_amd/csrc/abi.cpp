@@ -1277,17 +1277,18 @@ static mns_status run_nsb_fused(const Geo& g, int c, const NsbBuffers& b, int T,
     // E' times sc[t + 1].e; Q X comes with e / S (of K) times S (of X): e, as P E does
     const float r = (float)(sc[t + 1].e / sc[t].e);
     const double gr = sc[t].gram;
+    const double p = f16 ? sc[t].p / (r > 1.0f ? r : 1.0f) : 1.0;          // a power of two
     MNS_HIP(timed("nsb_square", 3.0 * nn * g.n, 0.0, s, [&] {
       return nsb_square(b.C2, b.PQ, b.ld_t, b.pq_stride, g.elem, c, (int)g.n, n, abc[3 * t],
                         (float)(abc[3 * t + 1] / gr), (float)(abc[3 * t + 2] / (gr * gr)), r,
-                        t == 0 && f16 ? b.scale : nullptr, g.S, s); }));
+                        (float)p, t == 0 && f16 ? b.scale : nullptr, g.S, s); }));
     if (f16) {
       const bool flip = last && g.tall;
       MNS_HIP(timed("nsb_update", (last ? 4.0 : 6.0) * nn * g.m, 0.0, s, [&] {
         return nsb_update(b.PQ, b.ld_t, b.pq_stride, b.V[cur], g.ld_x, b.v_stride,
                           flip ? b.Vt[cur ^ 1] : b.V[cur ^ 1], flip ? b.ld_t : g.ld_x,
-                          flip ? b.vt_stride : b.v_stride, c, (int)g.n, n, g.m, m, t == 0, last, flip,
-                          s); }));
+                          flip ? b.vt_stride : b.v_stride, c, (int)g.n, n, g.m, m, (float)(1.0 / p),
+                          t == 0, last, flip, s); }));
       cur ^= 1;
       continue;
     }

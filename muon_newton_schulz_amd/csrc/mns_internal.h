@@ -217,21 +217,22 @@ hipError_t symmetrise(const void* K, int64_t ldk, int64_t sK, const void* D, int
                       int64_t sD, void* C, int64_t ldc, int64_t sC, Elem e, int count, int64_t n_p,
                       float beta, float gamma, hipStream_t s);
 // The n x n side of an iteration at once: from C2 = [E; X] [E; X]^T (2 n_p square, pitch ld, matrix
-// stride `stride`) to PQ: float32 [r P, r Q; 0, P], float16 [r P, r Q; P, dP; r dP, -] with dP = 2^11 (P
-// less its float16 value). P = a I + b A + c A^2 (I on the first n), Q = b S + c (A S + S A), A and S =
+// stride `stride`) to PQ: float32 [r P, r Q; 0, P], float16 p [r P, r Q; P, dP; r dP, -] with dP = 2^11
+// (P less its float16 value). P = a I + b A + c A^2 (I on the first n), Q = b S + c (A S + S A), A and S =
 // K + K^T the blocks of C2. scale: nsb_scales' with exact, in the first iteration, else null.
 hipError_t nsb_square(const void* C2, void* PQ, int64_t ld, int64_t stride, Elem e, int count, int n,
-                      int n_p, float a, float b, float c, float r, const double* scale, double S,
-                      hipStream_t s);
+                      int n_p, float a, float b, float c, float r, float p, const double* scale,
+                      double S, hipStream_t s);
 // float16, C2 for nsb_square from V = [E; X] (X n_p rows behind E) times alpha: A, K and K^T, as far as it
 // reads.
 hipError_t nsb_gram(const void* V, int64_t ldv, int64_t sV, void* C2, int64_t ld, int64_t stride,
                     int count, int n, int n_p, int64_t m, float alpha, hipStream_t s);
 // float16: [E'; X'; dX'] (out; only_e: E', transposed if trans) from that PQ and V = [E; X; dX] (first:
-// [E; X]), n_p rows from block to block, n x m in them, dX = 2^11 (X less its float16 value); padding (to n_p, m_p: multiples of 128) is written as zeros.
+// [E; X]) times inv (1 / p), n_p rows from block to block, n x m in them, dX = 2^11 (X less its float16 value); padding (to n_p, m_p: multiples of 128) is written as zeros.
 hipError_t nsb_update(const void* PQ, int64_t ld, int64_t stride, const void* V, int64_t ldv,
                       int64_t sV, void* out, int64_t ldo, int64_t sO, int count, int n, int n_p,
-                      int64_t m, int64_t m_p, bool first, bool only_e, bool trans, hipStream_t s);
+                      int64_t m, int64_t m_p, float inv, bool first, bool only_e, bool trans,
+                      hipStream_t s);
 // Matrices whose short side is at most 64 (kNsbSmall): one launch per iteration. V: [E; X], 128 x ld
 // floats per matrix, ld = m rounded up to 64; part: two buffers of blocks * 2 * 64 * 64 floats per
 // matrix; Et (tall): m x 64 floats per matrix, E_T as the tall matrix is stored.

@@ -258,7 +258,7 @@ __global__ __launch_bounds__(kThreads) void k_symmetrise(const T* K, int64_t ldk
 // the operand of the update: float32
 //   [ r P  r Q ; 0  P ],
 // float16, for k_nsb_update,
-//   [ r P  r Q ; P  dP ; r dP ],   dP = 2^11 (P - its float16 value).
+//   [ r P  r Q ; P  dP ; r dP ],   dP = 2^11 (P - its float16 value), all times p.
 // In P E + Q X the two terms cancel, which makes P's rounding the largest of an iteration (relative
 // error of the gradient at 3 x 1111x333, 1.7e-3 of it the output's own rounding: 2.6e-3 without dP, 2.1e-3
 // with it).
@@ -288,7 +288,7 @@ struct SquareArgs {
   int64_t ld, stride;        // of both (elements)
   int n, n_p;
   int tiles;                 // of 32 rows: up to n_p; float16: as far as k_nsb_update reads
-  float a, b, c, r;
+  float a, b, c, r, p;
   const double* scale;       // k_nsb_scales' (exact), in the first iteration
   double S;
 };
@@ -367,12 +367,13 @@ __global__ __launch_bounds__(256) void k_nsb_square(SquareArgs g) {
     const float qs = part[0][1][x][lane] + part[1][1][x][lane] + part[2][1][x][lane] + part[3][1][x][lane];
     float p = b * (float)av[e] + c * ps;
     if (i == j + e && i < g.n) p += g.a;
+    p *= g.p;
     const float rp = g.r * p, sp = s * p;
     p1[e] = (T)rp;
     p2[e] = (T)sp;
     rlo[e] = (T)(2048.f * (rp - (float)p1[e]));
     lo[e] = (T)(2048.f * (sp - (float)p2[e]));
-    q[e] = (T)(g.r * (b * (float)(kv[e] + kt[e]) + c * qs));
+    q[e] = (T)(g.r * g.p * (b * (float)(kv[e] + kt[e]) + c * qs));
   }
   T* top = PQ + i * g.ld + j;
   T* low = top + g.n_p * g.ld;
@@ -537,6 +538,7 @@ struct UpdateArgs {
   int64_t m;
   int row_tiles, col_tiles, columns;   // row tiles of E' and X'; columns of tiles of all matrices
   int first;                 // no dX
+  float inv;                 // 1 / p
 };
 
 template <int BT, bool TRANS>
@@ -673,8 +675,9 @@ __global__ __launch_bounds__(4 * BT) void k_nsb_update(UpdateArgs g) {
       half4 h, d;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        h[e] = (_Float16)acc[j][4 * q + e];
-        d[e] = (_Float16)(2048.f * (acc[j][4 * q + e] - (float)h[e]));
+        const float v = acc[j][4 * q + e] * g.inv;
+        h[e] = (_Float16)v;
+        d[e] = (_Float16)(2048.f * (v - (float)h[e]));
       }
       *reinterpret_cast<half4*>(o + 8 * q) = h;
       if (x_rows) *reinterpret_cast<half4*>(o + g.n_p * g.ldo + 8 * q) = d;
@@ -1015,10 +1018,10 @@ hipError_t symmetrise(const void* K, int64_t ldk, int64_t sK, const void* D, int
 }
 
 hipError_t nsb_square(const void* C2, void* PQ, int64_t ld, int64_t stride, Elem e, int count, int n,
-                      int n_p, float a, float b, float c, float r, const double* scale, double S,
-                      hipStream_t s) {
+                      int n_p, float a, float b, float c, float r, float p, const double* scale,
+                      double S, hipStream_t s) {
   const int tiles = (e == Elem::F16 ? (n + 127) / 128 * 128 : n_p) / 32;
-  const SquareArgs g{C2, PQ, ld, stride, n, n_p, tiles, a, b, c, r, scale, S};
+  const SquareArgs g{C2, PQ, ld, stride, n, n_p, tiles, a, b, c, r, p, scale, S};
   const dim3 grid(tiles * tiles, count);
   if (e == Elem::F16) hipLaunchKernelGGL(k_nsb_square<_Float16>, grid, dim3(256), 0, s, g);
   else hipLaunchKernelGGL(k_nsb_square<float>, grid, dim3(256), 0, s, g);
@@ -1036,7 +1039,8 @@ hipError_t nsb_gram(const void* V, int64_t ldv, int64_t sV, void* C2, int64_t ld
 
 hipError_t nsb_update(const void* PQ, int64_t ld, int64_t stride, const void* V, int64_t ldv,
                       int64_t sV, void* out, int64_t ldo, int64_t sO, int count, int n, int n_p,
-                      int64_t m, int64_t m_p, bool first, bool only_e, bool trans, hipStream_t s) {
+                      int64_t m, int64_t m_p, float inv, bool first, bool only_e, bool trans,
+                      hipStream_t s) {
   // 64 x 64 where the products fill at most 100 tiles of 128 x 128 (the whole call, T = 5, before dX and
   // k_nsb_gram, us, 64 / 128:
   // 512x512 173 / 208, three of them 234 / 246, 333x1111 184 / 199; two of those, 108 tiles, 244 / 238,
@@ -1046,7 +1050,7 @@ hipError_t nsb_update(const void* PQ, int64_t ld, int64_t stride, const void* V,
   const int rt = n_p / bt * (only_e ? 1 : 2), ct = (int)(m_p / bt);
   const UpdateArgs g{static_cast<const _Float16*>(PQ), ld, stride, static_cast<const _Float16*>(V),
                      ldv, sV, static_cast<_Float16*>(out), ldo, sO, n, n_p, m, rt, ct, ct * count,
-                     first};
+                     first, inv};
   const dim3 grid((unsigned)((ct * count + 7) / 8 * 8 * rt)), block(4 * bt);
   if (bt == 64) {
     if (trans) hipLaunchKernelGGL((k_nsb_update<64, true>), grid, block, 0, s, g);

@@ -206,3 +206,23 @@ def test_last_chunk_of_another_form():
         err = rel(to_f64(dX[i]), ref.gradient(X[i].double().cpu().numpy(), G[i].double().cpu().numpy(), C5))
         _say("  matrix", i, "error", f"{err:.2e}")
         assert err <= 2.0 ** -8
+
+
+@pytest.mark.parametrize("coeffs", [[(70000.0, -1000.0, 0.0)], [(300.0, -500.0, 210.0), (1.5, -0.5, 0.0)],
+                                    [(0.01, 0.0, 0.0), (100.0, 3.0, 0.0)], [(1e-3, 0.5, -0.25)] * 2],
+                         ids=["large", "cancelling", "shrinking", "small"])
+def test_coefficients_of_odd_sizes(coeffs):
+    """Coefficients whose P passes float16's range, or whose iterations shrink a direction and let it
+    grow again, in both forms of the float16 arithmetic and in float32."""
+    for storage, batch, rows, cols in (("bf16", 1, 300, 500), ("bf16", 1, 900, 600), ("f32", 1, 130, 200)):
+        X, G, xs, gs = _batch("normal", batch, rows, cols, storage, 71)
+        if storage == "bf16" and coeffs[0][0] == 300.0:
+            # f_1 reaches 94.1 and f_2 = 1.5 f_1 - 0.5 f_1^3 has the slope (1.5 - 1.5 f_1^2) f_1':
+            # a direction grows 1.5e6 times, more than the 2^20 that float16 takes
+            with pytest.raises(mns._abi.MnsError):
+                mns.ns_orthogonalize_backward(X, G, coeffs)
+            continue
+        dX = mns.ns_orthogonalize_backward(X, G, coeffs)
+        err = rel(to_f64(dX[0]), ref.gradient(xs[0], gs[0], coeffs))
+        _say("case", storage, rows, cols, coeffs, f"error {err:.2e}")
+        assert err <= TOL[storage]
