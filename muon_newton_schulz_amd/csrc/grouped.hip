@@ -1497,10 +1497,12 @@ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // What the DMA kernels assume: bfloat16, 16-byte aligned operands and row pitches, a whole number of
 // k-tiles (the weight gradient's reduction may end anywhere), and for W read along the output one
-// expert's matrix below 2 GiB.
+// expert's matrix below 2 GiB. The weight gradient's resources end with the last row's last element,
+// and the hardware checks a load dword by dword: one that an odd width ends inside of would read as
+// zero, last element and all, so its widths are even.
 bool dma_ok(const GroupedDesc& d) {
   if (d.store != Store::BF16 || !on16(d.A) || !on16(d.B) || d.lda % 8) return false;
-  if (d.weight_grad) return d.ldb % 8 == 0;
+  if (d.weight_grad) return d.ldb % 8 == 0 && d.n % 2 == 0 && d.k % 2 == 0;
   const int64_t red = d.transpose_w ? d.n : d.k;
   return red % 64 == 0 && red >= 128 && d.k % 8 == 0 && (d.n * d.k) % 8 == 0 &&
          d.n * d.k < (int64_t(1) << 30);

@@ -380,3 +380,27 @@ def test_no_rows_but_a_workspace():
     C = _rand((2, 256, 256), F32, 1)
     G = mns.grouped_weight_grad(empty, empty, off, C=C, beta=2.0)
     assert torch.equal(G, 2.0 * C)
+
+
+@pytest.mark.parametrize("n,k", [(257, 260), (258, 257), (260, 262), (258, 1000), (1, 264)])
+@pytest.mark.parametrize("sizes", [[0, 1, 70, 300], [1500], [40, 0, 2]])
+def test_weight_gradients_of_widths_inside_an_aligned_pitch(n, k, sizes):
+    """Columns of wider, 16-byte aligned rows: the width ends inside a 16-byte piece, an odd one inside
+    a dword. Every expert's last row and the last columns count; what lies behind them (NaN) does
+    not. [1500] is computed in parts where the widths are even."""
+    bounds = ref.bounds_of(sizes, 2)
+    rows, e, off = bounds[-1] + 3, len(sizes), _offsets(bounds)
+    print("case", n, k, sizes, flush=True)
+
+    def columns(width, seed):
+        pitch = (width + 15) // 8 * 8
+        buf = torch.full((rows, pitch), float("nan"), dtype=BF, device="cuda")
+        buf[:, :width] = _rand((rows, width), BF, seed)
+        return buf[:, :width]
+
+    dY, X = columns(n, 1), columns(k, 2)
+    for out_dtype in (BF, F32):
+        C = _rand((e, n, k), out_dtype, 3)
+        for c, beta in ((None, 0.0), (C, 0.5)):
+            G = mns.grouped_weight_grad(dY, X, off, C=c, beta=beta, out_dtype=out_dtype)
+            ref.check(G, *ref.weight_grad(dY, X, bounds, c, beta, out_dtype), (n, k, sizes, out_dtype))
