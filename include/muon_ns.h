@@ -184,9 +184,10 @@ mns_status mns_ns_backward_workspace_size(int dtype, int64_t batch, int64_t rows
  * gradient is the derivative in the direction dO, carried along the iteration, and no iterate is
  * stored. A zero X or a zero dO gives dX = 0.
  *   Arithmetic: float32 for MNS_F32, and for MNS_BF16 when min(rows, cols) <= 256; else float16
- *   products with float32 sums, every quantity scaled by a power of two that its bound over the
- *   iterations keeps in range. MNS_ERR_PARAM when the coefficients amplify a direction more than
- *   2^20 times (float16; T = 10 with (3.4445, -4.775, 2.0315) still runs) or 10^30 times.
+ *   products with float32 sums. Every stored quantity, the iterate among them, is scaled by a power
+ *   of two from its bound over the iterations, so that coefficients may take it far above or below 1.
+ *   MNS_ERR_PARAM when they amplify a direction more than 2^20 times (float16; T = 10 with (3.4445,
+ *   -4.775, 2.0315) still runs) or 10^30 times, or when the terms of an update can pass 10^37.
  *   Sizes: as above, with the iterate counted twice (direction and iterate are stored together),
  *   else MNS_ERR_SHAPE. */
 mns_status ns_orthogonalize_backward(const void* X, const void* dO, void* dX, int dtype,

@@ -1023,6 +1023,8 @@ constexpr int64_t kNsbF32Short = 256;
 // Largest growth of a direction over the iterations that float16 can carry (2^14 of headroom
 // above 1, 2^6 below the smallest value that matters).
 constexpr double kNsbGrowthF16 = 1048576.0, kNsbGrowthF32 = 1e30;
+// Largest sum of the terms of an update, P E + Q X, that its float32 sums can hold.
+constexpr double kNsbTerms = 1e37;
 
 static Geo nsb_geo(int64_t rows, int64_t cols, Store st) {
   Geo g = make_geo(rows, cols, st);
@@ -1153,21 +1155,39 @@ static size_t nsb_need(const Geo& g, int64_t batch) {
   return full > last ? full : last;
 }
 
-// Powers of two that scale the stored quantities of one iteration: E by e, S and A S by kap, P by
-// p, Q by q = p e / S (so that P E and Q X add up), with the bounds below 2^14.
+// Powers of two that scale the stored quantities of one iteration: E by e, X by S / u (u the power
+// of two below the largest singular value it can have, 1 where that lies within a factor of 8 of 1),
+// S and A S by kap, P by p, Q by q = p e / S (so that P E and Q X add up), with the bounds below 2^14.
+// b and c are the coefficients for the iterate over u, b u^2 and c u^4; x is u over the next iteration's.
 // gram (run_nsb_fused): of A, and of K on top of e / S, so that float16 holds A's small entries.
 struct NsbScale {
-  double e, kap, p, q, gram;
+  double e, kap, p, q, gram, b, c, x;
 };
+
+// Largest |x (a + b x^2 + c x^4)| for x in [0, s]: at s or where a + 3 b y + 5 c y^2 = 0, y = x^2.
+static double poly_range(double s, double a, double b, double c) {
+  double top = std::fabs(s * (a + s * s * (b + s * s * c)));
+  const double disc = 9.0 * b * b - 20.0 * a * c;
+  if (!(disc >= 0.0)) return top;
+  const double w = -1.5 * b - std::copysign(0.5 * std::sqrt(disc), b);      // 5 c y = w or a = w y
+  for (const double y : {w / (5.0 * c), a / w}) {
+    if (!(y > 0.0 && y < s * s)) continue;                                  // (none where c or w is 0)
+    const double v = std::fabs(std::sqrt(y) * (a + y * (b + y * c)));
+    if (v > top) top = v;
+  }
+  return top;
+}
 
 // The scales of the T iterations and of the final direction, sc[T].e. A direction of norm 1 grows
 // to at most L_t = max over s in [0, 1] of |f_t'(s)| and |f_t(s) / s| (the factors of the
-// derivative of the composed polynomial f_t), and the singular values to sup |f_t|. False when L
-// leaves the range of the arithmetic.
+// derivative of the composed polynomial f_t), and the singular values to sup |f_t|; f_t takes [0, 1] to
+// all of [0, sup |f_t|] in magnitude, so the next sup is a single polynomial's. False when L or the
+// terms of an update leave the range of the arithmetic.
 static bool nsb_plan(int T, const float* abc, const Geo& g, NsbScale* sc) {
   const bool f16 = g.elem == Elem::F16;
   constexpr int kGrid = 2048;
-  double L = 1.0, sup = 1.0;
+  constexpr double kLeast = 0x1p-100;      // of L and of u over the one before: all may be gone
+  double L = 1.0, sup = 1.0, u = 1.0;
   double f[kGrid], d[kGrid];
   for (int i = 0; i < kGrid; ++i) {
     f[i] = (i + 1.0) / kGrid;
@@ -1176,39 +1196,47 @@ static bool nsb_plan(int T, const float* abc, const Geo& g, NsbScale* sc) {
   double slope0 = 1.0;       // f_t'(0)
   for (int t = 0; t <= T; ++t) {
     const double lim = 16384.0;
-    sc[t] = NsbScale{1.0, 1.0, 1.0, 1.0, 1.0};
+    sc[t] = NsbScale{1.0, 1.0, 1.0, 1.0, 1.0, 0.0, 0.0, 1.0};
     if (!std::isfinite(L) || !std::isfinite(sup) || L > (f16 ? kNsbGrowthF16 : kNsbGrowthF32))
       return false;
     if (f16) sc[t].e = pow2_floor(lim / L);
     if (t == T) break;
-    const double a = abc[3 * t], b = abc[3 * t + 1], c = abc[3 * t + 2];
+    const double a = abc[3 * t], b0 = abc[3 * t + 1], c0 = abc[3 * t + 2];
+    const double b = b0 * u * u, c = c0 * u * u * u * u, top = sup / u;
+    sc[t].b = b;
+    sc[t].c = c;
+    const double s2 = top * top;
+    const double pmax = std::fabs(a) + std::fabs(b) * s2 + std::fabs(c) * s2 * s2;
+    const double qmax = (std::fabs(b) + 2.0 * std::fabs(c) * s2) * 2.0 * L * top;
+    if (!(pmax * (L > 1.0 ? L : 1.0) + qmax * top < kNsbTerms)) return false;
     if (f16) {
-      const double s2 = sup * sup;
       const double big = s2 > 1.0 ? s2 : 1.0;
-      sc[t].kap = pow2_floor(lim / (2.0 * L * (sup > 1.0 ? sup : 1.0) * big));
-      const double pmax = std::fabs(a) + std::fabs(b) * s2 + std::fabs(c) * s2 * s2;
-      const double qmax = (std::fabs(b) + 2.0 * std::fabs(c) * s2) * 2.0 * L * sup;
+      sc[t].kap = pow2_floor(lim / (2.0 * L * (top > 1.0 ? top : 1.0) * big));
       double p = 256.0;
-      if (p * pmax > lim) p = pow2_floor(lim / pmax);
+      if (p * pmax > lim || (pmax > 0.0 && p * pmax < 1.0)) p = pow2_floor(lim / pmax);
       if (p * sc[t].e / g.S * qmax > lim) p = pow2_floor(lim * g.S / (sc[t].e * qmax));
       sc[t].p = p;
       sc[t].q = p * sc[t].e / g.S;
-      // K <= e L sup gram / S <= 2^14, A <= sup S
-      sc[t].gram = pow2_floor(g.S / (sup > 1.0 ? sup : 1.0));
+      // K <= e L top gram / S <= 2^14, A <= top S
+      sc[t].gram = pow2_floor(g.S / (top > 1.0 ? top : 1.0));
     }
     slope0 *= a;
-    L = std::fabs(slope0) > 1.0 ? std::fabs(slope0) : 1.0;
-    sup = 0.0;
+    L = std::fabs(slope0) > kLeast ? std::fabs(slope0) : kLeast;
     for (int i = 0; i < kGrid; ++i) {
       const double x = f[i], x2 = x * x;
-      f[i] = x * (a + x2 * (b + x2 * c));
-      d[i] *= a + x2 * (3.0 * b + x2 * 5.0 * c);
+      f[i] = x * (a + x2 * (b0 + x2 * c0));
+      d[i] *= a + x2 * (3.0 * b0 + x2 * 5.0 * c0);
       const double s = (i + 1.0) / kGrid;
       if (std::fabs(d[i]) > L) L = std::fabs(d[i]);
       if (std::fabs(f[i]) / s > L) L = std::fabs(f[i]) / s;
-      if (std::fabs(f[i]) > sup) sup = std::fabs(f[i]);
       if (!std::isfinite(f[i]) || !std::isfinite(d[i])) return false;
     }
+    sup = poly_range(sup, a, b0, c0);
+    double next = 1.0;
+    if (sup > 0.0 && !(sup > 0.125 && sup < 8.0)) next = pow2_floor(sup);
+    if (next < u * kLeast) next = u * kLeast;
+    if (t < T - 1) sc[t].x = u / next;
+    u = next;
   }
   return true;
 }
@@ -1277,10 +1305,11 @@ static mns_status run_nsb_fused(const Geo& g, int c, const NsbBuffers& b, int T,
     // E' times sc[t + 1].e; Q X comes with e / S (of K) times S (of X): e, as P E does
     const float r = (float)(sc[t + 1].e / sc[t].e);
     const double gr = sc[t].gram;
-    const double p = f16 ? sc[t].p / (r > 1.0f ? r : 1.0f) : 1.0;          // a power of two
+    const double wide = r > sc[t].x ? r : sc[t].x;
+    const double p = f16 ? sc[t].p / wide : 1.0;                           // a power of two
     MNS_HIP(timed("nsb_square", 3.0 * nn * g.n, 0.0, s, [&] {
       return nsb_square(b.C2, b.PQ, b.ld_t, b.pq_stride, g.elem, c, (int)g.n, n, abc[3 * t],
-                        (float)(abc[3 * t + 1] / gr), (float)(abc[3 * t + 2] / (gr * gr)), r,
+                        (float)(sc[t].b / gr), (float)(sc[t].c / (gr * gr)), r, (float)sc[t].x,
                         (float)p, t == 0 && f16 ? b.scale : nullptr, g.S, s); }));
     if (f16) {
       const bool flip = last && g.tall;
@@ -1366,7 +1395,7 @@ static mns_status run_nsb(const Geo& g, int c, const NsbBuffers& b, int T, const
   int cur = 0;
   for (int t = 0; t < T; ++t) {
     const bool last = t == T - 1;
-    const double a = abc[3 * t], bb = abc[3 * t + 1], cc = abc[3 * t + 2];
+    const double a = abc[3 * t], bb = sc[t].b, cc = sc[t].c;
     const void* E = b.V[cur];
     const void* X = at(b.V[cur], xoff);
     GemmDesc gram = square(X, X, g.ld_x, b.v_stride, m, b.A);
@@ -1399,7 +1428,7 @@ static mns_status run_nsb(const Geo& g, int c, const NsbBuffers& b, int T, const
     MNS_HIP(timed_gemm(dir, 4.0 * nn * g.m, s));
     if (!last) {
       GemmDesc upd = update(false, cur, km, false);
-      upd.alpha = (float)(1.0 / sc[t].p);
+      upd.alpha = (float)(sc[t].x / sc[t].p);
       MNS_HIP(timed_gemm(upd, 2.0 * nn * g.m, s));
     }
     cur ^= 1;
@@ -1460,8 +1489,8 @@ mns_status ns_orthogonalize_backward(const void* X, const void* dO, void* dX, in
       const double nn = (double)c * g.n * g.n;
       for (int t = 0; t < T; ++t)
         MNS_HIP(timed("nsb_small_step", nn * (9.0 * g.m + 3.0 * g.n), 0, s, [&] {
-          return nsb_small_step(small, t, t == T - 1, abc[3 * t], abc[3 * t + 1], abc[3 * t + 2],
-                                s); }));
+          return nsb_small_step(small, t, t == T - 1, abc[3 * t], (float)sc[t].b, (float)sc[t].c,
+                                (float)sc[t].x, s); }));
       MNS_HIP(timed("nsb_finish", 0, all * (3.0 * ss + 2.0 * es), s, [&] {
         return nsb_finish(x, sto, g.tall ? small.Et : small.V, Elem::F32, c, rows, cols,
                           g.tall ? 64 : small.ld, g.tall ? g.m * 64 : 128 * small.ld, b.dot,

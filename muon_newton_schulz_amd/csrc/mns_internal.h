@@ -217,12 +217,12 @@ hipError_t symmetrise(const void* K, int64_t ldk, int64_t sK, const void* D, int
                       int64_t sD, void* C, int64_t ldc, int64_t sC, Elem e, int count, int64_t n_p,
                       float beta, float gamma, hipStream_t s);
 // The n x n side of an iteration at once: from C2 = [E; X] [E; X]^T (2 n_p square, pitch ld, matrix
-// stride `stride`) to PQ: float32 [r P, r Q; 0, P], float16 p [r P, r Q; P, dP; r dP, -] with dP = 2^11
+// stride `stride`) to PQ: float32 [r P, r Q; 0, x P], float16 p [r P, r Q; x P, x dP; r dP, -] with dP = 2^11
 // (P less its float16 value). P = a I + b A + c A^2 (I on the first n), Q = b S + c (A S + S A), A and S =
 // K + K^T the blocks of C2. scale: nsb_scales' with exact, in the first iteration, else null.
 hipError_t nsb_square(const void* C2, void* PQ, int64_t ld, int64_t stride, Elem e, int count, int n,
-                      int n_p, float a, float b, float c, float r, float p, const double* scale,
-                      double S, hipStream_t s);
+                      int n_p, float a, float b, float c, float r, float x, float p,
+                      const double* scale, double S, hipStream_t s);
 // float16, C2 for nsb_square from V = [E; X] (X n_p rows behind E) times alpha: A, K and K^T, as far as it
 // reads.
 hipError_t nsb_gram(const void* V, int64_t ldv, int64_t sV, void* C2, int64_t ld, int64_t stride,
@@ -247,8 +247,9 @@ struct NsbSmall {
 };
 hipError_t nsb_small_load(const NsbSmall& d, const void* X, const void* G, Store st,
                           const double* scale, hipStream_t s);
+// (x: of the new X, a power of two)
 hipError_t nsb_small_step(const NsbSmall& d, int t, bool last_step, float a, float b, float c,
-                          hipStream_t s);
+                          float x, hipStream_t s);
 // out = (E' - X_0 <X_0, E'>) / ||X|| with E' = E ||dO|| inv_eT, E in the stored layout (row pitch
 // ld, matrix stride sE). part: count * nsb_dot_blocks(rows) doubles.
 int nsb_dot_blocks(int64_t rows);

@@ -256,9 +256,9 @@ __global__ __launch_bounds__(kThreads) void k_symmetrise(const T* K, int64_t ldk
 //   P_ij = a I + b A_ij + c A_i A_j^T,   Q_ij = b S_ij + c (A_i S_j^T + S_i A_j^T),
 // from the row blocks A_i, A_j, S_i = K_i + K^T_i, S_j (A and S are symmetric), and writes them as
 // the operand of the update: float32
-//   [ r P  r Q ; 0  P ],
+//   [ r P  r Q ; 0  x P ],
 // float16, for k_nsb_update,
-//   [ r P  r Q ; P  dP ; r dP ],   dP = 2^11 (P - its float16 value), all times p.
+//   [ r P  r Q ; x P  x dP ; r dP ],   dP = 2^11 (P - its float16 value), all times p.
 // In P E + Q X the two terms cancel, which makes P's rounding the largest of an iteration (relative
 // error of the gradient at 3 x 1111x333, 1.7e-3 of it the output's own rounding: 2.6e-3 without dP, 2.1e-3
 // with it).
@@ -288,7 +288,7 @@ struct SquareArgs {
   int64_t ld, stride;        // of both (elements)
   int n, n_p;
   int tiles;                 // of 32 rows: up to n_p; float16: as far as k_nsb_update reads
-  float a, b, c, r, p;
+  float a, b, c, r, x, p;
   const double* scale;       // k_nsb_scales' (exact), in the first iteration
   double S;
 };
@@ -368,7 +368,7 @@ __global__ __launch_bounds__(256) void k_nsb_square(SquareArgs g) {
     float p = b * (float)av[e] + c * ps;
     if (i == j + e && i < g.n) p += g.a;
     p *= g.p;
-    const float rp = g.r * p, sp = s * p;
+    const float rp = g.r * p, sp = s * g.x * p;
     p1[e] = (T)rp;
     p2[e] = (T)sp;
     rlo[e] = (T)(2048.f * (rp - (float)p1[e]));
@@ -779,8 +779,9 @@ __global__ __launch_bounds__(256) void k_nsb_small_load(const TX* X, const TX* G
   leave_parts(g, 0, aa, kk, qi, qj);
 }
 
+// xr: the new X's scale over the old one's, a power of two
 __global__ __launch_bounds__(256) void k_nsb_small_step(SmallArgs g, float a, float bb, float c,
-                                                        int parity, bool last) {
+                                                        float xr, int parity, bool last) {
   __shared__ float P[kN * kNP], Q[kN * kNP], E[kN * kNP], X[kN * kNP];
   const int b = blockIdx.y, tid = threadIdx.x, wave = tid >> 6, qi = wave >> 1, qj = wave & 1;
   {
@@ -864,6 +865,7 @@ __global__ __launch_bounds__(256) void k_nsb_small_step(SmallArgs g, float a, fl
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const int i = quad_row(e, qi), j = quad_col(qj);
+      xn[e] *= xr;
       E[i * kNP + j] = en[e];
       X[i * kNP + j] = xn[e];
       if (!last || !g.Et) V[i * g.ld + j] = en[e];
@@ -1018,10 +1020,10 @@ hipError_t symmetrise(const void* K, int64_t ldk, int64_t sK, const void* D, int
 }
 
 hipError_t nsb_square(const void* C2, void* PQ, int64_t ld, int64_t stride, Elem e, int count, int n,
-                      int n_p, float a, float b, float c, float r, float p, const double* scale,
-                      double S, hipStream_t s) {
+                      int n_p, float a, float b, float c, float r, float x, float p,
+                      const double* scale, double S, hipStream_t s) {
   const int tiles = (e == Elem::F16 ? (n + 127) / 128 * 128 : n_p) / 32;
-  const SquareArgs g{C2, PQ, ld, stride, n, n_p, tiles, a, b, c, r, p, scale, S};
+  const SquareArgs g{C2, PQ, ld, stride, n, n_p, tiles, a, b, c, r, x, p, scale, S};
   const dim3 grid(tiles * tiles, count);
   if (e == Elem::F16) hipLaunchKernelGGL(k_nsb_square<_Float16>, grid, dim3(256), 0, s, g);
   else hipLaunchKernelGGL(k_nsb_square<float>, grid, dim3(256), 0, s, g);
@@ -1092,9 +1094,9 @@ hipError_t nsb_small_load(const NsbSmall& d, const void* X, const void* G, Store
 }
 
 hipError_t nsb_small_step(const NsbSmall& d, int t, bool last_step, float a, float b, float c,
-                          hipStream_t s) {
+                          float x, hipStream_t s) {
   hipLaunchKernelGGL(k_nsb_small_step, dim3(d.blocks, d.count), dim3(256), 0, s, small_args(d), a, b,
-                     c, t & 1, last_step);
+                     c, x, t & 1, last_step);
   return last();
 }
 

@@ -226,3 +226,34 @@ def test_coefficients_of_odd_sizes(coeffs):
         err = rel(to_f64(dX[0]), ref.gradient(xs[0], gs[0], coeffs))
         _say("case", storage, rows, cols, coeffs, f"error {err:.2e}")
         assert err <= TOL[storage]
+
+
+RANGES = {
+    "grown": [(70000.0, -1000.0, 0.0), (1.5, 0.0, 0.0)],
+    "doubled": [(2.0, 0.0, 0.0)] * 10,
+    "shrunk": [(0.01, 0.0, 0.0)] * 4,
+    "down_and_up": [(1e-3, 0.0, 0.0), (1e-3, 0.0, 0.0), (900.0, -3e14, 0.0)],
+    "up_and_down": [(300.0, 0.0, 0.0), (300.0, 0.0, 0.0), (1e-4, -5e-15, 0.0)],
+    "float32": [(1e15, 0.0, 0.0), (1e14, 0.0, 0.0), (1e-10, 0.0, 0.0)],
+}
+
+
+@pytest.mark.parametrize("name", sorted(RANGES))
+@pytest.mark.parametrize("kind", ["normal", "rank_one"])
+def test_iterates_far_from_one(name, kind):
+    """Iterations that take the singular values of X, and the directions, far above or below 1 and go on
+    from there: what is stored in between (X, A = X X^T, E, P) stays in the range of its type, in every
+    form of the arithmetic. In float16 one step of a value at the top of its range is 2^-11 of it."""
+    coeffs = RANGES[name]
+    for storage, rows, cols in (("bf16", 300, 500), ("bf16", 600, 900), ("bf16", 900, 600),
+                                ("bf16", 40, 90), ("f32", 130, 200), ("f32", 600, 900), ("f32", 60, 200)):
+        if name == "float32" and storage == "bf16":
+            continue
+        X, G, xs, gs = _batch("normal", 1, rows, cols, storage, 83)
+        if kind == "rank_one":
+            X[0] = (X[0, :, :1].float() @ X[0, :1].float()).to(X.dtype)
+            xs = [to_f64(X[0])]
+        dX = mns.ns_orthogonalize_backward(X, G, coeffs)
+        err = rel(to_f64(dX[0]), ref.gradient(xs[0], gs[0], coeffs))
+        _say("case", name, kind, storage, rows, cols, f"error {err:.2e}")
+        assert err <= TOL[storage]
