@@ -32,6 +32,7 @@ struct GroupedArgs {
   int groups;
   int N, K;                     // NT, NN: output columns and reduction; TN: output rows, columns
   int tiles_n;
+  int most_tiles;               // NT, NN: of rows that belong to one expert each
   int fill_rest;                // NT, NN: rows of no expert are written as zeros
   float beta;                   // TN
   int split_cap;                // most parts of a tile of the last round (k_grouped_big)
@@ -81,8 +82,8 @@ __device__ __forceinline__ void walk_batch(const GroupedArgs& p, int BM, int til
       expert_rows(p, e, w.lo, w.hi);
     }
   }
-  // The host refuses calls of 2^31 tiles; only offsets that overlap can add up to more (find_place
-  // then checks what it finds).
+  // The host refuses calls of 2^31 tiles; only offsets that overlap can add up to more (walk_start
+  // then cuts the list off, find_place checks what it finds).
   w.incl = (w.hi - w.lo + (BM - 1)) / BM * tiles_n;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -91,16 +92,17 @@ __device__ __forceinline__ void walk_batch(const GroupedArgs& p, int BM, int til
   }
 }
 
-// The first batch, and the total over all of them.
+// The first batch, and the total over all of them: at most most_tiles, so that overlapping offsets
+// (experts that each claim all rows) do not multiply the rounds of blocks that go from tile to tile.
 __device__ __forceinline__ Walk walk_start(const GroupedArgs& p, int BM, int tiles_n, int rest) {
   Walk w;
   const int count = p.groups + 2 * rest;
-  int total = 0;
+  int64_t total = 0;
   for (int g0 = (count - 1) / 64 * 64; g0 >= 0; g0 -= 64) {
     walk_batch(p, BM, tiles_n, rest, g0, w);
-    total += __builtin_amdgcn_readlane(w.incl, 63);
+    total += (unsigned)__builtin_amdgcn_readlane(w.incl, 63);
   }
-  w.total = total;
+  w.total = total < p.most_tiles ? (int)total : p.most_tiles;
   return w;
 }
 
@@ -1664,6 +1666,7 @@ hipError_t grouped(const GroupedDesc& d, hipStream_t s) {
   a.offsets = d.offsets;
   a.total_rows = (int)d.total_rows;
   a.groups = (int)d.groups;
+  a.most_tiles = (int)blocks;
   a.fill_rest = d.fill_rest ? 1 : 0;
   a.beta = d.beta;
   a.sB = a.sC = d.n * d.k;

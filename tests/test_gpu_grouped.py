@@ -404,3 +404,34 @@ def test_weight_gradients_of_widths_inside_an_aligned_pitch(n, k, sizes):
         for c, beta in ((None, 0.0), (C, 0.5)):
             G = mns.grouped_weight_grad(dY, X, off, C=c, beta=beta, out_dtype=out_dtype)
             ref.check(G, *ref.weight_grad(dY, X, bounds, c, beta, out_dtype), (n, k, sizes, out_dtype))
+
+
+@pytest.mark.parametrize("transpose_w", [False, True])
+def test_overlapping_offsets_take_no_more_rounds(transpose_w):
+    """Experts that each claim all rows: unspecified values, but within the output, and not 32 times
+    the work of the rows dealt out once (at most one part tile of 256 rows more per expert, which is
+    about twice the tiles here)."""
+    n, k, rows, e = 2048, 1024, 16384, 64
+    W = _rand((e, n, k), BF, 1, 0.3)
+    X = _rand((rows, n if transpose_w else k), BF, 2)
+    width = k if transpose_w else n
+    buf = torch.full((rows + 2, width), 7.0, dtype=BF, device="cuda")
+    out = buf[1:-1]
+
+    def time_of(bounds):
+        off = _offsets(bounds)
+        best = 1e9
+        for _ in range(4):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            mns.grouped_matmul(X, W, off, transpose_w=transpose_w, out=out)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+
+    once = time_of([i * rows // e for i in range(e + 1)])
+    over = time_of([0, rows] * (e // 2) + [0])
+    print("once", once, "overlapping", over, flush=True)
+    assert over <= 8 * once
+    assert (buf[0] == 7.0).all() and (buf[-1] == 7.0).all()
