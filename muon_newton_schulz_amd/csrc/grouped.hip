@@ -1306,6 +1306,7 @@ __global__ __launch_bounds__(256) void k_grouped_join(GroupedArgs p) {
 
 // ---- a middling number of rows, bfloat16 ------------------------------------------------------
 //
+// Also for more rows whose 256 x 256 tiles would leave most CUs without work (plan_of).
 // Up to some hundred rows per expert the weights' bytes still bound a forward or input gradient,
 // and the rows fit one or two tiles of 128: a block takes 128 rows x BN columns, so most weights
 // are read once. What counts is bytes in flight: a ring of NS k-tiles in LDS (160 KB a CU), all but
@@ -1527,8 +1528,12 @@ bool dma_ok(const GroupedDesc& d) {
 //   k_grouped_big; 1024x4096 x 4: 16 / 30 / 26; 40 rows: 41 / 40 / 51 and 20 / 35 / 27), else
 //   k_grouped_ring up to 256 rows each (4096x2048 x 8, 100 rows: 41 / 52 of k_grouped_big; input
 //   gradient 12 rows 43 / 52, 100 rows 57 / 55) if it has a block for every other CU or the
-//   reduction is too short for k_grouped_big to split, k_grouped_big beyond (300 rows: 54 / 92 of
-//   k_grouped_ring, input gradient 74 / 113).
+//   reduction is too short for k_grouped_big to split; beyond, k_grouped_big (300 rows: 54 / 92 of
+//   k_grouped_ring, input gradient 74 / 113) unless its grid is small: where tiles of k_grouped_ring
+//   fill about one round and the reduction is at most 2048, those (in a cache; one expert of 2048 rows,
+//   512x1024: 14 of k_grouped_ring / 24, 1024x2048 30 / 32, 512x4096 37 / 30; four of 1024, 512x512
+//   13 / 16, of 300, 2048x512 13 / 16, of 2048, 1024x512, two rounds, 28 / 18; over 734 sizes of 1 to 8
+//   experts of 300 to 8192 rows 2 % from the faster of the two, k_grouped_big alone 23 %).
 //   What the DMA cannot take: k_grouped_rows up to 96 rows each (forward); k_grouped_split up to 160
 //   tiles of 128 x 128 (float32, 1021 rows over 5 experts of 513x1277: forward 36 against 103,
 //   input gradient 37 / 47; bfloat16 45 / 62 and 26 / 26; 200 tiles: 142 / 124, 51 / 38), else
@@ -1551,8 +1556,16 @@ Plan plan_of(const GroupedDesc& d) {
     const int64_t bn = tiles_up(out, 128) * used >= cus / 2 ? 128 : 64;
     const int64_t ring_tiles = (used + d.total_rows / 128) * tiles_up(out, bn);
     const bool few = !d.transpose_w && d.total_rows <= 24 * used;
-    if (4 * big_tiles >= 7 * cus || d.total_rows > 256 * d.groups ||
-        (!few && 2 * ring_tiles < cus && red >= 1536)) {
+    const bool many = d.total_rows > 256 * d.groups;
+    if (many && red <= 2048) {
+      const int64_t row_tiles = used + d.total_rows / 128;
+      p.bn = out <= 64 || row_tiles * tiles_up(out, 64) <= cus ? 64 : 128;
+      if (8 * row_tiles * tiles_up(out, p.bn) <= 9 * cus) {
+        p.kernel = Kernel::Ring;
+        return p;
+      }
+    }
+    if (4 * big_tiles >= 7 * cus || many || (!few && 2 * ring_tiles < cus && red >= 1536)) {
       p.kernel = Kernel::Big;
       p.bm = p.bn = 256;
       return p;

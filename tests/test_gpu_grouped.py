@@ -435,3 +435,45 @@ def test_overlapping_offsets_take_no_more_rounds(transpose_w):
     print("once", once, "overlapping", over, flush=True)
     assert over <= 8 * once
     assert (buf[0] == 7.0).all() and (buf[-1] == 7.0).all()
+
+
+def _both_ways(sizes, out, red, what):
+    bounds = ref.bounds_of(sizes, 1)
+    rows, e, off = bounds[-1] + 2, len(sizes), _offsets(bounds)
+    print("case", what, sizes, out, red, flush=True)
+    W, X = _rand((e, out, red), BF, 1, 0.3), _rand((rows, red), BF, 2)
+    Y = mns.grouped_matmul(X, W, off)
+    ref.check(Y, *ref.matmul(X, W, bounds, False, torch.zeros_like(Y)), (what, "forward"))
+    W, dY = _rand((e, red, out), BF, 3, 0.3), _rand((rows, red), BF, 4)
+    dX = mns.grouped_matmul(dY, W, off, transpose_w=True)
+    ref.check(dX, *ref.matmul(dY, W, bounds, True, torch.zeros_like(dX)), (what, "input gradient"))
+
+
+@pytest.mark.parametrize("sizes,out,red", [([2048], 512, 1024), ([1030, 0, 290], 136, 192),
+                                           ([300, 301, 299, 400], 2048, 512), ([8192], 64, 1024),
+                                           ([8000, 700], 256, 128), ([700], 72, 2048)])
+def test_many_rows_of_a_small_grid(sizes, out, red):
+    """Many rows per expert whose 256 x 256 tiles would be few: 128 x 64 or 128 x 128 tiles."""
+    _both_ways(sizes, out, red, "small grid")
+
+
+@pytest.mark.parametrize("sizes", [[600, 150, 0, 400], [3000], [1100, 1500]])
+def test_longer_reductions_in_parts(sizes):
+    """Reductions long enough that few 256 x 256 tiles are computed in parts and joined."""
+    _both_ways(sizes, 384, 4096, "parts")
+
+
+@pytest.mark.parametrize("rows,experts,out,red,kernel", [
+    (2048, 1, 512, 1024, "grouped_ring_nt"),        # 16 large tiles, 128 small ones: 23 against 14 us
+    (8192, 1, 64, 1024, "grouped_ring_nt"),         # three quarters of a large tile's columns unused
+    (2048, 1, 512, 4096, "grouped_256_nt"),         # long enough to be cut: 30 against 37
+    (2048, 16, 512, 1024, "grouped_256_nt"),        # large tiles for every block
+])
+def test_kernel_of_many_rows(rows, experts, out, red, kernel):
+    """Many rows go to 256 x 256 tiles only where these occupy the chip."""
+    W, X = _rand((experts, out, red), BF, 1), _rand((rows * experts, red), BF, 2)
+    off = _offsets([rows * i for i in range(experts + 1)])
+    mns.profile_begin()
+    mns.grouped_matmul(X, W, off)
+    torch.cuda.synchronize()
+    assert [k["name"] for k in mns.profile_end()] == [kernel]
