@@ -477,3 +477,100 @@ def test_kernel_of_many_rows(rows, experts, out, red, kernel):
     mns.grouped_matmul(X, W, off)
     torch.cuda.synchronize()
     assert [k["name"] for k in mns.profile_end()] == [kernel]
+
+
+# sizes whose forward, input gradient and weight gradient take the 256 x 256 kernel (the forward in
+# parts that are joined), and the ring kernel
+MODES = {
+    "large": ([600, 150, 0, 700], 512, 4096, ["grouped_256_nt", "grouped_256_nn", "grouped_256_tn"]),
+    "ring": ([60, 100, 0, 31, 128, 77, 5, 90], 1024, 512,
+             ["grouped_ring_nt", "grouped_ring_nn", "grouped_256_tn"]),
+}
+
+
+def _mode(mode, seed=0):
+    sizes, n, k, names = MODES[mode]
+    bounds = ref.bounds_of(sizes, 3)
+    rows, e = bounds[-1] + 4, len(sizes)
+    return (_rand((rows, k), BF, seed), _rand((e, n, k), BF, seed + 1, 0.3),
+            _rand((rows, n), BF, seed + 2), bounds, names)
+
+
+def _three(X, W, dY, off):
+    return [mns.grouped_matmul(X, W, off), mns.grouped_matmul(dY, W, off, transpose_w=True),
+            mns.grouped_weight_grad(dY, X, off)]
+
+
+@pytest.mark.parametrize("mode", sorted(MODES))
+def test_nothing_leaks_through_the_dma_kernels(mode):
+    X, W, dY, bounds, names = _mode(mode)
+    off = _offsets(bounds)
+    mns.profile_begin()
+    clean = _three(X, W, dY, off)
+    torch.cuda.synchronize()
+    assert [k["name"] for k in mns.profile_end()] == names
+    rows, bad = X.shape[0], slice(bounds[1], bounds[2])
+    for t in (X, dY):
+        t[:bounds[0]] = float("nan")
+        t[bad] = float("inf")
+        t[bounds[-1]:] = float("nan")
+    W[1] = float("nan")
+    W[2] = float("inf")
+    got = _three(X, W, dY, off)
+    keep = torch.ones(rows, dtype=torch.bool)
+    keep[bad] = False
+    for c, g in zip(clean[:2], got[:2]):
+        assert torch.equal(g.cpu()[keep], c.cpu()[keep])
+        assert not torch.isfinite(g.cpu()[~keep]).any()
+    others = [i for i in range(W.shape[0]) if i != 1]
+    assert torch.equal(got[2][others], clean[2][others])
+    assert not torch.isfinite(got[2][1]).any()
+
+
+@pytest.mark.parametrize("mode", sorted(MODES))
+def test_dma_kernels_captured_and_replayed(mode):
+    """Every replay against the eager call: other tokens, other routings (all rows to one expert, none
+    to most), eager work and synchronisation in between."""
+    X, W, dY, bounds, _ = _mode(mode)
+    rows, e = X.shape[0], W.shape[0]
+    off = _offsets(bounds)
+    M = torch.zeros(W.shape, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _chain(X, W, dY, off, M)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Y, dX = _chain(X, W, dY, off, M)
+    even = [i * rows // e for i in range(e + 1)]
+    for i, b in enumerate([even, [0] * e + [rows], [0] + [rows] * e, bounds]):
+        off.copy_(_offsets(b))
+        X.copy_(_rand(X.shape, BF, 20 + i))
+        M.copy_(_rand(M.shape, F32, 30 + i))
+        M2 = M.clone()
+        Y2, dX2 = _chain(X, W, dY, off, M2)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, Y2) and torch.equal(dX, dX2) and torch.equal(M, M2), (mode, i)
+
+
+@pytest.mark.parametrize("mode", sorted(MODES))
+def test_dma_kernels_on_two_streams_at_once(mode):
+    sets = [_mode(mode, 10 * i)[:4] for i in range(2)]
+    sets = [(X, W, dY, _offsets(b)) for X, W, dY, b in sets]
+    alone = [_three(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(3):
+        for i, (s, args) in enumerate(zip(streams, sets)):
+            with torch.cuda.stream(s):
+                got[i].append(_three(*args))
+    torch.cuda.synchronize()
+    for want, rounds in zip(alone, got):
+        for outs in rounds:
+            for a, b in zip(want, outs):
+                assert torch.equal(a, b)
