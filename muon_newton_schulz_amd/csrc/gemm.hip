@@ -62,6 +62,7 @@
 //     block's k-range, each with its own LDS stages and no barrier in the k loop, and add
 //     their partial tiles in wave order before the same epilogue (gemm_epilogue.inc, which
 //     both kernels expand inline).
+#include "lds_dma.h"
 #include "mns_internal.h"
 
 #include <type_traits>
@@ -69,14 +70,9 @@
 namespace mns {
 namespace {
 
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) void lds_void;
-
-constexpr int kChunks = 8;   // 16-byte chunks per LDS row (one 128-byte k-tile)
-constexpr int kBufferFlags = 0x00020000;   // buffer resource word 3: raw loads, gfx9 family
 
 template <typename T>
 struct Traits;
@@ -105,35 +101,9 @@ struct Traits<float> {
   }
 };
 
-__device__ __forceinline__ int swz(int row, int chunk) {
-  return row * kChunks + (chunk ^ ((row ^ ((row >> 3) & 3)) & 7));
-}
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
-  const int n = bytes > 0x7FFFFFFFLL ? 0x7FFFFFFF : (int)bytes;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, n, kBufferFlags);
-}
-
-// 16-byte-per-lane global -> LDS copy: lane l's 16 bytes land at dst + 16 l (dst is the
-// wave-uniform LDS base, carried in M0). Kept out of lambdas: the host pass of a kernel
-// must not see the LDS address-space cast.
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, u32x4* dst, int voff, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, voff, soff, 0, 0);
-}
-
-// s_waitcnt immediate (gfx9 encoding: vmcnt[3:0] | expcnt[6:4] | lgkmcnt[11:8] | vmcnt[15:14]).
-constexpr int kWaitVm0Lgkm0 = 0x0070;     // vmcnt(0) lgkmcnt(0)
-// vmcnt(n) alone (n < 64): at most n of this wave's vector-memory operations outstanding
+// s_waitcnt immediate of vmcnt(n) alone (n < 64): at most n of this wave's vector-memory operations
+// outstanding
 constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | 0x70 | 0xF00; }
-
-__device__ __forceinline__ void block_sync() {
-  // All of this wave's LDS-DMA writes and LDS accesses are done, then the workgroup meets.
-  // No memory fence: the DMA traffic is ordered by the explicit counters.
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(kWaitVm0Lgkm0);
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
 
 struct GemmArgs {
   const void* A; const void* B; const void* D;
@@ -380,7 +350,6 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_gemm(GemmArgs p) {
   }
   auto load_b = [&](int buf, int ks, int slot) {
     if constexpr (KB) {
-      typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
       u32x2 t00, t01, t10, t11;
       const uint32_t o = (uint32_t)(buf * STAGE * 16 + ks * 16 * KRB);
       const uint32_t a0 = b_addr[0] + o, a1 = b_addr[1] + o;

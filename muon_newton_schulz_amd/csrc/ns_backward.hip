@@ -526,7 +526,6 @@ __global__ __launch_bounds__(512) void k_nsb_gram(GramArgs g) {
 // zeros, without a product, and the k-tiles stop at n. TRANS (the last iteration of tall matrices): E'
 // alone, transposed. 19 us on 3 x 1111x333 (18 dependent k-tiles of about 0.7 us; the padded
 // product on the general GEMM, one part of P, 14 us and 7 for joining its parts).
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 struct UpdateArgs {
   const _Float16* PQ;        // of k_nsb_square, 3 n_p rows
   int64_t ld, stride;
