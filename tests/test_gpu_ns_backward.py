@@ -257,3 +257,20 @@ def test_iterates_far_from_one(name, kind):
         err = rel(to_f64(dX[0]), ref.gradient(xs[0], gs[0], coeffs))
         _say("case", name, kind, storage, rows, cols, f"error {err:.2e}")
         assert err <= TOL[storage]
+
+
+@pytest.mark.parametrize("dist", ["normal", "lowrank"])
+@pytest.mark.parametrize("batch,rows,cols", [(1, 513, 513), (1, 700, 700), (1, 900, 600), (3, 600, 900),
+                                             (1, 1024, 1024), (1, 1024, 4096), (12, 512, 1100)])
+def test_larger_bfloat16_within_half_a_step(batch, rows, cols, dist):
+    """As test_small_bfloat16_within_half_a_step, where the products run on float16 operands of one
+    part each: arithmetic and output rounding together stay below 2^-8 of the gradient, the largest
+    rounding of a bfloat16 value."""
+    _say("case", dist, batch, rows, cols)
+    X, G, xs, gs = _batch(dist, batch, rows, cols, "bf16", 91)
+    ws = torch.full((mns.ns_backward_workspace_size(X),), 0xFF, dtype=torch.uint8, device="cuda")
+    dX = mns.ns_orthogonalize_backward(X, G, C5, workspace=ws)
+    for i in range(0, batch, max(1, batch // 3)):
+        err = rel(to_f64(dX[i]), ref.gradient(xs[i], gs[i], C5))
+        _say("  matrix", i, "error", f"{err:.2e}")
+        assert err <= 2.0 ** -8
