@@ -188,6 +188,9 @@ mns_status mns_ns_backward_workspace_size(int dtype, int64_t batch, int64_t rows
  *   of two from its bound over the iterations, so that coefficients may take it far above or below 1.
  *   MNS_ERR_PARAM when they amplify a direction more than 2^20 times (float16; T = 10 with (3.4445,
  *   -4.775, 2.0315) still runs) or 10^30 times, or when the terms of an update can pass 10^37.
+ *   float16 errors grow with the amplification, most where X has singular values below float16's
+ *   last place (rank one as bfloat16 rounds it): with that quintic 2e-3 to 3e-3 at T = 5, at T = 10
+ *   1e-2, there 1e-1 (the forward call's own: 3e-3, there 2e-1).
  *   Sizes: as above, with the iterate counted twice (direction and iterate are stored together),
  *   else MNS_ERR_SHAPE. */
 mns_status ns_orthogonalize_backward(const void* X, const void* dO, void* dX, int dtype,
@@ -222,12 +225,13 @@ mns_status normuon_scale(void* O, int dtype, int64_t batch, int64_t rows, int64_
  *   need only the alignment of their dtype, as do W and G. 16-byte aligned pointers with widths
  *   and pitches of whole 16 bytes run faster.
  *   Sizes: 1 <= groups <= 65536; 0 <= total_rows <= 2^30 (the token pointers may be NULL when it is
- *   0); 1 <= n, k <= 65536, n*k <= 2^31 - 1; pitches <= 2^21; at most 2^31 - 1 output tiles
- *   of 16 x 16; else MNS_ERR_SHAPE.
+ *   0); 1 <= n, k <= 65536, n*k <= 2^31 - 1; pitches <= 2^21; at most 2^31 - 1 tiles of the kernel
+ *   that takes the call (16 x 16 to 256 x 256; an output of more does not fit the memory);
+ *   else MNS_ERR_SHAPE.
  *   workspace (may be NULL when the size query returns 0, which goes by the sizes alone and covers
  *   every alignment and addend) must be 256-byte aligned.
- *   Rounding: the order of a sum's float32 additions depends on the sizes and the number of CUs
- *   only, so equal calls give equal bits. */
+ *   Rounding: the order of a sum's float32 additions depends on the sizes, types, alignment and
+ *   pitches, the presence of an addend and the number of CUs only, so equal calls give equal bits. */
 
 /* Workspace bytes of grouped_matmul (weight_grad = 0) or grouped_weight_grad (1). */
 mns_status mns_grouped_workspace_size(int weight_grad, int dtype, int64_t groups,

@@ -413,7 +413,10 @@ def grouped_matmul(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, *,
     W is a contiguous (experts, n, k) stack; expert e owns rows offsets[e]:offsets[e + 1] of X
     (offsets: int64 on the GPU, read by the kernels only). X and ``out`` are 2-D with contiguous
     rows at any row pitch. Rows that belong to no expert come back as zeros in a new output and
-    are left as they are in a given ``out``."""
+    are left as they are in a given ``out``.
+
+    Autograd does not see the call (its result never requires grad): the gradients are calls of
+    their own, ``transpose_w`` for X's and grouped_weight_grad for W's."""
     what = "grouped_matmul"
     if W.dim() != 3:
         raise ValueError(f"{what}: W must be 3-D (experts, n, k)")
@@ -459,7 +462,7 @@ def grouped_weight_grad(dY: torch.Tensor, X: torch.Tensor, offsets: torch.Tensor
     (experts, n, k) for dY of width n and X of width k, rows sorted by expert as in
     grouped_matmul. The output is of ``out``'s dtype, else C's, else ``out_dtype``, else X's;
     float32 outputs take bfloat16 products unrounded. ``out`` may be C itself: with a float32
-    momentum, ``C=M, beta=mu, out=M`` is M <- mu M + dY^T X."""
+    momentum, ``C=M, beta=mu, out=M`` is M <- mu M + dY^T X. Autograd does not see the call."""
     what = "grouped_weight_grad"
     code = _dtype_code(X)
     if dY.dtype != X.dtype:
@@ -585,7 +588,8 @@ def ns_orthogonalize_backward(X: torch.Tensor, dO: torch.Tensor, coeffs,
                               workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Gradient dX of ns_orthogonalize(X, coeffs) for the gradient dO of its output (the same for
     gram_ns_orthogonalize, whose map is the same). X and dO: one matrix or a 3-D batch, of one
-    shape and storage dtype; X is the forward call's input, nothing else is kept from it."""
+    shape and storage dtype; X is the forward call's input, nothing else is kept from it. Autograd
+    sees neither the forward call nor this one."""
     what = "ns_orthogonalize_backward"
     if dO.shape != X.shape or dO.dtype != X.dtype:
         raise ValueError(f"{what}: dO must match X in shape and dtype "

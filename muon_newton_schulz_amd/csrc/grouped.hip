@@ -809,11 +809,12 @@ __device__ __forceinline__ bool tile_at(const GroupedArgs& p, const Walk& w, int
 // tile's first k-tiles land while this one's last products and its epilogue run.
 //
 // 16384 rows over 32 experts of 8192 x 1024: forward 298 us, input gradient 310 with the join, weight
-// gradient 334 (923, 887, 823 TFLOP/s; before the tiles ran into each other 329, 384, 442). Bound by
-// the matrix units under the card's power limit (busy 51, 51 and 42 % of the cycles at 1.76 to 1.9 GHz;
-// the same calls take 240 to 270 us before the clock comes down), the weight gradient with its eight
-// k-tiles a tile also by the transposing reads' waits and 537 MB of output. 16 rows over 32 experts:
-// 46 us, the weights at 5.8 TB/s.
+// gradient 334 (923, 887, 823 TFLOP/s; before the tiles ran into each other 329, 384, 442). The matrix
+// units are busy 51, 51 and 42 % of the cycles, at 1.76 to 1.9 GHz (the power limit; 240 to 270 us before
+// the clock comes down). The other half: part tiles (up to 255 rows of every expert's last one), an
+// epilogue every 16 k-tiles (forward), 1.3 rounds of tiles (input gradient), the transposing reads'
+// waits and 537 MB of output after eight k-tiles a tile (weight gradient). 16 rows over 32 experts: 46 us,
+// the weights at 5.8 TB/s.
 template <typename TO, int FORM, bool ADD>
 __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
   constexpr int BM = 256, BN = 256, BK = 64, FM = 4, FN = 2, INST = 4;   // DMA per wave and operand

@@ -79,8 +79,9 @@ __device__ __forceinline__ void store8(T* p, const T* v) {
 
 // scale[4 b ..]: S / ||X||, 1 / ||X||, e0 / ||dO||, ||dO|| of matrix b (zeros for a zero norm),
 // from nblk partial sums of squares of X and, behind them, of dO. exact: the first and third rounded
-// down to powers of two, so that a bfloat16 matrix keeps every bit in float16; k_nsb_square makes up
-// for X's in the first iteration, and the fourth is e0 / (third).
+// down to powers of two, so that in float16 a bfloat16 element keeps every bit if its scaled magnitude is
+// at least 2^-17 (below, float16's smallest step of 2^-24 cuts bits off); k_nsb_square makes up for X's in
+// the first iteration, and the fourth is e0 / (third).
 __global__ __launch_bounds__(kThreads) void k_nsb_scales(const double* px, const double* pg,
                                                          int nblk, double S, double e0,
                                                          bool exact, double* scale) {
