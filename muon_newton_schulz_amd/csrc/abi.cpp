@@ -1186,7 +1186,7 @@ static double poly_range(double s, double a, double b, double c) {
 static bool nsb_plan(int T, const float* abc, const Geo& g, NsbScale* sc) {
   const bool f16 = g.elem == Elem::F16;
   constexpr int kGrid = 2048;
-  constexpr double kLeast = 0x1p-100;      // of L and of u over the one before: all may be gone
+  constexpr double kLeast = 0x1p-100;      // of L, 1 / p and of u over the one before: all may be gone
   double L = 1.0, sup = 1.0, u = 1.0;
   double f[kGrid], d[kGrid];
   for (int i = 0; i < kGrid; ++i) {
@@ -1214,6 +1214,7 @@ static bool nsb_plan(int T, const float* abc, const Geo& g, NsbScale* sc) {
       sc[t].kap = pow2_floor(lim / (2.0 * L * (top > 1.0 ? top : 1.0) * big));
       double p = 256.0;
       if (p * pmax > lim || (pmax > 0.0 && p * pmax < 1.0)) p = pow2_floor(lim / pmax);
+      if (p > 1.0 / kLeast) p = 1.0 / kLeast;
       if (p * sc[t].e / g.S * qmax > lim) p = pow2_floor(lim * g.S / (sc[t].e * qmax));
       sc[t].p = p;
       sc[t].q = p * sc[t].e / g.S;

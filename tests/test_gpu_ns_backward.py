@@ -274,3 +274,15 @@ def test_larger_bfloat16_within_half_a_step(batch, rows, cols, dist):
         err = rel(to_f64(dX[i]), ref.gradient(xs[i], gs[i], C5))
         _say("  matrix", i, "error", f"{err:.2e}")
         assert err <= 2.0 ** -8
+
+
+@pytest.mark.parametrize("coeffs", [[(1e-38, 0.0, 0.0)] * 3, [(0.0, 0.0, 0.0)] * 2,
+                                    [(0.0, 0.0, 0.0), (3.0, -1.0, 0.0)], [(1e-44, 0.0, 0.0)] * 4],
+                         ids=["tiny", "zero", "zero_first", "denormal"])
+def test_coefficients_that_leave_nothing(coeffs):
+    """The gradient is zero, or below anything its type can hold: zeros, not NaN."""
+    for storage, rows, cols in (("bf16", 300, 500), ("bf16", 600, 900), ("bf16", 40, 90),
+                                ("f32", 130, 200), ("f32", 600, 900), ("f32", 60, 200)):
+        X, G, _, _ = _batch("normal", 1, rows, cols, storage, 83)
+        _say("case", storage, rows, cols, coeffs)
+        assert not mns.ns_orthogonalize_backward(X, G, coeffs).any()
