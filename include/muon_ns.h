@@ -62,6 +62,16 @@ typedef enum mns_status {
 
 typedef enum mns_dtype { MNS_F32 = 0, MNS_BF16 = 1 } mns_dtype;
 
+/* Activation of a layer: relu max(z, 0); relu2 max(z, 0)^2; gelu z Phi(z), Phi the normal distribution's
+ * mass below z; silu z / (1 + e^-z). */
+typedef enum mns_activation {
+  MNS_ACT_NONE = 0,
+  MNS_ACT_RELU = 1,
+  MNS_ACT_RELU2 = 2,
+  MNS_ACT_GELU = 3,
+  MNS_ACT_SILU = 4
+} mns_activation;
+
 typedef enum mns_ns_kind {
   MNS_NS_STANDARD = 0,     /* quintic NS on the rectangular iterate ("Standard Newton-Schulz") */
   MNS_NS_GRAM = 1          /* Gram NS on the small n x n side (Theorem 2 + restarts) */
@@ -259,6 +269,116 @@ mns_status grouped_weight_grad(const void* dY, int64_t lddy, const void* X, int6
                                int64_t total_rows, int64_t n, int64_t k, const void* C, float beta,
                                void* G, int out_dtype, void* workspace, size_t workspace_bytes,
                                void* stream);
+
+/* ---- Layers of experts -----------------------------------------------------------------------
+ * The products above with what a layer does around them in the same kernel, and the gradient of its
+ * bias. Rows, offsets, pitches, sizes, alignment and the workspace (mns_grouped_workspace_size) as above;
+ * a plain layer is a stack of one. Everything between the product and the output's one rounding
+ * is float32. Rows of no expert are left as they are, or with fill_rest written as zeros, in every
+ * row-wise output. NaN and infinities stay in their rows (bias: in their expert). */
+
+/* Z_e = X_e W_e^T + bias_e; Y = act(Z) + R.
+ *   bias in  dtype [groups][n], or NULL (none);   R  in  dtype, total_rows x n, pitch ldr, or NULL
+ *   Z    out dtype, total_rows x n, pitch ldz, or NULL (not kept): what the gradients need. act is
+ *            taken of the float32 sum, before Z's rounding.
+ *   Y    out dtype, total_rows x n, pitch ldy; may be R itself (with its pitch); Y and Z may not overlap
+ *            each other or any other input. */
+mns_status grouped_linear(const void* X, int64_t ldx, const void* W, const void* bias, int activation,
+                          const void* R, int64_t ldr, void* Z, int64_t ldz, void* Y, int64_t ldy,
+                          int dtype, const int64_t* offsets, int64_t groups, int64_t total_rows,
+                          int64_t n, int64_t k, int fill_rest, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Gradient of a layer's input: dX_e = (dY_e W_e) act'(Z) + R, act and Z those of the layer that produced
+ * that input (none: MNS_ACT_NONE and Z NULL), so that dX is the gradient of its Z.
+ *   dY in  dtype, total_rows x n, pitch lddy;   Z, R  in  dtype, total_rows x k, pitches ldz, ldr;
+ *   R (may be NULL): a gradient that reaches the input past the layer
+ *   dX out dtype, total_rows x k, pitch lddx; may be Z or R itself (with its pitch), may not overlap an
+ *          input otherwise. relu's slope at 0 is 0. */
+mns_status grouped_input_grad(const void* dY, int64_t lddy, const void* W, int activation,
+                              const void* Z, int64_t ldz, const void* R, int64_t ldr, void* dX,
+                              int64_t lddx, int dtype, const int64_t* offsets, int64_t groups,
+                              int64_t total_rows, int64_t n, int64_t k, int fill_rest,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of grouped_bias_grad. */
+mns_status mns_grouped_bias_grad_workspace_size(int64_t groups, int64_t total_rows, int64_t n,
+                                                size_t* bytes /* (host) out */);
+
+/* Gradient of a layer's bias: dZ = dY act'(Z); db_e = the sum of dZ's rows of expert e (float32 sums of
+ * the unrounded products; zeros for an expert without rows).
+ *   dY, Z in  dtype, total_rows x n, pitches lddy, ldz;  Z NULL with MNS_ACT_NONE (then dZ is dY)
+ *   dZ    out dtype, total_rows x n, pitch lddz, or NULL; may be dY or Z itself (with its pitch)
+ *   db    out out_dtype [groups][n]; out_dtype: dtype, or MNS_F32
+ * Equal calls give equal bits. Sizes: groups, total_rows, n and pitches as above. */
+mns_status grouped_bias_grad(const void* dY, int64_t lddy, int activation, const void* Z, int64_t ldz,
+                             void* dZ, int64_t lddz, int dtype, const int64_t* offsets,
+                             int64_t groups, int64_t total_rows, int64_t n, void* db, int out_dtype,
+                             int fill_rest, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- A router's bookkeeping ---------------------------------------------------------------------
+ * Up to 2048 experts; 0 <= assignments, tokens * top <= 2^30; else MNS_ERR_SHAPE. ids (device): the
+ * expert of each assignment, token by token, read by the kernels only; a value outside 0 ..
+ * experts - 1 (-1 for a padded or dropped token) is an assignment to no expert. */
+
+/* Workspace bytes of expert_order. */
+mns_status mns_expert_order_workspace_size(int64_t assignments, int64_t experts,
+                                           size_t* bytes /* (host) out */);
+
+/* Assignments by expert: counts [experts], offsets [experts + 1] (what the grouped calls take: expert
+ * e's rows are offsets[e] .. offsets[e+1]-1) and order [assignments], or NULL: the assignments' indices by
+ * expert, each expert's in their own order, those of no expert last (row r of the sorted tokens is token
+ * order[r] / top). ids may be NULL when assignments is 0; outputs may not overlap it or each other. */
+mns_status expert_order(const int64_t* ids, int64_t assignments, int64_t experts, int64_t* counts,
+                        int64_t* offsets, int64_t* order, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* Workspace bytes of balance_loss. */
+mns_status mns_balance_workspace_size(int64_t tokens, int64_t experts,
+                                      size_t* bytes /* (host) out */);
+
+/* The balance loss of a router and its gradient. With p_t = softmax(logits_t), c_e = counts[e], N their
+ * sum and a_t the token's assignments to experts:
+ *   loss = scale experts / N^2 sum_t a_t sum_e c_e p_te
+ *   dlogits_te = scale experts / N^2 a_t p_te (c_e - sum_j c_j p_tj)
+ * that is, scale experts sum_e f_e P_e of the shares f_e = c_e / N and the mean probabilities P_e of the
+ * assigned tokens; f is taken as constant. A token without an assignment adds nothing and has a zero
+ * gradient, whatever its logits hold; so does one whose logits are all -infinity. N = 0 gives zeros.
+ *   logits  in  dtype [tokens][experts], row pitch ldl (elements);   ids  in  [tokens][top]
+ *   counts  in  [experts], those of ids (expert_order's)
+ *   loss    out float32, one value;   dlogits  out  dtype, row pitch ldd, or NULL; may be logits itself */
+mns_status balance_loss(const void* logits, int64_t ldl, int dtype, const int64_t* ids, int64_t top,
+                        const int64_t* counts, int64_t tokens, int64_t experts, float scale,
+                        float* loss, void* dlogits, int64_t ldd, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* ---- Global norm and clipping -------------------------------------------------------------------- */
+
+/* One gradient: numel elements of dtype at `in` (aligned to its dtype); scaled into `out`, which may be
+ * `in`. numel may be 0. */
+typedef struct mns_tensor {
+  const void* in;
+  void* out;
+  int64_t numel;
+  int32_t dtype;
+} mns_tensor;
+
+/* Workspace bytes of grad_norm and clip_grad_norm for a list of `count` tensors. */
+mns_status mns_clip_workspace_size(int count, size_t* bytes /* (host) out */);
+
+/* norm (float32, device) = sqrt(sum of g^2 over every element of every tensor); squares and sums in
+ * float64, rounded once (a norm beyond float32's range is written as infinity). `out` is not used; a
+ * tensor listed twice counts twice. tensors (host), 1 <= count <= 65536. */
+mns_status grad_norm(const mns_tensor* tensors, int count, float* norm, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* grad_norm, then out = in * min(1, max_norm / (norm + eps)) for every tensor, the factor formed in
+ * float64 and rounded to float32, the product rounded to the dtype. A NaN norm gives NaN, an infinite one
+ * zeros (and NaN where the gradient is infinite). A tensor scaled in place by 1 is not written.
+ * max_norm >= 0 (may be infinite), eps >= 0 and finite, else MNS_ERR_PARAM; so is an output that overlaps
+ * another output, another tensor's input, or its own input without being it. */
+mns_status clip_grad_norm(const mns_tensor* tensors, int count, float max_norm, float eps, float* norm,
+                          void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace bytes muon_step_grouped needs. */
 mns_status mns_grouped_step_workspace_size(int64_t groups, int64_t total_rows, int64_t rows,

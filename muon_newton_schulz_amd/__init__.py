@@ -22,10 +22,14 @@ __all__ = ["muon_step", "ns_orthogonalize", "ns_orthogonalize_noalloc",
            "ns_orthogonalize_backward", "ns_backward_workspace_size",
            "grouped_matmul", "grouped_weight_grad", "muon_step_grouped",
            "grouped_step_workspace_size",
+           "grouped_linear", "grouped_input_grad", "grouped_bias_grad",
+           "expert_order", "balance_loss", "grad_norm", "clip_grad_norm",
            "step_workspace_size", "ns_workspace_size", "normuon_workspace_size",
            "restart_mask", "profile_begin", "profile_set_flush", "profile_end", "MnsError",
            "load"]
 
+_ACTIVATIONS = {None: _abi.MNS_ACT_NONE, "relu": _abi.MNS_ACT_RELU, "relu2": _abi.MNS_ACT_RELU2,
+                "gelu": _abi.MNS_ACT_GELU, "silu": _abi.MNS_ACT_SILU}
 _KINDS = {"standard": MNS_NS_STANDARD, "gram": MNS_NS_GRAM}
 
 
@@ -502,6 +506,326 @@ def grouped_weight_grad(dY: torch.Tensor, X: torch.Tensor, offsets: torch.Tensor
                                          MNS_F32 if out_dtype == torch.float32 else MNS_BF16, ws,
                                          nbytes, handle), what)
     return G
+
+
+def _activation(activation, what: str) -> int:
+    if activation not in _ACTIVATIONS:
+        names = sorted(a for a in _ACTIVATIONS if a)
+        raise ValueError(f"{what}: activation must be None or one of {names}")
+    return _ACTIVATIONS[activation]
+
+
+def _rowwise(t: torch.Tensor | None, name: str, shape, dtype, what: str) -> int:
+    """Row pitch of an optional 2-D tensor of the given shape and dtype (0 for None)."""
+    if t is None:
+        return 0
+    if tuple(t.shape) != shape or t.dtype != dtype:
+        raise ValueError(f"{what}: {name} must be {shape} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    return _pitch(t, name, what)
+
+
+def _itself_or_apart(out, name: str, same, others, what: str) -> None:
+    """`out` may be one of `same` (its memory and pitch) and otherwise overlap nothing."""
+    if out is None:
+        return
+    for other_name, t in others:
+        if t is not None and not _apart(out, t):
+            raise ValueError(f"{what}: {name} may not overlap {other_name}")
+    for other_name, t in same:
+        if t is None or _apart(out, t):
+            continue
+        if t.data_ptr() != out.data_ptr() or t.stride() != out.stride():
+            raise ValueError(f"{what}: {name} must be {other_name} itself or lie apart from it")
+
+
+def _ptr_or_none(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def _layer_operands(A, W, transpose_w: bool, a_name: str, what: str):
+    """Checks of a layer's rows and weights: dtype code, (groups, n, k), rows, pitch, output width."""
+    code = _dtype_code(A)
+    if W.dim() != 3:
+        raise ValueError(f"{what}: W must be 3-D (experts, n, k)")
+    if W.dtype != A.dtype:
+        raise TypeError(f"{what}: {a_name} and W must share one storage dtype "
+                        f"({a_name} {A.dtype}, W {W.dtype})")
+    groups, n, k = W.shape
+    inner, width = (n, k) if transpose_w else (k, n)
+    if A.dim() != 2 or A.shape[1] != inner:
+        raise ValueError(f"{what}: {a_name} must be 2-D with rows of {inner}, got {tuple(A.shape)}")
+    if not W.is_contiguous():
+        raise ValueError(f"{what}: W must be contiguous")
+    return code, groups, n, k, A.shape[0], _pitch(A, a_name, what), width
+
+
+def _new_rows(rows: int, width: int, like: torch.Tensor, zeros: bool) -> torch.Tensor:
+    """A new row-wise output; zeros when the call's own filling of unowned rows is off."""
+    make = torch.zeros if zeros else torch.empty
+    return make((rows, width), dtype=like.dtype, device=like.device)
+
+
+def grouped_linear(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, *,
+                   bias: torch.Tensor | None = None, activation: str | None = None,
+                   residual: torch.Tensor | None = None, keep_z: bool = False,
+                   out: torch.Tensor | None = None, out_z: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None):
+    """A layer of experts in one product: Z_e = X_e W_e^T + bias_e, Y = act(Z) + residual, rows sorted
+    by expert as in grouped_matmul (a plain layer is a stack of one). Returns Y, or (Y, Z) with
+    ``keep_z`` (or a given ``out_z``): Z is what grouped_input_grad and grouped_bias_grad take.
+
+    bias: contiguous (experts, n); residual, ``out``, ``out_z``: (rows, n) at any row pitch, ``out`` may
+    be the residual itself; all of X's dtype. activation: None, "relu", "relu2" (relu squared), "gelu"
+    (z Phi(z)) or "silu". Between the product and each output's one rounding everything is float32.
+    Rows that belong to no expert come back as zeros in new outputs and are left as they are in given
+    ones. Autograd does not see the call."""
+    what = "grouped_linear"
+    code, groups, n, k, rows, ldx, _ = _layer_operands(X, W, False, "X", what)
+    act = _activation(activation, what)
+    keep_z = keep_z or out_z is not None
+    if bias is not None:
+        if tuple(bias.shape) != (groups, n) or bias.dtype != X.dtype:
+            raise ValueError(f"{what}: bias must be {(groups, n)} {X.dtype}, "
+                             f"got {tuple(bias.shape)} {bias.dtype}")
+        if not bias.is_contiguous():
+            raise ValueError(f"{what}: bias must be contiguous")
+    ldr = _rowwise(residual, "residual", (rows, n), X.dtype, what)
+    ldy = _rowwise(out, "out", (rows, n), X.dtype, what)
+    ldz = _rowwise(out_z, "out_z", (rows, n), X.dtype, what)
+    others = [("X", X), ("W", W), ("bias", bias), ("offsets", offsets)]
+    _itself_or_apart(out, "out", [("residual", residual)], others + [("out_z", out_z)], what)
+    _itself_or_apart(out_z, "out_z", [], others + [("residual", residual)], what)
+    dev = _grouped_checks([("X", X)], [W, bias, residual, out, out_z], offsets, groups, what)
+    with _OnStream(dev, stream) as handle:
+        fill = out is None and out_z is None        # else what is new is made of zeros
+        Y, Z = out, out_z
+        if Y is None:
+            Y, ldy = _new_rows(rows, n, X, not fill), n
+        if keep_z and Z is None:
+            Z, ldz = _new_rows(rows, n, X, not fill), n
+        keep, ws, nbytes = _grouped_workspace(0, code, groups, rows, n, k, dev, workspace)
+        check(load().grouped_linear(X.data_ptr(), ldx, W.data_ptr(), _ptr_or_none(bias), act,
+                                    _ptr_or_none(residual), ldr, _ptr_or_none(Z), ldz, Y.data_ptr(),
+                                    ldy, code, offsets.data_ptr(), groups, rows, n, k, int(fill), ws,
+                                    nbytes, handle), what)
+    return (Y, Z) if keep_z else Y
+
+
+def grouped_input_grad(dY: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, *,
+                       activation: str | None = None, Z: torch.Tensor | None = None,
+                       residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient of a layer's input: dX_e = (dY_e W_e) act'(Z) + residual. ``activation`` and ``Z`` are
+    those of the layer that produced the input (then dX is the gradient of that layer's Z); ``residual``
+    is a gradient that reaches the input past this layer. Z, residual and ``out``: (rows, k) at any row
+    pitch; ``out`` may be Z or the residual itself. relu's slope at 0 is 0. Rows that belong to no
+    expert as in grouped_matmul. Autograd does not see the call."""
+    what = "grouped_input_grad"
+    code, groups, n, k, rows, lddy, _ = _layer_operands(dY, W, True, "dY", what)
+    act = _activation(activation, what)
+    if (Z is None) != (activation is None):
+        raise ValueError(f"{what}: activation and Z go together")
+    ldz = _rowwise(Z, "Z", (rows, k), dY.dtype, what)
+    ldr = _rowwise(residual, "residual", (rows, k), dY.dtype, what)
+    lddx = _rowwise(out, "out", (rows, k), dY.dtype, what)
+    _itself_or_apart(out, "out", [("Z", Z), ("residual", residual)],
+                     [("dY", dY), ("W", W), ("offsets", offsets)], what)
+    dev = _grouped_checks([("dY", dY)], [W, Z, residual, out], offsets, groups, what)
+    with _OnStream(dev, stream) as handle:
+        dX = out
+        if dX is None:
+            dX, lddx = _new_rows(rows, k, dY, False), k
+        keep, ws, nbytes = _grouped_workspace(0, code, groups, rows, n, k, dev, workspace)
+        check(load().grouped_input_grad(dY.data_ptr(), lddy, W.data_ptr(), act, _ptr_or_none(Z), ldz,
+                                        _ptr_or_none(residual), ldr, dX.data_ptr(), lddx, code,
+                                        offsets.data_ptr(), groups, rows, n, k, int(out is None), ws,
+                                        nbytes, handle), what)
+    return dX
+
+
+def grouped_bias_grad(dY: torch.Tensor, offsets: torch.Tensor, *, activation: str | None = None,
+                      Z: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                      out_dtype: torch.dtype | None = None, out_dz: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None):
+    """Gradient of a layer's bias, db_e = the sum of expert e's rows of dZ = dY act'(Z), as (experts, n).
+    With an activation returns (db, dZ), else db (dZ is dY). dY, Z and ``out_dz``: (rows, n) at any row
+    pitch, ``out_dz`` may be dY or Z itself; db is of ``out``'s dtype, else ``out_dtype``, else dY's
+    (dY's or float32; the sums are float32 and of the unrounded products). Rows that belong to no
+    expert as in grouped_matmul. Autograd does not see the call."""
+    what = "grouped_bias_grad"
+    code = _dtype_code(dY)
+    act = _activation(activation, what)
+    if dY.dim() != 2:
+        raise ValueError(f"{what}: dY must be 2-D (rows x width)")
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError(f"{what}: offsets must hold at least two entries")
+    if (Z is None) != (activation is None):
+        raise ValueError(f"{what}: activation and Z go together")
+    if out_dz is not None and activation is None:
+        raise ValueError(f"{what}: without an activation dZ is dY, and out_dz is not written")
+    rows, n, groups = dY.shape[0], dY.shape[1], offsets.shape[0] - 1
+    lddy = _pitch(dY, "dY", what)
+    ldz = _rowwise(Z, "Z", (rows, n), dY.dtype, what)
+    lddz = _rowwise(out_dz, "out_dz", (rows, n), dY.dtype, what)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else dY.dtype
+    if out_dtype not in (dY.dtype, torch.float32):
+        raise TypeError(f"{what}: the output must be {dY.dtype} or float32, not {out_dtype}")
+    if out is not None:
+        if tuple(out.shape) != (groups, n) or out.dtype != out_dtype:
+            raise ValueError(f"{what}: out must be {(groups, n)} {out_dtype}, "
+                             f"got {tuple(out.shape)} {out.dtype}")
+        if not out.is_contiguous():
+            raise ValueError(f"{what}: out must be contiguous")
+    _itself_or_apart(out, "out", [], [("dY", dY), ("Z", Z), ("out_dz", out_dz),
+                                      ("offsets", offsets)], what)
+    _itself_or_apart(out_dz, "out_dz", [("dY", dY), ("Z", Z)], [("offsets", offsets)], what)
+    dev = _grouped_checks([("dY", dY)], [Z, out, out_dz], offsets, groups, what)
+    lib = load()
+    need = ctypes.c_size_t(0)
+    check(lib.mns_grouped_bias_grad_workspace_size(groups, rows, n, ctypes.byref(need)),
+          "mns_grouped_bias_grad_workspace_size")
+    with _OnStream(dev, stream) as handle:
+        db = torch.empty((groups, n), dtype=out_dtype, device=dev) if out is None else out
+        dZ = out_dz
+        if activation is not None and dZ is None:
+            dZ, lddz = _new_rows(rows, n, dY, False), n
+        ws = _workspace(need.value, dev, workspace) if need.value else None
+        check(lib.grouped_bias_grad(dY.data_ptr(), lddy, act, _ptr_or_none(Z), ldz, _ptr_or_none(dZ),
+                                    lddz, code, offsets.data_ptr(), groups, rows, n, db.data_ptr(),
+                                    MNS_F32 if out_dtype == torch.float32 else MNS_BF16,
+                                    int(out_dz is None), _ptr_or_none(ws),
+                                    0 if ws is None else ws.numel() * ws.element_size(), handle), what)
+    return db if activation is None else (db, dZ)
+
+
+def _ids(expert_ids: torch.Tensor, what: str) -> None:
+    if expert_ids.dtype != torch.int64 or not expert_ids.is_contiguous():
+        raise ValueError(f"{what}: expert_ids must be a contiguous int64 tensor")
+
+
+def expert_order(expert_ids: torch.Tensor, experts: int, *, order: bool = True,
+                 workspace: torch.Tensor | None = None, stream=None):
+    """A router's assignments by expert: (counts, offsets, order), int64 on the GPU, nothing read by the
+    host. expert_ids: int64, any shape ((tokens, top) as torch.topk gives it), contiguous; a value outside
+    0 .. experts - 1, such as -1 for a padded token, is an assignment to no expert. counts: (experts,).
+    offsets: (experts + 1,), what the grouped calls take. order: the flat indices of the assignments by
+    expert, each expert's in their own order, those of no expert last, so ``X[order // top]`` are the rows
+    the grouped calls take (None with ``order=False``). At most 2048 experts."""
+    what = "expert_order"
+    _ids(expert_ids, what)
+    dev = _on_one_gpu([expert_ids], what)
+    m = expert_ids.numel()
+    lib = load()
+    need = ctypes.c_size_t(0)
+    check(lib.mns_expert_order_workspace_size(m, experts, ctypes.byref(need)),
+          "mns_expert_order_workspace_size")
+    with _OnStream(dev, stream) as handle:
+        counts = torch.empty(experts, dtype=torch.int64, device=dev)
+        offsets = torch.empty(experts + 1, dtype=torch.int64, device=dev)
+        places = torch.empty(m, dtype=torch.int64, device=dev) if order else None
+        ws = _workspace(need.value, dev, workspace) if need.value else None
+        check(lib.expert_order(expert_ids.data_ptr(), m, experts, counts.data_ptr(),
+                               offsets.data_ptr(), _ptr_or_none(places), _ptr_or_none(ws),
+                               0 if ws is None else ws.numel() * ws.element_size(), handle), what)
+    return counts, offsets, places
+
+
+def balance_loss(logits: torch.Tensor, expert_ids: torch.Tensor, counts: torch.Tensor, *,
+                 scale: float = 1.0, grad: bool = True, out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None):
+    """The balance loss of a router and its gradient: (loss, dlogits), loss a float32 scalar tensor.
+
+    loss = scale E sum_e f_e P_e, with f_e = counts_e / N expert e's share of the N assignments and P_e the
+    mean of softmax(logits)_e over the assigned tokens, each weighted by its assignments; dlogits is its
+    gradient (f is taken as constant), for an upstream gradient of 1: ``scale`` takes any other. logits:
+    (tokens, E) float32 or bfloat16 at any row pitch; expert_ids: (tokens, top) int64; counts: (E,) int64,
+    expert_order's. A token without an assignment adds nothing and gets zeros, whatever its logits hold, and
+    so does one whose logits are all -inf. dlogits has the logits' dtype: a new tensor, ``out`` (may be the
+    logits themselves), or None with ``grad=False``. Autograd does not see the call."""
+    what = "balance_loss"
+    code = _dtype_code(logits)
+    if logits.dim() != 2 or expert_ids.dim() != 2 or expert_ids.shape[0] != logits.shape[0]:
+        raise ValueError(f"{what}: logits must be (tokens, experts) and expert_ids (tokens, top)")
+    _ids(expert_ids, what)
+    tokens, experts = logits.shape
+    if counts.dtype != torch.int64 or tuple(counts.shape) != (experts,) or not counts.is_contiguous():
+        raise ValueError(f"{what}: counts must be contiguous int64 of shape ({experts},)")
+    if out is not None and not grad:
+        raise ValueError(f"{what}: out without a gradient")
+    ldl = _pitch(logits, "logits", what)
+    ldd = _rowwise(out, "out", (tokens, experts), logits.dtype, what)
+    _itself_or_apart(out, "out", [("logits", logits)],
+                     [("expert_ids", expert_ids), ("counts", counts)], what)
+    dev = _on_one_gpu([logits, expert_ids, counts, out], what)
+    lib = load()
+    need = ctypes.c_size_t(0)
+    check(lib.mns_balance_workspace_size(tokens, experts, ctypes.byref(need)),
+          "mns_balance_workspace_size")
+    with _OnStream(dev, stream) as handle:
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+        dlogits = out
+        if grad and dlogits is None:
+            dlogits, ldd = _new_rows(tokens, experts, logits, False), experts
+        ws = _workspace(need.value, dev, workspace) if need.value else None
+        check(lib.balance_loss(logits.data_ptr(), ldl, code, expert_ids.data_ptr(),
+                               expert_ids.shape[1], counts.data_ptr(), tokens, experts, scale,
+                               loss.data_ptr(), _ptr_or_none(dlogits), ldd, _ptr_or_none(ws),
+                               0 if ws is None else ws.numel() * ws.element_size(), handle), what)
+    return loss, dlogits
+
+
+def _tensor_list(grads, out, what: str):
+    grads = _as_list(grads)
+    if not grads:
+        raise ValueError(f"{what}: no gradients")
+    outs = grads if out is None else _as_list(out)
+    if len(outs) != len(grads):
+        raise ValueError(f"{what}: out must hold as many tensors as grads")
+    arr = (_abi.MnsTensor * len(grads))()
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        if not g.is_contiguous():
+            raise ValueError(f"{what}: gradient {i} must be contiguous")
+        if o is not g and (o.shape != g.shape or o.dtype != g.dtype or not o.is_contiguous()):
+            raise ValueError(f"{what}: out {i} must match its gradient and be contiguous")
+        arr[i] = (g.data_ptr(), o.data_ptr(), g.numel(), _dtype_code(g))
+    return arr, len(grads), _on_one_gpu(grads if out is None else grads + outs, what)
+
+
+def _clip_workspace(count: int, dev, workspace):
+    need = ctypes.c_size_t(0)
+    check(load().mns_clip_workspace_size(count, ctypes.byref(need)), "mns_clip_workspace_size")
+    return _workspace(need.value, dev, workspace)
+
+
+def grad_norm(grads, *, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The global norm over one gradient or a list of them (contiguous, float32 or bfloat16 in any
+    mixture, any shapes): sqrt of the sum of every element's square, summed in float64, as a float32
+    scalar tensor. Nothing is read by the host."""
+    what = "grad_norm"
+    arr, count, dev = _tensor_list(grads, None, what)
+    with _OnStream(dev, stream) as handle:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        ws = _clip_workspace(count, dev, workspace)
+        check(load().grad_norm(arr, count, norm.data_ptr(), ws.data_ptr(),
+                               ws.numel() * ws.element_size(), handle), what)
+    return norm
+
+
+def clip_grad_norm(grads, max_norm: float, *, eps: float = 1e-6, out=None,
+                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Scales gradients by min(1, max_norm / (norm + eps)), norm their global norm (grad_norm), which is
+    returned: the step before muon_step. In place, or into ``out`` (a tensor, or a list of them, like the
+    gradients). A NaN norm makes every gradient NaN, an infinite one makes finite gradients 0. No output may
+    overlap another one or another gradient, so no gradient may be listed twice."""
+    what = "clip_grad_norm"
+    arr, count, dev = _tensor_list(grads, out, what)
+    with _OnStream(dev, stream) as handle:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        ws = _clip_workspace(count, dev, workspace)
+        check(load().clip_grad_norm(arr, count, max_norm, eps, norm.data_ptr(), ws.data_ptr(),
+                                    ws.numel() * ws.element_size(), handle), what)
+    return norm
 
 
 def _grouped_step(W, M, dY, X, offsets, v, normuon, what):

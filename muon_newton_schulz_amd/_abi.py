@@ -20,6 +20,12 @@ MNS_BF16 = 1
 MNS_NS_STANDARD = 0
 MNS_NS_GRAM = 1
 
+MNS_ACT_NONE = 0
+MNS_ACT_RELU = 1
+MNS_ACT_RELU2 = 2
+MNS_ACT_GELU = 3
+MNS_ACT_SILU = 4
+
 # Every symbol include/muon_ns.h declares.
 EXPORTS = (
     "mns_status_string", "mns_version", "mns_step_workspace_size", "muon_step",
@@ -29,6 +35,11 @@ EXPORTS = (
     "mns_grouped_workspace_size", "grouped_matmul", "grouped_weight_grad",
     "mns_grouped_step_workspace_size", "muon_step_grouped",
     "mns_ns_backward_workspace_size", "ns_orthogonalize_backward",
+    "grouped_linear", "grouped_input_grad",
+    "mns_grouped_bias_grad_workspace_size", "grouped_bias_grad",
+    "mns_expert_order_workspace_size", "expert_order",
+    "mns_balance_workspace_size", "balance_loss",
+    "mns_clip_workspace_size", "grad_norm", "clip_grad_norm",
 )
 
 
@@ -55,6 +66,15 @@ class MnsHparams(ctypes.Structure):
         ("beta2", ctypes.c_float),
         ("eps", ctypes.c_float),
         ("row_fraction", ctypes.c_double),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class MnsTensor(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("numel", ctypes.c_int64),
         ("dtype", ctypes.c_int32),
     ]
 
@@ -142,6 +162,32 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.muon_step_grouped.restype = ci
     lib.muon_step_grouped.argtypes = [vp, vp, vp, vp, i64, vp, i64, vp, i64, i64, i64, i64, hpp, vp,
                                       csz, vp]
+    lib.grouped_linear.restype = ci
+    lib.grouped_linear.argtypes = [vp, i64, vp, vp, ci, vp, i64, vp, i64, vp, i64, ci, vp, i64, i64,
+                                   i64, i64, ci, vp, csz, vp]
+    lib.grouped_input_grad.restype = ci
+    lib.grouped_input_grad.argtypes = [vp, i64, vp, ci, vp, i64, vp, i64, vp, i64, ci, vp, i64, i64,
+                                       i64, i64, ci, vp, csz, vp]
+    lib.mns_grouped_bias_grad_workspace_size.restype = ci
+    lib.mns_grouped_bias_grad_workspace_size.argtypes = [i64, i64, i64, sz]
+    lib.grouped_bias_grad.restype = ci
+    lib.grouped_bias_grad.argtypes = [vp, i64, ci, vp, i64, vp, i64, ci, vp, i64, i64, i64, vp, ci,
+                                      ci, vp, csz, vp]
+    lib.mns_expert_order_workspace_size.restype = ci
+    lib.mns_expert_order_workspace_size.argtypes = [i64, i64, sz]
+    lib.expert_order.restype = ci
+    lib.expert_order.argtypes = [vp, i64, i64, vp, vp, vp, vp, csz, vp]
+    lib.mns_balance_workspace_size.restype = ci
+    lib.mns_balance_workspace_size.argtypes = [i64, i64, sz]
+    lib.balance_loss.restype = ci
+    lib.balance_loss.argtypes = [vp, i64, ci, vp, i64, vp, i64, i64, cf, vp, vp, i64, vp, csz, vp]
+    tp = ctypes.POINTER(MnsTensor)
+    lib.mns_clip_workspace_size.restype = ci
+    lib.mns_clip_workspace_size.argtypes = [ci, sz]
+    lib.grad_norm.restype = ci
+    lib.grad_norm.argtypes = [tp, ci, vp, vp, csz, vp]
+    lib.clip_grad_norm.restype = ci
+    lib.clip_grad_norm.argtypes = [tp, ci, cf, cf, vp, vp, csz, vp]
     lib.mns_profile_set_flush.restype = ctypes.c_int
     lib.mns_profile_set_flush.argtypes = [vp, ctypes.c_size_t]
     _lib = lib

@@ -19,8 +19,8 @@ LIB_NAME = "libmuon_ns.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 ARCH = "gfx950"
 
-SOURCES = ["abi.cpp", "elementwise.hip", "gemm.hip", "grouped.hip",
-           "ns_backward.hip"]
+SOURCES = ["abi.cpp", "elementwise.hip", "gemm.hip", "grouped.hip", "grouped_bias.hip",
+           "ns_backward.hip", "router.hip", "clip.hip"]
 PROBE_NAME = "libmns_probe.so"
 PROBE_PATH = os.path.join(PKG, PROBE_NAME)
 PROBE_SOURCES = ["probe.hip"]

@@ -6,8 +6,10 @@
 // Algorithm 4 (Dion3 row selection), section "4. Megabatched Communication" (matrices of
 // one shape are processed as one batch).
 #include "muon_ns.h"
+#include "activation.h"
 #include "mns_internal.h"
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -893,6 +895,7 @@ mns_status normuon_scale(void* O, int dtype, int64_t batch, int64_t rows, int64_
 constexpr int64_t kMaxGroups = 65536;
 constexpr int64_t kMaxRows = int64_t(1) << 30;      // row arithmetic in the kernels is 32-bit
 constexpr int64_t kMaxPitch = int64_t(1) << 21;
+constexpr int64_t kMaxTensorElems = int64_t(1) << 40;
 
 static mns_status check_grouped(int dtype, int64_t groups, int64_t total_rows, int64_t n, int64_t k) {
   const mns_status st = check_dtype(dtype);
@@ -1005,6 +1008,354 @@ mns_status grouped_weight_grad(const void* dY, int64_t lddy, const void* X, int6
   d.k = k;
   d.weight_grad = true;
   return run_grouped(d, workspace, workspace_bytes, stream);
+}
+
+// ---- layers of experts ---------------------------------------------------------------------------
+
+static_assert((int)MNS_ACT_NONE == ACT_NONE && (int)MNS_ACT_RELU == ACT_RELU &&
+              (int)MNS_ACT_RELU2 == ACT_RELU2 && (int)MNS_ACT_GELU == ACT_GELU &&
+              (int)MNS_ACT_SILU == ACT_SILU, "one numbering");
+
+static bool act_ok(int act) { return act >= MNS_ACT_NONE && act <= MNS_ACT_SILU; }
+
+static bool pitch_ok(const void* p, int64_t ld, int64_t width) {
+  return !p || (ld >= width && ld <= kMaxPitch);
+}
+
+// The byte range of rows x width elements, empty for no rows.
+struct Range {
+  uintptr_t lo, hi;
+};
+static Range range_of(const void* p, int64_t rows, int64_t ld, int64_t width, size_t es) {
+  const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+  if (!p || rows < 1) return {b, b};
+  return {b, b + ((size_t)(rows - 1) * ld + width) * es};
+}
+static bool apart(const Range& a, const Range& b) { return a.hi <= b.lo || b.hi <= a.lo; }
+
+mns_status grouped_linear(const void* X, int64_t ldx, const void* W, const void* bias, int activation,
+                          const void* R, int64_t ldr, void* Z, int64_t ldz, void* Y, int64_t ldy,
+                          int dtype, const int64_t* offsets, int64_t groups, int64_t total_rows,
+                          int64_t n, int64_t k, int fill_rest, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  const mns_status st = check_grouped(dtype, groups, total_rows, n, k);
+  if (st != MNS_OK) return st;
+  if (!act_ok(activation) || (fill_rest != 0 && fill_rest != 1)) return MNS_ERR_PARAM;
+  if (ldx < k || ldx > kMaxPitch || ldy < n || ldy > kMaxPitch || !pitch_ok(R, ldr, n) ||
+      !pitch_ok(Z, ldz, n))
+    return MNS_ERR_SHAPE;
+  if (!W || !offsets || (total_rows > 0 && (!X || !Y))) return MNS_ERR_NULL;
+  const size_t es = store_bytes(dtype);
+  if (!aligned(X, es) || !aligned(W, es) || !aligned(Y, es) || !aligned(bias, es) ||
+      !aligned(R, es) || !aligned(Z, es) || !aligned(offsets, 8))
+    return MNS_ERR_PARAM;
+  const Range x = range_of(X, total_rows, ldx, k, es), w = range_of(W, groups * n, k, k, es),
+              b = range_of(bias, groups, n, n, es), r = range_of(R, total_rows, ldr, n, es),
+              z = range_of(Z, total_rows, ldz, n, es), y = range_of(Y, total_rows, ldy, n, es),
+              o = range_of(offsets, groups + 1, 1, 1, 8);
+  if (!apart(y, x) || !apart(y, w) || !apart(y, b) || !apart(y, z) || !apart(y, o) ||
+      !apart(z, x) || !apart(z, w) || !apart(z, b) || !apart(z, r) || !apart(z, o) ||
+      (!apart(y, r) && (Y != R || ldy != ldr)))
+    return MNS_ERR_PARAM;
+  if (total_rows == 0) return MNS_OK;
+  GroupedDesc d;
+  d.store = d.out_store = store_of(dtype);
+  d.A = X; d.lda = ldx;
+  d.B = W;
+  d.C = Y; d.ldc = ldy;
+  d.offsets = offsets;
+  d.groups = groups;
+  d.total_rows = total_rows;
+  d.n = n;
+  d.k = k;
+  d.fill_rest = fill_rest == 1;
+  d.layer = true;
+  d.bias = bias;
+  d.R = R; d.ldr = ldr;
+  d.Z = Z; d.ldz = ldz;
+  d.act = activation;
+  return run_grouped(d, workspace, workspace_bytes, stream);
+}
+
+mns_status grouped_input_grad(const void* dY, int64_t lddy, const void* W, int activation,
+                              const void* Z, int64_t ldz, const void* R, int64_t ldr, void* dX,
+                              int64_t lddx, int dtype, const int64_t* offsets, int64_t groups,
+                              int64_t total_rows, int64_t n, int64_t k, int fill_rest,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  const mns_status st = check_grouped(dtype, groups, total_rows, n, k);
+  if (st != MNS_OK) return st;
+  if (!act_ok(activation) || (fill_rest != 0 && fill_rest != 1)) return MNS_ERR_PARAM;
+  if (lddy < n || lddy > kMaxPitch || lddx < k || lddx > kMaxPitch || !pitch_ok(R, ldr, k) ||
+      !pitch_ok(Z, ldz, k))
+    return MNS_ERR_SHAPE;
+  const bool act = activation != MNS_ACT_NONE;
+  if (!act && Z) return MNS_ERR_PARAM;
+  if (!W || !offsets || (total_rows > 0 && (!dY || !dX || (act && !Z)))) return MNS_ERR_NULL;
+  const size_t es = store_bytes(dtype);
+  if (!aligned(dY, es) || !aligned(W, es) || !aligned(dX, es) || !aligned(R, es) ||
+      !aligned(Z, es) || !aligned(offsets, 8))
+    return MNS_ERR_PARAM;
+  const Range g = range_of(dY, total_rows, lddy, n, es), w = range_of(W, groups * n, k, k, es),
+              r = range_of(R, total_rows, ldr, k, es), z = range_of(Z, total_rows, ldz, k, es),
+              x = range_of(dX, total_rows, lddx, k, es), o = range_of(offsets, groups + 1, 1, 1, 8);
+  if (!apart(x, g) || !apart(x, w) || !apart(x, o) || (!apart(x, r) && (dX != R || lddx != ldr)) ||
+      (!apart(x, z) && (dX != Z || lddx != ldz)))
+    return MNS_ERR_PARAM;
+  if (total_rows == 0) return MNS_OK;
+  GroupedDesc d;
+  d.store = d.out_store = store_of(dtype);
+  d.A = dY; d.lda = lddy;
+  d.B = W;
+  d.C = dX; d.ldc = lddx;
+  d.offsets = offsets;
+  d.groups = groups;
+  d.total_rows = total_rows;
+  d.n = n;
+  d.k = k;
+  d.transpose_w = true;
+  d.fill_rest = fill_rest == 1;
+  d.layer = true;
+  d.R = R; d.ldr = ldr;
+  d.Z = const_cast<void*>(Z); d.ldz = ldz;       // read only (transpose_w)
+  d.act = activation;
+  return run_grouped(d, workspace, workspace_bytes, stream);
+}
+
+static mns_status check_bias_grad(int64_t groups, int64_t total_rows, int64_t n) {
+  if (groups < 1 || groups > kMaxGroups || total_rows < 0 || total_rows > kMaxRows || n < 1 ||
+      n > kMaxDim || bias_grad_blocks(groups, total_rows, n) > kMaxElems)
+    return MNS_ERR_SHAPE;
+  return MNS_OK;
+}
+
+mns_status mns_grouped_bias_grad_workspace_size(int64_t groups, int64_t total_rows, int64_t n,
+                                                size_t* bytes) {
+  if (!bytes) return MNS_ERR_NULL;
+  const mns_status st = check_bias_grad(groups, total_rows, n);
+  if (st != MNS_OK) return st;
+  *bytes = bias_grad_workspace(groups, total_rows, n);
+  return MNS_OK;
+}
+
+mns_status grouped_bias_grad(const void* dY, int64_t lddy, int activation, const void* Z, int64_t ldz,
+                             void* dZ, int64_t lddz, int dtype, const int64_t* offsets,
+                             int64_t groups, int64_t total_rows, int64_t n, void* db, int out_dtype,
+                             int fill_rest, void* workspace, size_t workspace_bytes, void* stream) {
+  mns_status st = check_dtype(dtype);
+  if (st != MNS_OK) return st;
+  st = check_dtype(out_dtype);
+  if (st != MNS_OK) return st;
+  if (out_dtype != dtype && out_dtype != MNS_F32) return MNS_ERR_DTYPE;
+  st = check_bias_grad(groups, total_rows, n);
+  if (st != MNS_OK) return st;
+  if (!act_ok(activation) || (fill_rest != 0 && fill_rest != 1)) return MNS_ERR_PARAM;
+  if (lddy < n || lddy > kMaxPitch || !pitch_ok(Z, ldz, n) || !pitch_ok(dZ, lddz, n))
+    return MNS_ERR_SHAPE;
+  const bool act = activation != MNS_ACT_NONE;
+  if (!act && Z) return MNS_ERR_PARAM;
+  if (!db || !offsets || (total_rows > 0 && (!dY || (act && !Z)))) return MNS_ERR_NULL;
+  const size_t es = store_bytes(dtype), os = store_bytes(out_dtype);
+  if (!aligned(dY, es) || !aligned(Z, es) || !aligned(dZ, es) || !aligned(db, os) ||
+      !aligned(offsets, 8))
+    return MNS_ERR_PARAM;
+  const Range g = range_of(dY, total_rows, lddy, n, es), z = range_of(Z, total_rows, ldz, n, es),
+              x = range_of(dZ, total_rows, lddz, n, es), b = range_of(db, groups, n, n, os),
+              o = range_of(offsets, groups + 1, 1, 1, 8);
+  if (!apart(b, g) || !apart(b, z) || !apart(b, x) || !apart(b, o) || !apart(x, o) ||
+      (!apart(x, g) && (dZ != dY || lddz != lddy)) || (!apart(x, z) && (dZ != Z || lddz != ldz)))
+    return MNS_ERR_PARAM;
+  BiasGradDesc d;
+  d.store = store_of(dtype);
+  d.out_store = store_of(out_dtype);
+  d.dY = dY; d.lddy = lddy;
+  d.Z = Z; d.ldz = ldz;
+  d.dZ = dZ; d.lddz = lddz;
+  d.db = db;
+  d.offsets = offsets;
+  d.groups = groups;
+  d.total_rows = total_rows;
+  d.n = n;
+  d.act = activation;
+  d.fill_rest = fill_rest == 1;
+  const size_t need = bias_grad_workspace(groups, total_rows, n);
+  if (need) {
+    st = check_ws(workspace, workspace_bytes, need);
+    if (st != MNS_OK) return st;
+    d.workspace = static_cast<float*>(workspace);
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const double bytes = (double)total_rows * n * es * (1 + (Z ? 1 : 0) + (dZ ? 1 : 0));
+  MNS_HIP(timed("grouped_bias_grad", 0, bytes, s, [&] { return bias_grad(d, s); }));
+  return MNS_OK;
+}
+
+// ---- a router's bookkeeping ------------------------------------------------------------------------
+
+static mns_status check_routed(int64_t assignments, int64_t experts) {
+  return assignments >= 0 && assignments <= kMaxRows && experts >= 1 && experts <= kMaxRouted
+             ? MNS_OK : MNS_ERR_SHAPE;
+}
+
+mns_status mns_expert_order_workspace_size(int64_t assignments, int64_t experts, size_t* bytes) {
+  if (!bytes) return MNS_ERR_NULL;
+  const mns_status st = check_routed(assignments, experts);
+  if (st != MNS_OK) return st;
+  *bytes = order_workspace(assignments, experts);
+  return MNS_OK;
+}
+
+mns_status expert_order(const int64_t* ids, int64_t assignments, int64_t experts, int64_t* counts,
+                        int64_t* offsets, int64_t* order, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  mns_status st = check_routed(assignments, experts);
+  if (st != MNS_OK) return st;
+  if (!counts || !offsets || (assignments > 0 && !ids)) return MNS_ERR_NULL;
+  if (!aligned(ids, 8) || !aligned(counts, 8) || !aligned(offsets, 8) || !aligned(order, 8))
+    return MNS_ERR_PARAM;
+  const Range all[4] = {range_of(ids, assignments, 1, 1, 8), range_of(counts, experts, 1, 1, 8),
+                        range_of(offsets, experts + 1, 1, 1, 8),
+                        range_of(order, assignments, 1, 1, 8)};
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < i; ++j)
+      if (!apart(all[i], all[j])) return MNS_ERR_PARAM;
+  const size_t need = order_workspace(assignments, experts);
+  if (need) {
+    st = check_ws(workspace, workspace_bytes, need);
+    if (st != MNS_OK) return st;
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  MNS_HIP(timed("expert_order", 0, 8.0 * assignments * (order ? 2 : 1), s, [&] {
+    return mns::expert_order(ids, assignments, experts, counts, offsets, order, workspace, s); }));
+  return MNS_OK;
+}
+
+mns_status mns_balance_workspace_size(int64_t tokens, int64_t experts, size_t* bytes) {
+  if (!bytes) return MNS_ERR_NULL;
+  const mns_status st = check_routed(tokens, experts);
+  if (st != MNS_OK) return st;
+  *bytes = balance_workspace(tokens, experts);
+  return MNS_OK;
+}
+
+mns_status balance_loss(const void* logits, int64_t ldl, int dtype, const int64_t* ids, int64_t top,
+                        const int64_t* counts, int64_t tokens, int64_t experts, float scale,
+                        float* loss, void* dlogits, int64_t ldd, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  mns_status st = check_dtype(dtype);
+  if (st != MNS_OK) return st;
+  st = check_routed(tokens, experts);
+  if (st != MNS_OK) return st;
+  if (top < 1 || (tokens > 0 && top > kMaxRows / tokens)) return MNS_ERR_SHAPE;
+  if (ldl < experts || ldl > kMaxPitch || !pitch_ok(dlogits, ldd, experts)) return MNS_ERR_SHAPE;
+  if (!std::isfinite(scale)) return MNS_ERR_PARAM;
+  if (!counts || !loss || (tokens > 0 && (!logits || !ids))) return MNS_ERR_NULL;
+  const size_t es = store_bytes(dtype);
+  if (!aligned(logits, es) || !aligned(dlogits, es) || !aligned(ids, 8) || !aligned(counts, 8) ||
+      !aligned(loss, 4))
+    return MNS_ERR_PARAM;
+  const Range l = range_of(logits, tokens, ldl, experts, es),
+              g = range_of(dlogits, tokens, ldd, experts, es),
+              i = range_of(ids, tokens, top, top, 8), c = range_of(counts, experts, 1, 1, 8),
+              o = range_of(loss, 1, 1, 1, 4);
+  if (!apart(o, l) || !apart(o, g) || !apart(o, i) || !apart(o, c) || !apart(g, i) ||
+      !apart(g, c) || (!apart(g, l) && (dlogits != logits || ldd != ldl)))
+    return MNS_ERR_PARAM;
+  const size_t need = balance_workspace(tokens, experts);
+  if (need) {
+    st = check_ws(workspace, workspace_bytes, need);
+    if (st != MNS_OK) return st;
+  }
+  BalanceDesc d;
+  d.store = store_of(dtype);
+  d.logits = logits; d.ld = ldl;
+  d.ids = ids;
+  d.counts = counts;
+  d.grad = dlogits; d.ldg = ldd;
+  d.loss = loss;
+  d.tokens = tokens;
+  d.experts = experts;
+  d.top = top;
+  d.scale = scale;
+  d.workspace = workspace;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const double bytes = (double)tokens * (experts * es * (dlogits ? 2 : 1) + 8.0 * top);
+  MNS_HIP(timed("balance_loss", 0, bytes, s, [&] { return balance(d, s); }));
+  return MNS_OK;
+}
+
+// ---- global norm and clipping ----------------------------------------------------------------------
+
+constexpr int kMaxTensors = 65536;
+
+mns_status mns_clip_workspace_size(int count, size_t* bytes) {
+  if (!bytes) return MNS_ERR_NULL;
+  if (count < 1 || count > kMaxTensors) return MNS_ERR_SHAPE;
+  *bytes = clip_workspace(count);
+  return MNS_OK;
+}
+
+static mns_status run_clip(const mns_tensor* tensors, int count, bool scale, float max_norm, float eps,
+                           float* norm, void* workspace, size_t workspace_bytes, void* stream) {
+  if (count < 1 || count > kMaxTensors) return MNS_ERR_SHAPE;
+  if (!tensors || !norm) return MNS_ERR_NULL;
+  if (scale && (!(max_norm >= 0.f) || !(eps >= 0.f) || !std::isfinite(eps))) return MNS_ERR_PARAM;
+  if (!aligned(norm, 4)) return MNS_ERR_PARAM;
+  double bytes = 0;
+  std::vector<ClipTensor> list;
+  std::vector<Range> outs;
+  try {
+    list.resize(count);
+    outs.reserve(count);
+  } catch (...) {
+    return MNS_ERR_PARAM;
+  }
+  for (int i = 0; i < count; ++i) {
+    const mns_tensor& t = tensors[i];
+    const mns_status st = check_dtype(t.dtype);
+    if (st != MNS_OK) return st;
+    if (t.numel < 0 || t.numel > kMaxTensorElems) return MNS_ERR_SHAPE;
+    if (t.numel > 0 && (!t.in || (scale && !t.out))) return MNS_ERR_NULL;
+    const size_t es = store_bytes(t.dtype);
+    if (!aligned(t.in, es) || (scale && !aligned(t.out, es))) return MNS_ERR_PARAM;
+    list[i] = {t.in, scale ? t.out : nullptr, t.numel, store_of(t.dtype)};
+    bytes += (double)t.numel * es;
+    if (scale && t.numel > 0) outs.push_back(range_of(t.out, 1, 1, t.numel, es));
+  }
+  if (scale) {
+    const Range nr = range_of(norm, 1, 1, 1, 4);
+    outs.push_back(nr);
+    std::sort(outs.begin(), outs.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    for (size_t i = 1; i < outs.size(); ++i)
+      if (outs[i - 1].hi > outs[i].lo) return MNS_ERR_PARAM;
+    // An input may meet no output but its own, and that one only as a whole. The outputs lie apart, so
+    // those that meet it are neighbours in the sorted list.
+    for (int i = 0; i < count; ++i) {
+      if (tensors[i].numel == 0) continue;
+      const Range in = range_of(tensors[i].in, 1, 1, tensors[i].numel, store_bytes(tensors[i].dtype));
+      auto it = std::lower_bound(outs.begin(), outs.end(), in.lo,
+                                 [](const Range& r, uintptr_t v) { return r.hi <= v; });
+      for (; it != outs.end() && it->lo < in.hi; ++it)
+        if (tensors[i].in != tensors[i].out || it->lo != in.lo || it->hi != in.hi)
+          return MNS_ERR_PARAM;
+    }
+  }
+  const mns_status st = check_ws(workspace, workspace_bytes, clip_workspace(count));
+  if (st != MNS_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  MNS_HIP(timed(scale ? "clip_grad_norm" : "grad_norm", 0, bytes * (scale ? 3 : 1), s, [&] {
+    return clip_grads(list.data(), count, scale, max_norm, eps, norm,
+                      static_cast<double*>(workspace), s); }));
+  return MNS_OK;
+}
+
+mns_status grad_norm(const mns_tensor* tensors, int count, float* norm, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  return run_clip(tensors, count, false, 0.f, 0.f, norm, workspace, workspace_bytes, stream);
+}
+
+mns_status clip_grad_norm(const mns_tensor* tensors, int count, float max_norm, float eps, float* norm,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  return run_clip(tensors, count, true, max_norm, eps, norm, workspace, workspace_bytes, stream);
 }
 
 // ---- gradient of the orthogonalisation ---------------------------------------------------------

@@ -9,8 +9,11 @@
 // the kernels only: no host copy, no synchronisation, so the calls can be captured. Every offset
 // is clamped to [0, total_rows] and an end before its begin is an empty group, so wrong offsets
 // give wrong results but never an access outside the buffers.
+#include "activation.h"
+#include "grouped_walk.h"
 #include "lds_dma.h"
 #include "mns_internal.h"
+#include "row_vectors.h"
 
 #include <type_traits>
 
@@ -23,114 +26,17 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 enum Form { NT = 0, NN = 1, TN = 2 };
 
-struct GroupedArgs {
-  const void* A; const void* B; const void* D; void* C;
-  int64_t lda, ldb, ldc;        // row pitches, elements (ldc: of C and D)
-  int64_t sB, sC;               // per-expert strides of W (NT, NN) and of C, D (TN)
-  const int64_t* offsets;
-  int total_rows;
-  int groups;
-  int N, K;                     // NT, NN: output columns and reduction; TN: output rows, columns
-  int tiles_n;
-  int most_tiles;               // NT, NN: of rows that belong to one expert each
-  int fill_rest;                // NT, NN: rows of no expert are written as zeros
-  float beta;                   // TN
-  int split_cap;                // most parts of a tile of the last round (k_grouped_big)
-  float* partial;               // their sums, 256 KB a part
+// A product with a layer's epilogue: NT: Z = X W^T + bias, C = act(Z) + R, Z kept where it is given;
+// NN: C = (dY W) act'(Z) + R. The forward and input-gradient kernels take either arguments.
+struct LayerArgs : GroupedArgs {
+  const void* bias;             // groups x N, or null
+  const void* R;                // the rows of C, pitch ldr, or null
+  void* Z;                      // the rows of C, pitch ldz: written (NT) or read (NN), or null
+  int64_t ldr, ldz;
+  int act;
 };
-
-__device__ __forceinline__ int clamp_row(int64_t v, int lo, int hi) {
-  return v < lo ? lo : v > hi ? hi : (int)v;
-}
-
-// Rows [lo, hi) of expert e.
-__device__ __forceinline__ void expert_rows(const GroupedArgs& p, int e, int& lo, int& hi) {
-  lo = clamp_row(p.offsets[e], 0, p.total_rows);
-  hi = clamp_row(p.offsets[e + 1], lo, p.total_rows);
-}
-
-// Where a block of a forward or input-gradient call works: an expert (-1: the rows of no expert,
-// to be filled with zeros), its rows [lo, hi), and the block's place among the expert's tiles.
-struct Place {
-  int expert, lo, hi, inside;
-};
-
-// The list of tiles that walks the experts in order, each cut into row tiles of BM rows with
-// tiles_n tiles per row tile (with `rest`, the rows before the first expert and behind the last
-// one come first and last). Every wave reads 64 experts' bounds at a time, one per lane, and adds
-// their tile counts by a shuffle scan, so it finds its place by itself, without a launch or a
-// barrier; up to 64 entries stay in registers for the next lookups.
-struct Walk {
-  int lo, hi;            // this lane's expert
-  int incl;              // tiles up to and with it, from the start of its 64
-  int total;             // tiles of all experts
-};
-
-__device__ __forceinline__ void walk_batch(const GroupedArgs& p, int BM, int tiles_n, int rest,
-                                           int g0, Walk& w) {
-  const int lane = threadIdx.x & 63;
-  const int g = g0 + lane, e = g - rest;
-  w.lo = w.hi = 0;
-  if (g < p.groups + 2 * rest) {
-    if (e < 0) {
-      w.hi = clamp_row(p.offsets[0], 0, p.total_rows);
-    } else if (e >= p.groups) {
-      int first;
-      expert_rows(p, p.groups - 1, first, w.lo);     // from the last expert's end
-      w.hi = p.total_rows;
-    } else {
-      expert_rows(p, e, w.lo, w.hi);
-    }
-  }
-  // The host refuses calls of 2^31 tiles; only offsets that overlap can add up to more (walk_start
-  // then cuts the list off, find_place checks what it finds).
-  w.incl = (w.hi - w.lo + (BM - 1)) / BM * tiles_n;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int up = __shfl_up(w.incl, o);
-    if (lane >= o) w.incl += up;
-  }
-}
-
-// The first batch, and the total over all of them: at most most_tiles, so that overlapping offsets
-// (experts that each claim all rows) do not multiply the rounds of blocks that go from tile to tile.
-__device__ __forceinline__ Walk walk_start(const GroupedArgs& p, int BM, int tiles_n, int rest) {
-  Walk w;
-  const int count = p.groups + 2 * rest;
-  int64_t total = 0;
-  for (int g0 = (count - 1) / 64 * 64; g0 >= 0; g0 -= 64) {
-    walk_batch(p, BM, tiles_n, rest, g0, w);
-    total += (unsigned)__builtin_amdgcn_readlane(w.incl, 63);
-  }
-  w.total = total < p.most_tiles ? (int)total : p.most_tiles;
-  return w;
-}
-
-// The place of position `lin` (false past the last tile). Everything found is read from one lane
-// into scalar registers: a buffer resource computed from vector registers would make each load a
-// loop over its values.
-__device__ __forceinline__ bool find_place(const GroupedArgs& p, int BM, int tiles_n, int rest,
-                                           Walk w, int lin, Place& at) {
-  if (lin >= w.total) return false;
-  const int count = p.groups + 2 * rest;
-  int g0 = 0;
-  if (count > 64) {
-    for (; g0 < count; g0 += 64) {
-      walk_batch(p, BM, tiles_n, rest, g0, w);
-      const int sum = __builtin_amdgcn_readlane(w.incl, 63);
-      if (lin < sum) break;
-      lin -= sum;
-    }
-  }
-  const unsigned long long over = __ballot(w.incl > lin);
-  const int src = over ? __ffsll(over) - 1 : 63;
-  at.inside = lin - (src ? __builtin_amdgcn_readlane(w.incl, src - 1) : 0);
-  at.lo = __builtin_amdgcn_readlane(w.lo, src);
-  at.hi = __builtin_amdgcn_readlane(w.hi, src);
-  const int ge = g0 + src - rest;
-  at.expert = ge >= 0 && ge < p.groups ? ge : -1;
-  return at.inside >= 0 && at.inside < (at.hi - at.lo + (BM - 1)) / BM * tiles_n;
-}
+template <typename Args>
+constexpr bool kLayer = std::is_same_v<Args, LayerArgs>;
 
 template <typename T>
 struct Frag;
@@ -153,24 +59,6 @@ struct Frag<float> {
                                                  0, 0, 0);
   }
 };
-
-// 16 bytes from any address of T's alignment, of which the first `valid` elements exist; the
-// others read as zero and are not touched. (A whole chunk is one 16-byte load: this part loads
-// from any address.)
-template <typename T>
-__device__ __forceinline__ u32x4 load_chunk(const T* p, int valid) {
-  constexpr int VEC = Frag<T>::VEC;
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (valid >= VEC) {
-    __builtin_memcpy(&v, p, 16);
-  } else if (valid > 0) {
-    T e[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) e[i] = i < valid ? p[i] : (T)0.f;
-    __builtin_memcpy(&v, e, 16);
-  }
-  return v;
-}
 
 // Writes a wave's FM x FN fragments of 32 x 32 at rows m0, columns n0 of the tile whose first
 // element is `origin`: acc[i][j][4g + e] is row 32 i + (lane & 31), column 32 j + 8 g + 4 (lane >> 5)
@@ -221,6 +109,98 @@ __device__ __forceinline__ void store_fragments(const GroupedArgs& p, const floa
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (n + e < n_valid) out[n + e] = t[e];
+      }
+    }
+  }
+}
+
+// ---- the epilogue of a layer ------------------------------------------------------------------
+//
+// A wave's fragments go through 4 KB of LDS of its own, 32 rows x 32 columns or 16 x 64 of float32 at a
+// time, so that a lane holds eight consecutive columns of a row: the addends and outputs then move as
+// whole pieces of 16 bytes, 128-byte lines of bfloat16, and one copy of the activation's code serves
+// all fragments of a row. Everything is float32 until the output's one rounding; act sees the sum, not
+// Z as it is kept (the gradient then is that of the rounded Z, up to 2^-8 of it away).
+// Zeros over a tile of rows that belong to no expert (m_rows x n_cols of it, threads of one block).
+template <typename T, int FORM>
+__device__ __forceinline__ void zero_tile(const LayerArgs& p, int64_t row, int col, int m_rows,
+                                          int n_cols) {
+  for (int i = threadIdx.x; i < m_rows * n_cols; i += blockDim.x) {
+    const int m = i / n_cols, n = col + i % n_cols;
+    static_cast<T*>(p.C)[(row + m) * p.ldc + n] = (T)0.f;
+    if (FORM == NT && p.Z) static_cast<T*>(p.Z)[(row + m) * p.ldz + n] = (T)0.f;
+  }
+}
+
+// The epilogue of a wave's FM x FN fragments (as in store_fragments) at rows m0, columns n0 of the tile
+// that starts at row `row`, column `col`.
+template <typename T, int FORM, int FM, int FN>
+__device__ __forceinline__ void finish_fragments(const LayerArgs& p, const floatx16 (&acc)[FM][FN],
+                                                 floatx4* stage, int expert, int64_t row, int col,
+                                                 int m0, int n0, int m_valid, int n_valid) {
+  constexpr bool EXACT = sizeof(T) == 4;
+  constexpr int ROWS = 32 / FN, CH = 8 * FN, LANES = 4 * FN, STEP = 64 / LANES;
+  int ln = threadIdx.x & 63;
+  asm volatile("" : "+v"(ln));       // addresses computed here, not kept across a caller's loop
+  const int c = ln % LANES, r0 = ln / LANES;
+  const int n = n0 + 8 * c, left = n_valid - n;
+  // chunk k of staged row r: the 16-byte accesses of 16 lanes cover all banks, writing and reading
+  auto at = [](int r, int k) { return r * CH + (k ^ (FN == 2 ? r & 15 : (r >> 1) & 7)); };
+  Eight<T> bias;
+  if (FORM == NT)
+    bias.load(static_cast<const T*>(p.bias) + (int64_t)expert * p.N + col + n, p.bias ? left : 0);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+#pragma unroll
+    for (int pass = 0; pass < FN; ++pass) {
+      const int m = m0 + 32 * i + ROWS * pass + r0;
+      Eight<T> z[2], r[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int64_t t = row + m + STEP * q;
+        const int have = m + STEP * q < m_valid ? left : 0;
+        if (FORM == NN)
+          z[q].load(static_cast<const T*>(p.Z) + t * p.ldz + col + n, p.Z ? have : 0);
+        r[q].load(static_cast<const T*>(p.R) + t * p.ldr + col + n, p.R ? have : 0);
+      }
+      if (FN == 1 || ((ln >> 4) & 1) == pass) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            floatx4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g + e];
+            stage[at(ln & (ROWS - 1), 8 * j + 2 * g + (ln >> 5))] = v;
+          }
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const floatx4 lo = stage[at(r0 + STEP * q, 2 * c)], hi = stage[at(r0 + STEP * q, 2 * c + 1)];
+        if (m + STEP * q >= m_valid || left <= 0) continue;
+        const int64_t t = row + m + STEP * q;
+        float v[8], x[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = lo[e], v[4 + e] = hi[e];
+        Eight<T> out;
+        if constexpr (FORM == NT) {
+          bias.get(x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += x[e];
+          if (p.Z) {
+            out.set(v);
+            out.store(static_cast<T*>(p.Z) + t * p.ldz + col + n, left);
+          }
+          activate<EXACT>(p.act, v);
+        } else {
+          z[q].get(x);
+          times_slope<EXACT>(p.act, v, x);
+        }
+        r[q].get(x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += x[e];
+        out.set(v);
+        out.store(static_cast<T*>(p.C) + t * p.ldc + col + n, left);
       }
     }
   }
@@ -288,8 +268,8 @@ __device__ __forceinline__ void store_lanes(const GroupedArgs& p, const floatx16
 // With an addend, few rows: bound by HBM (384 rows over 16 experts of 2048 x 2048, float32 output: 105 us,
 // 5.1 TB/s); else by the loads' latency (one k-tile ahead is what two blocks a CU have registers
 // for; two ahead measured 10 to 60 % slower).
-template <typename T, typename TO, int FORM>
-__global__ __launch_bounds__(256) void k_grouped(GroupedArgs p) {
+template <typename T, typename TO, int FORM, typename Args>
+__global__ __launch_bounds__(256) void k_grouped(Args p) {
   using F = Frag<T>;
   constexpr int BM = 128, BN = 128, VEC = F::VEC, BK = F::BK;
   constexpr int PITCH = BK + VEC;                        // 144 bytes
@@ -321,6 +301,12 @@ __global__ __launch_bounds__(256) void k_grouped(GroupedArgs p) {
     expert = at.expert;
     m0 = at.lo + at.inside / p.tiles_n * BM;
     n0 = at.inside % p.tiles_n * BN;
+    if constexpr (kLayer<Args>) {
+      if (expert < 0) {
+        zero_tile<T, FORM>(p, m0, n0, at.hi - m0 < BM ? at.hi - m0 : BM, p.N - n0 < BN ? p.N - n0 : BN);
+        return;
+      }
+    }
     red = expert < 0 ? 0 : p.K;
     A = static_cast<const T*>(p.A) + m0 * p.lda;
     B = static_cast<const T*>(p.B) + (expert < 0 ? 0 : expert) * p.sB +
@@ -427,6 +413,10 @@ __global__ __launch_bounds__(256) void k_grouped(GroupedArgs p) {
       for (int j = 0; j < 2; ++j)
         store_lanes<TO>(p, acc[i][j], origin, wm * 64 + 32 * i, wn * 64 + 32 * j, m_valid, n_valid,
                         add[i][j]);
+  } else if constexpr (kLayer<Args>) {
+    // (behind the loop's last barrier the operands' LDS is free)
+    finish_fragments<T, FORM>(p, acc, reinterpret_cast<floatx4*>(As) + wave * 256, expert, m0, n0,
+                              wm * 64, wn * 64, m_valid, n_valid);
   } else {
     store_fragments<TO, 2, 2, false>(p, acc, origin, wm * 64, wn * 64, m_valid, n_valid);
   }
@@ -437,8 +427,8 @@ __global__ __launch_bounds__(256) void k_grouped(GroupedArgs p) {
 // no barrier in the loop; the four sums are added in wave order through LDS. A fourth of the steps
 // of memory latency one after the other, and four times the blocks. Bound by those steps (1021 rows
 // over 5 experts of 513 x 1277, bfloat16, input gradient: 23 us).
-template <typename T, int FORM>
-__global__ __launch_bounds__(256) void k_grouped_split(GroupedArgs p) {
+template <typename T, int FORM, typename Args>
+__global__ __launch_bounds__(256) void k_grouped_split(Args p) {
   using F = Frag<T>;
   constexpr int BM = 64, BN = 64, VEC = F::VEC, BK = F::BK, PITCH = BK + VEC;
   constexpr int NCH = 8;                                 // chunks per lane and operand
@@ -452,6 +442,12 @@ __global__ __launch_bounds__(256) void k_grouped_split(GroupedArgs p) {
     return;
   const int m0 = at.lo + at.inside / p.tiles_n * BM, n0 = at.inside % p.tiles_n * BN;
   const int m_valid = at.hi - m0, n_valid = p.N - n0;
+  if constexpr (kLayer<Args>) {
+    if (at.expert < 0) {
+      zero_tile<T, FORM>(p, m0, n0, m_valid < BM ? m_valid : BM, n_valid < BN ? n_valid : BN);
+      return;
+    }
+  }
   const int red = at.expert < 0 ? 0 : p.K;
   const T* A = static_cast<const T*>(p.A) + m0 * p.lda;
   const T* B = static_cast<const T*>(p.B) + (at.expert < 0 ? 0 : at.expert) * p.sB +
@@ -537,7 +533,13 @@ __global__ __launch_bounds__(256) void k_grouped_split(GroupedArgs p) {
   for (int e = 0; e < 16; ++e)
     sum[0][0][e] = part[0][wave][e][lane] + part[1][wave][e][lane] + part[2][wave][e][lane] +
                    part[3][wave][e][lane];
-  store_fragments<T, 1, 1, false>(p, sum, m0 * p.ldc + n0, mi, nj, m_valid, n_valid);
+  if constexpr (kLayer<Args>) {
+    __syncthreads();                   // every wave has read the sums
+    finish_fragments<T, FORM>(p, sum, reinterpret_cast<floatx4*>(lds) + wave * 256, at.expert, m0, n0,
+                              mi, nj, m_valid, n_valid);
+  } else {
+    store_fragments<T, 1, 1, false>(p, sum, m0 * p.ldc + n0, mi, nj, m_valid, n_valid);
+  }
 }
 
 // Few rows per expert (forward): the product is bound by reading the weights once, so the weights
@@ -570,8 +572,8 @@ struct Small<float> {
   }
 };
 
-template <typename T, int MT, int NTW, int WK>
-__global__ __launch_bounds__(256) void k_grouped_rows(GroupedArgs p) {
+template <typename T, int MT, int NTW, int WK, typename Args>
+__global__ __launch_bounds__(256) void k_grouped_rows(Args p) {
   constexpr int VEC = Frag<T>::VEC, STEP = 4 * VEC;     // k per step: 64 bytes of a row
   constexpr int BM = 16 * MT, BN = 16 * NTW * (4 / WK);
   constexpr int D = MT >= 4 ? 3 : 4;                    // operand sets: loads D - 1 steps ahead
@@ -584,6 +586,13 @@ __global__ __launch_bounds__(256) void k_grouped_rows(GroupedArgs p) {
   const int row0 = at.lo + at.inside / p.tiles_n * BM;
   const int n0 = at.inside % p.tiles_n * BN + (WK == 1 ? wave * 16 * NTW : 0);
   const int m_valid = at.hi - row0 < BM ? at.hi - row0 : BM;
+  if constexpr (kLayer<Args>) {
+    if (expert < 0) {
+      const int col = at.inside % p.tiles_n * BN;
+      zero_tile<T, NT>(p, row0, col, m_valid, p.N - col < BN ? p.N - col : BN);
+      return;
+    }
+  }
   const int K = expert < 0 ? 0 : p.K;
   const int steps = (K + STEP - 1) / STEP;
   const int s_begin = WK == 1 ? 0 : (int)((int64_t)wave * steps / WK);
@@ -665,23 +674,72 @@ __global__ __launch_bounds__(256) void k_grouped_rows(GroupedArgs p) {
   auto put = [&](int i, int j, const floatx4& v) {
     const int m = 16 * i + r16, n = n0 + 16 * j + 4 * (lane >> 4);
     if (m >= m_valid) return;
-    T* out = static_cast<T*>(p.C) + (int64_t)(row0 + m) * p.ldc + n;
-    T t[4];
+    auto store = [&](void* base, int64_t ld, const float (&x)[4]) {
+      T* out = static_cast<T*>(base) + (int64_t)(row0 + m) * ld + n;
+      T t[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) t[e] = (T)v[e];
-    if (n + 4 <= p.N) {
-      __builtin_memcpy(out, t, sizeof(t));
-    } else {
+      for (int e = 0; e < 4; ++e) t[e] = (T)x[e];
+      if (n + 4 <= p.N) {
+        __builtin_memcpy(out, t, sizeof(t));
+      } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (n + e < p.N) out[e] = t[e];
+        for (int e = 0; e < 4; ++e)
+          if (n + e < p.N) out[e] = t[e];
+      }
+    };
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = v[e];
+    if constexpr (kLayer<Args>) {
+      auto load = [&](const T* src, T (&t)[4]) {
+        if (n + 4 <= p.N) {
+          __builtin_memcpy(t, src, sizeof(t));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t[e] = n + e < p.N ? src[e] : (T)0.f;
+        }
+      };
+      T bias[4] = {}, r[4] = {};
+      if (p.bias) load(static_cast<const T*>(p.bias) + (int64_t)expert * p.N + n, bias);
+      if (p.R) load(static_cast<const T*>(p.R) + (int64_t)(row0 + m) * p.ldr + n, r);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] += (float)bias[e];
+      if (p.Z) store(p.Z, p.ldz, x);
+      activate<sizeof(T) == 4>(p.act, x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] += (float)r[e];
     }
+    store(p.C, p.ldc, x);
   };
-  if constexpr (WK == 1) {
+  if constexpr (WK == 1 && kLayer<Args>) {
+    // a row of fragments at a time through LDS, so that the epilogue is one loop's body
+    __shared__ floatx4 row[4][NTW][64];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+      for (int j = 0; j < NTW; ++j) row[wave][j][lane] = acc[i][j];
+#pragma unroll 1
+      for (int j = 0; j < NTW; ++j) put(i, j, row[wave][j][lane]);
+    }
+  } else if constexpr (WK == 1) {
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int j = 0; j < NTW; ++j) put(i, j, acc[i][j]);
+  } else if constexpr (kLayer<Args>) {
+    __shared__ floatx4 ex[WK][MT * NTW][64];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NTW; ++j) ex[wave][i * NTW + j][lane] = acc[i][j];
+    __syncthreads();
+#pragma unroll 1
+    for (int t = wave; t < MT * NTW; t += WK) {
+      floatx4 v = ex[0][t][lane];
+#pragma unroll
+      for (int w = 1; w < WK; ++w) v += ex[w][t][lane];
+      put(t / NTW, t % NTW, v);
+    }
   } else {
     __shared__ floatx4 ex[WK][MT * NTW][64];
 #pragma unroll
@@ -773,6 +831,7 @@ struct Unit {
   int KL;
   int m_valid, n_valid;
   int64_t origin;
+  int expert, row, col;         // a layer's epilogue
   int slot;                     // of the part's sums; -1: the whole tile
 };
 
@@ -815,8 +874,8 @@ __device__ __forceinline__ bool tile_at(const GroupedArgs& p, const Walk& w, int
 // epilogue every 16 k-tiles (forward), 1.3 rounds of tiles (input gradient), the transposing reads'
 // waits and 537 MB of output after eight k-tiles a tile (weight gradient). 16 rows over 32 experts: 46 us,
 // the weights at 5.8 TB/s.
-template <typename TO, int FORM, bool ADD>
-__global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
+template <typename TO, int FORM, bool ADD, typename Args>
+__global__ __launch_bounds__(512) void k_grouped_big(Args p) {
   constexpr int BM = 256, BN = 256, BK = 64, FM = 4, FN = 2, INST = 4;   // DMA per wave and operand
   constexpr int SLOT = 256 * kChunks;                   // u32x4 of one operand's k-tile (32 KB)
   constexpr bool AK = FORM == TN, BKM = FORM != NT;     // operand stored along the output
@@ -858,6 +917,9 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
     const int k1 = parts > 1 ? (part + 1) * tiles / parts : tiles;
     u.KL = k1 - k0 < 2 ? 2 : k1 - k0;                   // the DMA looks two k-tiles ahead
     u.n_valid = (FORM == TN ? p.K : p.N) - n0;
+    u.expert = expert;
+    u.row = m0;
+    u.col = n0;
     if constexpr (FORM == TN) {
       const int left = red - k0 * BK, most = (k1 - k0) * BK;
       u.rows = left < most ? left : most;
@@ -1040,7 +1102,7 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
   // HBM, and has 1.75 k-tiles to land; A is shared by more tiles, mostly comes from L2, and has one.
   // After a whole tile's epilogue its stores (one instruction per 16 bytes of a lane: kStores) lie
   // between those loads and k-tile kl + 1, and the first barrier leaves them in flight too.
-  constexpr int kStores = ADD ? 0 : sizeof(TO) == 2 ? FM * FN * 2 : FM * FN * 4;
+  constexpr int kStores = ADD || kLayer<Args> ? 0 : sizeof(TO) == 2 ? FM * FN * 2 : FM * FN * 4;
   constexpr int kVm = 4 + kStores, kLate = (kVm & 15) | (kVm >> 4) << 14 | 0x70;
   static_assert(kVm < 64, "vmcnt has six bits");
   bool late = false;
@@ -1227,6 +1289,12 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
             for (int e = 0; e < 4; ++e) v[e] = acc[m / FN][m % FN][4 * g + e];
             P[(m * 4 + g) * 512 + tid] = v;
           }
+      } else if constexpr (kLayer<Args>) {
+        const int free_slot = b == 0 ? 2 : b - 1;      // as for store_rows
+        finish_fragments<TO, FORM>(p, acc,
+                                   reinterpret_cast<floatx4*>(lds + (2 + free_slot) * SLOT + wave * 256),
+                                   cur.expert, cur.row, cur.col, wm * 128, wn * 64, cur.m_valid,
+                                   cur.n_valid);
       } else if constexpr (ADD) {
         store_sums(b == 0 ? 2 : b - 1);
       } else if constexpr (sizeof(TO) == 2) {
@@ -1235,7 +1303,7 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
         store_fragments<TO, FM, FN, false>(p, acc, cur.origin, wm * 128, wn * 64, cur.m_valid,
                                            cur.n_valid);
       }
-      late = !ADD && cur.slot < 0 && cur.m_valid >= BM && cur.n_valid >= BN;
+      late = !ADD && !kLayer<Args> && cur.slot < 0 && cur.m_valid >= BM && cur.n_valid >= BN;
       clear();
       cur = nxt;
     }
@@ -1247,17 +1315,22 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
     expert_rows(p, 0, first, x);
     expert_rows(p, p.groups - 1, x, last);
     const int rest = first + (p.total_rows - last);
-    __bf16* out = static_cast<__bf16*>(p.C);
-    for (int r = blockIdx.x; r < rest; r += gridDim.x) {
-      const int64_t row = r < first ? r : last + (r - first);
-      for (int n = tid * 8; n < p.N; n += 512 * 8) {
-        if (n + 8 <= p.N) {
-          const u32x4 z = {0u, 0u, 0u, 0u};
-          __builtin_memcpy(out + row * p.ldc + n, &z, 16);
-        } else {
-          for (int e = n; e < p.N; ++e) out[row * p.ldc + e] = (__bf16)0.f;
+    auto zero = [&](__bf16* out, int64_t ld) {
+      for (int r = blockIdx.x; r < rest; r += gridDim.x) {
+        const int64_t row = r < first ? r : last + (r - first);
+        for (int n = tid * 8; n < p.N; n += 512 * 8) {
+          if (n + 8 <= p.N) {
+            const u32x4 z = {0u, 0u, 0u, 0u};
+            __builtin_memcpy(out + row * ld + n, &z, 16);
+          } else {
+            for (int e = n; e < p.N; ++e) out[row * ld + e] = (__bf16)0.f;
+          }
         }
       }
+    };
+    zero(static_cast<__bf16*>(p.C), p.ldc);
+    if constexpr (kLayer<Args> && FORM == NT) {
+      if (p.Z) zero(static_cast<__bf16*>(p.Z), p.ldz);
     }
   }
 }
@@ -1265,8 +1338,8 @@ __global__ __launch_bounds__(512) void k_grouped_big(GroupedArgs p) {
 // Adds the parts of the last round's split tiles in part order and stores them: one block per
 // 64 x 64 piece of a tile (the product kernel's fragment order: float4 (m * 4 + g) * 512 + thread).
 // Bound by reading the parts from memory: 3 to 15 us, 64 MB of them at most.
-template <typename TO, int FORM>
-__global__ __launch_bounds__(256) void k_grouped_join(GroupedArgs p) {
+template <typename TO, int FORM, typename Args>
+__global__ __launch_bounds__(256) void k_grouped_join(Args p) {
   Walk walk = {};
   int rank = -1;
   if constexpr (FORM == TN) {
@@ -1300,9 +1373,15 @@ __global__ __launch_bounds__(256) void k_grouped_join(GroupedArgs p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[0][0][4 * g + e] += v[g][e];
   }
-  store_fragments<TO, 1, 1, FORM == TN>(p, acc, (FORM == TN ? expert * p.sC : 0) + m0 * p.ldc + n0,
-                                        wm * 128 + 32 * (i0 + q / 2), wn * 64 + 32 * (q % 2), m_valid,
-                                        n_valid);
+  if constexpr (kLayer<Args>) {
+    __shared__ floatx4 stage[4 * 256];
+    finish_fragments<TO, FORM>(p, acc, stage + q * 256, expert, m0, n0, wm * 128 + 32 * (i0 + q / 2),
+                               wn * 64 + 32 * (q % 2), m_valid, n_valid);
+  } else {
+    store_fragments<TO, 1, 1, FORM == TN>(p, acc, (FORM == TN ? expert * p.sC : 0) + m0 * p.ldc + n0,
+                                          wm * 128 + 32 * (i0 + q / 2), wn * 64 + 32 * (q % 2),
+                                          m_valid, n_valid);
+  }
 }
 
 // ---- a middling number of rows, bfloat16 ------------------------------------------------------
@@ -1316,8 +1395,8 @@ __global__ __launch_bounds__(256) void k_grouped_join(GroupedArgs p) {
 // without a row are skipped;
 // operand layouts as in k_grouped_big (a [k][BN] operand with BN = 64 has chunk c of k-row r at
 // c ^ 4 (r >> 1 & 1)).
-template <int FORM, int BN>
-__global__ __launch_bounds__(256) void k_grouped_ring(GroupedArgs p) {
+template <int FORM, int BN, typename Args>
+__global__ __launch_bounds__(256) void k_grouped_ring(Args p) {
   constexpr int BM = 128, BK = 64, FM = 2, FN = BN / 64, AI = 4, BI = BN / 32;
   constexpr bool BKM = FORM == NN;
   constexpr int NS = BN == 128 ? 5 : 6;
@@ -1334,6 +1413,12 @@ __global__ __launch_bounds__(256) void k_grouped_ring(GroupedArgs p) {
     return;
   const int m0 = at.lo + at.inside / p.tiles_n * BM, n0 = at.inside % p.tiles_n * BN;
   const int m_valid = at.hi - m0, n_valid = p.N - n0;
+  if constexpr (kLayer<Args>) {
+    if (at.expert < 0) {
+      zero_tile<__bf16, FORM>(p, m0, n0, m_valid < BM ? m_valid : BM, n_valid < BN ? n_valid : BN);
+      return;
+    }
+  }
   const int KL = at.expert < 0 ? 0 : p.K / BK;
 
   floatx16 acc[FM][FN];
@@ -1458,21 +1543,25 @@ __global__ __launch_bounds__(256) void k_grouped_ring(GroupedArgs p) {
     }
     block_sync();                 // no DMA is in flight when the block ends
   }
-  store_fragments<__bf16, FM, FN, false>(p, acc, m0 * p.ldc + n0, wm * 64, wn * (BN / 2), m_valid,
-                                         n_valid);
+  if constexpr (kLayer<Args>)
+    finish_fragments<__bf16, FORM>(p, acc, reinterpret_cast<floatx4*>(lds) + wave * 256, at.expert, m0,
+                                   n0, wm * 64, wn * (BN / 2), m_valid, n_valid);
+  else
+    store_fragments<__bf16, FM, FN, false>(p, acc, m0 * p.ldc + n0, wm * 64, wn * (BN / 2), m_valid,
+                                           n_valid);
 }
 
-template <typename T, typename TO, int FORM>
-hipError_t launch_grouped(const GroupedArgs& a, int64_t blocks, hipStream_t s) {
-  hipLaunchKernelGGL((k_grouped<T, TO, FORM>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+template <typename T, typename TO, int FORM, typename Args>
+hipError_t launch_grouped(const Args& a, int64_t blocks, hipStream_t s) {
+  hipLaunchKernelGGL((k_grouped<T, TO, FORM, Args>), dim3((unsigned)blocks), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
-template <typename T>
-hipError_t launch_split(const GroupedArgs& a, bool transpose_w, int64_t blocks, hipStream_t s) {
+template <typename T, typename Args>
+hipError_t launch_split(const Args& a, bool transpose_w, int64_t blocks, hipStream_t s) {
   const dim3 grid((unsigned)blocks), block(256);
-  if (transpose_w) hipLaunchKernelGGL((k_grouped_split<T, NN>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((k_grouped_split<T, NT>), grid, block, 0, s, a);
+  if (transpose_w) hipLaunchKernelGGL((k_grouped_split<T, NN, Args>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_grouped_split<T, NT, Args>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -1596,20 +1685,20 @@ Plan plan_of(const GroupedDesc& d) {
   return p;
 }
 
-template <typename T, int MT>
-hipError_t launch_rows(const GroupedArgs& a, const Plan& p, int64_t blocks, hipStream_t s) {
+template <typename T, int MT, typename Args>
+hipError_t launch_rows(const Args& a, const Plan& p, int64_t blocks, hipStream_t s) {
   const dim3 grid((unsigned)blocks), block(256);
   if (p.ntw == 4 && p.wk == 1)
-    hipLaunchKernelGGL((k_grouped_rows<T, MT, 4, 1>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((k_grouped_rows<T, MT, 4, 1, Args>), grid, block, 0, s, a);
   else if (p.ntw == 4)
-    hipLaunchKernelGGL((k_grouped_rows<T, MT, 4, 4>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((k_grouped_rows<T, MT, 4, 4, Args>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((k_grouped_rows<T, MT, 1, 4>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((k_grouped_rows<T, MT, 1, 4, Args>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
-template <typename T>
-hipError_t launch_rows(const GroupedArgs& a, const Plan& p, int64_t blocks, hipStream_t s) {
+template <typename T, typename Args>
+hipError_t launch_rows(const Args& a, const Plan& p, int64_t blocks, hipStream_t s) {
   if (p.mt == 1) return launch_rows<T, 1>(a, p, blocks, s);
   if (p.mt == 2) return launch_rows<T, 2>(a, p, blocks, s);
   return launch_rows<T, 4>(a, p, blocks, s);
@@ -1625,16 +1714,16 @@ int64_t grouped_blocks(const GroupedDesc& d) {
          tiles_up(d.transpose_w ? d.k : d.n, p.bn);
 }
 
-template <typename TO, int FORM>
-static hipError_t launch_big(const GroupedArgs& a, hipStream_t s) {
+template <typename TO, int FORM, typename Args>
+static hipError_t launch_big(const Args& a, hipStream_t s) {
   if (FORM == TN && a.D)
-    hipLaunchKernelGGL((k_grouped_big<TO, FORM, FORM == TN>), dim3(256), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((k_grouped_big<TO, FORM, FORM == TN, Args>), dim3(256), dim3(512), 0, s, a);
   else
-    hipLaunchKernelGGL((k_grouped_big<TO, FORM, false>), dim3(256), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((k_grouped_big<TO, FORM, false, Args>), dim3(256), dim3(512), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.split_cap < 2) return e;
   // a split last round has at most 128 tiles
-  hipLaunchKernelGGL((k_grouped_join<TO, FORM>), dim3(128 * 16), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((k_grouped_join<TO, FORM, Args>), dim3(128 * 16), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -1670,11 +1759,43 @@ const char* grouped_name(const GroupedDesc& d) {
   }
 }
 
+// A forward or input gradient: the plan's kernel, with or without a layer's epilogue.
+template <typename Args>
+static hipError_t launch_rowwise(const GroupedDesc& d, const Plan& pl, const Args& a, int64_t blocks,
+                                 hipStream_t s) {
+  if (pl.kernel == Kernel::Rows)
+    return d.store == Store::F32 ? launch_rows<float>(a, pl, blocks, s)
+                                 : launch_rows<__bf16>(a, pl, blocks, s);
+  if (pl.kernel == Kernel::Split64)
+    return d.store == Store::F32 ? launch_split<float>(a, d.transpose_w, blocks, s)
+                                 : launch_split<__bf16>(a, d.transpose_w, blocks, s);
+  if (pl.kernel == Kernel::Ring) {
+    const dim3 grid((unsigned)blocks), block(256);
+    if (d.transpose_w && pl.bn == 128)
+      hipLaunchKernelGGL((k_grouped_ring<NN, 128, Args>), grid, block, 0, s, a);
+    else if (d.transpose_w)
+      hipLaunchKernelGGL((k_grouped_ring<NN, 64, Args>), grid, block, 0, s, a);
+    else if (pl.bn == 128)
+      hipLaunchKernelGGL((k_grouped_ring<NT, 128, Args>), grid, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((k_grouped_ring<NT, 64, Args>), grid, block, 0, s, a);
+    return hipGetLastError();
+  }
+  if (pl.kernel == Kernel::Big)
+    return d.transpose_w ? launch_big<__bf16, NN>(a, s) : launch_big<__bf16, NT>(a, s);
+  if (d.store == Store::F32)
+    return d.transpose_w ? launch_grouped<float, float, NN>(a, blocks, s)
+                         : launch_grouped<float, float, NT>(a, blocks, s);
+  return d.transpose_w ? launch_grouped<__bf16, __bf16, NN>(a, blocks, s)
+                       : launch_grouped<__bf16, __bf16, NT>(a, blocks, s);
+}
+
 hipError_t grouped(const GroupedDesc& d, hipStream_t s) {
   const Plan pl = plan_of(d);
   const int64_t blocks = grouped_blocks(d);
   if (blocks < 1 || blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  GroupedArgs a;
+  LayerArgs layer;
+  GroupedArgs& a = layer;
   a.A = d.A; a.B = d.B; a.D = d.D; a.C = d.C;
   a.lda = d.lda;
   a.offsets = d.offsets;
@@ -1703,27 +1824,14 @@ hipError_t grouped(const GroupedDesc& d, hipStream_t s) {
   a.N = (int)(d.transpose_w ? d.k : d.n);
   a.K = (int)(d.transpose_w ? d.n : d.k);
   a.tiles_n = (int)tiles_up(a.N, pl.bn);
-  if (pl.kernel == Kernel::Rows)
-    return d.store == Store::F32 ? launch_rows<float>(a, pl, blocks, s)
-                                 : launch_rows<__bf16>(a, pl, blocks, s);
-  if (pl.kernel == Kernel::Split64)
-    return d.store == Store::F32 ? launch_split<float>(a, d.transpose_w, blocks, s)
-                                 : launch_split<__bf16>(a, d.transpose_w, blocks, s);
-  if (pl.kernel == Kernel::Ring) {
-    const dim3 grid((unsigned)blocks), block(256);
-    if (d.transpose_w && pl.bn == 128) hipLaunchKernelGGL((k_grouped_ring<NN, 128>), grid, block, 0, s, a);
-    else if (d.transpose_w) hipLaunchKernelGGL((k_grouped_ring<NN, 64>), grid, block, 0, s, a);
-    else if (pl.bn == 128) hipLaunchKernelGGL((k_grouped_ring<NT, 128>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_grouped_ring<NT, 64>), grid, block, 0, s, a);
-    return hipGetLastError();
-  }
-  if (pl.kernel == Kernel::Big)
-    return d.transpose_w ? launch_big<__bf16, NN>(a, s) : launch_big<__bf16, NT>(a, s);
-  if (d.store == Store::F32)
-    return d.transpose_w ? launch_grouped<float, float, NN>(a, blocks, s)
-                         : launch_grouped<float, float, NT>(a, blocks, s);
-  return d.transpose_w ? launch_grouped<__bf16, __bf16, NN>(a, blocks, s)
-                       : launch_grouped<__bf16, __bf16, NT>(a, blocks, s);
+  if (!d.layer) return launch_rowwise(d, pl, a, blocks, s);
+  layer.bias = d.bias;
+  layer.R = d.R;
+  layer.ldr = d.ldr;
+  layer.Z = d.Z;
+  layer.ldz = d.ldz;
+  layer.act = d.act;
+  return launch_rowwise(d, pl, layer, blocks, s);
 }
 
 }  // namespace mns

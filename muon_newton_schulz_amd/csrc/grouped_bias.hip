@@ -1,0 +1,166 @@
+// The gradient of a layer's bias, for rows sorted by expert: dZ = dY act'(Z) and db_e = the sum of
+// dZ's rows of expert e.
+//
+// Bound by HBM: dY and Z are read once and dZ is written once, with no reuse. A block takes a chunk of
+// `chunk` rows of one expert x 256 columns, eight columns a thread (16 bytes of bfloat16), eight rows
+// side by side; its float32 column sums go to the workspace, one row of 256 a chunk, and are added by a
+// second launch in chunk order, so equal calls give equal bits. An expert of at most one chunk needs
+// no second launch; nor does a call of at most `chunk` rows.
+#include "activation.h"
+#include "grouped_walk.h"
+#include "row_vectors.h"
+
+namespace mns {
+namespace {
+
+constexpr int kCols = 256;                    // columns of a block
+constexpr int kRowsAtOnce = 8;                // rows a block reads side by side
+
+struct BiasArgs : GroupedArgs {               // A: dY (lda), C: dZ (ldc), B: Z (ldb), D: unused
+  void* db;                                   // groups x N
+  int act;
+  int chunk;                                  // rows, a multiple of kRowsAtOnce
+};
+
+template <typename T, typename TO>
+__global__ __launch_bounds__(256) void k_bias_grad(BiasArgs p) {
+  const int tid = threadIdx.x, cg = tid & 31, rg = tid >> 5;
+  Place at;
+  const int lin = (int)blockIdx.x;
+  if (!find_place(p, p.chunk, p.tiles_n, p.fill_rest,
+                  walk_start(p, p.chunk, p.tiles_n, p.fill_rest, 1), lin, at, 1))
+    return;
+  const int part = at.inside / p.tiles_n, n = at.inside % p.tiles_n * kCols + 8 * cg;
+  const int left = p.N - n;
+  const int64_t r0 = at.lo + (int64_t)part * p.chunk;
+  const int rows = at.hi - r0 < p.chunk ? (int)(at.hi - r0) : p.chunk;
+  const T* dY = static_cast<const T*>(p.A) + r0 * p.lda + n;
+  const T* Z = static_cast<const T*>(p.B) + r0 * p.ldb + n;
+  T* dZ = static_cast<T*>(p.C) + r0 * p.ldc + n;
+  if (at.expert < 0) {                        // rows of no expert
+    Eight<T> zero;
+    const float none[8] = {};
+    zero.set(none);
+    for (int m = rg; m < rows; m += kRowsAtOnce) zero.store(dZ + m * p.ldc, left);
+    return;
+  }
+  float sum[8] = {};
+  constexpr int AHEAD = 4;                    // rows a thread loads before it uses the first
+  for (int m = rg; m < rows; m += AHEAD * kRowsAtOnce) {
+    Eight<T> g[AHEAD], z[AHEAD];
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) {
+      const int r = m + q * kRowsAtOnce, have = r < rows ? left : 0;
+      g[q].load(dY + r * p.lda, have);
+      z[q].load(Z + r * p.ldb, p.act ? have : 0);
+    }
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) {
+      const int r = m + q * kRowsAtOnce;
+      if (r >= rows) continue;
+      float v[8], x[8];
+      g[q].get(v);
+      z[q].get(x);
+      times_slope<sizeof(T) == 4>(p.act, v, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += v[e];
+      if (p.C) {
+        Eight<T> out;
+        out.set(v);
+        out.store(dZ + r * p.ldc, left);
+      }
+    }
+  }
+  __shared__ float part_sum[kRowsAtOnce][kCols];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) part_sum[rg][8 * cg + e] = sum[e];
+  __syncthreads();
+  float total = 0.f;
+#pragma unroll
+  for (int r = 0; r < kRowsAtOnce; ++r) total += part_sum[r][tid];
+  const int col = at.inside % p.tiles_n * kCols + tid;
+  if (at.hi - at.lo <= p.chunk) {
+    if (col < p.N) static_cast<TO*>(p.db)[(int64_t)at.expert * p.N + col] = (TO)total;
+  } else {
+    p.partial[(int64_t)lin * kCols + tid] = total;
+  }
+}
+
+// The same list of tiles: the block of an expert's first chunk adds the chunks' sums, four quarters of
+// them side by side (each in order), then the quarters in order.
+template <typename TO>
+__global__ __launch_bounds__(1024) void k_bias_join(BiasArgs p) {
+  Place at;
+  const int lin = (int)blockIdx.x;
+  const Walk w = walk_start(p, p.chunk, p.tiles_n, p.fill_rest, 1);
+  if (!find_place(p, p.chunk, p.tiles_n, p.fill_rest, w, lin, at, 1)) return;
+  if (at.expert < 0 || at.inside >= p.tiles_n || at.hi - at.lo <= p.chunk) return;
+  int chunks = (at.hi - at.lo + p.chunk - 1) / p.chunk;
+  const int listed = (w.total - 1 - lin) / p.tiles_n + 1;     // fewer only where offsets overlap
+  if (chunks > listed) chunks = listed;
+  const int tid = threadIdx.x & 255, quarter = threadIdx.x >> 8;
+  const int c0 = (int)((int64_t)chunks * quarter / 4), c1 = (int)((int64_t)chunks * (quarter + 1) / 4);
+  float total = 0.f;
+#pragma unroll 8
+  for (int c = c0; c < c1; ++c)
+    total += p.partial[((int64_t)lin + (int64_t)c * p.tiles_n) * kCols + tid];
+  __shared__ float part_sum[4][kCols];
+  part_sum[quarter][tid] = total;
+  __syncthreads();
+  const int col = at.inside * kCols + tid;
+  if (quarter == 0 && col < p.N)
+    static_cast<TO*>(p.db)[(int64_t)at.expert * p.N + col] =
+        (TO)(part_sum[0][tid] + part_sum[1][tid] + part_sum[2][tid] + part_sum[3][tid]);
+}
+
+int chunk_rows(int64_t total_rows) {
+  int64_t c = 128;
+  while (total_rows > 512 * c) c *= 2;
+  return (int)c;
+}
+
+}  // namespace
+
+int64_t bias_grad_blocks(int64_t groups, int64_t total_rows, int64_t n) {
+  const int64_t chunk = chunk_rows(total_rows);
+  return ((total_rows + chunk - 1) / chunk + groups + 2) * ((n + kCols - 1) / kCols);
+}
+
+size_t bias_grad_workspace(int64_t groups, int64_t total_rows, int64_t n) {
+  if (total_rows <= chunk_rows(total_rows)) return 0;
+  return (size_t)bias_grad_blocks(groups, total_rows, n) * kCols * sizeof(float);
+}
+
+hipError_t bias_grad(const BiasGradDesc& d, hipStream_t s) {
+  BiasArgs a = {};
+  a.A = d.dY; a.lda = d.lddy;
+  a.B = d.Z; a.ldb = d.ldz;
+  a.C = d.dZ; a.ldc = d.lddz;
+  a.offsets = d.offsets;
+  a.total_rows = (int)d.total_rows;
+  a.groups = (int)d.groups;
+  a.N = (int)d.n;
+  a.tiles_n = (int)((d.n + kCols - 1) / kCols);
+  const int64_t blocks = bias_grad_blocks(d.groups, d.total_rows, d.n);
+  a.most_tiles = (int)blocks;
+  a.fill_rest = d.dZ && d.fill_rest ? 1 : 0;
+  a.partial = d.workspace;
+  a.db = d.db;
+  a.act = d.act;
+  a.chunk = chunk_rows(d.total_rows);
+  const dim3 grid((unsigned)blocks);
+  const bool out32 = d.out_store == Store::F32;
+  if (d.store == Store::F32)
+    hipLaunchKernelGGL((k_bias_grad<float, float>), grid, dim3(256), 0, s, a);
+  else if (out32)
+    hipLaunchKernelGGL((k_bias_grad<__bf16, float>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_bias_grad<__bf16, __bf16>), grid, dim3(256), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || d.total_rows <= a.chunk) return e;
+  if (out32) hipLaunchKernelGGL(k_bias_join<float>, grid, dim3(1024), 0, s, a);
+  else hipLaunchKernelGGL(k_bias_join<__bf16>, grid, dim3(1024), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace mns

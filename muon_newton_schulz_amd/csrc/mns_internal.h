@@ -101,6 +101,13 @@ struct GroupedDesc {
   bool weight_grad = false, transpose_w = false;
   float* workspace = nullptr;  // grouped_workspace() bytes
   bool fill_rest = false;      // rows of no expert are written as zeros (else left as they are)
+  // A layer's epilogue. Forward: Z = A W_e^T + bias_e, C = act(Z) + R, and Z kept; transpose_w: C =
+  // (A W_e) act'(Z) + R. bias (groups x n), R, Z (rows as C's): may be null, in `store`.
+  bool layer = false;
+  const void* bias = nullptr;
+  const void* R = nullptr; int64_t ldr = 0;
+  void* Z = nullptr; int64_t ldz = 0;
+  int act = 0;                 // Act (activation.h)
 };
 hipError_t grouped(const GroupedDesc& d, hipStream_t s);
 // Blocks grouped() launches for these sizes (a launch holds at most 2^31 - 1).
@@ -108,6 +115,62 @@ int64_t grouped_blocks(const GroupedDesc& d);
 // Workspace bytes of grouped() for these sizes.
 size_t grouped_workspace(const GroupedDesc& d);
 const char* grouped_name(const GroupedDesc& d);
+
+// ---------------------------------------------------------------------------------------
+// Gradient of a layer's bias (grouped_bias.hip), rows sorted by expert: dZ = dY act'(Z), db_e = the
+// sum of dZ's rows of expert e.
+// ---------------------------------------------------------------------------------------
+struct BiasGradDesc {
+  Store store = Store::BF16, out_store = Store::BF16;     // dY, Z, dZ; db
+  const void* dY = nullptr; int64_t lddy = 0;
+  const void* Z = nullptr; int64_t ldz = 0;               // null: no activation
+  void* dZ = nullptr; int64_t lddz = 0;                   // null: not written
+  void* db = nullptr;                                     // groups x n
+  const int64_t* offsets = nullptr;
+  int64_t groups = 0, total_rows = 0, n = 0;
+  int act = 0;
+  bool fill_rest = false;      // dZ's rows of no expert are written as zeros
+  float* workspace = nullptr;  // bias_grad_workspace() bytes
+};
+hipError_t bias_grad(const BiasGradDesc& d, hipStream_t s);
+int64_t bias_grad_blocks(int64_t groups, int64_t total_rows, int64_t n);
+size_t bias_grad_workspace(int64_t groups, int64_t total_rows, int64_t n);
+
+// ---------------------------------------------------------------------------------------
+// A router's bookkeeping (router.hip): up to kMaxRouted experts (their counters lie in LDS).
+// ---------------------------------------------------------------------------------------
+constexpr int kMaxRouted = 2048;
+size_t order_workspace(int64_t assignments, int64_t experts);
+hipError_t expert_order(const int64_t* ids, int64_t assignments, int64_t experts, int64_t* counts,
+                        int64_t* offsets, int64_t* order, void* workspace, hipStream_t s);
+struct BalanceDesc {
+  Store store = Store::F32;                               // logits, grad
+  const void* logits = nullptr; int64_t ld = 0;           // tokens x experts
+  const int64_t* ids = nullptr;                           // tokens x top
+  const int64_t* counts = nullptr;                        // experts
+  void* grad = nullptr; int64_t ldg = 0;                  // may be null
+  float* loss = nullptr;
+  int64_t tokens = 0, experts = 0, top = 0;
+  float scale = 1.f;
+  void* workspace = nullptr;   // balance_workspace() bytes
+};
+hipError_t balance(const BalanceDesc& d, hipStream_t s);
+size_t balance_workspace(int64_t tokens, int64_t experts);
+
+// ---------------------------------------------------------------------------------------
+// Global norm and clipping (clip.hip).
+// ---------------------------------------------------------------------------------------
+constexpr int kClipPack = 112;      // tensors a launch: 32 bytes each, below 4 KB of arguments
+struct ClipTensor {
+  const void* in;
+  void* out;
+  int64_t numel;
+  Store store;
+};
+size_t clip_workspace(int count);
+// norm = the root of the sum of all squares; with scale, out = in min(1, max_norm / (norm + eps)).
+hipError_t clip_grads(const ClipTensor* list, int count, bool scale, float max_norm, float eps,
+                      float* norm, double* partial, hipStream_t s);
 
 // ---------------------------------------------------------------------------------------
 // Elementwise / reduction kernels (elementwise.hip). All are deterministic: fixed

@@ -1,0 +1,355 @@
+// A router's bookkeeping: the assignments of tokens to experts counted and put in the experts' order,
+// and the balance loss with its gradient.
+#include "mns_internal.h"
+
+namespace mns {
+namespace {
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+
+// ---- counts, offsets and order ------------------------------------------------------------------
+//
+// A stable counting sort of M assignments by expert (those of no expert last). Every block takes one
+// piece of the list and every wave a part of that, both in order, so a place is: the expert's begin,
+// plus what earlier blocks and waves hold of it, plus the rank inside the wave. With more than one
+// block, a first launch counts each block's piece; the second adds the other blocks' counts by itself
+// (E integers a block, from L2), scans them and deals the places. No atomics but counts in LDS, so the
+// result is the one stable order.
+struct OrderArgs {
+  const int64_t* ids;
+  int64_t* counts;
+  int64_t* offsets;
+  int64_t* order;              // may be null
+  int* hist;                   // blocks x (E + 1)
+  int M, E, blocks, piece;     // piece: assignments of a block, a multiple of kThreads
+};
+
+__device__ __forceinline__ int bin_of(const OrderArgs& p, int i) {
+  const int64_t id = p.ids[i];
+  return id >= 0 && id < p.E ? (int)id : p.E;
+}
+
+__global__ __launch_bounds__(kThreads) void k_count(OrderArgs p) {
+  __shared__ int bins[kMaxRouted + 1];
+  for (int e = threadIdx.x; e <= p.E; e += kThreads) bins[e] = 0;
+  __syncthreads();
+  const int64_t first = (int64_t)blockIdx.x * p.piece;
+  const int end = (int)(first + p.piece < p.M ? first + p.piece : p.M);
+  for (int i = (int)first + threadIdx.x; i < end; i += kThreads) atomicAdd(&bins[bin_of(p, i)], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e <= p.E; e += kThreads)
+    p.hist[(int64_t)blockIdx.x * (p.E + 1) + e] = bins[e];
+}
+
+__global__ __launch_bounds__(kThreads) void k_order(OrderArgs p) {
+  __shared__ int cursor[kWaves][kMaxRouted + 1];     // counts, then the wave's next place, by expert
+  __shared__ int carry[kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int bins = p.E + 1;
+  for (int e = tid; e < bins; e += kThreads)
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) cursor[w][e] = 0;
+  __syncthreads();
+  const int64_t first = (int64_t)blockIdx.x * p.piece + (int64_t)wave * (p.piece / kWaves);
+  const int begin = (int)(first < p.M ? first : p.M);
+  const int end = (int)(first + p.piece / kWaves < p.M ? first + p.piece / kWaves : p.M);
+  for (int i = begin + lane; i < end; i += 64) atomicAdd(&cursor[wave][bin_of(p, i)], 1);
+  __syncthreads();
+  // Bins in order, kThreads at a time: all assignments of a bin, those of earlier blocks, and a scan.
+  int running = 0;
+  for (int e0 = 0; e0 < bins; e0 += kThreads) {
+    const int e = e0 + tid;
+    int total = 0, before = 0, own[kWaves] = {};
+    if (e < bins) {
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) total += own[w] = cursor[w][e];
+      if (p.blocks > 1) {
+        total = 0;
+#pragma unroll 8
+        for (int b = 0; b < p.blocks; ++b) {
+          const int h = p.hist[(int64_t)b * bins + e];
+          total += h;
+          before += b < (int)blockIdx.x ? h : 0;
+        }
+      }
+    }
+    int incl = total;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int up = __shfl_up(incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 63) carry[wave] = incl;
+    __syncthreads();
+    int start = running + incl - total;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < wave) start += carry[w];
+      running += carry[w];
+    }
+    if (e < bins) {
+      if (blockIdx.x == 0) {
+        p.offsets[e] = start;
+        if (e < p.E) p.counts[e] = total;
+      }
+      int place = start + before;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        cursor[w][e] = place;
+        place += own[w];
+      }
+    }
+    __syncthreads();
+  }
+  if (!p.order) return;
+  for (int i0 = begin; i0 < end; i0 += 64) {
+    const int i = i0 + lane;
+    const bool in = i < end;
+    const int bin = in ? bin_of(p, i) : -1;
+    // the lanes of the same bin, one bit of the bin at a time (-1 differs from all in its sign bit)
+    unsigned long long same = __ballot(in);
+    for (int bit = 1; bit < bins; bit <<= 1) {
+      const unsigned long long set = __ballot((bin & bit) != 0);
+      same &= (bin & bit) ? set : ~set;
+    }
+    if (in) {
+      const int rank = __popcll(same & ((1ull << lane) - 1));
+      const int place = cursor[wave][bin];
+      p.order[place + rank] = i;
+      if (rank == 0) cursor[wave][bin] = place + __popcll(same);
+    }
+  }
+}
+
+// ---- the balance loss ------------------------------------------------------------------------------
+//
+// loss = scale E / N^2 sum_t a_t s_t with s_t = sum_e c_e p_te, p_t = softmax(logits_t); c_e: assignments
+// of expert e, N: of all, a_t: of token t. Its gradient scale E / N^2 a_t p_te (c_e - s_t) needs a token's
+// own row only, once the counts are known, so one pass reads the logits, adds up a_t s_t and writes the
+// gradient: no sums over the tokens for each expert. G lanes hold a row, four neighbouring columns a
+// lane and step; a row without an assignment is not looked at (whatever its logits hold).
+struct BalanceArgs {
+  const void* logits; int64_t ld;
+  const int64_t* ids;          // T x top
+  const int64_t* counts;
+  void* grad; int64_t ldg;     // may be null
+  float* loss;
+  double* partial;             // a block's sum of a_t s_t
+  int T, E, top, blocks;
+  float scale;
+};
+
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, int valid, float (&v)[4], float rest) {
+  T t[4];
+  if (valid >= 4) {
+    __builtin_memcpy(t, p, sizeof(t));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (float)t[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < valid ? (float)p[i] : rest;
+  }
+}
+
+__device__ __forceinline__ void finish_loss(const BalanceArgs& p, double sum, double n) {
+  *p.loss = n > 0. ? (float)((double)p.scale * p.E / (n * n) * sum) : 0.f;
+}
+
+template <typename T, int G, int Q>
+__global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs p) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane % G;
+  constexpr int ROWS = 64 / G;                     // rows of a wave
+  auto sum_of = [](auto v) {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, G);
+    return v;
+  };
+  float c[Q][4];
+  double n = 0.;
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = (q * G + l) * 4 + i;
+      const int64_t v = e < p.E ? p.counts[e] : 0;
+      c[q][i] = (float)v;
+      n += (double)v;
+    }
+  n = sum_of(n);
+  const float factor = n > 0. ? (float)((double)p.scale * p.E / (n * n)) : 0.f;
+  double total = 0.;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * ROWS; t0 < p.T;
+       t0 += (int64_t)p.blocks * kWaves * ROWS) {
+    const int64_t t = t0 + lane / G;
+    const bool in = t < p.T;
+    int a = 0;
+    for (int j = l; in && j < p.top; j += G) {
+      const int64_t id = p.ids[t * p.top + j];
+      a += id >= 0 && id < p.E;
+    }
+    a = sum_of(a);
+    const bool use = in && a > 0;
+    float x[Q][4], m = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int col = (q * G + l) * 4;
+      load4(static_cast<const T*>(p.logits) + t * p.ld + col, use ? p.E - col : 0, x[q], -INFINITY);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = fmaxf(m, x[q][i]);
+    }
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, G));
+    float z = 0.f, s = 0.f;
+    // a row of lowest infinities has no probabilities: zeros (a NaN passes through the comparison)
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[q][i] = expf(x[q][i] - base);
+        z += x[q][i];
+        s += x[q][i] * c[q][i];
+      }
+    z = sum_of(z);
+    s = sum_of(s);
+    const float inv = z == 0.f ? 0.f : 1.f / z;
+    s *= inv;
+    if (use && l == 0) total += (double)a * (double)s;
+    if (p.grad && in) {
+      const float f = use ? factor * (float)a * inv : 0.f;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const int col = (q * G + l) * 4;
+        T out[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = (T)(use ? f * x[q][i] * (c[q][i] - s) : 0.f);
+        T* dst = static_cast<T*>(p.grad) + t * p.ldg + col;
+        if (col + 4 <= p.E) {
+          __builtin_memcpy(dst, out, sizeof(out));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (col + i < p.E) dst[i] = out[i];
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o);
+  __shared__ double waves[kWaves];
+  if (lane == 0) waves[wave] = total;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double all = 0.;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) all += waves[w];
+    if (p.blocks == 1) finish_loss(p, all, n);
+    else p.partial[blockIdx.x] = all;
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void k_balance_join(BalanceArgs p) {
+  const int tid = threadIdx.x;
+  double sum = 0., n = 0.;
+  for (int b = tid; b < p.blocks; b += kThreads) sum += p.partial[b];
+  for (int e = tid; e < p.E; e += kThreads) n += (double)p.counts[e];
+  __shared__ double s[2][kThreads];
+  s[0][tid] = sum;
+  s[1][tid] = n;
+  __syncthreads();
+  for (int o = kThreads / 2; o > 0; o >>= 1) {
+    if (tid < o) {
+      s[0][tid] += s[0][tid + o];
+      s[1][tid] += s[1][tid + o];
+    }
+    __syncthreads();
+  }
+  if (tid == 0) finish_loss(p, s[0][0], s[1][0]);
+}
+
+int order_blocks(int64_t m, int* piece) {
+  int64_t c = (m + 255) / 256;
+  if (c < 2048) c = 2048;
+  c = (c + kThreads - 1) / kThreads * kThreads;
+  *piece = (int)c;
+  return (int)((m + c - 1) / c);
+}
+
+constexpr int kBalanceBlocks = 1024;
+
+template <typename T>
+hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)a.blocks), block(kThreads);
+  if (a.E <= 32) hipLaunchKernelGGL((k_balance<T, 8, 1>), grid, block, 0, s, a);
+  else if (a.E <= 64) hipLaunchKernelGGL((k_balance<T, 16, 1>), grid, block, 0, s, a);
+  else if (a.E <= 128) hipLaunchKernelGGL((k_balance<T, 32, 1>), grid, block, 0, s, a);
+  else if (a.E <= 256) hipLaunchKernelGGL((k_balance<T, 64, 1>), grid, block, 0, s, a);
+  else if (a.E <= 512) hipLaunchKernelGGL((k_balance<T, 64, 2>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_balance<T, 64, kMaxRouted / 256>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+int balance_blocks(int64_t tokens, int64_t experts) {
+  const int64_t lanes = experts <= 32 ? 8 : experts <= 64 ? 16 : experts <= 128 ? 32 : 64;
+  const int64_t rows = kWaves * 64 / lanes, blocks = (tokens + rows - 1) / rows;
+  return (int)(blocks < 1 ? 1 : blocks > kBalanceBlocks ? kBalanceBlocks : blocks);
+}
+
+}  // namespace
+
+size_t order_workspace(int64_t assignments, int64_t experts) {
+  int piece;
+  const int blocks = order_blocks(assignments, &piece);
+  return blocks > 1 ? (size_t)blocks * (experts + 1) * sizeof(int) : 0;
+}
+
+hipError_t expert_order(const int64_t* ids, int64_t assignments, int64_t experts, int64_t* counts,
+                        int64_t* offsets, int64_t* order, void* workspace, hipStream_t s) {
+  OrderArgs a;
+  a.ids = ids;
+  a.counts = counts;
+  a.offsets = offsets;
+  a.order = order;
+  a.hist = static_cast<int*>(workspace);
+  a.M = (int)assignments;
+  a.E = (int)experts;
+  a.blocks = order_blocks(assignments, &a.piece);
+  if (a.blocks < 1) a.blocks = 1;
+  if (a.blocks > 1) {
+    hipLaunchKernelGGL(k_count, dim3((unsigned)a.blocks), dim3(kThreads), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(k_order, dim3((unsigned)a.blocks), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+size_t balance_workspace(int64_t tokens, int64_t experts) {
+  const int b = balance_blocks(tokens, experts);
+  return b > 1 ? (size_t)b * sizeof(double) : 0;
+}
+
+hipError_t balance(const BalanceDesc& d, hipStream_t s) {
+  BalanceArgs a;
+  a.logits = d.logits;
+  a.ld = d.ld;
+  a.ids = d.ids;
+  a.counts = d.counts;
+  a.grad = d.grad;
+  a.ldg = d.ldg;
+  a.loss = d.loss;
+  a.partial = static_cast<double*>(d.workspace);
+  a.T = (int)d.tokens;
+  a.E = (int)d.experts;
+  a.top = (int)d.top;
+  a.blocks = balance_blocks(d.tokens, d.experts);
+  a.scale = d.scale;
+  const hipError_t e = d.store == Store::F32 ? launch_balance<float>(a, s)
+                                             : launch_balance<__bf16>(a, s);
+  if (e != hipSuccess || a.blocks == 1) return e;
+  hipLaunchKernelGGL(k_balance_join, dim3(1), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace mns

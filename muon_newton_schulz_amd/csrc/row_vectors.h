@@ -1,0 +1,65 @@
+// Pieces of a row of bfloat16 or float32, at any alignment of the type and cut at the row's end.
+#pragma once
+#include "lds_dma.h"
+
+namespace mns {
+namespace {
+
+// 16 bytes from any address of T's alignment, of which the first `valid` elements exist; the
+// others read as zero and are not touched. (A whole chunk is one 16-byte load: this part loads
+// from any address.)
+template <typename T>
+__device__ __forceinline__ u32x4 load_chunk(const T* p, int valid) {
+  constexpr int VEC = 16 / sizeof(T);
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (valid >= VEC) {
+    __builtin_memcpy(&v, p, 16);
+  } else if (valid > 0) {
+    T e[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) e[i] = i < valid ? p[i] : (T)0.f;
+    __builtin_memcpy(&v, e, 16);
+  }
+  return v;
+}
+
+// Eight consecutive elements of a row.
+template <typename T>
+struct Eight {
+  static constexpr int VEC = 16 / sizeof(T);
+  u32x4 r[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p, int valid) {
+#pragma unroll
+    for (int h = 0; h < (int)sizeof(T) / 2; ++h)
+      r[h] = load_chunk(p + h * VEC, valid - h * VEC);
+  }
+  __device__ __forceinline__ void store(T* p, int valid) const {
+    T e[8];
+    __builtin_memcpy(e, r, sizeof(e));
+#pragma unroll
+    for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
+      if (valid >= (h + 1) * VEC) {
+        __builtin_memcpy(p + h * VEC, &r[h], 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          if (h * VEC + i < valid) p[h * VEC + i] = e[h * VEC + i];
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    T e[8];
+    __builtin_memcpy(e, r, sizeof(e));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (float)e[i];
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    T e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = (T)v[i];
+    __builtin_memcpy(r, e, sizeof(e));
+  }
+};
+
+}  // namespace
+}  // namespace mns
