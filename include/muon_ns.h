@@ -279,8 +279,8 @@ mns_status grouped_weight_grad(const void* dY, int64_t lddy, const void* X, int6
 
 /* Z_e = X_e W_e^T + bias_e; Y = act(Z) + R.
  *   bias in  dtype [groups][n], or NULL (none);   R  in  dtype, total_rows x n, pitch ldr, or NULL
- *   Z    out dtype, total_rows x n, pitch ldz, or NULL (not kept): what the gradients need. act is
- *            taken of the float32 sum, before Z's rounding.
+ *   Z    out dtype, total_rows x n, pitch ldz, or NULL (not kept; with MNS_ACT_NONE it must be NULL):
+ *            what the gradients need. act is taken of the float32 sum, before Z's rounding.
  *   Y    out dtype, total_rows x n, pitch ldy; may be R itself (with its pitch); Y and Z may not overlap
  *            each other or any other input. */
 mns_status grouped_linear(const void* X, int64_t ldx, const void* W, const void* bias, int activation,

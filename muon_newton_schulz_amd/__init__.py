@@ -571,8 +571,9 @@ def grouped_linear(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, *,
                    out: torch.Tensor | None = None, out_z: torch.Tensor | None = None,
                    workspace: torch.Tensor | None = None, stream=None):
     """A layer of experts in one product: Z_e = X_e W_e^T + bias_e, Y = act(Z) + residual, rows sorted
-    by expert as in grouped_matmul (a plain layer is a stack of one). Returns Y, or (Y, Z) with
-    ``keep_z`` (or a given ``out_z``): Z is what grouped_input_grad and grouped_bias_grad take.
+    by expert as in grouped_matmul (a plain layer is a stack of one). Returns Y, or with an
+    activation and ``keep_z`` (or a given ``out_z``) (Y, Z): Z is what grouped_input_grad and
+    grouped_bias_grad take.
 
     bias: contiguous (experts, n); residual, ``out``, ``out_z``: (rows, n) at any row pitch, ``out`` may
     be the residual itself; all of X's dtype. activation: None, "relu", "relu2" (relu squared), "gelu"
@@ -583,6 +584,8 @@ def grouped_linear(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, *,
     code, groups, n, k, rows, ldx, _ = _layer_operands(X, W, False, "X", what)
     act = _activation(activation, what)
     keep_z = keep_z or out_z is not None
+    if keep_z and activation is None:
+        raise ValueError(f"{what}: without an activation no gradient needs Z")
     if bias is not None:
         if tuple(bias.shape) != (groups, n) or bias.dtype != X.dtype:
             raise ValueError(f"{what}: bias must be {(groups, n)} {X.dtype}, "

@@ -1044,6 +1044,7 @@ mns_status grouped_linear(const void* X, int64_t ldx, const void* W, const void*
   if (ldx < k || ldx > kMaxPitch || ldy < n || ldy > kMaxPitch || !pitch_ok(R, ldr, n) ||
       !pitch_ok(Z, ldz, n))
     return MNS_ERR_SHAPE;
+  if (Z && activation == MNS_ACT_NONE) return MNS_ERR_PARAM;
   if (!W || !offsets || (total_rows > 0 && (!X || !Y))) return MNS_ERR_NULL;
   const size_t es = store_bytes(dtype);
   if (!aligned(X, es) || !aligned(W, es) || !aligned(Y, es) || !aligned(bias, es) ||

@@ -831,8 +831,10 @@ struct Unit {
   int KL;
   int m_valid, n_valid;
   int64_t origin;
-  int expert, row, col;         // a layer's epilogue
   int slot;                     // of the part's sums; -1: the whole tile
+};
+struct LayerUnit : Unit {
+  int expert, row, col;         // of the tile
 };
 
 // The tile of position lin: expert, rows of the expert, tile coordinates in the output.
@@ -874,7 +876,10 @@ __device__ __forceinline__ bool tile_at(const GroupedArgs& p, const Walk& w, int
 // epilogue every 16 k-tiles (forward), 1.3 rounds of tiles (input gradient), the transposing reads'
 // waits and 537 MB of output after eight k-tiles a tile (weight gradient). 16 rows over 32 experts: 46 us,
 // the weights at 5.8 TB/s.
-template <typename TO, int FORM, bool ADD, typename Args>
+// (ACT, KEEP, RES: a layer's activation, whether Z is kept and whether there is a residual. As run-time
+// choices their branches in the epilogue made the compiler spill up to 500 bytes a lane.)
+template <typename TO, int FORM, bool ADD, typename Args, int ACT = ACT_NONE, bool KEEP = false,
+          bool RES = false>
 __global__ __launch_bounds__(512) void k_grouped_big(Args p) {
   constexpr int BM = 256, BN = 256, BK = 64, FM = 4, FN = 2, INST = 4;   // DMA per wave and operand
   constexpr int SLOT = 256 * kChunks;                   // u32x4 of one operand's k-tile (32 KB)
@@ -896,7 +901,8 @@ __global__ __launch_bounds__(512) void k_grouped_big(Args p) {
   }
   const Deal dl = deal(walk.total, p.split_cap);
 
-  auto unit = [&](int i, Unit& u) {
+  using TileUnit = std::conditional_t<kLayer<Args>, LayerUnit, Unit>;
+  auto unit = [&](int i, TileUnit& u) {
     int part = 0, parts = 1;
     int lin = i * 256 + block;
     u.slot = -1;
@@ -917,9 +923,11 @@ __global__ __launch_bounds__(512) void k_grouped_big(Args p) {
     const int k1 = parts > 1 ? (part + 1) * tiles / parts : tiles;
     u.KL = k1 - k0 < 2 ? 2 : k1 - k0;                   // the DMA looks two k-tiles ahead
     u.n_valid = (FORM == TN ? p.K : p.N) - n0;
-    u.expert = expert;
-    u.row = m0;
-    u.col = n0;
+    if constexpr (kLayer<Args>) {
+      u.expert = expert;
+      u.row = m0;
+      u.col = n0;
+    }
     if constexpr (FORM == TN) {
       const int left = red - k0 * BK, most = (k1 - k0) * BK;
       u.rows = left < most ? left : most;
@@ -1061,7 +1069,7 @@ __global__ __launch_bounds__(512) void k_grouped_big(Args p) {
       bf[slot][1] = u32x4{t2.x, t2.y, t3.x, t3.y};
     }
   };
-  Unit cur, nxt;
+  TileUnit cur, nxt;
   int frags = FM;
   // DMA instruction q of the A (B) half of k-tile kt into A (B) slot `slot`.
   auto dma_one = [&](__amdgpu_buffer_rsrc_t r, int kt, int slot, bool b, int q) {
@@ -1102,7 +1110,8 @@ __global__ __launch_bounds__(512) void k_grouped_big(Args p) {
   // HBM, and has 1.75 k-tiles to land; A is shared by more tiles, mostly comes from L2, and has one.
   // After a whole tile's epilogue its stores (one instruction per 16 bytes of a lane: kStores) lie
   // between those loads and k-tile kl + 1, and the first barrier leaves them in flight too.
-  constexpr int kStores = ADD || kLayer<Args> ? 0 : sizeof(TO) == 2 ? FM * FN * 2 : FM * FN * 4;
+  // (A layer's epilogue stores that much too; where it kept Z as well, or read anything, more lies between.)
+  constexpr int kStores = ADD ? 0 : sizeof(TO) == 2 ? FM * FN * 2 : FM * FN * 4;
   constexpr int kVm = 4 + kStores, kLate = (kVm & 15) | (kVm >> 4) << 14 | 0x70;
   static_assert(kVm < 64, "vmcnt has six bits");
   bool late = false;
@@ -1183,6 +1192,149 @@ __global__ __launch_bounds__(512) void k_grouped_big(Args p) {
           for (int e = 0; e < 8; ++e)
             if (n + e < cur.n_valid) dst[e] = x[e];
         }
+      }
+    }
+  };
+
+  // A layer's epilogue: the arithmetic on the accumulators as they lie (a lane: one row, four neighbouring
+  // columns of every eight), each row-wise operand and output through the same 4 KB as in store_rows, 32
+  // rows x 64 columns of bfloat16 at a time. The operands of the next 32 rows are loaded before the
+  // current ones are finished. Row-wise memory is reached through buffer resources that end with the
+  // tile's last row, so no access is guarded by a branch: what lies outside is not read (zeros) nor
+  // written, and the number of accesses in flight is known (kStores).
+  auto layer_rows = [&](int b) {
+    if constexpr (kLayer<Args>) {
+      int ln = lane;
+      asm volatile("" : "+v"(ln));
+      char* const stage = reinterpret_cast<char*>(lds + (2 + b) * SLOT + wave * 256);
+      const int c = ln & 7, r8 = ln >> 3;
+      const bool in = wn * 64 + 8 * c < cur.n_valid;       // whole chunks: p.N is a multiple of 8
+      // bytes of element (row of 32, column of 64) in the stage, for 8-byte (one row a lane) and for
+      // 16-byte accesses (row r8 + 8 q, whose halves are swapped from row 16 on)
+      const int rr = ln & 31;
+      auto own = [&](int j, int g) {
+        const int k = 32 * j + 8 * g + 4 * (ln >> 5);
+        return rr * 128 + ((k >> 3) ^ ((rr >> 1) & 7)) * 16 + (((k & 4) ^ ((rr >> 2) & 4)) << 1);
+      };
+      auto wide = [&](int q) { return (r8 + 8 * q) * 128 + (c ^ (((r8 + 8 * q) >> 1) & 7)) * 16; };
+      auto rows_of = [&](const void* base, int64_t ld) {
+        return make_rsrc(static_cast<const __bf16*>(base) + (int64_t)cur.row * ld + cur.col,
+                         ((int64_t)(cur.m_valid < BM ? cur.m_valid - 1 : BM - 1) * ld +
+                          (cur.n_valid < BN ? cur.n_valid : BN)) * 2);
+      };
+      auto lane_at = [&](int64_t ld) { return in ? (r8 * (int)ld + 8 * c) * 2 : 0x70000000; };
+      auto row_at = [&](int64_t ld, int i, int q) {
+        return ((wm * 128 + 32 * i + 8 * q) * (int)ld + wn * 64) * 2;
+      };
+      auto fetch = [&](const void* base, int64_t ld, int i, u32x4 (&v)[4]) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          v[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                               rows_of(base, ld), lane_at(ld), row_at(ld, i, q), 0));
+      };
+      auto into_stage = [&](const u32x4 (&v)[4]) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<u32x4*>(stage + wide(q)) =
+              q >= 2 ? u32x4{v[q].z, v[q].w, v[q].x, v[q].y} : v[q];
+      };
+      auto staged = [&](int j, int g, float* x) {
+        const u32x2 v = *reinterpret_cast<const u32x2*>(stage + own(j, g));
+        x[0] = __uint_as_float(v.x << 16);
+        x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+        x[2] = __uint_as_float(v.y << 16);
+        x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+      };
+      auto put = [&](int i, void* base, int64_t ld) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            __bf16 t[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[e] = (__bf16)acc[i][j][4 * g + e];
+            *reinterpret_cast<u32x2*>(stage + own(j, g)) = __builtin_bit_cast(u32x2, t);
+          }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          u32x4 v = *reinterpret_cast<const u32x4*>(stage + wide(q));
+          if (q >= 2) v = u32x4{v.z, v.w, v.x, v.y};
+          // (the whole offset per lane, none in a scalar register: behind a 16-byte buffer store with one
+          // the compiler lets the next instruction overwrite the store's data, and on this part that
+          // instruction won)
+          __builtin_amdgcn_raw_buffer_store_b128(v, rows_of(base, ld), lane_at(ld) + row_at(ld, i, q), 0, 0);
+        }
+      };
+      // Four bias columns a lane for each of its accumulators' groups of four; with a residual's registers
+      // beside them too many to keep, so loaded for every 32 rows there (from L1).
+      u32x2 bias[FN][4];
+      auto load_bias = [&] {
+        const __amdgpu_buffer_rsrc_t r =
+            make_rsrc(static_cast<const __bf16*>(p.bias) + (int64_t)cur.expert * p.N + cur.col,
+                      p.bias ? (cur.n_valid < BN ? cur.n_valid : BN) * 2 : 0);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            bias[j][g] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(
+                                                       r, 8 * (ln >> 5), (wn * 64 + 32 * j + 8 * g) * 2, 0));
+      };
+      constexpr bool gate = FORM == NN && ACT != ACT_NONE;
+      u32x4 ahead[4];
+      if (gate) fetch(p.Z, p.ldz, 0, ahead);
+      else if (RES) fetch(p.R, p.ldr, 0, ahead);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        if constexpr (FORM == NT) {
+          if (RES || i == 0) load_bias();
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              acc[i][j][4 * g] += __uint_as_float(bias[j][g].x << 16);
+              acc[i][j][4 * g + 1] += __uint_as_float(bias[j][g].x & 0xFFFF0000u);
+              acc[i][j][4 * g + 2] += __uint_as_float(bias[j][g].y << 16);
+              acc[i][j][4 * g + 3] += __uint_as_float(bias[j][g].y & 0xFFFF0000u);
+            }
+          if constexpr (KEEP) put(i, p.Z, p.ldz);
+        } else if constexpr (gate) {
+          into_stage(ahead);
+          if (RES) fetch(p.R, p.ldr, i, ahead);
+          else if (i + 1 < FM) fetch(p.Z, p.ldz, i + 1, ahead);
+        }
+#pragma unroll
+        for (int h = 0; h < 2 * FN; ++h) {
+          float v[8], x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = acc[i][h / 2][8 * (h % 2) + e];
+          if constexpr (FORM == NT) {
+            activate<false>(ACT, v);
+          } else if constexpr (gate) {
+            staged(h / 2, 2 * (h % 2), x);
+            staged(h / 2, 2 * (h % 2) + 1, x + 4);
+            times_slope<false>(ACT, v, x);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[i][h / 2][8 * (h % 2) + e] = v[e];
+        }
+        if constexpr (RES) {
+          into_stage(ahead);
+          if (i + 1 < FM) {
+            if (gate) fetch(p.Z, p.ldz, i + 1, ahead);
+            else fetch(p.R, p.ldr, i + 1, ahead);
+          }
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              float t[4];
+              staged(j, g, t);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][j][4 * g + e] += t[e];
+            }
+        }
+        put(i, p.C, p.ldc);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
@@ -1290,11 +1442,7 @@ __global__ __launch_bounds__(512) void k_grouped_big(Args p) {
             P[(m * 4 + g) * 512 + tid] = v;
           }
       } else if constexpr (kLayer<Args>) {
-        const int free_slot = b == 0 ? 2 : b - 1;      // as for store_rows
-        finish_fragments<TO, FORM>(p, acc,
-                                   reinterpret_cast<floatx4*>(lds + (2 + free_slot) * SLOT + wave * 256),
-                                   cur.expert, cur.row, cur.col, wm * 128, wn * 64, cur.m_valid,
-                                   cur.n_valid);
+        layer_rows(b == 0 ? 2 : b - 1);
       } else if constexpr (ADD) {
         store_sums(b == 0 ? 2 : b - 1);
       } else if constexpr (sizeof(TO) == 2) {
@@ -1303,8 +1451,10 @@ __global__ __launch_bounds__(512) void k_grouped_big(Args p) {
         store_fragments<TO, FM, FN, false>(p, acc, cur.origin, wm * 128, wn * 64, cur.m_valid,
                                            cur.n_valid);
       }
-      late = !ADD && !kLayer<Args> && cur.slot < 0 && cur.m_valid >= BM && cur.n_valid >= BN;
+      late = !ADD && cur.slot < 0 && (kLayer<Args> || (cur.m_valid >= BM && cur.n_valid >= BN));
       clear();
+      // the next tile's first fragments again: they need not stay in registers over the epilogue
+      if constexpr (kLayer<Args> && FORM == NT) load_frags(a, b, 0, 0);
       cur = nxt;
     }
     block_sync();                 // no DMA is in flight when the block ends
@@ -1315,22 +1465,20 @@ __global__ __launch_bounds__(512) void k_grouped_big(Args p) {
     expert_rows(p, 0, first, x);
     expert_rows(p, p.groups - 1, x, last);
     const int rest = first + (p.total_rows - last);
-    auto zero = [&](__bf16* out, int64_t ld) {
-      for (int r = blockIdx.x; r < rest; r += gridDim.x) {
-        const int64_t row = r < first ? r : last + (r - first);
-        for (int n = tid * 8; n < p.N; n += 512 * 8) {
-          if (n + 8 <= p.N) {
-            const u32x4 z = {0u, 0u, 0u, 0u};
-            __builtin_memcpy(out + row * ld + n, &z, 16);
-          } else {
-            for (int e = n; e < p.N; ++e) out[row * ld + e] = (__bf16)0.f;
+    __bf16* out = static_cast<__bf16*>(p.C);
+    for (int r = blockIdx.x; r < rest; r += gridDim.x) {
+      const int64_t row = r < first ? r : last + (r - first);
+      for (int n = tid * 8; n < p.N; n += 512 * 8) {
+        if (n + 8 <= p.N) {
+          const u32x4 z = {0u, 0u, 0u, 0u};
+          __builtin_memcpy(out + row * p.ldc + n, &z, 16);
+          if constexpr (kLayer<Args> && FORM == NT) {      // (p.N is a multiple of 8 there)
+            if (KEEP) __builtin_memcpy(static_cast<__bf16*>(p.Z) + row * p.ldz + n, &z, 16);
           }
+        } else {
+          for (int e = n; e < p.N; ++e) out[row * p.ldc + e] = (__bf16)0.f;
         }
       }
-    };
-    zero(static_cast<__bf16*>(p.C), p.ldc);
-    if constexpr (kLayer<Args> && FORM == NT) {
-      if (p.Z) zero(static_cast<__bf16*>(p.Z), p.ldz);
     }
   }
 }
@@ -1597,6 +1745,10 @@ bool dma_ok(const GroupedDesc& d) {
   if (d.store != Store::BF16 || !on16(d.A) || !on16(d.B) || d.lda % 8) return false;
   if (d.weight_grad) return d.ldb % 8 == 0 && d.n % 2 == 0 && d.k % 2 == 0;
   const int64_t red = d.transpose_w ? d.n : d.k;
+  // a layer's epilogue moves whole chunks
+  if (d.layer && ((d.transpose_w ? d.k : d.n) % 8 || !on16(d.C) || !on16(d.R) || !on16(d.Z) ||
+                  d.ldc % 8 || (d.R && d.ldr % 8) || (d.Z && d.ldz % 8)))
+    return false;
   return red % 64 == 0 && red >= 128 && d.k % 8 == 0 && (d.n * d.k) % 8 == 0 &&
          d.n * d.k < (int64_t(1) << 30);
 }
@@ -1714,12 +1866,39 @@ int64_t grouped_blocks(const GroupedDesc& d) {
          tiles_up(d.transpose_w ? d.k : d.n, p.bn);
 }
 
+template <typename TO, int FORM, int ACT>
+static void launch_layer(const LayerArgs& a, hipStream_t s) {
+  const dim3 grid(256), block(512);
+  if constexpr (FORM == NT && ACT != ACT_NONE) {
+    if (a.Z && a.R) {
+      hipLaunchKernelGGL((k_grouped_big<TO, FORM, false, LayerArgs, ACT, true, true>), grid, block, 0, s, a);
+      return;
+    }
+    if (a.Z) {
+      hipLaunchKernelGGL((k_grouped_big<TO, FORM, false, LayerArgs, ACT, true, false>), grid, block, 0, s, a);
+      return;
+    }
+  }
+  if (a.R)
+    hipLaunchKernelGGL((k_grouped_big<TO, FORM, false, LayerArgs, ACT, false, true>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((k_grouped_big<TO, FORM, false, LayerArgs, ACT, false, false>), grid, block, 0, s, a);
+}
+
 template <typename TO, int FORM, typename Args>
 static hipError_t launch_big(const Args& a, hipStream_t s) {
-  if (FORM == TN && a.D)
-    hipLaunchKernelGGL((k_grouped_big<TO, FORM, FORM == TN, Args>), dim3(256), dim3(512), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_grouped_big<TO, FORM, false, Args>), dim3(256), dim3(512), 0, s, a);
+  const dim3 grid(256), block(512);
+  if constexpr (kLayer<Args>) {
+    if (a.act == ACT_RELU) launch_layer<TO, FORM, ACT_RELU>(a, s);
+    else if (a.act == ACT_RELU2) launch_layer<TO, FORM, ACT_RELU2>(a, s);
+    else if (a.act == ACT_GELU) launch_layer<TO, FORM, ACT_GELU>(a, s);
+    else if (a.act == ACT_SILU) launch_layer<TO, FORM, ACT_SILU>(a, s);
+    else launch_layer<TO, FORM, ACT_NONE>(a, s);
+  } else if (FORM == TN && a.D) {
+    hipLaunchKernelGGL((k_grouped_big<TO, FORM, FORM == TN, Args>), grid, block, 0, s, a);
+  } else {
+    hipLaunchKernelGGL((k_grouped_big<TO, FORM, false, Args>), grid, block, 0, s, a);
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.split_cap < 2) return e;
   // a split last round has at most 128 tiles

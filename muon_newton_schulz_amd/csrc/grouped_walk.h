@@ -72,7 +72,7 @@ __device__ __forceinline__ void walk_batch(const GroupedArgs& p, int BM, int til
   // The host refuses calls of 2^31 tiles; only offsets that overlap can add up to more (walk_start
   // then cuts the list off, find_place checks what it finds).
   w.incl = (w.hi - w.lo + (BM - 1)) / BM * tiles_n;
-  if (w.incl < floor) w.incl = floor;
+  if (least && w.incl < floor) w.incl = floor;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const int up = __shfl_up(w.incl, o);
@@ -119,7 +119,7 @@ __device__ __forceinline__ bool find_place(const GroupedArgs& p, int BM, int til
   const int ge = g0 + src - rest;
   at.expert = ge >= 0 && ge < p.groups ? ge : -1;
   int tiles = (at.hi - at.lo + (BM - 1)) / BM * tiles_n;
-  if (at.expert >= 0 && tiles < least * tiles_n) tiles = tiles_n;
+  if (least && at.expert >= 0 && tiles == 0) tiles = tiles_n;
   return at.inside >= 0 && at.inside < tiles;
 }
 

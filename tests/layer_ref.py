@@ -5,8 +5,11 @@ Activations. A value off by d before the activation is off by at most L d behind
 between (relu 1; relu2 2 (|z| + d); gelu 1.13; silu 1.1). The activations themselves, A = a relative
 error: float32 storage evaluates exp and erfc to a few units in the last place (2^-23 each), and erfc's
 and exp's arguments are rounded, which moves erfc(-z / sqrt 2) by up to z^2 2^-23 in the tail: A = (16 + z^2)
-2^-23. bfloat16 storage uses a polynomial within 2.9e-5 of Phi and 8 roundings: A = 2^-14. The slopes are
-sums of two such terms, each off by A of itself; silu's 1 - s is off by up to 2^-23 of 1 besides."""
+2^-23. bfloat16 storage uses approximations: gelu = max(z, 0) - |z| Q with Q = Phi(-|z|) off by up to 2e-4 of
+itself for |z| <= 5, 6e-4 up to 8 and 8e-3 beyond (and less than 1e-40 past 13.3), evaluated with 10 roundings
+of a logarithm up to 132: 10 132 2^-24 = 8e-5; its slope and silu are within 2.9e-5 and 8 roundings: A = 2^-14.
+The slopes are sums of two such terms, each off by A of itself; silu's 1 - s is off by up to 2^-23 of 1
+besides."""
 import math
 
 import torch
@@ -43,6 +46,10 @@ def act_error(name, z, dtype):
     # Phi + z phi and s (1 + z (1 - s)) by 1 + |z| of it.
     flush = 2.0 ** -126 * (1 + z.abs())
     value = act(name, z)[0].abs() * rel + flush
+    if name == "gelu" and dtype != torch.float32:
+        far = z.abs()
+        q = torch.where(far <= 5, 2.8e-4, torch.where(far <= 8, 6.8e-4, 8.1e-3))
+        value = far * 0.5 * torch.erfc(far / math.sqrt(2)) * q + ULP * z.abs() + flush
     if name == "gelu":
         parts = 0.5 * torch.erfc(-z / math.sqrt(2)) + z.abs() * torch.exp(-z * z / 2)
         return value, parts * rel + flush

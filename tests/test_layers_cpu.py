@@ -34,13 +34,14 @@ def _layer():
     (lambda c: {"bias": c["bias"][0]}, ValueError),
     (lambda c: {"bias": torch.zeros(16, 3, dtype=BF).t()}, ValueError),
     (lambda c: {"activation": "tanh"}, ValueError),
+    (lambda c: {"keep_z": True}, ValueError),                          # without an activation
     (lambda c: {"residual": c["X"]}, ValueError),
     (lambda c: {"residual": c["Yn"].float()}, ValueError),
     (lambda c: {"residual": c["Yn"][:1].expand(12, 16)}, ValueError),  # overlapping rows
     (lambda c: {"out": c["X"][:, :16]}, ValueError),
-    (lambda c: {"out_z": c["X"][:, :16]}, ValueError),
-    (lambda c: {"out": c["Yn"], "out_z": c["Yn"]}, ValueError),
-    (lambda c: {"residual": c["Yn"], "out_z": c["Yn"]}, ValueError),
+    (lambda c: {"out_z": c["X"][:, :16], "activation": "relu"}, ValueError),
+    (lambda c: {"out": c["Yn"], "out_z": c["Yn"], "activation": "relu"}, ValueError),
+    (lambda c: {"residual": c["Yn"], "out_z": c["Yn"], "activation": "relu"}, ValueError),
     (lambda c: {"residual": torch.zeros(13, 16, dtype=BF)[1:], "out": None}, ValueError),
 ])
 def test_linear_refusals(change, error):
@@ -147,6 +148,7 @@ def _linear(lib, **kw):
     (dict(off=0x700004), BAD_PARAM), (dict(Y=0x500000), BAD_PARAM), (dict(Y=0x100010), BAD_PARAM),
     (dict(Y=0x400020), BAD_PARAM), (dict(Y=0x400000, ldy=17), BAD_PARAM), (dict(Z=0x400000), BAD_PARAM),
     (dict(Y=0x300000), BAD_PARAM), (dict(Z=0x200000), BAD_PARAM), (dict(Y=0x6ffff0), BAD_PARAM),
+    (dict(act=0), BAD_PARAM),
     (dict(rows=0, X=None, Y=None), 0),
 ])
 def test_library_refuses_linear(kw, status):
