@@ -355,7 +355,7 @@ mns_status balance_loss(const void* logits, int64_t ldl, int dtype, const int64_
 /* ---- Global norm and clipping -------------------------------------------------------------------- */
 
 /* One gradient: numel elements of dtype at `in` (aligned to its dtype); scaled into `out`, which may be
- * `in`. numel may be 0. */
+ * `in`. 0 <= numel <= 2^36, else MNS_ERR_SHAPE. */
 typedef struct mns_tensor {
   const void* in;
   void* out;

@@ -9,6 +9,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
+import struct
 from typing import Iterable, Sequence
 
 import torch
@@ -30,6 +32,7 @@ __all__ = ["muon_step", "ns_orthogonalize", "ns_orthogonalize_noalloc",
 
 _ACTIVATIONS = {None: _abi.MNS_ACT_NONE, "relu": _abi.MNS_ACT_RELU, "relu2": _abi.MNS_ACT_RELU2,
                 "gelu": _abi.MNS_ACT_GELU, "silu": _abi.MNS_ACT_SILU}
+_STORAGE = {torch.bfloat16: MNS_BF16, torch.float32: MNS_F32}
 _KINDS = {"standard": MNS_NS_STANDARD, "gram": MNS_NS_GRAM}
 
 
@@ -508,6 +511,23 @@ def grouped_weight_grad(dY: torch.Tensor, X: torch.Tensor, offsets: torch.Tensor
     return G
 
 
+@functools.lru_cache(maxsize=4096)
+def _size_query(name: str, *args) -> int:
+    """Bytes a workspace query of the library answers (a function of its arguments alone; asking costs
+    a small call 1.5 us)."""
+    need = ctypes.c_size_t(0)
+    check(getattr(load(), name)(*args, ctypes.byref(need)), name)
+    return need.value
+
+
+def _optional_workspace(nbytes: int, dev, workspace):
+    """(tensor, pointer, bytes) of a call's workspace, nothing for a call without one."""
+    if nbytes == 0:
+        return None, None, 0
+    ws = _workspace(nbytes, dev, workspace)
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _activation(activation, what: str) -> int:
     if activation not in _ACTIVATIONS:
         names = sorted(a for a in _ACTIVATIONS if a)
@@ -606,7 +626,8 @@ def grouped_linear(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, *,
             Y, ldy = _new_rows(rows, n, X, not fill), n
         if keep_z and Z is None:
             Z, ldz = _new_rows(rows, n, X, not fill), n
-        keep, ws, nbytes = _grouped_workspace(0, code, groups, rows, n, k, dev, workspace)
+        keep, ws, nbytes = _optional_workspace(
+            _size_query("mns_grouped_workspace_size", 0, code, groups, rows, n, k), dev, workspace)
         check(load().grouped_linear(X.data_ptr(), ldx, W.data_ptr(), _ptr_or_none(bias), act,
                                     _ptr_or_none(residual), ldr, _ptr_or_none(Z), ldz, Y.data_ptr(),
                                     ldy, code, offsets.data_ptr(), groups, rows, n, k, int(fill), ws,
@@ -638,7 +659,8 @@ def grouped_input_grad(dY: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor,
         dX = out
         if dX is None:
             dX, lddx = _new_rows(rows, k, dY, False), k
-        keep, ws, nbytes = _grouped_workspace(0, code, groups, rows, n, k, dev, workspace)
+        keep, ws, nbytes = _optional_workspace(
+            _size_query("mns_grouped_workspace_size", 0, code, groups, rows, n, k), dev, workspace)
         check(load().grouped_input_grad(dY.data_ptr(), lddy, W.data_ptr(), act, _ptr_or_none(Z), ldz,
                                         _ptr_or_none(residual), ldr, dX.data_ptr(), lddx, code,
                                         offsets.data_ptr(), groups, rows, n, k, int(out is None), ws,
@@ -684,21 +706,18 @@ def grouped_bias_grad(dY: torch.Tensor, offsets: torch.Tensor, *, activation: st
                                       ("offsets", offsets)], what)
     _itself_or_apart(out_dz, "out_dz", [("dY", dY), ("Z", Z)], [("offsets", offsets)], what)
     dev = _grouped_checks([("dY", dY)], [Z, out, out_dz], offsets, groups, what)
-    lib = load()
-    need = ctypes.c_size_t(0)
-    check(lib.mns_grouped_bias_grad_workspace_size(groups, rows, n, ctypes.byref(need)),
-          "mns_grouped_bias_grad_workspace_size")
+    need = _size_query("mns_grouped_bias_grad_workspace_size", groups, rows, n)
     with _OnStream(dev, stream) as handle:
         db = torch.empty((groups, n), dtype=out_dtype, device=dev) if out is None else out
         dZ = out_dz
         if activation is not None and dZ is None:
             dZ, lddz = _new_rows(rows, n, dY, False), n
-        ws = _workspace(need.value, dev, workspace) if need.value else None
-        check(lib.grouped_bias_grad(dY.data_ptr(), lddy, act, _ptr_or_none(Z), ldz, _ptr_or_none(dZ),
-                                    lddz, code, offsets.data_ptr(), groups, rows, n, db.data_ptr(),
-                                    MNS_F32 if out_dtype == torch.float32 else MNS_BF16,
-                                    int(out_dz is None), _ptr_or_none(ws),
-                                    0 if ws is None else ws.numel() * ws.element_size(), handle), what)
+        keep, ws, nbytes = _optional_workspace(need, dev, workspace)
+        check(load().grouped_bias_grad(dY.data_ptr(), lddy, act, _ptr_or_none(Z), ldz,
+                                       _ptr_or_none(dZ), lddz, code, offsets.data_ptr(), groups, rows,
+                                       n, db.data_ptr(),
+                                       MNS_F32 if out_dtype == torch.float32 else MNS_BF16,
+                                       int(out_dz is None), ws, nbytes, handle), what)
     return db if activation is None else (db, dZ)
 
 
@@ -719,18 +738,14 @@ def expert_order(expert_ids: torch.Tensor, experts: int, *, order: bool = True,
     _ids(expert_ids, what)
     dev = _on_one_gpu([expert_ids], what)
     m = expert_ids.numel()
-    lib = load()
-    need = ctypes.c_size_t(0)
-    check(lib.mns_expert_order_workspace_size(m, experts, ctypes.byref(need)),
-          "mns_expert_order_workspace_size")
+    need = _size_query("mns_expert_order_workspace_size", m, experts)
     with _OnStream(dev, stream) as handle:
         counts = torch.empty(experts, dtype=torch.int64, device=dev)
         offsets = torch.empty(experts + 1, dtype=torch.int64, device=dev)
         places = torch.empty(m, dtype=torch.int64, device=dev) if order else None
-        ws = _workspace(need.value, dev, workspace) if need.value else None
-        check(lib.expert_order(expert_ids.data_ptr(), m, experts, counts.data_ptr(),
-                               offsets.data_ptr(), _ptr_or_none(places), _ptr_or_none(ws),
-                               0 if ws is None else ws.numel() * ws.element_size(), handle), what)
+        keep, ws, nbytes = _optional_workspace(need, dev, workspace)
+        check(load().expert_order(expert_ids.data_ptr(), m, experts, counts.data_ptr(),
+                                  offsets.data_ptr(), _ptr_or_none(places), ws, nbytes, handle), what)
     return counts, offsets, places
 
 
@@ -761,20 +776,17 @@ def balance_loss(logits: torch.Tensor, expert_ids: torch.Tensor, counts: torch.T
     _itself_or_apart(out, "out", [("logits", logits)],
                      [("expert_ids", expert_ids), ("counts", counts)], what)
     dev = _on_one_gpu([logits, expert_ids, counts, out], what)
-    lib = load()
-    need = ctypes.c_size_t(0)
-    check(lib.mns_balance_workspace_size(tokens, experts, ctypes.byref(need)),
-          "mns_balance_workspace_size")
+    need = _size_query("mns_balance_workspace_size", tokens, experts)
     with _OnStream(dev, stream) as handle:
         loss = torch.empty((), dtype=torch.float32, device=dev)
         dlogits = out
         if grad and dlogits is None:
             dlogits, ldd = _new_rows(tokens, experts, logits, False), experts
-        ws = _workspace(need.value, dev, workspace) if need.value else None
-        check(lib.balance_loss(logits.data_ptr(), ldl, code, expert_ids.data_ptr(),
-                               expert_ids.shape[1], counts.data_ptr(), tokens, experts, scale,
-                               loss.data_ptr(), _ptr_or_none(dlogits), ldd, _ptr_or_none(ws),
-                               0 if ws is None else ws.numel() * ws.element_size(), handle), what)
+        keep, ws, nbytes = _optional_workspace(need, dev, workspace)
+        check(load().balance_loss(logits.data_ptr(), ldl, code, expert_ids.data_ptr(),
+                                  expert_ids.shape[1], counts.data_ptr(), tokens, experts, scale,
+                                  loss.data_ptr(), _ptr_or_none(dlogits), ldd, ws, nbytes, handle),
+              what)
     return loss, dlogits
 
 
@@ -785,20 +797,21 @@ def _tensor_list(grads, out, what: str):
     outs = grads if out is None else _as_list(out)
     if len(outs) != len(grads):
         raise ValueError(f"{what}: out must hold as many tensors as grads")
-    arr = (_abi.MnsTensor * len(grads))()
-    for i, (g, o) in enumerate(zip(grads, outs)):
+    dev = grads[0].device
+    index, codes, flat = dev.index, _STORAGE, []
+    for i, g in enumerate(grads):
+        o = outs[i]
+        code = codes.get(g.dtype)
+        if code is None:
+            _dtype_code(g)
         if not g.is_contiguous():
             raise ValueError(f"{what}: gradient {i} must be contiguous")
         if o is not g and (o.shape != g.shape or o.dtype != g.dtype or not o.is_contiguous()):
             raise ValueError(f"{what}: out {i} must match its gradient and be contiguous")
-        arr[i] = (g.data_ptr(), o.data_ptr(), g.numel(), _dtype_code(g))
-    return arr, len(grads), _on_one_gpu(grads if out is None else grads + outs, what)
-
-
-def _clip_workspace(count: int, dev, workspace):
-    need = ctypes.c_size_t(0)
-    check(load().mns_clip_workspace_size(count, ctypes.byref(need)), "mns_clip_workspace_size")
-    return _workspace(need.value, dev, workspace)
+        if not g.is_cuda or g.get_device() != index or not o.is_cuda or o.get_device() != index:
+            _on_one_gpu(grads + outs, what)
+        flat += (g.data_ptr(), o.data_ptr(), g.numel(), code)
+    return struct.pack("QQqi4x" * len(grads), *flat), len(grads), dev
 
 
 def grad_norm(grads, *, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -809,7 +822,7 @@ def grad_norm(grads, *, workspace: torch.Tensor | None = None, stream=None) -> t
     arr, count, dev = _tensor_list(grads, None, what)
     with _OnStream(dev, stream) as handle:
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        ws = _clip_workspace(count, dev, workspace)
+        ws = _workspace(_size_query("mns_clip_workspace_size", count), dev, workspace)
         check(load().grad_norm(arr, count, norm.data_ptr(), ws.data_ptr(),
                                ws.numel() * ws.element_size(), handle), what)
     return norm
@@ -825,7 +838,7 @@ def clip_grad_norm(grads, max_norm: float, *, eps: float = 1e-6, out=None,
     arr, count, dev = _tensor_list(grads, out, what)
     with _OnStream(dev, stream) as handle:
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        ws = _clip_workspace(count, dev, workspace)
+        ws = _workspace(_size_query("mns_clip_workspace_size", count), dev, workspace)
         check(load().clip_grad_norm(arr, count, max_norm, eps, norm.data_ptr(), ws.data_ptr(),
                                     ws.numel() * ws.element_size(), handle), what)
     return norm

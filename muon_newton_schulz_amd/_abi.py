@@ -181,13 +181,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mns_balance_workspace_size.argtypes = [i64, i64, sz]
     lib.balance_loss.restype = ci
     lib.balance_loss.argtypes = [vp, i64, ci, vp, i64, vp, i64, i64, cf, vp, vp, i64, vp, csz, vp]
-    tp = ctypes.POINTER(MnsTensor)
     lib.mns_clip_workspace_size.restype = ci
     lib.mns_clip_workspace_size.argtypes = [ci, sz]
     lib.grad_norm.restype = ci
-    lib.grad_norm.argtypes = [tp, ci, vp, vp, csz, vp]
+    lib.grad_norm.argtypes = [vp, ci, vp, vp, csz, vp]
     lib.clip_grad_norm.restype = ci
-    lib.clip_grad_norm.argtypes = [tp, ci, cf, cf, vp, vp, csz, vp]
+    lib.clip_grad_norm.argtypes = [vp, ci, cf, cf, vp, vp, csz, vp]
     lib.mns_profile_set_flush.restype = ctypes.c_int
     lib.mns_profile_set_flush.argtypes = [vp, ctypes.c_size_t]
     _lib = lib

@@ -1,12 +1,17 @@
 // The global norm over many gradients, and their scaling by min(1, max_norm / (norm + eps)).
 //
 // Both passes are bound by HBM: the norm reads every gradient once, the scaling reads and writes it once.
-// Every tensor is cut into pieces of 16 KB, which a grid of at most kNormBlocks (kScaleBlocks) blocks
-// deals out in turn; the tensors' pointers and first pieces travel as kernel arguments, kClipPack tensors a launch,
-// so nothing is uploaded. Squares are formed and added in float64 (as everywhere in this library: no
-// underflow or overflow for any float32 gradient), a partial sum per block; every block of the scaling
-// adds all partial sums itself, in the same order, instead of waiting for a launch in between that
-// would do nothing else. The scaling walks the pieces backwards: those read last are still in the caches.
+// Every tensor is cut into pieces of 16 KB; the tensors' pointers and first pieces travel as kernel
+// arguments, kClipPack tensors a launch, so nothing is uploaded. Squares are formed and added in float64
+// (as everywhere in this library: no underflow or overflow for any float32 gradient), a partial sum per
+// block of at most kNormBlocks, added in the same order by everyone who needs the norm.
+//
+// Few pieces (kFewPieces): every block of the scaling adds the partial sums itself, which takes less than a
+// launch in between. More: a launch of one block adds them, and each block of the scaling takes one piece
+// (1.5 GB, out of place: 470 us; blocks that go from piece to piece 510 to 525). Lists beyond the 256 MB
+// last-level cache are read and written with non-temporal accesses (the norm 260 us instead of 300, the
+// scaling 470 instead of 517); smaller ones stay in the caches for the step that follows. Walking the
+// pieces backwards, so that those read last are found in the caches, gained nothing.
 #include "mns_internal.h"
 #include "row_vectors.h"
 
@@ -15,7 +20,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPieceBytes = 16384;
-constexpr int kNormBlocks = 2048, kScaleBlocks = 2048;
+constexpr int kNormBlocks = 2048, kFewPieces = 512;
+constexpr double kStreamBytes = double(256 << 20);
 
 struct Table {
   struct Entry {
@@ -28,34 +34,54 @@ struct Table {
   int64_t pieces;
 };
 
-// The tensor of piece i: the last one whose first piece is not behind it (uniform: scalar registers).
-__device__ __forceinline__ int tensor_of(const Table& a, int64_t i) {
-  int lo = 0, hi = a.count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.t[mid].first <= i) lo = mid;
-    else hi = mid;
+// The tensor that holds the pieces a block comes to, one after the other: looked up in the arguments only
+// when a piece lies outside the current one (uniform: scalar registers).
+struct Cursor {
+  const void* in;
+  void* out;
+  int64_t numel, first, end;    // pieces [first, end)
+  bool f32;
+  __device__ __forceinline__ void to(const Table& a, int64_t i) {
+    int lo = 0, hi = a.count;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.t[mid].first <= i) lo = mid;
+      else hi = mid;
+    }
+    in = a.t[lo].in;
+    out = a.t[lo].out;
+    numel = a.t[lo].numel;
+    first = a.t[lo].first;
+    end = lo + 1 < a.count ? a.t[lo + 1].first : a.pieces;
+    f32 = lo >= a.f32_from;
   }
-  return lo;
-}
+};
 
 // The n elements of a piece (more: of a whole one), zeros behind them.
-template <typename T>
+template <typename T, bool STREAM>
 __device__ __forceinline__ void load_piece(const T* p, int64_t n, u32x4* v) {
   constexpr int VEC = 16 / sizeof(T), PER = kPieceBytes / 16 / kThreads;
-  const bool whole = n >= kPieceBytes / (int)sizeof(T);
+  if (n >= kPieceBytes / (int)sizeof(T)) {
 #pragma unroll
-  for (int q = 0; q < PER; ++q) {
-    const int at = (q * kThreads + threadIdx.x) * VEC;
-    v[q] = load_chunk(p + at, whole ? VEC : (int)n - at);
+    for (int q = 0; q < PER; ++q) {
+      const T* at = p + (q * kThreads + threadIdx.x) * VEC;
+      if (STREAM) v[q] = load_streaming(at);
+      else __builtin_memcpy(&v[q], at, 16);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const int at = (q * kThreads + threadIdx.x) * VEC;
+      v[q] = load_chunk(p + at, (int)n - at);
+    }
   }
 }
 
-template <typename T>
+template <typename T, bool STREAM>
 __device__ __forceinline__ double piece_squares(const T* p, int64_t n) {
   constexpr int VEC = 16 / sizeof(T), PER = kPieceBytes / 16 / kThreads;
   u32x4 v[PER];
-  load_piece<T>(p, n, v);
+  load_piece<T, STREAM>(p, n, v);
   double s[PER] = {};
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
@@ -84,28 +110,26 @@ __device__ __forceinline__ double block_sum(double v) {
   return all;
 }
 
+template <bool STREAM>
 __global__ __launch_bounds__(kThreads) void k_grad_squares(Table a, double* partial) {
   double sum = 0.;
+  Cursor c;
+  c.end = 0;
   for (int64_t i = blockIdx.x; i < a.pieces; i += gridDim.x) {
-    const int t = tensor_of(a, i);
-    const int64_t k = i - a.t[t].first;
-    if (t >= a.f32_from) {
-      const int64_t at = k * (kPieceBytes / 4);
-      sum += piece_squares(static_cast<const float*>(a.t[t].in) + at, a.t[t].numel - at);
-    } else {
-      const int64_t at = k * (kPieceBytes / 2);
-      sum += piece_squares(static_cast<const __bf16*>(a.t[t].in) + at, a.t[t].numel - at);
-    }
+    if (i >= c.end) c.to(a, i);
+    const int64_t at = (i - c.first) * (kPieceBytes / (c.f32 ? 4 : 2));
+    if (c.f32) sum += piece_squares<float, STREAM>(static_cast<const float*>(c.in) + at, c.numel - at);
+    else sum += piece_squares<__bf16, STREAM>(static_cast<const __bf16*>(c.in) + at, c.numel - at);
   }
   sum = block_sum(sum);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
-template <typename T>
+template <typename T, bool STREAM>
 __device__ __forceinline__ void scale_piece(const T* p, T* out, int64_t n, float factor) {
   constexpr int VEC = 16 / sizeof(T), PER = kPieceBytes / 16 / kThreads;
   u32x4 v[PER];
-  load_piece<T>(p, n, v);
+  load_piece<T, STREAM>(p, n, v);
   const bool whole = n >= kPieceBytes / (int)sizeof(T);
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
@@ -114,7 +138,9 @@ __device__ __forceinline__ void scale_piece(const T* p, T* out, int64_t n, float
     __builtin_memcpy(e, &v[q], 16);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) e[i] = (T)((float)e[i] * factor);
-    if (whole || at + VEC <= (int)n) {
+    if (STREAM && whole) {
+      store_streaming(out + at, e);
+    } else if (whole || at + VEC <= (int)n) {
       __builtin_memcpy(out + at, e, 16);
     } else {
 #pragma unroll
@@ -124,30 +150,51 @@ __device__ __forceinline__ void scale_piece(const T* p, T* out, int64_t n, float
   }
 }
 
-// norm: written by block 0 of the first launch (null in the others).
-__global__ __launch_bounds__(kThreads) void k_grad_scale(Table a, const double* partial, int partials,
-                                                         float max_norm, float eps, float* norm) {
+// The norm and the factor from the partial sums (in every thread of the block).
+__device__ __forceinline__ float clip_factor(const double* partial, int partials, float max_norm,
+                                             float eps, double& total) {
   double sum = 0.;
+#pragma unroll 4
   for (int i = threadIdx.x; i < partials; i += kThreads) sum += partial[i];
-  const double total = sqrt(block_sum(sum));
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
+  total = sqrt(block_sum(sum));
   const double floor = total + (double)eps, ratio = (double)max_norm / floor;
-  const float factor = ratio >= 1. || floor == 0. ? 1.f : (float)ratio;       // a NaN stays one
-  for (int64_t b = blockIdx.x; b < a.pieces; b += gridDim.x) {
-    const int64_t i = a.pieces - 1 - b;
-    const int t = tensor_of(a, i);
-    if (factor == 1.f && a.t[t].in == a.t[t].out) continue;
-    const int64_t k = i - a.t[t].first;
-    if (t >= a.f32_from) {
-      const int64_t at = k * (kPieceBytes / 4);
-      scale_piece(static_cast<const float*>(a.t[t].in) + at, static_cast<float*>(a.t[t].out) + at,
-                  a.t[t].numel - at, factor);
-    } else {
-      const int64_t at = k * (kPieceBytes / 2);
-      scale_piece(static_cast<const __bf16*>(a.t[t].in) + at, static_cast<__bf16*>(a.t[t].out) + at,
-                  a.t[t].numel - at, factor);
-    }
+  return ratio >= 1. || floor == 0. ? 1.f : (float)ratio;       // a NaN stays one
+}
+
+__global__ __launch_bounds__(kThreads) void k_grad_norm(const double* partial, int partials,
+                                                        float max_norm, float eps, float* norm,
+                                                        float* factor) {
+  double total;
+  const float f = clip_factor(partial, partials, max_norm, eps, total);
+  if (threadIdx.x == 0) {
+    *norm = (float)total;
+    *factor = f;
   }
+}
+
+// One piece a block. factor null: from the partial sums, and block 0 writes the norm.
+template <bool STREAM>
+__global__ __launch_bounds__(kThreads) void k_grad_scale(Table a, const double* partial, int partials,
+                                                         float max_norm, float eps, float* norm,
+                                                         const float* factor) {
+  float f;
+  if (factor) {
+    f = *factor;
+  } else {
+    double total;
+    f = clip_factor(partial, partials, max_norm, eps, total);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
+  }
+  Cursor c;
+  c.to(a, blockIdx.x);
+  if (f == 1.f && c.in == c.out) return;
+  const int64_t at = (blockIdx.x - c.first) * (kPieceBytes / (c.f32 ? 4 : 2));
+  if (c.f32)
+    scale_piece<float, STREAM>(static_cast<const float*>(c.in) + at, static_cast<float*>(c.out) + at,
+                               c.numel - at, f);
+  else
+    scale_piece<__bf16, STREAM>(static_cast<const __bf16*>(c.in) + at,
+                                static_cast<__bf16*>(c.out) + at, c.numel - at, f);
 }
 
 // Tensors [first, first + kClipPack) of the list, bfloat16 ones before float32 ones.
@@ -166,36 +213,50 @@ void fill_table(Table& a, const ClipTensor* list, int count) {
   }
 }
 
-int grid_of(const Table& a, int most) { return (int)(a.pieces < most ? a.pieces : most); }
-
 }  // namespace
 
+// The partial sums, and the factor behind them.
 size_t clip_workspace(int count) {
-  return (size_t)((count + kClipPack - 1) / kClipPack) * kNormBlocks * sizeof(double);
+  return (size_t)((count + kClipPack - 1) / kClipPack) * kNormBlocks * sizeof(double) + 256;
 }
 
 hipError_t clip_grads(const ClipTensor* list, int count, bool scale, float max_norm, float eps,
                       float* norm, double* partial, hipStream_t s) {
+  double bytes = 0;
+  for (int i = 0; i < count; ++i) bytes += (double)list[i].numel * (list[i].store == Store::F32 ? 4 : 2);
+  const bool stream = bytes > kStreamBytes;
+  float* factor = reinterpret_cast<float*>(partial + clip_workspace(count) / sizeof(double) - 32);
+  const dim3 block(kThreads);
   int partials = 0;
+  int64_t pieces = 0;
   Table a;
+  hipError_t e;
   for (int i = 0; i < count; i += kClipPack) {
     fill_table(a, list + i, count - i < kClipPack ? count - i : kClipPack);
     if (a.pieces == 0) continue;
-    const int grid = grid_of(a, kNormBlocks);
-    hipLaunchKernelGGL(k_grad_squares, dim3((unsigned)grid), dim3(kThreads), 0, s, a, partial + partials);
-    const hipError_t e = hipGetLastError();
+    const int grid = (int)(a.pieces < kNormBlocks ? a.pieces : kNormBlocks);
+    if (stream) hipLaunchKernelGGL(k_grad_squares<true>, dim3((unsigned)grid), block, 0, s, a, partial + partials);
+    else hipLaunchKernelGGL(k_grad_squares<false>, dim3((unsigned)grid), block, 0, s, a, partial + partials);
+    e = hipGetLastError();
     if (e != hipSuccess) return e;
     partials += grid;
+    pieces += a.pieces;
   }
-  // The first launch also writes the norm; without scaling, or without elements, it does only that.
-  for (int i = 0; i < count; i += kClipPack) {
-    fill_table(a, list + i, scale ? (count - i < kClipPack ? count - i : kClipPack) : 0);
-    if (a.pieces == 0 && i > 0) continue;
-    const int grid = a.pieces == 0 ? 1 : grid_of(a, kScaleBlocks);
-    hipLaunchKernelGGL(k_grad_scale, dim3((unsigned)grid), dim3(kThreads), 0, s, a, partial, partials,
-                       max_norm, eps, i == 0 ? norm : nullptr);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !scale) return e;
+  const bool few = scale && count <= kClipPack && pieces > 0 && pieces <= kFewPieces;
+  if (!few) {
+    hipLaunchKernelGGL(k_grad_norm, dim3(1), block, 0, s, partial, partials, max_norm, eps, norm, factor);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  for (int i = 0; scale && i < count; i += kClipPack) {
+    if (count > kClipPack) fill_table(a, list + i, count - i < kClipPack ? count - i : kClipPack);
+    if (a.pieces == 0) continue;
+    const dim3 grid((unsigned)a.pieces);
+    const float* given = few ? nullptr : factor;
+    if (stream) hipLaunchKernelGGL(k_grad_scale<true>, grid, block, 0, s, a, partial, partials, max_norm, eps, norm, given);
+    else hipLaunchKernelGGL(k_grad_scale<false>, grid, block, 0, s, a, partial, partials, max_norm, eps, norm, given);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }

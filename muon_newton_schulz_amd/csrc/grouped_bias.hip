@@ -86,30 +86,38 @@ __global__ __launch_bounds__(256) void k_bias_grad(BiasArgs p) {
   }
 }
 
-// The same list of tiles: the block of an expert's first chunk adds the chunks' sums, four quarters of
-// them side by side (each in order), then the quarters in order.
+// One block per expert and 256 columns, which only experts of several chunks keep: it adds the chunks' sums,
+// four quarters of them side by side (each in order), then the quarters in order.
 template <typename TO>
 __global__ __launch_bounds__(1024) void k_bias_join(BiasArgs p) {
-  Place at;
-  const int lin = (int)blockIdx.x;
-  const Walk w = walk_start(p, p.chunk, p.tiles_n, p.fill_rest, 1);
-  if (!find_place(p, p.chunk, p.tiles_n, p.fill_rest, w, lin, at, 1)) return;
-  if (at.expert < 0 || at.inside >= p.tiles_n || at.hi - at.lo <= p.chunk) return;
-  int chunks = (at.hi - at.lo + p.chunk - 1) / p.chunk;
-  const int listed = (w.total - 1 - lin) / p.tiles_n + 1;     // fewer only where offsets overlap
+  const int expert = (int)(blockIdx.x / p.tiles_n), column_tile = (int)(blockIdx.x % p.tiles_n);
+  int lo, hi;
+  expert_rows(p, expert, lo, hi);
+  if (hi - lo <= p.chunk) return;
+  // its first chunk's place in the list of tiles: behind those of the entries before it
+  Walk w;
+  const int entry = expert + p.fill_rest;
+  int64_t first = 0;
+  for (int g0 = 0; g0 <= entry; g0 += 64) {
+    walk_batch(p, p.chunk, p.tiles_n, p.fill_rest, g0, w, 1);
+    const int at = entry - g0 < 64 ? entry - g0 : 64;
+    if (at > 0) first += (unsigned)__builtin_amdgcn_readlane(w.incl, at - 1);
+  }
+  int64_t chunks = (hi - lo + p.chunk - 1) / p.chunk;
+  const int64_t listed = (p.most_tiles - first) / p.tiles_n;      // fewer only where offsets overlap
   if (chunks > listed) chunks = listed;
   const int tid = threadIdx.x & 255, quarter = threadIdx.x >> 8;
-  const int c0 = (int)((int64_t)chunks * quarter / 4), c1 = (int)((int64_t)chunks * (quarter + 1) / 4);
+  const int c0 = (int)(chunks * quarter / 4), c1 = (int)(chunks * (quarter + 1) / 4);
   float total = 0.f;
 #pragma unroll 8
   for (int c = c0; c < c1; ++c)
-    total += p.partial[((int64_t)lin + (int64_t)c * p.tiles_n) * kCols + tid];
+    total += p.partial[(first + (int64_t)c * p.tiles_n + column_tile) * kCols + tid];
   __shared__ float part_sum[4][kCols];
   part_sum[quarter][tid] = total;
   __syncthreads();
-  const int col = at.inside * kCols + tid;
+  const int col = column_tile * kCols + tid;
   if (quarter == 0 && col < p.N)
-    static_cast<TO*>(p.db)[(int64_t)at.expert * p.N + col] =
+    static_cast<TO*>(p.db)[(int64_t)expert * p.N + col] =
         (TO)(part_sum[0][tid] + part_sum[1][tid] + part_sum[2][tid] + part_sum[3][tid]);
 }
 
@@ -158,8 +166,9 @@ hipError_t bias_grad(const BiasGradDesc& d, hipStream_t s) {
     hipLaunchKernelGGL((k_bias_grad<__bf16, __bf16>), grid, dim3(256), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || d.total_rows <= a.chunk) return e;
-  if (out32) hipLaunchKernelGGL(k_bias_join<float>, grid, dim3(1024), 0, s, a);
-  else hipLaunchKernelGGL(k_bias_join<__bf16>, grid, dim3(1024), 0, s, a);
+  const dim3 joins((unsigned)(d.groups * a.tiles_n));
+  if (out32) hipLaunchKernelGGL(k_bias_join<float>, joins, dim3(1024), 0, s, a);
+  else hipLaunchKernelGGL(k_bias_join<__bf16>, joins, dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 

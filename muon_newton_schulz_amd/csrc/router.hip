@@ -13,15 +13,15 @@ constexpr int kWaves = 4, kThreads = 64 * kWaves;
 // piece of the list and every wave a part of that, both in order, so a place is: the expert's begin,
 // plus what earlier blocks and waves hold of it, plus the rank inside the wave. With more than one
 // block, a first launch counts each block's piece; the second adds the other blocks' counts by itself
-// (E integers a block, from L2), scans them and deals the places. No atomics but counts in LDS, so the
-// result is the one stable order.
+// (four groups of threads side by side, E integers a block, from L2), scans them and deals the places. No
+// atomics but counts in LDS, so the result is the one stable order. Bound by latency: few, long steps.
 struct OrderArgs {
   const int64_t* ids;
   int64_t* counts;
   int64_t* offsets;
   int64_t* order;              // may be null
   int* hist;                   // blocks x (E + 1)
-  int M, E, blocks, piece;     // piece: assignments of a block, a multiple of kThreads
+  int M, E, blocks, piece;     // piece: assignments of a block, a multiple of the block's threads
 };
 
 __device__ __forceinline__ int bin_of(const OrderArgs& p, int i) {
@@ -29,72 +29,92 @@ __device__ __forceinline__ int bin_of(const OrderArgs& p, int i) {
   return id >= 0 && id < p.E ? (int)id : p.E;
 }
 
-__global__ __launch_bounds__(kThreads) void k_count(OrderArgs p) {
+__global__ __launch_bounds__(1024) void k_count(OrderArgs p) {
   __shared__ int bins[kMaxRouted + 1];
-  for (int e = threadIdx.x; e <= p.E; e += kThreads) bins[e] = 0;
+  for (int e = threadIdx.x; e <= p.E; e += 1024) bins[e] = 0;
   __syncthreads();
   const int64_t first = (int64_t)blockIdx.x * p.piece;
   const int end = (int)(first + p.piece < p.M ? first + p.piece : p.M);
-  for (int i = (int)first + threadIdx.x; i < end; i += kThreads) atomicAdd(&bins[bin_of(p, i)], 1);
+#pragma unroll 4
+  for (int i = (int)first + threadIdx.x; i < end; i += 1024) atomicAdd(&bins[bin_of(p, i)], 1);
   __syncthreads();
-  for (int e = threadIdx.x; e <= p.E; e += kThreads)
+  for (int e = threadIdx.x; e <= p.E; e += 1024)
     p.hist[(int64_t)blockIdx.x * (p.E + 1) + e] = bins[e];
 }
 
-__global__ __launch_bounds__(kThreads) void k_order(OrderArgs p) {
-  __shared__ int cursor[kWaves][kMaxRouted + 1];     // counts, then the wave's next place, by expert
-  __shared__ int carry[kWaves];
+// WAVES waves, whose counters for up to MOST experts fit the LDS.
+template <int WAVES, int MOST>
+__global__ __launch_bounds__(64 * WAVES) void k_order(OrderArgs p) {
+  constexpr int THREADS = 64 * WAVES, BINS = 256, SIDE = THREADS / BINS;
+  static_assert(SIDE >= 1, "a thread for each bin of a step");
+  __shared__ int cursor[WAVES][MOST + 1];     // counts, then the wave's next place, by expert
+  __shared__ int sums[2][SIDE][BINS];         // of the blocks' counts: all, and those of earlier blocks
+  __shared__ int carry[BINS / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int bins = p.E + 1;
-  for (int e = tid; e < bins; e += kThreads)
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) cursor[w][e] = 0;
+  for (int e = tid; e < bins * WAVES; e += THREADS) cursor[e / bins][e % bins] = 0;
   __syncthreads();
-  const int64_t first = (int64_t)blockIdx.x * p.piece + (int64_t)wave * (p.piece / kWaves);
+  const int share = p.piece / WAVES;
+  const int64_t first = (int64_t)blockIdx.x * p.piece + (int64_t)wave * share;
   const int begin = (int)(first < p.M ? first : p.M);
-  const int end = (int)(first + p.piece / kWaves < p.M ? first + p.piece / kWaves : p.M);
+  const int end = (int)(first + share < p.M ? first + share : p.M);
+#pragma unroll 4
   for (int i = begin + lane; i < end; i += 64) atomicAdd(&cursor[wave][bin_of(p, i)], 1);
-  __syncthreads();
-  // Bins in order, kThreads at a time: all assignments of a bin, those of earlier blocks, and a scan.
+  // Bins in order, BINS at a time.
   int running = 0;
-  for (int e0 = 0; e0 < bins; e0 += kThreads) {
-    const int e = e0 + tid;
-    int total = 0, before = 0, own[kWaves] = {};
-    if (e < bins) {
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) total += own[w] = cursor[w][e];
-      if (p.blocks > 1) {
-        total = 0;
+  for (int e0 = 0; e0 < bins; e0 += BINS) {
+    const int e = e0 + tid % BINS, side = tid / BINS;
+    if (p.blocks > 1) {
+      int total = 0, before = 0;
+      if (e < bins) {
 #pragma unroll 8
-        for (int b = 0; b < p.blocks; ++b) {
+        for (int b = side; b < p.blocks; b += SIDE) {
           const int h = p.hist[(int64_t)b * bins + e];
           total += h;
           before += b < (int)blockIdx.x ? h : 0;
         }
       }
+      sums[0][side][tid % BINS] = total;
+      sums[1][side][tid % BINS] = before;
     }
-    int incl = total;
+    __syncthreads();
+    int total = 0, before = 0, own[WAVES], incl = 0;
+    if (tid < BINS) {
+      if (e < bins) {
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int up = __shfl_up(incl, o);
-      if (lane >= o) incl += up;
+        for (int w = 0; w < WAVES; ++w) total += own[w] = cursor[w][e];
+        if (p.blocks > 1) {
+          total = 0;
+#pragma unroll
+          for (int s = 0; s < SIDE; ++s) {
+            total += sums[0][s][tid];
+            before += sums[1][s][tid];
+          }
+        }
+      }
+      incl = total;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int up = __shfl_up(incl, o);
+        if (lane >= o) incl += up;
+      }
+      if (lane == 63) carry[wave] = incl;
     }
-    if (lane == 63) carry[wave] = incl;
     __syncthreads();
     int start = running + incl - total;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < BINS / 64; ++w) {
       if (w < wave) start += carry[w];
       running += carry[w];
     }
-    if (e < bins) {
+    if (tid < BINS && e < bins) {
       if (blockIdx.x == 0) {
         p.offsets[e] = start;
         if (e < p.E) p.counts[e] = total;
       }
       int place = start + before;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
+      for (int w = 0; w < WAVES; ++w) {
         cursor[w][e] = place;
         place += own[w];
       }
@@ -102,11 +122,13 @@ __global__ __launch_bounds__(kThreads) void k_order(OrderArgs p) {
     __syncthreads();
   }
   if (!p.order) return;
+  int next = begin + lane < end ? bin_of(p, begin + lane) : -1;
   for (int i0 = begin; i0 < end; i0 += 64) {
     const int i = i0 + lane;
     const bool in = i < end;
-    const int bin = in ? bin_of(p, i) : -1;
-    // the lanes of the same bin, one bit of the bin at a time (-1 differs from all in its sign bit)
+    const int bin = next;
+    next = i + 64 < end ? bin_of(p, i + 64) : -1;      // loaded a step ahead
+    // the lanes of the same bin, one bit of the bin at a time
     unsigned long long same = __ballot(in);
     for (int bit = 1; bit < bins; bit <<= 1) {
       const unsigned long long set = __ballot((bin & bit) != 0);
@@ -252,31 +274,40 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs p) {
 __global__ __launch_bounds__(kThreads) void k_balance_join(BalanceArgs p) {
   const int tid = threadIdx.x;
   double sum = 0., n = 0.;
+#pragma unroll 4
   for (int b = tid; b < p.blocks; b += kThreads) sum += p.partial[b];
   for (int e = tid; e < p.E; e += kThreads) n += (double)p.counts[e];
-  __shared__ double s[2][kThreads];
-  s[0][tid] = sum;
-  s[1][tid] = n;
-  __syncthreads();
-  for (int o = kThreads / 2; o > 0; o >>= 1) {
-    if (tid < o) {
-      s[0][tid] += s[0][tid + o];
-      s[1][tid] += s[1][tid + o];
-    }
-    __syncthreads();
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    sum += __shfl_xor(sum, o);
+    n += __shfl_xor(n, o);
   }
-  if (tid == 0) finish_loss(p, s[0][0], s[1][0]);
+  __shared__ double s[2][kWaves];
+  if ((tid & 63) == 0) {
+    s[0][tid >> 6] = sum;
+    s[1][tid >> 6] = n;
+  }
+  __syncthreads();
+  if (tid != 0) return;
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) {
+    sum += s[0][w];
+    n += s[1][w];
+  }
+  finish_loss(p, sum, n);
 }
 
+// One block up to kOneBlock assignments (one launch), else pieces of at least kPiece and at most 128 blocks.
+constexpr int64_t kOneBlock = 8192, kPiece = 2048;
 int order_blocks(int64_t m, int* piece) {
-  int64_t c = (m + 255) / 256;
-  if (c < 2048) c = 2048;
-  c = (c + kThreads - 1) / kThreads * kThreads;
-  *piece = (int)c;
-  return (int)((m + c - 1) / c);
+  int64_t c = m <= kOneBlock ? m : (m + 127) / 128;
+  if (m > kOneBlock && c < kPiece) c = kPiece;
+  c = (c + 1023) / 1024 * 1024;
+  *piece = (int)(c < 1024 ? 1024 : c);
+  return m <= kOneBlock ? 1 : (int)((m + c - 1) / c);
 }
 
-constexpr int kBalanceBlocks = 1024;
+constexpr int kBalanceBlocks = 2048;
 
 template <typename T>
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
@@ -293,6 +324,7 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
 int balance_blocks(int64_t tokens, int64_t experts) {
   const int64_t lanes = experts <= 32 ? 8 : experts <= 64 ? 16 : experts <= 128 ? 32 : 64;
   const int64_t rows = kWaves * 64 / lanes, blocks = (tokens + rows - 1) / rows;
+  if (blocks <= 4) return 1;          // a few rounds of one block take less than a second launch
   return (int)(blocks < 1 ? 1 : blocks > kBalanceBlocks ? kBalanceBlocks : blocks);
 }
 
@@ -315,13 +347,14 @@ hipError_t expert_order(const int64_t* ids, int64_t assignments, int64_t experts
   a.M = (int)assignments;
   a.E = (int)experts;
   a.blocks = order_blocks(assignments, &a.piece);
-  if (a.blocks < 1) a.blocks = 1;
   if (a.blocks > 1) {
-    hipLaunchKernelGGL(k_count, dim3((unsigned)a.blocks), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL(k_count, dim3((unsigned)a.blocks), dim3(1024), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(k_order, dim3((unsigned)a.blocks), dim3(kThreads), 0, s, a);
+  const dim3 grid((unsigned)a.blocks);
+  if (experts <= 512) hipLaunchKernelGGL((k_order<16, 512>), grid, dim3(1024), 0, s, a);
+  else hipLaunchKernelGGL((k_order<4, kMaxRouted>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -23,6 +23,19 @@ __device__ __forceinline__ u32x4 load_chunk(const T* p, int valid) {
   return v;
 }
 
+// The same 16 bytes past the caches, for data that is not used again before it would leave them.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+template <typename T>
+__device__ __forceinline__ u32x4 load_streaming(const T* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+}
+template <typename T>
+__device__ __forceinline__ void store_streaming(T* p, const void* v) {
+  u32x4 x;
+  __builtin_memcpy(&x, v, 16);
+  __builtin_nontemporal_store(x, reinterpret_cast<u32x4_any*>(p));
+}
+
 // Eight consecutive elements of a row.
 template <typename T>
 struct Eight {
