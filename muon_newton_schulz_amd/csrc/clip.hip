@@ -21,7 +21,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPieceBytes = 16384;
 constexpr int kNormBlocks = 2048, kFewPieces = 512;
-constexpr double kStreamBytes = double(256 << 20);
 
 struct Table {
   struct Entry {

@@ -133,36 +133,64 @@ __device__ __forceinline__ void zero_tile(const LayerArgs& p, int64_t row, int c
 }
 
 // The epilogue of a wave's FM x FN fragments (as in store_fragments) at rows m0, columns n0 of the tile
-// that starts at row `row`, column `col`.
+// that starts at row `row`, column `col`, in FM * FN steps. load() takes a step's operands; a step's are
+// loaded before the one before it is finished, the first ones by the caller where its registers allow
+// that before the product itself.
 template <typename T, int FORM, int FM, int FN>
-__device__ __forceinline__ void finish_fragments(const LayerArgs& p, const floatx16 (&acc)[FM][FN],
-                                                 floatx4* stage, int expert, int64_t row, int col,
-                                                 int m0, int n0, int m_valid, int n_valid) {
-  constexpr bool EXACT = sizeof(T) == 4;
-  constexpr int ROWS = 32 / FN, CH = 8 * FN, LANES = 4 * FN, STEP = 64 / LANES;
-  int ln = threadIdx.x & 63;
-  asm volatile("" : "+v"(ln));       // addresses computed here, not kept across a caller's loop
-  const int c = ln % LANES, r0 = ln / LANES;
-  const int n = n0 + 8 * c, left = n_valid - n;
-  // chunk k of staged row r: the 16-byte accesses of 16 lanes cover all banks, writing and reading
-  auto at = [](int r, int k) { return r * CH + (k ^ (FN == 2 ? r & 15 : (r >> 1) & 7)); };
+struct Finish {
+  static constexpr bool EXACT = sizeof(T) == 4;
+  static constexpr int ROWS = 32 / FN, CH = 8 * FN, LANES = 4 * FN, STEP = 64 / LANES;
+  struct Operands {
+    Eight<T> z[2], r[2];
+  };
+  int ln, c, r0, n, left, col, m0, m_valid, expert;
+  int64_t row;
   Eight<T> bias;
-  if (FORM == NT)
-    bias.load(static_cast<const T*>(p.bias) + (int64_t)expert * p.N + col + n, p.bias ? left : 0);
+  Operands first;
+
+  __device__ __forceinline__ Finish(int expert_, int64_t row_, int col_, int m0_, int n0,
+                                    int m_valid_, int n_valid) {
+    ln = threadIdx.x & 63;
+    asm volatile("" : "+v"(ln));       // addresses computed here, not kept across a caller's loop
+    c = ln % LANES;
+    r0 = ln / LANES;
+    n = n0 + 8 * c;
+    left = n_valid - n;
+    col = col_;
+    m0 = m0_;
+    m_valid = m_valid_;
+    expert = expert_;
+    row = row_;
+  }
+  // chunk k of staged row r: the 16-byte accesses of 16 lanes cover all banks, writing and reading
+  __device__ __forceinline__ static int at(int r, int k) {
+    return r * CH + (k ^ (FN == 2 ? r & 15 : (r >> 1) & 7));
+  }
+  __device__ __forceinline__ int row_of(int step) const {
+    return m0 + 32 * (step / FN) + ROWS * (step % FN) + r0;
+  }
+  __device__ __forceinline__ void load(const LayerArgs& p, int step, Operands& o) const {
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
+    for (int q = 0; q < 2; ++q) {
+      const int m = row_of(step) + STEP * q, have = m < m_valid ? left : 0;
+      if (FORM == NN)
+        o.z[q].load(static_cast<const T*>(p.Z) + (row + m) * p.ldz + col + n, p.Z ? have : 0);
+      o.r[q].load(static_cast<const T*>(p.R) + (row + m) * p.ldr + col + n, p.R ? have : 0);
+    }
+  }
+  __device__ __forceinline__ void load_first(const LayerArgs& p) {
+    if (FORM == NT)
+      bias.load(static_cast<const T*>(p.bias) + (int64_t)expert * p.N + col + n, p.bias ? left : 0);
+    load(p, 0, first);
+  }
+  __device__ __forceinline__ void run(const LayerArgs& p, const floatx16 (&acc)[FM][FN],
+                                      floatx4* stage) const {
+    Operands now = first;
 #pragma unroll
-    for (int pass = 0; pass < FN; ++pass) {
-      const int m = m0 + 32 * i + ROWS * pass + r0;
-      Eight<T> z[2], r[2];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int64_t t = row + m + STEP * q;
-        const int have = m + STEP * q < m_valid ? left : 0;
-        if (FORM == NN)
-          z[q].load(static_cast<const T*>(p.Z) + t * p.ldz + col + n, p.Z ? have : 0);
-        r[q].load(static_cast<const T*>(p.R) + t * p.ldr + col + n, p.R ? have : 0);
-      }
+    for (int step = 0; step < FM * FN; ++step) {
+      const int i = step / FN, pass = step % FN;
+      Operands next;
+      if (step + 1 < FM * FN) load(p, step + 1, next);
       if (FN == 1 || ((ln >> 4) & 1) == pass) {
 #pragma unroll
         for (int j = 0; j < FN; ++j)
@@ -177,8 +205,8 @@ __device__ __forceinline__ void finish_fragments(const LayerArgs& p, const float
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const floatx4 lo = stage[at(r0 + STEP * q, 2 * c)], hi = stage[at(r0 + STEP * q, 2 * c + 1)];
-        if (m + STEP * q >= m_valid || left <= 0) continue;
-        const int64_t t = row + m + STEP * q;
+        const int m = row_of(step) + STEP * q;
+        if (m >= m_valid || left <= 0) continue;
         float v[8], x[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = lo[e], v[4 + e] = hi[e];
@@ -189,22 +217,31 @@ __device__ __forceinline__ void finish_fragments(const LayerArgs& p, const float
           for (int e = 0; e < 8; ++e) v[e] += x[e];
           if (p.Z) {
             out.set(v);
-            out.store(static_cast<T*>(p.Z) + t * p.ldz + col + n, left);
+            out.store(static_cast<T*>(p.Z) + (row + m) * p.ldz + col + n, left);
           }
           activate<EXACT>(p.act, v);
         } else {
-          z[q].get(x);
+          now.z[q].get(x);
           times_slope<EXACT>(p.act, v, x);
         }
-        r[q].get(x);
+        now.r[q].get(x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += x[e];
         out.set(v);
-        out.store(static_cast<T*>(p.C) + t * p.ldc + col + n, left);
+        out.store(static_cast<T*>(p.C) + (row + m) * p.ldc + col + n, left);
       }
+      if (step + 1 < FM * FN) now = next;
     }
   }
-}
+};
+
+// (a plain product has none)
+struct NoFinish {
+  template <typename... A>
+  __device__ __forceinline__ NoFinish(A...) {}
+};
+template <typename Args, typename T, int FORM, int FM, int FN>
+using FinishOf = std::conditional_t<kLayer<Args>, Finish<T, FORM, FM, FN>, NoFinish>;
 
 // The other orientation (A feeds the MFMA's A input): element e of a lane is row m0 + 8 (e / 4)
 // + 4 (lane >> 5) + e % 4, column n0 + (lane & 31). 32 lanes hold 32 neighbouring columns, so a
@@ -415,8 +452,9 @@ __global__ __launch_bounds__(256) void k_grouped(Args p) {
                         add[i][j]);
   } else if constexpr (kLayer<Args>) {
     // (behind the loop's last barrier the operands' LDS is free)
-    finish_fragments<T, FORM>(p, acc, reinterpret_cast<floatx4*>(As) + wave * 256, expert, m0, n0,
-                              wm * 64, wn * 64, m_valid, n_valid);
+    Finish<T, FORM, 2, 2> end(expert, m0, n0, wm * 64, wn * 64, m_valid, n_valid);
+    end.load_first(p);
+    end.run(p, acc, reinterpret_cast<floatx4*>(As) + wave * 256);
   } else {
     store_fragments<TO, 2, 2, false>(p, acc, origin, wm * 64, wn * 64, m_valid, n_valid);
   }
@@ -482,6 +520,10 @@ __global__ __launch_bounds__(256) void k_grouped_split(Args p) {
       }
     }
   };
+  // wave w finishes fragment (w / 2, w % 2)
+  const int mi = 32 * (wave >> 1), nj = 32 * (wave & 1);
+  FinishOf<Args, T, FORM, 1, 1> end(at.expert, m0, n0, mi, nj, m_valid, n_valid);
+  if constexpr (kLayer<Args>) end.load_first(p);
   floatx16 acc[2][2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -519,8 +561,6 @@ __global__ __launch_bounds__(256) void k_grouped_split(Args p) {
         for (int j = 0; j < 2; ++j) F::mma(acc[i][j], b[j], a[i]);
     }
   }
-  // wave w finishes fragment (w / 2, w % 2)
-  const int mi = 32 * (wave >> 1), nj = 32 * (wave & 1);
   __syncthreads();
   float(*part)[4][16][64] = reinterpret_cast<float(*)[4][16][64]>(lds);     // [wave][fragment]
 #pragma unroll
@@ -535,8 +575,7 @@ __global__ __launch_bounds__(256) void k_grouped_split(Args p) {
                    part[3][wave][e][lane];
   if constexpr (kLayer<Args>) {
     __syncthreads();                   // every wave has read the sums
-    finish_fragments<T, FORM>(p, sum, reinterpret_cast<floatx4*>(lds) + wave * 256, at.expert, m0, n0,
-                              mi, nj, m_valid, n_valid);
+    end.run(p, sum, reinterpret_cast<floatx4*>(lds) + wave * 256);
   } else {
     store_fragments<T, 1, 1, false>(p, sum, m0 * p.ldc + n0, mi, nj, m_valid, n_valid);
   }
@@ -622,6 +661,26 @@ __global__ __launch_bounds__(256) void k_grouped_rows(Args p) {
 #pragma unroll
     for (int j = 0; j < NTW; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 
+  // A layer's bias and residual at a fragment's place; where the waves share fragments, those of a wave's
+  // first one are loaded before the product.
+  T bias[4] = {}, res[4] = {};
+  auto operands = [&](int i, int j) {
+    if constexpr (kLayer<Args>) {
+      const int m = 16 * i + r16, n = n0 + 16 * j + 4 * (lane >> 4);
+      auto load = [&](const T* src, T (&t)[4]) {
+        if (n + 4 <= p.N) {
+          __builtin_memcpy(t, src, sizeof(t));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t[e] = n + e < p.N ? src[e] : (T)0.f;
+        }
+      };
+      if (p.bias) load(static_cast<const T*>(p.bias) + (int64_t)expert * p.N + n, bias);
+      if (p.R && m < m_valid) load(static_cast<const T*>(p.R) + (int64_t)(row0 + m) * p.ldr + n, res);
+    }
+  };
+  if (WK > 1 && wave < MT * NTW) operands(wave / NTW, wave % NTW);
+
   u32x4 xa[D][MT], wa[D][NTW];
   auto load = [&](int s, int d) {
     const int64_t o = (int64_t)s * STEP;
@@ -691,23 +750,12 @@ __global__ __launch_bounds__(256) void k_grouped_rows(Args p) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = v[e];
     if constexpr (kLayer<Args>) {
-      auto load = [&](const T* src, T (&t)[4]) {
-        if (n + 4 <= p.N) {
-          __builtin_memcpy(t, src, sizeof(t));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) t[e] = n + e < p.N ? src[e] : (T)0.f;
-        }
-      };
-      T bias[4] = {}, r[4] = {};
-      if (p.bias) load(static_cast<const T*>(p.bias) + (int64_t)expert * p.N + n, bias);
-      if (p.R) load(static_cast<const T*>(p.R) + (int64_t)(row0 + m) * p.ldr + n, r);
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] += (float)bias[e];
       if (p.Z) store(p.Z, p.ldz, x);
       activate<sizeof(T) == 4>(p.act, x);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] += (float)r[e];
+      for (int e = 0; e < 4; ++e) x[e] += (float)res[e];
     }
     store(p.C, p.ldc, x);
   };
@@ -719,7 +767,10 @@ __global__ __launch_bounds__(256) void k_grouped_rows(Args p) {
 #pragma unroll
       for (int j = 0; j < NTW; ++j) row[wave][j][lane] = acc[i][j];
 #pragma unroll 1
-      for (int j = 0; j < NTW; ++j) put(i, j, row[wave][j][lane]);
+      for (int j = 0; j < NTW; ++j) {
+        operands(i, j);
+        put(i, j, row[wave][j][lane]);
+      }
     }
   } else if constexpr (WK == 1) {
 #pragma unroll
@@ -738,6 +789,7 @@ __global__ __launch_bounds__(256) void k_grouped_rows(Args p) {
       floatx4 v = ex[0][t][lane];
 #pragma unroll
       for (int w = 1; w < WK; ++w) v += ex[w][t][lane];
+      if (t != wave) operands(t / NTW, t % NTW);
       put(t / NTW, t % NTW, v);
     }
   } else {
@@ -1508,6 +1560,9 @@ __global__ __launch_bounds__(256) void k_grouped_join(Args p) {
   const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;       // wave q: fragment (i0 + q / 2, q % 2)
   const floatx4* P = reinterpret_cast<const floatx4*>(p.partial) +
                      (((i0 + q / 2) * 2 + q % 2) * 4) * 512 + (wm * 4 + wn) * 64 + lane;
+  const int pm = wm * 128 + 32 * (i0 + q / 2), pn = wn * 64 + 32 * (q % 2);
+  FinishOf<Args, TO, FORM, 1, 1> end(expert, m0, n0, pm, pn, m_valid, n_valid);
+  if constexpr (kLayer<Args>) end.load_first(p);
   floatx16 acc[1][1];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[0][0][e] = 0.f;
@@ -1523,12 +1578,10 @@ __global__ __launch_bounds__(256) void k_grouped_join(Args p) {
   }
   if constexpr (kLayer<Args>) {
     __shared__ floatx4 stage[4 * 256];
-    finish_fragments<TO, FORM>(p, acc, stage + q * 256, expert, m0, n0, wm * 128 + 32 * (i0 + q / 2),
-                               wn * 64 + 32 * (q % 2), m_valid, n_valid);
+    end.run(p, acc, stage + q * 256);
   } else {
     store_fragments<TO, 1, 1, FORM == TN>(p, acc, (FORM == TN ? expert * p.sC : 0) + m0 * p.ldc + n0,
-                                          wm * 128 + 32 * (i0 + q / 2), wn * 64 + 32 * (q % 2),
-                                          m_valid, n_valid);
+                                          pm, pn, m_valid, n_valid);
   }
 }
 
@@ -1568,6 +1621,8 @@ __global__ __launch_bounds__(256) void k_grouped_ring(Args p) {
     }
   }
   const int KL = at.expert < 0 ? 0 : p.K / BK;
+  FinishOf<Args, __bf16, FORM, FM, FN> end(at.expert, m0, n0, wm * 64, wn * (BN / 2), m_valid, n_valid);
+  if constexpr (kLayer<Args>) end.load_first(p);
 
   floatx16 acc[FM][FN];
 #pragma unroll
@@ -1692,8 +1747,7 @@ __global__ __launch_bounds__(256) void k_grouped_ring(Args p) {
     block_sync();                 // no DMA is in flight when the block ends
   }
   if constexpr (kLayer<Args>)
-    finish_fragments<__bf16, FORM>(p, acc, reinterpret_cast<floatx4*>(lds) + wave * 256, at.expert, m0,
-                                   n0, wm * 64, wn * (BN / 2), m_valid, n_valid);
+    end.run(p, acc, reinterpret_cast<floatx4*>(lds) + wave * 256);
   else
     store_fragments<__bf16, FM, FN, false>(p, acc, m0 * p.ldc + n0, wm * 64, wn * (BN / 2), m_valid,
                                            n_valid);

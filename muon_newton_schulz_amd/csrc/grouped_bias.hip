@@ -22,7 +22,7 @@ struct BiasArgs : GroupedArgs {               // A: dY (lda), C: dZ (ldc), B: Z 
   int chunk;                                  // rows, a multiple of kRowsAtOnce
 };
 
-template <typename T, typename TO>
+template <typename T, typename TO, bool STREAM>
 __global__ __launch_bounds__(256) void k_bias_grad(BiasArgs p) {
   const int tid = threadIdx.x, cg = tid & 31, rg = tid >> 5;
   Place at;
@@ -51,8 +51,8 @@ __global__ __launch_bounds__(256) void k_bias_grad(BiasArgs p) {
 #pragma unroll
     for (int q = 0; q < AHEAD; ++q) {
       const int r = m + q * kRowsAtOnce, have = r < rows ? left : 0;
-      g[q].load(dY + r * p.lda, have);
-      z[q].load(Z + r * p.ldb, p.act ? have : 0);
+      g[q].template load<STREAM>(dY + r * p.lda, have);
+      z[q].template load<STREAM>(Z + r * p.ldb, p.act ? have : 0);
     }
 #pragma unroll
     for (int q = 0; q < AHEAD; ++q) {
@@ -67,7 +67,7 @@ __global__ __launch_bounds__(256) void k_bias_grad(BiasArgs p) {
       if (p.C) {
         Eight<T> out;
         out.set(v);
-        out.store(dZ + r * p.ldc, left);
+        out.template store<STREAM>(dZ + r * p.ldc, left);
       }
     }
   }
@@ -121,6 +121,17 @@ __global__ __launch_bounds__(1024) void k_bias_join(BiasArgs p) {
         (TO)(part_sum[0][tid] + part_sum[1][tid] + part_sum[2][tid] + part_sum[3][tid]);
 }
 
+template <bool STREAM>
+hipError_t launch_bias(const BiasArgs& a, Store store, bool out32, dim3 grid, hipStream_t s) {
+  if (store == Store::F32)
+    hipLaunchKernelGGL((k_bias_grad<float, float, STREAM>), grid, dim3(256), 0, s, a);
+  else if (out32)
+    hipLaunchKernelGGL((k_bias_grad<__bf16, float, STREAM>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_bias_grad<__bf16, __bf16, STREAM>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
 int chunk_rows(int64_t total_rows) {
   int64_t c = 128;
   while (total_rows > 512 * c) c *= 2;
@@ -158,13 +169,10 @@ hipError_t bias_grad(const BiasGradDesc& d, hipStream_t s) {
   a.chunk = chunk_rows(d.total_rows);
   const dim3 grid((unsigned)blocks);
   const bool out32 = d.out_store == Store::F32;
-  if (d.store == Store::F32)
-    hipLaunchKernelGGL((k_bias_grad<float, float>), grid, dim3(256), 0, s, a);
-  else if (out32)
-    hipLaunchKernelGGL((k_bias_grad<__bf16, float>), grid, dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_bias_grad<__bf16, __bf16>), grid, dim3(256), 0, s, a);
-  const hipError_t e = hipGetLastError();
+  const double bytes = (double)d.total_rows * d.n * (d.store == Store::F32 ? 4 : 2) *
+                       (1 + (d.Z ? 1 : 0) + (d.dZ ? 1 : 0));
+  const hipError_t e = bytes > kStreamBytes ? launch_bias<true>(a, d.store, out32, grid, s)
+                                            : launch_bias<false>(a, d.store, out32, grid, s);
   if (e != hipSuccess || d.total_rows <= a.chunk) return e;
   const dim3 joins((unsigned)(d.groups * a.tiles_n));
   if (out32) hipLaunchKernelGGL(k_bias_join<float>, joins, dim3(1024), 0, s, a);

@@ -23,7 +23,8 @@ __device__ __forceinline__ u32x4 load_chunk(const T* p, int valid) {
   return v;
 }
 
-// The same 16 bytes past the caches, for data that is not used again before it would leave them.
+// The same 16 bytes past the caches, for calls whose data does not fit the 256 MB last-level cache.
+constexpr double kStreamBytes = double(256 << 20);
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 template <typename T>
 __device__ __forceinline__ u32x4 load_streaming(const T* p) {
@@ -41,17 +42,23 @@ template <typename T>
 struct Eight {
   static constexpr int VEC = 16 / sizeof(T);
   u32x4 r[sizeof(T) / 2];
+  template <bool STREAM = false>
   __device__ __forceinline__ void load(const T* p, int valid) {
 #pragma unroll
-    for (int h = 0; h < (int)sizeof(T) / 2; ++h)
-      r[h] = load_chunk(p + h * VEC, valid - h * VEC);
+    for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
+      if (STREAM && valid >= (h + 1) * VEC) r[h] = load_streaming(p + h * VEC);
+      else r[h] = load_chunk(p + h * VEC, valid - h * VEC);
+    }
   }
+  template <bool STREAM = false>
   __device__ __forceinline__ void store(T* p, int valid) const {
     T e[8];
     __builtin_memcpy(e, r, sizeof(e));
 #pragma unroll
     for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
-      if (valid >= (h + 1) * VEC) {
+      if (STREAM && valid >= (h + 1) * VEC) {
+        store_streaming(p + h * VEC, &r[h]);
+      } else if (valid >= (h + 1) * VEC) {
         __builtin_memcpy(p + h * VEC, &r[h], 16);
       } else {
 #pragma unroll
