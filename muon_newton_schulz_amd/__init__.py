@@ -333,7 +333,7 @@ class _OnStream:
     def __init__(self, device: torch.device, stream):
         self._ctx = None
         if stream is None:
-            if device.index != torch.cuda.current_device():
+            if device.index != torch._C._cuda_getDevice():
                 self._ctx = torch.cuda.device(device)
             # the current stream's handle, without building a stream object around it (3.5 us of a
             # small call's 12)
@@ -366,6 +366,8 @@ class _OnStream:
 def _pitch(t: torch.Tensor, name: str, what: str) -> int:
     """Row pitch of a 2-D tensor whose rows are contiguous and do not overlap."""
     rows, cols = t.shape
+    if t.is_contiguous():
+        return cols
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{what}: the rows of {name} must be contiguous")
     if rows <= 1:
@@ -511,6 +513,23 @@ def grouped_weight_grad(dY: torch.Tensor, X: torch.Tensor, offsets: torch.Tensor
     return G
 
 
+def _one_gpu(first: torch.Tensor, others, what: str) -> torch.device:
+    """_on_one_gpu of tensors that are rarely elsewhere: compares device numbers (-1: not a GPU)."""
+    index = first.get_device()
+    if index >= 0:
+        for t in others:
+            if t is not None and t.get_device() != index:
+                break
+        else:
+            return first.device
+    return _on_one_gpu([first, *others], what)
+
+
+def _check_offsets(offsets: torch.Tensor, groups: int, what: str) -> None:
+    if offsets.dtype != torch.int64 or offsets.shape != (groups + 1,) or not offsets.is_contiguous():
+        raise ValueError(f"{what}: offsets must be contiguous int64 of shape ({groups + 1},)")
+
+
 @functools.lru_cache(maxsize=4096)
 def _size_query(name: str, *args) -> int:
     """Bytes a workspace query of the library answers (a function of its arguments alone; asking costs
@@ -539,7 +558,7 @@ def _rowwise(t: torch.Tensor | None, name: str, shape, dtype, what: str) -> int:
     """Row pitch of an optional 2-D tensor of the given shape and dtype (0 for None)."""
     if t is None:
         return 0
-    if tuple(t.shape) != shape or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what}: {name} must be {shape} {dtype}, got {tuple(t.shape)} {t.dtype}")
     return _pitch(t, name, what)
 
@@ -581,8 +600,11 @@ def _layer_operands(A, W, transpose_w: bool, a_name: str, what: str):
 
 def _new_rows(rows: int, width: int, like: torch.Tensor, zeros: bool) -> torch.Tensor:
     """A new row-wise output; zeros when the call's own filling of unowned rows is off."""
-    make = torch.zeros if zeros else torch.empty
-    return make((rows, width), dtype=like.dtype, device=like.device)
+    if zeros:
+        return like.new_zeros((rows, width))
+    if like.shape[1] == width and like.is_contiguous():
+        return torch.empty_like(like)
+    return like.new_empty((rows, width))
 
 
 def grouped_linear(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, *,
@@ -607,7 +629,7 @@ def grouped_linear(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, *,
     if keep_z and activation is None:
         raise ValueError(f"{what}: without an activation no gradient needs Z")
     if bias is not None:
-        if tuple(bias.shape) != (groups, n) or bias.dtype != X.dtype:
+        if bias.shape != (groups, n) or bias.dtype != X.dtype:
             raise ValueError(f"{what}: bias must be {(groups, n)} {X.dtype}, "
                              f"got {tuple(bias.shape)} {bias.dtype}")
         if not bias.is_contiguous():
@@ -615,10 +637,12 @@ def grouped_linear(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, *,
     ldr = _rowwise(residual, "residual", (rows, n), X.dtype, what)
     ldy = _rowwise(out, "out", (rows, n), X.dtype, what)
     ldz = _rowwise(out_z, "out_z", (rows, n), X.dtype, what)
-    others = [("X", X), ("W", W), ("bias", bias), ("offsets", offsets)]
-    _itself_or_apart(out, "out", [("residual", residual)], others + [("out_z", out_z)], what)
-    _itself_or_apart(out_z, "out_z", [], others + [("residual", residual)], what)
-    dev = _grouped_checks([("X", X)], [W, bias, residual, out, out_z], offsets, groups, what)
+    if out is not None or out_z is not None:
+        others = [("X", X), ("W", W), ("bias", bias), ("offsets", offsets)]
+        _itself_or_apart(out, "out", [("residual", residual)], others + [("out_z", out_z)], what)
+        _itself_or_apart(out_z, "out_z", [], others + [("residual", residual)], what)
+    _check_offsets(offsets, groups, what)
+    dev = _one_gpu(X, (W, bias, residual, out, out_z, offsets), what)
     with _OnStream(dev, stream) as handle:
         fill = out is None and out_z is None        # else what is new is made of zeros
         Y, Z = out, out_z
@@ -654,7 +678,8 @@ def grouped_input_grad(dY: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor,
     lddx = _rowwise(out, "out", (rows, k), dY.dtype, what)
     _itself_or_apart(out, "out", [("Z", Z), ("residual", residual)],
                      [("dY", dY), ("W", W), ("offsets", offsets)], what)
-    dev = _grouped_checks([("dY", dY)], [W, Z, residual, out], offsets, groups, what)
+    _check_offsets(offsets, groups, what)
+    dev = _one_gpu(dY, (W, Z, residual, out, offsets), what)
     with _OnStream(dev, stream) as handle:
         dX = out
         if dX is None:
@@ -705,10 +730,11 @@ def grouped_bias_grad(dY: torch.Tensor, offsets: torch.Tensor, *, activation: st
     _itself_or_apart(out, "out", [], [("dY", dY), ("Z", Z), ("out_dz", out_dz),
                                       ("offsets", offsets)], what)
     _itself_or_apart(out_dz, "out_dz", [("dY", dY), ("Z", Z)], [("offsets", offsets)], what)
-    dev = _grouped_checks([("dY", dY)], [Z, out, out_dz], offsets, groups, what)
+    _check_offsets(offsets, groups, what)
+    dev = _one_gpu(dY, (Z, out, out_dz, offsets), what)
     need = _size_query("mns_grouped_bias_grad_workspace_size", groups, rows, n)
     with _OnStream(dev, stream) as handle:
-        db = torch.empty((groups, n), dtype=out_dtype, device=dev) if out is None else out
+        db = dY.new_empty((groups, n), dtype=out_dtype) if out is None else out
         dZ = out_dz
         if activation is not None and dZ is None:
             dZ, lddz = _new_rows(rows, n, dY, False), n
@@ -736,13 +762,12 @@ def expert_order(expert_ids: torch.Tensor, experts: int, *, order: bool = True,
     the grouped calls take (None with ``order=False``). At most 2048 experts."""
     what = "expert_order"
     _ids(expert_ids, what)
-    dev = _on_one_gpu([expert_ids], what)
+    dev = _one_gpu(expert_ids, (), what)
     m = expert_ids.numel()
     need = _size_query("mns_expert_order_workspace_size", m, experts)
     with _OnStream(dev, stream) as handle:
-        counts = torch.empty(experts, dtype=torch.int64, device=dev)
-        offsets = torch.empty(experts + 1, dtype=torch.int64, device=dev)
-        places = torch.empty(m, dtype=torch.int64, device=dev) if order else None
+        counts, offsets = expert_ids.new_empty(experts), expert_ids.new_empty(experts + 1)
+        places = expert_ids.new_empty(m) if order else None
         keep, ws, nbytes = _optional_workspace(need, dev, workspace)
         check(load().expert_order(expert_ids.data_ptr(), m, experts, counts.data_ptr(),
                                   offsets.data_ptr(), _ptr_or_none(places), ws, nbytes, handle), what)
@@ -767,7 +792,7 @@ def balance_loss(logits: torch.Tensor, expert_ids: torch.Tensor, counts: torch.T
         raise ValueError(f"{what}: logits must be (tokens, experts) and expert_ids (tokens, top)")
     _ids(expert_ids, what)
     tokens, experts = logits.shape
-    if counts.dtype != torch.int64 or tuple(counts.shape) != (experts,) or not counts.is_contiguous():
+    if counts.dtype != torch.int64 or counts.shape != (experts,) or not counts.is_contiguous():
         raise ValueError(f"{what}: counts must be contiguous int64 of shape ({experts},)")
     if out is not None and not grad:
         raise ValueError(f"{what}: out without a gradient")
@@ -775,7 +800,7 @@ def balance_loss(logits: torch.Tensor, expert_ids: torch.Tensor, counts: torch.T
     ldd = _rowwise(out, "out", (tokens, experts), logits.dtype, what)
     _itself_or_apart(out, "out", [("logits", logits)],
                      [("expert_ids", expert_ids), ("counts", counts)], what)
-    dev = _on_one_gpu([logits, expert_ids, counts, out], what)
+    dev = _one_gpu(logits, (expert_ids, counts, out), what)
     need = _size_query("mns_balance_workspace_size", tokens, experts)
     with _OnStream(dev, stream) as handle:
         loss = torch.empty((), dtype=torch.float32, device=dev)
