@@ -174,13 +174,16 @@ struct Finish {
     for (int q = 0; q < 2; ++q) {
       const int m = row_of(step) + STEP * q, have = m < m_valid ? left : 0;
       if (FORM == NN)
-        o.z[q].load(static_cast<const T*>(p.Z) + (row + m) * p.ldz + col + n, p.Z ? have : 0);
-      o.r[q].load(static_cast<const T*>(p.R) + (row + m) * p.ldr + col + n, p.R ? have : 0);
+        o.z[q].load(static_cast<const T*>(p.Z) + (row + m) * p.ldz + col + n, p.Z ? have : 0,
+                    rows_end(static_cast<const T*>(p.Z), p, p.ldz, p.N));
+      o.r[q].load(static_cast<const T*>(p.R) + (row + m) * p.ldr + col + n, p.R ? have : 0,
+                  rows_end(static_cast<const T*>(p.R), p, p.ldr, p.N));
     }
   }
   __device__ __forceinline__ void load_first(const LayerArgs& p) {
     if (FORM == NT)
-      bias.load(static_cast<const T*>(p.bias) + (int64_t)expert * p.N + col + n, p.bias ? left : 0);
+      bias.load(static_cast<const T*>(p.bias) + (int64_t)expert * p.N + col + n, p.bias ? left : 0,
+                static_cast<const T*>(p.bias) + (int64_t)p.groups * p.N);
     load(p, 0, first);
   }
   __device__ __forceinline__ void run(const LayerArgs& p, const floatx16 (&acc)[FM][FN],
@@ -319,6 +322,9 @@ __global__ __launch_bounds__(256) void k_grouped(Args p) {
   int red;                  // length of the reduction
   const T* A;
   const T* B;
+  const T* a_end = rows_end(static_cast<const T*>(p.A), p, p.lda, FORM == TN ? p.N : p.K);
+  const T* b_end = FORM == TN ? rows_end(static_cast<const T*>(p.B), p, p.ldb, p.K)
+                              : static_cast<const T*>(p.B) + p.groups * p.sB;
   int m_valid;
   if constexpr (FORM == TN) {
     const int per = (p.N + BM - 1) / BM * p.tiles_n, t = (int)(blockIdx.x % per);
@@ -366,29 +372,32 @@ __global__ __launch_bounds__(256) void k_grouped(Args p) {
   // Chunk q of this thread of a k-contiguous operand: row, first k; of a k-major one: k-row,
   // first column (16 k-rows x 4 chunks per wave: 64-byte pieces of a row).
   u32x4 ra[NCH], rb[NCH];
-  auto load = [&](const T* base, int64_t ld, bool kmajor, int valid, int k0, u32x4* r) {
+  // Past the ends: rows of the reduction are zeros, and so are the reduction's columns (store); columns
+  // of the output hold what follows in the operand and are not stored.
+  auto load = [&](const T* base, int64_t ld, bool kmajor, int valid, int k0, const T* end, u32x4* r) {
 #pragma unroll
     for (int q = 0; q < NCH; ++q) {
       if (!kmajor) {
         const int c = tid + 256 * q, row = c >> 3, kk = (c & 7) * VEC;
         const int left = red - k0 - kk;
-        r[q] = load_chunk(base + row * ld + k0 + kk, row < valid ? left : 0);
+        r[q] = load_piece_of_row(base + row * ld + k0 + kk, row < valid ? left : 0, end);
       } else {
         constexpr int KW = BK / 16;                     // waves' worth of k-rows
         const int u = q * 4 + wave;                     // 16 units of 16 k-rows x 4 chunks
         const int kr = (u % KW) * 16 + (lane & 15);
         const int col = ((u / KW) * 4 + (lane >> 4)) * VEC;
         const int left = valid - col;
-        r[q] = load_chunk(base + (int64_t)(k0 + kr) * ld + col, k0 + kr < red ? left : 0);
+        r[q] = load_piece_of_row(base + (int64_t)(k0 + kr) * ld + col, k0 + kr < red ? left : 0, end);
       }
     }
   };
-  auto store = [&](T* dst, bool kmajor, const u32x4* r) {
+  auto store = [&](T* dst, bool kmajor, int k0, const u32x4* r) {
 #pragma unroll
     for (int q = 0; q < NCH; ++q) {
       if (!kmajor) {
         const int c = tid + 256 * q, row = c >> 3, kk = (c & 7) * VEC;
-        *reinterpret_cast<u32x4*>(dst + row * PITCH + kk) = r[q];
+        *reinterpret_cast<u32x4*>(dst + row * PITCH + kk) =
+            k0 + BK <= red ? r[q] : cut_chunk<T>(r[q], red - k0 - kk);
       } else {
         constexpr int KW = BK / 16;
         const int u = q * 4 + wave;
@@ -410,16 +419,16 @@ __global__ __launch_bounds__(256) void k_grouped(Args p) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
   if (red > 0) {
-    load(A, p.lda, FORM == TN, m_valid, 0, ra);
-    load(B, p.ldb, FORM != NT, n_valid, 0, rb);
+    load(A, p.lda, FORM == TN, m_valid, 0, a_end, ra);
+    load(B, p.ldb, FORM != NT, n_valid, 0, b_end, rb);
   }
   for (int k0 = 0; k0 < red; k0 += BK) {
-    store(As, FORM == TN, ra);
-    store(Bs, FORM != NT, rb);
+    store(As, FORM == TN, k0, ra);
+    store(Bs, FORM != NT, k0, rb);
     __syncthreads();
     if (k0 + BK < red) {
-      load(A, p.lda, FORM == TN, m_valid, k0 + BK, ra);
-      load(B, p.ldb, FORM != NT, n_valid, k0 + BK, rb);
+      load(A, p.lda, FORM == TN, m_valid, k0 + BK, a_end, ra);
+      load(B, p.ldb, FORM != NT, n_valid, k0 + BK, b_end, rb);
     }
 #pragma unroll
     for (int s = 0; s < BK / (2 * VEC); ++s) {
@@ -491,25 +500,29 @@ __global__ __launch_bounds__(256) void k_grouped_split(Args p) {
   const T* B = static_cast<const T*>(p.B) + (at.expert < 0 ? 0 : at.expert) * p.sB +
                (FORM == NT ? n0 * p.ldb : (int64_t)n0);
 
-  auto load = [&](const T* base, int64_t ld, bool kmajor, int valid, int k0, u32x4* r) {
+  const T* a_end = rows_end(static_cast<const T*>(p.A), p, p.lda, p.K);
+  const T* b_end = static_cast<const T*>(p.B) + p.groups * p.sB;
+  auto load = [&](const T* base, int64_t ld, bool kmajor, int valid, int k0, const T* end, u32x4* r) {
 #pragma unroll
     for (int q = 0; q < NCH; ++q) {
       if (!kmajor) {
         const int c = lane + 64 * q, row = c >> 3, kk = (c & 7) * VEC;
-        r[q] = load_chunk(base + row * ld + k0 + kk, row < valid ? red - k0 - kk : 0);
+        r[q] = load_piece_of_row(base + row * ld + k0 + kk, row < valid ? red - k0 - kk : 0, end);
       } else {
         constexpr int KW = BK / 16;
         const int kr = (q % KW) * 16 + (lane & 15), col = ((q / KW) * 4 + (lane >> 4)) * VEC;
-        r[q] = load_chunk(base + (int64_t)(k0 + kr) * ld + col, k0 + kr < red ? valid - col : 0);
+        r[q] = load_piece_of_row(base + (int64_t)(k0 + kr) * ld + col, k0 + kr < red ? valid - col : 0,
+                                 end);
       }
     }
   };
-  auto store = [&](T* dst, bool kmajor, const u32x4* r) {
+  auto store = [&](T* dst, bool kmajor, int k0, const u32x4* r) {
 #pragma unroll
     for (int q = 0; q < NCH; ++q) {
       if (!kmajor) {
         const int c = lane + 64 * q, row = c >> 3, kk = (c & 7) * VEC;
-        *reinterpret_cast<u32x4*>(dst + row * PITCH + kk) = r[q];
+        *reinterpret_cast<u32x4*>(dst + row * PITCH + kk) =
+            k0 + BK <= red ? r[q] : cut_chunk<T>(r[q], red - k0 - kk);
       } else {
         constexpr int KW = BK / 16;
         const int kr = (q % KW) * 16 + (lane & 15), col = ((q / KW) * 4 + (lane >> 4)) * VEC;
@@ -536,15 +549,15 @@ __global__ __launch_bounds__(256) void k_grouped_split(Args p) {
   u32x4 ra[NCH], rb[NCH];
   int k0 = wave * BK;
   if (k0 < red) {
-    load(A, p.lda, false, m_valid, k0, ra);
-    load(B, p.ldb, FORM != NT, n_valid, k0, rb);
+    load(A, p.lda, false, m_valid, k0, a_end, ra);
+    load(B, p.ldb, FORM != NT, n_valid, k0, b_end, rb);
   }
   for (; k0 < red; k0 += 4 * BK) {
-    store(As, false, ra);
-    store(Bs, FORM != NT, rb);
+    store(As, false, k0, ra);
+    store(Bs, FORM != NT, k0, rb);
     if (k0 + 4 * BK < red) {
-      load(A, p.lda, false, m_valid, k0 + 4 * BK, ra);
-      load(B, p.ldb, FORM != NT, n_valid, k0 + 4 * BK, rb);
+      load(A, p.lda, false, m_valid, k0 + 4 * BK, a_end, ra);
+      load(B, p.ldb, FORM != NT, n_valid, k0 + 4 * BK, b_end, rb);
     }
 #pragma unroll
     for (int s = 0; s < BK / (2 * VEC); ++s) {
@@ -720,9 +733,15 @@ __global__ __launch_bounds__(256) void k_grouped_rows(Args p) {
     const int left = K - s * STEP - kc;
     u32x4 w[NTW], x[MT];
 #pragma unroll
-    for (int j = 0; j < NTW; ++j) w[j] = load_chunk(wp[j] + o, left);
+    for (int j = 0; j < NTW; ++j)
+      w[j] = load_piece_of_row(wp[j] + o, left, static_cast<const T*>(p.B) + p.groups * p.sB);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) x[i] = load_chunk(xp[i] + o, left);
+    for (int i = 0; i < MT; ++i)
+      x[i] = load_piece_of_row(xp[i] + o, left, rows_end(static_cast<const T*>(p.A), p, p.lda, p.K));
+#pragma unroll
+    for (int j = 0; j < NTW; ++j) w[j] = cut_chunk<T>(w[j], left);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) x[i] = cut_chunk<T>(x[i], left);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll

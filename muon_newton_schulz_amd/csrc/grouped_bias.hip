@@ -37,6 +37,8 @@ __global__ __launch_bounds__(256) void k_bias_grad(BiasArgs p) {
   const T* dY = static_cast<const T*>(p.A) + r0 * p.lda + n;
   const T* Z = static_cast<const T*>(p.B) + r0 * p.ldb + n;
   T* dZ = static_cast<T*>(p.C) + r0 * p.ldc + n;
+  const T* dy_end = rows_end(static_cast<const T*>(p.A), p, p.lda, p.N);
+  const T* z_end = rows_end(static_cast<const T*>(p.B), p, p.ldb, p.N);
   if (at.expert < 0) {                        // rows of no expert
     Eight<T> zero;
     const float none[8] = {};
@@ -51,8 +53,8 @@ __global__ __launch_bounds__(256) void k_bias_grad(BiasArgs p) {
 #pragma unroll
     for (int q = 0; q < AHEAD; ++q) {
       const int r = m + q * kRowsAtOnce, have = r < rows ? left : 0;
-      g[q].template load<STREAM>(dY + r * p.lda, have);
-      z[q].template load<STREAM>(Z + r * p.ldb, p.act ? have : 0);
+      g[q].template load<STREAM>(dY + r * p.lda, have, dy_end);
+      z[q].template load<STREAM>(Z + r * p.ldb, p.act ? have : 0, z_end);
     }
 #pragma unroll
     for (int q = 0; q < AHEAD; ++q) {

@@ -33,6 +33,12 @@ __device__ __forceinline__ void expert_rows(const GroupedArgs& p, int e, int& lo
   hi = clamp_row(p.offsets[e + 1], lo, p.total_rows);
 }
 
+// Behind the last element of a token matrix.
+template <typename T>
+__device__ __forceinline__ const T* rows_end(const T* p, const GroupedArgs& a, int64_t ld, int width) {
+  return p + ((int64_t)(a.total_rows - 1) * ld + width);
+}
+
 // Where a block of a forward or input-gradient call works: an expert (-1: the rows of no expert,
 // to be filled with zeros), its rows [lo, hi), and the block's place among the expert's tiles.
 struct Place {

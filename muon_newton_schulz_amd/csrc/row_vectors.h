@@ -7,7 +7,7 @@ namespace {
 
 // 16 bytes from any address of T's alignment, of which the first `valid` elements exist; the
 // others read as zero and are not touched. (A whole chunk is one 16-byte load: this part loads
-// from any address.)
+// from any address.) For the end of a buffer: a partial chunk is read element by element and waited for.
 template <typename T>
 __device__ __forceinline__ u32x4 load_chunk(const T* p, int valid) {
   constexpr int VEC = 16 / sizeof(T);
@@ -19,6 +19,26 @@ __device__ __forceinline__ u32x4 load_chunk(const T* p, int valid) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) e[i] = i < valid ? p[i] : (T)0.f;
     __builtin_memcpy(&v, e, 16);
+  }
+  return v;
+}
+
+// The same for a piece of a row of a larger buffer that ends at `end`: one 16-byte load wherever the buffer
+// has that much left, so that a partial chunk costs no wait of its own (input gradient of 1021 rows, 5
+// experts of 513 x 1277, bfloat16: 23.6 -> 22.7 us). The elements behind the first `valid` are then
+// whatever follows in the buffer: unspecified.
+template <typename T, bool STREAM = false>
+__device__ __forceinline__ u32x4 load_piece_of_row(const T* p, int valid, const T* end);
+
+// Zeros behind the first `valid` elements.
+template <typename T>
+__device__ __forceinline__ u32x4 cut_chunk(u32x4 v, int valid) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    if constexpr (sizeof(T) == 4)
+      v[d] = d < valid ? v[d] : 0u;
+    else
+      v[d] = 2 * d + 1 < valid ? v[d] : 2 * d < valid ? v[d] & 0xFFFFu : 0u;
   }
   return v;
 }
@@ -37,18 +57,31 @@ __device__ __forceinline__ void store_streaming(T* p, const void* v) {
   __builtin_nontemporal_store(x, reinterpret_cast<u32x4_any*>(p));
 }
 
-// Eight consecutive elements of a row.
+template <typename T, bool STREAM>
+__device__ __forceinline__ u32x4 load_piece_of_row(const T* p, int valid, const T* end) {
+  constexpr int VEC = 16 / sizeof(T);
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (valid > 0) {
+    if (p + VEC <= end) {
+      if (STREAM) v = load_streaming(p);
+      else __builtin_memcpy(&v, p, 16);
+    } else {
+      v = load_chunk(p, valid);
+    }
+  }
+  return v;
+}
+
+// Eight consecutive elements of a row; load() leaves those behind `valid` unspecified.
 template <typename T>
 struct Eight {
   static constexpr int VEC = 16 / sizeof(T);
   u32x4 r[sizeof(T) / 2];
   template <bool STREAM = false>
-  __device__ __forceinline__ void load(const T* p, int valid) {
+  __device__ __forceinline__ void load(const T* p, int valid, const T* end) {
 #pragma unroll
-    for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
-      if (STREAM && valid >= (h + 1) * VEC) r[h] = load_streaming(p + h * VEC);
-      else r[h] = load_chunk(p + h * VEC, valid - h * VEC);
-    }
+    for (int h = 0; h < (int)sizeof(T) / 2; ++h)
+      r[h] = load_piece_of_row<T, STREAM>(p + h * VEC, valid - h * VEC, end);
   }
   template <bool STREAM = false>
   __device__ __forceinline__ void store(T* p, int valid) const {

@@ -308,6 +308,36 @@ def test_nan_and_infinity_stay_in_their_rows(dtype):
         assert y[5].isnan().all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("n,k", [(37, 45), (300, 129), (33, 515)])
+@pytest.mark.parametrize("rows", [12, 300, 3000])
+def test_what_follows_a_row_does_not_reach_it(dtype, n, k, rows):
+    """Odd widths, whose last vectors of a row reach into the next one: NaN in every second row, in the
+    other expert's weights and bias, and between the rows."""
+    bounds = [0, rows, rows, 2 * rows]
+    off = _offsets(bounds)
+    W, b = _rand((3, n, k), dtype, 1, 0.2), _rand((3, n), dtype, 2)
+    X, R, dY = _rand((2 * rows, k), dtype, 3), _rand((2 * rows, n), dtype, 4), _rand((2 * rows, n), dtype, 5)
+    Z = _rand((2 * rows, k), dtype, 6)
+    calls = (lambda: mns.grouped_linear(X, W, off, bias=b, activation="silu", residual=R),
+             lambda: mns.grouped_input_grad(dY, W, off, activation="silu", Z=Z),
+             lambda: mns.grouped_bias_grad(dY, off, activation="silu", Z=R)[1],
+             lambda: mns.grouped_matmul(X, W, off), lambda: mns.grouped_matmul(dY, W, off, transpose_w=True))
+    clean = [call() for call in calls]
+    keep = torch.arange(0, rows, 2)
+    nan = float("nan")
+    for t in (X, R, dY, Z):
+        t[1:rows:2] = nan
+        t[rows:] = nan
+    W[1:] = nan
+    b[1:] = nan
+    for i, (call, want) in enumerate(zip(calls, clean)):
+        print("case", dtype, n, k, rows, i, flush=True)
+        assert torch.equal(call()[keep], want[keep]), i
+    g = mns.grouped_weight_grad(dY[:rows:2], X[:rows:2], _offsets([0, len(keep)]))
+    assert torch.isfinite(g).all()
+
+
 def test_gradients_against_differences():
     """The layer's calls together: dX, dW and db of L = <C, gelu(X W^T + b) + R> against central
     differences of the float64 form."""
