@@ -1293,9 +1293,10 @@ __global__ __launch_bounds__(512) void k_grouped_big(Args p) {
                          ((int64_t)(cur.m_valid < BM ? cur.m_valid - 1 : BM - 1) * ld +
                           (cur.n_valid < BN ? cur.n_valid : BN)) * 2);
       };
-      auto lane_at = [&](int64_t ld) { return in ? (r8 * (int)ld + 8 * c) * 2 : 0x70000000; };
+      // byte offsets, below 2^30 for a tile's rows (pitches are at most 2^21); a column past the end: 7 2^28
+      auto lane_at = [&](int64_t ld) { return in ? unsigned(r8 * (int)ld + 8 * c) * 2u : 0x70000000u; };
       auto row_at = [&](int64_t ld, int i, int q) {
-        return ((wm * 128 + 32 * i + 8 * q) * (int)ld + wn * 64) * 2;
+        return unsigned((wm * 128 + 32 * i + 8 * q) * (int)ld + wn * 64) * 2u;
       };
       auto fetch = [&](const void* base, int64_t ld, int i, u32x4 (&v)[4]) {
 #pragma unroll

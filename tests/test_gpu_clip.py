@@ -122,6 +122,27 @@ def test_the_same_tensor_twice():
     assert torch.equal(o[0], o[1])
 
 
+@pytest.mark.parametrize("dtype,lead", [(BF, 1), (BF, 0), (F32, 3)])
+def test_lists_beyond_the_caches(dtype, lead):
+    """More than 256 MB, which is read and written past the caches, at odd addresses too."""
+    n = 150_000_001 if dtype == BF else 80_000_001
+    buf = torch.empty(n + 8, dtype=dtype, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    grads = [buf[lead:lead + n - 5000], buf[lead + n - 4999:lead + n]]
+    norm = math.sqrt(sum(float((p.double() ** 2).sum()) for g in grads for p in g.split(1 << 24)))
+    factor = min(1.0, 3.0 / (norm + 1e-6))
+    out = [torch.empty_like(g) for g in grads]
+    got = mns.clip_grad_norm(grads, 3.0, out=out)
+    assert abs(got.item() - norm) <= NORM * norm
+    for g, o in zip(grads, out):
+        for a, b in zip(g.split(1 << 24), o.split(1 << 24)):
+            want = a.double() * factor
+            bound = want.abs() * (2.0 ** -23 + grouped_ref.HALF_STEP[dtype] * (1 + 2.0 ** -23)) + 1e-38
+            assert ((b.double() - want).abs() <= bound).all()
+    between = buf[lead + n - 5000].clone()
+    mns.clip_grad_norm(grads, 3.0)
+    assert all(torch.equal(g, o) for g, o in zip(grads, out)) and buf[lead + n - 5000] == between
+
+
 def test_captured_replayed_and_on_two_streams():
     grads = _grads([(700, 300), (41,), (9000,)])
     out = [torch.empty_like(g) for g in grads]

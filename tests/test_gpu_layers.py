@@ -264,6 +264,30 @@ def test_bias_grad_chunks(rows):
     assert again is out and torch.equal(again, db) and torch.equal(dz2, dZ)
 
 
+def test_bias_grad_beyond_the_caches():
+    """More than 256 MB, read and written past the caches, odd widths and pitches."""
+    n, sizes = 8187, [1, 3000, 0, 4007]
+    bounds = grouped_ref.bounds_of(sizes, 1)
+    rows, off = bounds[-1] + 2, _offsets(bounds)
+    g = torch.Generator("cuda").manual_seed(1)
+    dY = torch.empty(rows, n + 3, dtype=BF, device="cuda").normal_(generator=g)[:, 1:n + 1]
+    Z = torch.empty(rows, n, dtype=BF, device="cuda").normal_(generator=g)
+    db, dZ = mns.grouped_bias_grad(dY, off, activation="relu", Z=Z, out_dtype=F32)
+    want = torch.where(Z > 0, dY, torch.zeros_like(dY))             # exact
+    want[:1], want[bounds[-1]:] = 0, 0
+    assert torch.equal(dZ, want)
+    for e, (lo, hi) in enumerate(zip(bounds, bounds[1:])):
+        part = want[lo:hi].double()
+        err = (hi - lo + 1) * 2.0 ** -23 * part.abs().sum(0) + 1e-38
+        assert ((db[e].double() - part.sum(0)).abs() <= err).all(), e
+
+
+def test_widths_the_large_kernels_do_not_take():
+    """A reduction of whole k-tiles with an odd output: no whole 16-byte pieces to store."""
+    for sizes, n, k in (([700, 900], 1001, 1024), ([40, 50], 77, 256), ([300], 2049, 2048)):
+        _both(sizes, 1, 2, n, k, BF, "silu", wscale=0.05)
+
+
 def test_no_rows_at_all():
     W, off = _rand((3, 16, 24), BF, 1), _offsets([0, 0, 0, 0])
     X, dY = torch.empty(0, 24, dtype=BF, device="cuda"), torch.empty(0, 16, dtype=BF, device="cuda")
