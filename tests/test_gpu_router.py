@@ -29,7 +29,8 @@ def _ids(tokens, top, experts, seed, kind="uniform"):
 @pytest.mark.parametrize("kind", ["uniform", "holes", "one", "none"])
 @pytest.mark.parametrize("tokens,top,experts", [
     (1, 1, 1), (1, 8, 8), (63, 1, 3), (64, 2, 32), (65, 3, 33), (511, 4, 256), (2048, 1, 7),
-    (2049, 1, 2048), (5000, 2, 100), (70001, 1, 60), (140000, 5, 129)])
+    (2049, 1, 2048), (5000, 2, 100), (8193, 1, 2048), (16384, 2, 32), (32769, 1, 513), (70001, 1, 60),
+    (140000, 5, 129)])
 def test_order(tokens, top, experts, kind):
     ids = _ids(tokens, top, experts, tokens + experts, kind)
     got = mns.expert_order(ids.cuda(), experts)
