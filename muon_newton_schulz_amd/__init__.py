@@ -532,8 +532,8 @@ def _check_offsets(offsets: torch.Tensor, groups: int, what: str) -> None:
 
 @functools.lru_cache(maxsize=4096)
 def _size_query(name: str, *args) -> int:
-    """Bytes a workspace query of the library answers (a function of its arguments alone; asking costs
-    a small call 1.5 us)."""
+    """Bytes a workspace query of the library answers: a function of its arguments alone, so asked once
+    for each."""
     need = ctypes.c_size_t(0)
     check(getattr(load(), name)(*args, ctypes.byref(need)), name)
     return need.value

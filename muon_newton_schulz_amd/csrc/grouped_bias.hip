@@ -1,7 +1,9 @@
 // The gradient of a layer's bias, for rows sorted by expert: dZ = dY act'(Z) and db_e = the sum of
 // dZ's rows of expert e.
 //
-// Bound by HBM: dY and Z are read once and dZ is written once, with no reuse. A block takes a chunk of
+// Bound by HBM: dY and Z are read once and dZ is written once, with no reuse (16384 rows x 8192, bfloat16, gelu,
+// 805 MB: 146 + 9 us, 5.5 TB/s; with accesses that stay in the caches 173, so operands beyond the last-level
+// cache take non-temporal ones). A block takes a chunk of
 // `chunk` rows of one expert x 256 columns, eight columns a thread (16 bytes of bfloat16), eight rows
 // side by side; its float32 column sums go to the workspace, one row of 256 a chunk, and are added by a
 // second launch in chunk order, so equal calls give equal bits. An expert of at most one chunk needs
@@ -89,7 +91,8 @@ __global__ __launch_bounds__(256) void k_bias_grad(BiasArgs p) {
 }
 
 // One block per expert and 256 columns, which only experts of several chunks keep: it adds the chunks' sums,
-// four quarters of them side by side (each in order), then the quarters in order.
+// four quarters of them side by side (each in order), then the quarters in order. Latency of dependent loads
+// from L2: 9 us for 32 experts of 8192, 27 with one block of 256 threads that walks all chunks.
 template <typename TO>
 __global__ __launch_bounds__(1024) void k_bias_join(BiasArgs p) {
   const int expert = (int)(blockIdx.x / p.tiles_n), column_tile = (int)(blockIdx.x % p.tiles_n);
