@@ -272,10 +272,15 @@ mns_status grouped_weight_grad(const void* dY, int64_t lddy, const void* X, int6
 
 /* ---- Layers of experts -----------------------------------------------------------------------
  * The products above with what a layer does around them in the same kernel, and the gradient of its
- * bias. Rows, offsets, pitches, sizes, alignment and the workspace (mns_grouped_workspace_size) as above;
- * a plain layer is a stack of one. Everything between the product and the output's one rounding
+ * bias. Rows, offsets, pitches, sizes, alignment and the workspace (its sizes from the queries below) as
+ * above; a plain layer is a stack of one. Everything between the product and the output's one rounding
  * is float32. Rows of no expert are left as they are, or with fill_rest written as zeros, in every
  * row-wise output. NaN and infinities stay in their rows (bias: in their expert). */
+
+/* Workspace bytes of grouped_linear (input_grad = 0) or grouped_input_grad (1). */
+mns_status mns_grouped_layer_workspace_size(int input_grad, int dtype, int64_t groups,
+                                            int64_t total_rows, int64_t n, int64_t k,
+                                            size_t* bytes /* (host) out */);
 
 /* Z_e = X_e W_e^T + bias_e; Y = act(Z) + R.
  *   bias in  dtype [groups][n], or NULL (none);   R  in  dtype, total_rows x n, pitch ldr, or NULL

@@ -651,7 +651,7 @@ def grouped_linear(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, *,
         if keep_z and Z is None:
             Z, ldz = _new_rows(rows, n, X, not fill), n
         keep, ws, nbytes = _optional_workspace(
-            _size_query("mns_grouped_workspace_size", 0, code, groups, rows, n, k), dev, workspace)
+            _size_query("mns_grouped_layer_workspace_size", 0, code, groups, rows, n, k), dev, workspace)
         check(load().grouped_linear(X.data_ptr(), ldx, W.data_ptr(), _ptr_or_none(bias), act,
                                     _ptr_or_none(residual), ldr, _ptr_or_none(Z), ldz, Y.data_ptr(),
                                     ldy, code, offsets.data_ptr(), groups, rows, n, k, int(fill), ws,
@@ -685,7 +685,7 @@ def grouped_input_grad(dY: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor,
         if dX is None:
             dX, lddx = _new_rows(rows, k, dY, False), k
         keep, ws, nbytes = _optional_workspace(
-            _size_query("mns_grouped_workspace_size", 0, code, groups, rows, n, k), dev, workspace)
+            _size_query("mns_grouped_layer_workspace_size", 1, code, groups, rows, n, k), dev, workspace)
         check(load().grouped_input_grad(dY.data_ptr(), lddy, W.data_ptr(), act, _ptr_or_none(Z), ldz,
                                         _ptr_or_none(residual), ldr, dX.data_ptr(), lddx, code,
                                         offsets.data_ptr(), groups, rows, n, k, int(out is None), ws,

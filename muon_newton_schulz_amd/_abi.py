@@ -36,7 +36,7 @@ EXPORTS = (
     "mns_grouped_step_workspace_size", "muon_step_grouped",
     "mns_ns_backward_workspace_size", "ns_orthogonalize_backward",
     "grouped_linear", "grouped_input_grad",
-    "mns_grouped_bias_grad_workspace_size", "grouped_bias_grad",
+    "mns_grouped_layer_workspace_size", "mns_grouped_bias_grad_workspace_size", "grouped_bias_grad",
     "mns_expert_order_workspace_size", "expert_order",
     "mns_balance_workspace_size", "balance_loss",
     "mns_clip_workspace_size", "grad_norm", "clip_grad_norm",
@@ -168,6 +168,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.grouped_input_grad.restype = ci
     lib.grouped_input_grad.argtypes = [vp, i64, vp, ci, vp, i64, vp, i64, vp, i64, ci, vp, i64, i64,
                                        i64, i64, ci, vp, csz, vp]
+    lib.mns_grouped_layer_workspace_size.restype = ci
+    lib.mns_grouped_layer_workspace_size.argtypes = [ci, ci, i64, i64, i64, i64, sz]
     lib.mns_grouped_bias_grad_workspace_size.restype = ci
     lib.mns_grouped_bias_grad_workspace_size.argtypes = [i64, i64, i64, sz]
     lib.grouped_bias_grad.restype = ci

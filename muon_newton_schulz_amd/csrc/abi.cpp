@@ -946,6 +946,30 @@ mns_status mns_grouped_workspace_size(int weight_grad, int dtype, int64_t groups
   return MNS_OK;
 }
 
+mns_status mns_grouped_layer_workspace_size(int input_grad, int dtype, int64_t groups,
+                                            int64_t total_rows, int64_t n, int64_t k, size_t* bytes) {
+  if (!bytes) return MNS_ERR_NULL;
+  if (input_grad != 0 && input_grad != 1) return MNS_ERR_PARAM;
+  const mns_status st = check_grouped(dtype, groups, total_rows, n, k);
+  if (st != MNS_OK) return st;
+  *bytes = 0;
+  if (total_rows == 0) return MNS_OK;
+  GroupedDesc d;
+  d.store = d.out_store = store_of(dtype);
+  d.groups = groups;
+  d.total_rows = total_rows;
+  d.n = n;
+  d.k = k;
+  d.transpose_w = input_grad == 1;
+  d.layer = true;
+  for (int64_t pitch = 0; pitch < 2; ++pitch) {      // of operands on 16 bytes, and not
+    d.lda = pitch;
+    const size_t need = grouped_workspace(d);
+    if (need > *bytes) *bytes = need;
+  }
+  return MNS_OK;
+}
+
 mns_status grouped_matmul(const void* X, int64_t ldx, const void* W, void* Y, int64_t ldy,
                           int dtype, const int64_t* offsets, int64_t groups, int64_t total_rows,
                           int64_t n, int64_t k, int transpose_w, int fill_rest, void* workspace,

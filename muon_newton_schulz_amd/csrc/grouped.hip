@@ -17,6 +17,7 @@
 #include "mns_internal.h"
 #include "row_vectors.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace mns {
@@ -36,6 +37,7 @@ struct LayerArgs : GroupedArgs {
   void* Z;                      // the rows of C, pitch ldz: written (NT) or read (NN), or null
   int64_t ldr, ldz;
   int act;
+  int parts, part_tiles;        // k_grouped_split: parts of the reduction, tiles that have room for them
 };
 template <typename Args>
 constexpr bool kLayer = std::is_same_v<Args, LayerArgs>;
@@ -479,6 +481,26 @@ __global__ __launch_bounds__(256) void k_grouped(Args p) {
 // no barrier in the loop; the four sums are added in wave order through LDS. A fourth of the steps
 // of memory latency one after the other, and four times the blocks. Bound by those steps (1021 rows
 // over 5 experts of 513 x 1277, bfloat16, input gradient: 23 us).
+//
+// A layer's reduction that is still long for its few tiles is cut into `parts` more (split_parts), a block
+// each: their float32 sums go to p.partial and are added in part order by k_split_join.
+
+// A block's tile: false where there is none. part: of the reduction; slot: of p.partial's tiles (those
+// of no expert have none), always below part_tiles where the offsets do not overlap.
+template <typename Args>
+__device__ __forceinline__ bool split_place(const Args& p, int lin, Place& at, int& slot) {
+  constexpr int BM = 64;
+  if (!find_place(p, BM, p.tiles_n, p.fill_rest, walk_start(p, BM, p.tiles_n, p.fill_rest), lin, at))
+    return false;
+  slot = lin;
+  if constexpr (kLayer<Args>) {
+    if (p.fill_rest)
+      slot -= (clamp_row(p.offsets[0], 0, p.total_rows) + BM - 1) / BM * p.tiles_n;
+    return p.parts == 1 || at.expert < 0 || (slot >= 0 && slot < p.part_tiles);
+  }
+  return true;
+}
+
 template <typename T, int FORM, typename Args>
 __global__ __launch_bounds__(256) void k_grouped_split(Args p) {
   using F = Frag<T>;
@@ -489,18 +511,29 @@ __global__ __launch_bounds__(256) void k_grouped_split(Args p) {
   static_assert(sizeof(lds) >= 4 * 4 * 16 * 64 * sizeof(float), "the waves' sums fit");
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   Place at;
-  if (!find_place(p, BM, p.tiles_n, p.fill_rest, walk_start(p, BM, p.tiles_n, p.fill_rest),
-                  (int)blockIdx.x, at))
-    return;
+  int slot, part = 0;
+  int lin = (int)blockIdx.x;
+  if constexpr (kLayer<Args>) {
+    part = lin % p.parts;
+    lin /= p.parts;
+  }
+  if (!split_place(p, lin, at, slot)) return;
   const int m0 = at.lo + at.inside / p.tiles_n * BM, n0 = at.inside % p.tiles_n * BN;
   const int m_valid = at.hi - m0, n_valid = p.N - n0;
   if constexpr (kLayer<Args>) {
     if (at.expert < 0) {
-      zero_tile<T, FORM>(p, m0, n0, m_valid < BM ? m_valid : BM, n_valid < BN ? n_valid : BN);
+      if (part == 0)
+        zero_tile<T, FORM>(p, m0, n0, m_valid < BM ? m_valid : BM, n_valid < BN ? n_valid : BN);
       return;
     }
   }
   const int red = at.expert < 0 ? 0 : p.K;
+  int k_first = 0, k_end = red;                          // of this block's part, whole k-tiles
+  if constexpr (kLayer<Args>) {
+    const int tiles = (red + BK - 1) / BK;
+    k_first = tiles * part / p.parts * BK;
+    if (part + 1 < p.parts) k_end = tiles * (part + 1) / p.parts * BK;
+  }
   const T* A = static_cast<const T*>(p.A) + m0 * p.lda;
   const T* B = static_cast<const T*>(p.B) + (at.expert < 0 ? 0 : at.expert) * p.sB +
                (FORM == NT ? n0 * p.ldb : (int64_t)n0);
@@ -541,7 +574,10 @@ __global__ __launch_bounds__(256) void k_grouped_split(Args p) {
   // wave w finishes fragment (w / 2, w % 2)
   const int mi = 32 * (wave >> 1), nj = 32 * (wave & 1);
   FinishOf<Args, T, FORM, 1, 1> end(at.expert, m0, n0, mi, nj, m_valid, n_valid);
-  if constexpr (kLayer<Args>) end.load_first(p);
+  if constexpr (kLayer<Args>) {
+    if (p.parts == 1) end.load_first(p);
+  }
+  const bool two = m_valid > 32;                         // else the rows behind are not multiplied
   floatx16 acc[2][2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -552,15 +588,15 @@ __global__ __launch_bounds__(256) void k_grouped_split(Args p) {
   T* As = lds + wave * WAVE;
   T* Bs = As + BM * PITCH;
   u32x4 ra[NCH], rb[NCH];
-  int k0 = wave * BK;
-  if (k0 < red) {
+  int k0 = k_first + wave * BK;
+  if (k0 < k_end) {
     load(A, p.lda, false, m_valid, k0, a_end, ra);
     load(B, p.ldb, FORM != NT, n_valid, k0, b_end, rb);
   }
-  for (; k0 < red; k0 += 4 * BK) {
+  for (; k0 < k_end; k0 += 4 * BK) {
     store(As, false, k0, ra);
     store(Bs, FORM != NT, k0, rb);
-    if (k0 + 4 * BK < red) {
+    if (k0 + 4 * BK < k_end) {
       load(A, p.lda, false, m_valid, k0 + 4 * BK, a_end, ra);
       load(B, p.ldb, FORM != NT, n_valid, k0 + 4 * BK, b_end, rb);
     }
@@ -575,28 +611,73 @@ __global__ __launch_bounds__(256) void k_grouped_split(Args p) {
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
+        if (i == 0 || two) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) F::mma(acc[i][j], b[j], a[i]);
+          for (int j = 0; j < 2; ++j) F::mma(acc[i][j], b[j], a[i]);
+        }
     }
   }
   __syncthreads();
-  float(*part)[4][16][64] = reinterpret_cast<float(*)[4][16][64]>(lds);     // [wave][fragment]
+  float(*sums)[4][16][64] = reinterpret_cast<float(*)[4][16][64]>(lds);     // [wave][fragment]
 #pragma unroll
   for (int f = 0; f < 4; ++f)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) part[wave][f][e][lane] = acc[f >> 1][f & 1][e];
+    for (int e = 0; e < 16; ++e) sums[wave][f][e][lane] = acc[f >> 1][f & 1][e];
   __syncthreads();
   floatx16 sum[1][1];
 #pragma unroll
   for (int e = 0; e < 16; ++e)
-    sum[0][0][e] = part[0][wave][e][lane] + part[1][wave][e][lane] + part[2][wave][e][lane] +
-                   part[3][wave][e][lane];
+    sum[0][0][e] = sums[0][wave][e][lane] + sums[1][wave][e][lane] + sums[2][wave][e][lane] +
+                   sums[3][wave][e][lane];
   if constexpr (kLayer<Args>) {
+    if (p.parts > 1) {
+      if (mi >= m_valid || nj >= n_valid) return;        // a fragment without an element
+      float* out = p.partial + ((((int64_t)slot * p.parts + part) * 4 + wave) * 64 + lane) * 16;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        floatx4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = sum[0][0][4 * g + e];
+        reinterpret_cast<floatx4*>(out)[g] = v;
+      }
+      return;
+    }
     __syncthreads();                   // every wave has read the sums
     end.run(p, sum, reinterpret_cast<floatx4*>(lds) + wave * 256);
   } else {
     store_fragments<T, 1, 1, false>(p, sum, m0 * p.ldc + n0, mi, nj, m_valid, n_valid);
   }
+}
+
+// Adds a tile's parts in part order and finishes the layer: one block a tile, one fragment a wave.
+template <typename T, int FORM>
+__global__ __launch_bounds__(256) void k_split_join(LayerArgs p) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  Place at;
+  int slot;
+  if (!split_place(p, (int)blockIdx.x, at, slot) || at.expert < 0) return;
+  const int m0 = at.lo + at.inside / p.tiles_n * 64, n0 = at.inside % p.tiles_n * 64;
+  const int m_valid = at.hi - m0, n_valid = p.N - n0;
+  const int mi = 32 * (wave >> 1), nj = 32 * (wave & 1);
+  if (mi >= m_valid || nj >= n_valid) return;
+  Finish<T, FORM, 1, 1> end(at.expert, m0, n0, mi, nj, m_valid, n_valid);
+  end.load_first(p);
+  floatx16 sum[1][1];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) sum[0][0][e] = 0.f;
+  const floatx4* src =
+      reinterpret_cast<const floatx4*>(p.partial) + (((int64_t)slot * p.parts * 4 + wave) * 64 + lane) * 4;
+#pragma unroll 4
+  for (int part = 0; part < p.parts; ++part) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const floatx4 v = src[part * 1024 + g];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[0][0][4 * g + e] += v[e];
+    }
+  }
+  __shared__ floatx4 stage[4 * 256];
+  end.run(p, sum, stage + wave * 256);
 }
 
 // Few rows per expert (forward): the product is bound by reading the weights once, so the weights
@@ -1791,10 +1872,20 @@ hipError_t launch_grouped(const Args& a, int64_t blocks, hipStream_t s) {
 
 template <typename T, typename Args>
 hipError_t launch_split(const Args& a, bool transpose_w, int64_t blocks, hipStream_t s) {
-  const dim3 grid((unsigned)blocks), block(256);
+  const dim3 block(256);
+  dim3 grid((unsigned)blocks);
+  if constexpr (kLayer<Args>) grid.x *= (unsigned)a.parts;
   if (transpose_w) hipLaunchKernelGGL((k_grouped_split<T, NN, Args>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((k_grouped_split<T, NT, Args>), grid, block, 0, s, a);
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  if constexpr (kLayer<Args>) {
+    if (e != hipSuccess || a.parts == 1) return e;
+    grid.x = (unsigned)blocks;
+    if (transpose_w) hipLaunchKernelGGL((k_split_join<T, NN>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_split_join<T, NT>), grid, block, 0, s, a);
+    return hipGetLastError();
+  }
+  return e;
 }
 
 int64_t tiles_up(int64_t x, int64_t t) { return (x + t - 1) / t; }
@@ -1945,9 +2036,25 @@ hipError_t launch_rows(const Args& a, const Plan& p, int64_t blocks, hipStream_t
 int64_t grouped_blocks(const GroupedDesc& d) {
   const Plan p = plan_of(d);
   if (d.weight_grad) return d.groups * tiles_up(d.n, p.bm) * tiles_up(d.k, p.bn);
-  // every expert can end in a part tile, and so can the rows of no expert
-  return (tiles_up(d.total_rows, p.bm) + d.groups + 2) *
-         tiles_up(d.transpose_w ? d.k : d.n, p.bn);
+  // every expert with rows can end in a part tile, and so can the rows of no expert
+  const int64_t ends = p.kernel == Kernel::Big ? d.groups : std::min(d.groups, d.total_rows);
+  return (tiles_up(d.total_rows, p.bm) + ends + 2) * tiles_up(d.transpose_w ? d.k : d.n, p.bn);
+}
+
+// Most 64 x 64 tiles of rows that belong to an expert.
+static int64_t split_tiles(const GroupedDesc& d) {
+  return (std::min(d.groups, d.total_rows) + d.total_rows / 64) *
+         tiles_up(d.transpose_w ? d.k : d.n, 64);
+}
+
+// Parts of a layer's reduction on k_grouped_split: as many as fill the CUs' two blocks each, of at least 8
+// k-tiles (two a wave), where there are 32 or more.
+static int split_parts(const GroupedDesc& d) {
+  if (!d.layer || plan_of(d).kernel != Kernel::Split64) return 1;
+  const int64_t k_tiles = tiles_up(d.transpose_w ? d.n : d.k, d.store == Store::F32 ? 32 : 64);
+  if (k_tiles < 32) return 1;
+  const int64_t parts = std::min(2 * (int64_t)cu_count() / split_tiles(d), std::min<int64_t>(k_tiles / 8, 16));
+  return parts < 2 ? 1 : (int)parts;
 }
 
 template <typename TO, int FORM, int ACT>
@@ -2002,7 +2109,9 @@ static int split_cap(const GroupedDesc& d) {
 }
 
 size_t grouped_workspace(const GroupedDesc& d) {
-  return split_cap(d) > 1 ? size_t(256) * 256 * 256 * sizeof(float) : 0;
+  if (split_cap(d) > 1) return size_t(256) * 256 * 256 * sizeof(float);
+  const int parts = split_parts(d);
+  return parts > 1 ? (size_t)split_tiles(d) * parts * 64 * 64 * sizeof(float) : 0;
 }
 
 const char* grouped_name(const GroupedDesc& d) {
@@ -2094,6 +2203,8 @@ hipError_t grouped(const GroupedDesc& d, hipStream_t s) {
   layer.Z = d.Z;
   layer.ldz = d.ldz;
   layer.act = d.act;
+  layer.parts = split_parts(d);
+  layer.part_tiles = (int)split_tiles(d);
   return launch_rowwise(d, pl, layer, blocks, s);
 }
 

@@ -1,12 +1,15 @@
 """Layers of experts (product, bias, activation, residual), their input and bias gradients, against float64
 on the CPU, element by element with derived bounds (layer_ref), on every kernel and at the sizes where a
 tile, a chunk or a group ends."""
+import ctypes
+
 import pytest
 import torch
 
 import grouped_ref
 import layer_ref as ref
 import muon_newton_schulz_amd as mns
+from muon_newton_schulz_amd import _abi
 
 pytestmark = pytest.mark.gpu
 
@@ -73,6 +76,39 @@ WIDTHS = [(64, 128), (1, 1), (65, 33), (256, 320), (130, 72), (24, 520)]
 def test_routes_and_widths(route, dtype):
     for i, (n, k) in enumerate(WIDTHS):
         _both(*ROUTES[route], n, k, dtype, (ref.ACTS + [None])[(i + len(route)) % 5])
+
+
+# Few tiles with a long reduction: cut into parts over the blocks, then joined. (route, output width,
+# reduction, dtype); the forward takes this way beyond 96 rows an expert.
+PARTS = [
+    (([141], 0, 0), 70, 2100, BF), (([100, 130], 3, 70), 65, 1090, F32), (([300, 0, 200], 0, 1), 130, 2049, BF),
+    (([1], 0, 0), 1, 2050, BF), (([0, 1, 0], 2, 66), 33, 1025, F32), (([1] * 9 + [0] * 60, 1, 2), 40, 1030, F32),
+    (([64, 65, 32, 33], 0, 64), 64, 6500, BF), (([31, 97], 64, 0), 320, 6080, F32),
+]
+
+
+@pytest.mark.parametrize("i", range(len(PARTS)))
+def test_reduction_in_parts(i):
+    route, width, red, dtype = PARTS[i]
+    need = ctypes.c_size_t(0)
+    rows = sum(route[0]) + route[1] + route[2]
+    for back, n, k in ((1, red, width), (0, width, red)):
+        _abi.check(mns.load().mns_grouped_layer_workspace_size(
+            back, _abi.MNS_F32 if dtype == F32 else _abi.MNS_BF16, len(route[0]), rows, n, k,
+            ctypes.byref(need)), "size")
+        assert need.value > 0 or (not back and rows <= 96 * len(route[0]))
+        _both(*route, n, k, dtype, (ref.ACTS + [None])[i % 5], wscale=0.05)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_parts_with_overlapping_offsets_stay_inside(dtype):
+    """Every expert claims all rows: values unspecified, nothing outside the rows is written."""
+    rows, e, n, k = 90, 7, 4100, 70
+    off = torch.tensor([v for _ in range(4) for v in (0, rows)], dtype=torch.int64, device="cuda")
+    buf = torch.full((rows + 8, k + 3), 7.0, dtype=dtype, device="cuda")
+    mns.grouped_input_grad(_rand((rows, n), dtype, 1), _rand((e, n, k), dtype, 2), off,
+                           residual=_rand((rows, k), dtype, 3), out=buf[4:4 + rows, :k])
+    assert (buf[:4] == 7).all() and (buf[4 + rows:] == 7).all() and (buf[:, k:] == 7).all()
 
 
 # (sizes, front, tail), n, k, dtype, the kernels that take the forward and the input gradient; the first

@@ -278,6 +278,14 @@ def test_workspace_queries():
     assert lib.mns_expert_order_workspace_size(1 << 20, 8, ref) == 0 and out.value > 0
     assert lib.mns_balance_workspace_size(10, 4096, ref) == BAD_SHAPE
     assert lib.mns_clip_workspace_size(0, ref) == BAD_SHAPE
+    size = lib.mns_grouped_layer_workspace_size
+    assert size(0, _abi.MNS_BF16, 3, 12, 16, 24, ref) == 0 and out.value == 0
+    assert size(1, _abi.MNS_F32, 3, 12, 4096, 24, ref) == 0 and out.value > 0      # parts of a reduction
+    assert size(1, _abi.MNS_F32, 3, 0, 4096, 24, ref) == 0 and out.value == 0
+    assert size(2, _abi.MNS_F32, 3, 12, 16, 24, ref) == BAD_PARAM
+    assert size(0, 9, 3, 12, 16, 24, ref) == _abi.MNS_ERR_DTYPE
+    assert size(0, _abi.MNS_F32, 0, 12, 16, 24, ref) == BAD_SHAPE
+    assert size(0, _abi.MNS_F32, 3, 12, 16, 24, None) == BAD_NULL
     for query in (lambda: lib.mns_grouped_bias_grad_workspace_size(3, 100, 16, None),
                   lambda: lib.mns_expert_order_workspace_size(100, 8, None),
                   lambda: lib.mns_balance_workspace_size(10, 8, None),
