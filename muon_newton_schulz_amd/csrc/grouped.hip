@@ -309,20 +309,32 @@ __device__ __forceinline__ void store_lanes(const GroupedArgs& p, const floatx16
   }
 }
 
+// A k-major bfloat16 W whose rows do not all start on 4 bytes (an odd pitch: every other one) is read from
+// the element before, where that makes it so: loads between dwords take up to twice as long (input gradient,
+// 16384 rows over 8 experts of 2048 x 4097: 999 -> 653 us; 1021 over 5 of 513 x 1277: 22.4 -> 18.4; where all
+// rows start on 4 bytes it would cost 5 to 15 %, so the host chooses, FIX). As the elements go to LDS one by one, transposed, a
+// chunk read one column early is stored one column early; column -1 has a place of its own in front, and
+// the tile's last column is an element more a row.
+template <bool FIX, typename T>
+__device__ __forceinline__ int early(const T* at, const T* start) {
+  return FIX && (reinterpret_cast<uintptr_t>(at) & 2) && at > start ? 1 : 0;
+}
+
 // Any sizes, pitches and alignment of both types: 128 x 128 tiles, four waves of 64 x 64, k-tiles
 // of 128 bytes a row loaded into registers one tile ahead and stored to LDS as [row][k] (144-byte
 // rows: 16 rows' 16-byte reads cover the 64 banks once), a k-major operand transposed on the way.
 // With an addend, few rows: bound by HBM (384 rows over 16 experts of 2048 x 2048, float32 output: 105 us,
 // 5.1 TB/s); else by the loads' latency (one k-tile ahead is what two blocks a CU have registers
 // for; two ahead measured 10 to 60 % slower).
-template <typename T, typename TO, int FORM, typename Args>
+template <typename T, typename TO, int FORM, typename Args, bool FIX>
 __global__ __launch_bounds__(256) void k_grouped(Args p) {
   using F = Frag<T>;
   constexpr int BM = 128, BN = 128, VEC = F::VEC, BK = F::BK;
   constexpr int PITCH = BK + VEC;                        // 144 bytes
   constexpr int NCH = 4;                                 // chunks per thread and operand
   __shared__ __align__(16) T As[BM * PITCH];
-  __shared__ __align__(16) T Bs[BN * PITCH];
+  __shared__ __align__(16) T Bbuf[(BN + (FIX ? 1 : 0)) * PITCH];
+  T* const Bs = Bbuf + (FIX ? PITCH : 0);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int expert, lo, hi, m0, n0;
@@ -393,10 +405,22 @@ __global__ __launch_bounds__(256) void k_grouped(Args p) {
         const int u = q * 4 + wave;                     // 16 units of 16 k-rows x 4 chunks
         const int kr = (u % KW) * 16 + (lane & 15);
         const int col = ((u / KW) * 4 + (lane >> 4)) * VEC;
-        const int left = valid - col;
-        r[q] = load_piece_of_row(base + (int64_t)(k0 + kr) * ld + col, k0 + kr < red ? left : 0, end);
+        const T* at = base + (int64_t)(k0 + kr) * ld + col;
+        const int s = early<FIX>(at, static_cast<const T*>(p.B));
+        const int left = valid - col + s;
+        r[q] = load_piece_of_row(at - s, k0 + kr < red ? left : 0, end);
       }
     }
+  };
+  const T* last_at = B + (int64_t)tid * p.ldb + BN - 1;  // FIX: the last column of k-row tid
+  auto last_missing = [&](int k0) {
+    return tid < BK && early<FIX>(last_at + (int64_t)k0 * p.ldb - (BN - 1), (const T*)nullptr);
+  };
+  auto load_last = [&](int k0) {
+    return last_missing(k0) && k0 + tid < red && n_valid >= BN ? last_at[(int64_t)k0 * p.ldb] : (T)0.f;
+  };
+  auto store_last = [&](int k0, T last) {
+    if (last_missing(k0)) Bs[(BN - 1) * PITCH + tid] = last;
   };
   auto store = [&](T* dst, bool kmajor, int k0, const u32x4* r) {
 #pragma unroll
@@ -412,8 +436,10 @@ __global__ __launch_bounds__(256) void k_grouped(Args p) {
         const int col = ((u / KW) * 4 + (lane >> 4)) * VEC;
         T e[VEC];
         __builtin_memcpy(e, &r[q], 16);
+        T* at = dst + col * PITCH + kr;
+        if (FIX) at -= early<FIX>(B + (int64_t)(k0 + kr) * p.ldb + col, static_cast<const T*>(p.B)) * PITCH;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) dst[(col + i) * PITCH + kr] = e[i];
+        for (int i = 0; i < VEC; ++i) at[i * PITCH] = e[i];
       }
     }
   };
@@ -425,17 +451,21 @@ __global__ __launch_bounds__(256) void k_grouped(Args p) {
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+  T last = (T)0.f;
   if (red > 0) {
     load(A, p.lda, FORM == TN, m_valid, 0, a_end, ra);
     load(B, p.ldb, FORM != NT, n_valid, 0, b_end, rb);
+    if (FIX) last = load_last(0);
   }
   for (int k0 = 0; k0 < red; k0 += BK) {
     store(As, FORM == TN, k0, ra);
     store(Bs, FORM != NT, k0, rb);
+    if (FIX) store_last(k0, last);
     __syncthreads();
     if (k0 + BK < red) {
       load(A, p.lda, FORM == TN, m_valid, k0 + BK, a_end, ra);
       load(B, p.ldb, FORM != NT, n_valid, k0 + BK, b_end, rb);
+      if (FIX) last = load_last(k0 + BK);
     }
 #pragma unroll
     for (int s = 0; s < BK / (2 * VEC); ++s) {
@@ -501,12 +531,12 @@ __device__ __forceinline__ bool split_place(const Args& p, int lin, Place& at, i
   return true;
 }
 
-template <typename T, int FORM, typename Args>
+template <typename T, int FORM, typename Args, bool FIX>
 __global__ __launch_bounds__(256) void k_grouped_split(Args p) {
   using F = Frag<T>;
   constexpr int BM = 64, BN = 64, VEC = F::VEC, BK = F::BK, PITCH = BK + VEC;
   constexpr int NCH = 8;                                 // chunks per lane and operand
-  constexpr int WAVE = (BM + BN) * PITCH;                // elements of one wave's LDS
+  constexpr int WAVE = (BM + BN + (FIX ? 1 : 0)) * PITCH;   // elements of one wave's LDS
   __shared__ __align__(16) T lds[4 * WAVE];
   static_assert(sizeof(lds) >= 4 * 4 * 16 * 64 * sizeof(float), "the waves' sums fit");
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -549,10 +579,21 @@ __global__ __launch_bounds__(256) void k_grouped_split(Args p) {
       } else {
         constexpr int KW = BK / 16;
         const int kr = (q % KW) * 16 + (lane & 15), col = ((q / KW) * 4 + (lane >> 4)) * VEC;
-        r[q] = load_piece_of_row(base + (int64_t)(k0 + kr) * ld + col, k0 + kr < red ? valid - col : 0,
-                                 end);
+        const T* at = base + (int64_t)(k0 + kr) * ld + col;
+        const int s = early<FIX>(at, static_cast<const T*>(p.B));
+        r[q] = load_piece_of_row(at - s, k0 + kr < red ? valid - col + s : 0, end);
       }
     }
+  };
+  const T* last_at = B + (int64_t)lane * p.ldb + BN - 1; // FIX: the last column of k-row `lane`
+  auto last_missing = [&](int k0) {
+    return early<FIX>(last_at + (int64_t)k0 * p.ldb - (BN - 1), (const T*)nullptr);
+  };
+  auto load_last = [&](int k0) {
+    return last_missing(k0) && k0 + lane < red && n_valid >= BN ? last_at[(int64_t)k0 * p.ldb] : (T)0.f;
+  };
+  auto store_last = [&](T* dst, int k0, T last) {
+    if (last_missing(k0)) dst[(BN - 1) * PITCH + lane] = last;
   };
   auto store = [&](T* dst, bool kmajor, int k0, const u32x4* r) {
 #pragma unroll
@@ -566,11 +607,14 @@ __global__ __launch_bounds__(256) void k_grouped_split(Args p) {
         const int kr = (q % KW) * 16 + (lane & 15), col = ((q / KW) * 4 + (lane >> 4)) * VEC;
         T e[VEC];
         __builtin_memcpy(e, &r[q], 16);
+        T* at = dst + col * PITCH + kr;
+        if (FIX) at -= early<FIX>(B + (int64_t)(k0 + kr) * p.ldb + col, static_cast<const T*>(p.B)) * PITCH;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) dst[(col + i) * PITCH + kr] = e[i];
+        for (int i = 0; i < VEC; ++i) at[i * PITCH] = e[i];
       }
     }
   };
+  static_assert(!FIX || BK == 64, "a lane for each k-row");
   // wave w finishes fragment (w / 2, w % 2)
   const int mi = 32 * (wave >> 1), nj = 32 * (wave & 1);
   FinishOf<Args, T, FORM, 1, 1> end(at.expert, m0, n0, mi, nj, m_valid, n_valid);
@@ -586,19 +630,23 @@ __global__ __launch_bounds__(256) void k_grouped_split(Args p) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
   T* As = lds + wave * WAVE;
-  T* Bs = As + BM * PITCH;
+  T* Bs = As + (BM + (FIX ? 1 : 0)) * PITCH;
   u32x4 ra[NCH], rb[NCH];
+  T last = (T)0.f;
   int k0 = k_first + wave * BK;
   if (k0 < k_end) {
     load(A, p.lda, false, m_valid, k0, a_end, ra);
     load(B, p.ldb, FORM != NT, n_valid, k0, b_end, rb);
+    if (FIX) last = load_last(k0);
   }
   for (; k0 < k_end; k0 += 4 * BK) {
     store(As, false, k0, ra);
     store(Bs, FORM != NT, k0, rb);
+    if (FIX) store_last(Bs, k0, last);
     if (k0 + 4 * BK < k_end) {
       load(A, p.lda, false, m_valid, k0 + 4 * BK, a_end, ra);
       load(B, p.ldb, FORM != NT, n_valid, k0 + 4 * BK, b_end, rb);
+      if (FIX) last = load_last(k0 + 4 * BK);
     }
 #pragma unroll
     for (int s = 0; s < BK / (2 * VEC); ++s) {
@@ -1864,9 +1912,21 @@ __global__ __launch_bounds__(256) void k_grouped_ring(Args p) {
                                            n_valid);
 }
 
+// Whether rows of a bfloat16 W start between two dwords (early).
+bool between_dwords(const GroupedArgs& a) {
+  return (reinterpret_cast<uintptr_t>(a.B) & 2) || (a.ldb & 1);
+}
+
 template <typename T, typename TO, int FORM, typename Args>
 hipError_t launch_grouped(const Args& a, int64_t blocks, hipStream_t s) {
-  hipLaunchKernelGGL((k_grouped<T, TO, FORM, Args>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+  const dim3 grid((unsigned)blocks), block(256);
+  if constexpr (FORM == NN && sizeof(T) == 2) {
+    if (between_dwords(a)) {
+      hipLaunchKernelGGL((k_grouped<T, TO, FORM, Args, true>), grid, block, 0, s, a);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((k_grouped<T, TO, FORM, Args, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -1875,8 +1935,10 @@ hipError_t launch_split(const Args& a, bool transpose_w, int64_t blocks, hipStre
   const dim3 block(256);
   dim3 grid((unsigned)blocks);
   if constexpr (kLayer<Args>) grid.x *= (unsigned)a.parts;
-  if (transpose_w) hipLaunchKernelGGL((k_grouped_split<T, NN, Args>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((k_grouped_split<T, NT, Args>), grid, block, 0, s, a);
+  if (!transpose_w) hipLaunchKernelGGL((k_grouped_split<T, NT, Args, false>), grid, block, 0, s, a);
+  else if (sizeof(T) == 2 && between_dwords(a))
+    hipLaunchKernelGGL((k_grouped_split<T, NN, Args, sizeof(T) == 2>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_grouped_split<T, NN, Args, false>), grid, block, 0, s, a);
   const hipError_t e = hipGetLastError();
   if constexpr (kLayer<Args>) {
     if (e != hipSuccess || a.parts == 1) return e;

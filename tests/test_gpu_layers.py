@@ -78,6 +78,26 @@ def test_routes_and_widths(route, dtype):
         _both(*ROUTES[route], n, k, dtype, (ref.ACTS + [None])[(i + len(route)) % 5])
 
 
+@pytest.mark.parametrize("lead", [0, 1])
+@pytest.mark.parametrize("k", [1, 2, 63, 64, 65, 127, 128, 129, 255, 257])
+def test_weights_between_dwords(k, lead):
+    """An odd pitch, or weights that start between two dwords: the input gradient on both kernels that take
+    any alignment, next to the tiles' widths; nothing of the neighbours gets into a column."""
+    for sizes, n in (([20, 1], 70), ([20, 1], 2100), ([6200, 0, 5200], 70)):
+        bounds = grouped_ref.bounds_of(sizes, 1)
+        rows, e = bounds[-1] + 2, len(sizes)
+        buf = torch.full((lead + e * n * k + 9,), float("nan"), dtype=BF, device="cuda")
+        W = buf[lead:lead + e * n * k].view(e, n, k)
+        W.copy_(_rand((e, n, k), BF, 1))
+        dY, R = _rand((rows, n), BF, 2), _rand((rows, k), BF, 3)
+        print("case", sizes, n, k, lead, flush=True)
+        zero = torch.zeros(rows, k, dtype=BF)
+        got = mns.grouped_input_grad(dY, W, _offsets(bounds), residual=R)
+        check(got, *ref.input_grad(dY, W, bounds, None, None, R, zero), (n, k))
+        got = mns.grouped_matmul(dY, W, _offsets(bounds), transpose_w=True)
+        check(got, *grouped_ref.matmul(dY, W, bounds, True, zero), (n, k))
+
+
 # Few tiles with a long reduction: cut into parts over the blocks, then joined. (route, output width,
 # reduction, dtype); the forward takes this way beyond 96 rows an expert.
 PARTS = [
