@@ -824,18 +824,23 @@ def _tensor_list(grads, out, what: str):
         raise ValueError(f"{what}: out must hold as many tensors as grads")
     dev = grads[0].device
     index, codes, flat = dev.index, _STORAGE, []
-    for i, g in enumerate(grads):
-        o = outs[i]
+    for i, g in enumerate(grads):             # few reads a tensor: lists are long
         code = codes.get(g.dtype)
         if code is None:
             _dtype_code(g)
         if not g.is_contiguous():
             raise ValueError(f"{what}: gradient {i} must be contiguous")
-        if o is not g and (o.shape != g.shape or o.dtype != g.dtype or not o.is_contiguous()):
-            raise ValueError(f"{what}: out {i} must match its gradient and be contiguous")
-        if not g.is_cuda or g.get_device() != index or not o.is_cuda or o.get_device() != index:
+        if g.get_device() != index:           # -1 is not a GPU, whose index is None
             _on_one_gpu(grads + outs, what)
-        flat += (g.data_ptr(), o.data_ptr(), g.numel(), code)
+        at = to = g.data_ptr()
+        if outs is not grads and outs[i] is not g:
+            o = outs[i]
+            if o.shape != g.shape or o.dtype != g.dtype or not o.is_contiguous():
+                raise ValueError(f"{what}: out {i} must match its gradient and be contiguous")
+            if o.get_device() != index:
+                _on_one_gpu(grads + outs, what)
+            to = o.data_ptr()
+        flat += (at, to, g.numel(), code)
     return struct.pack("QQqi4x" * len(grads), *flat), len(grads), dev
 
 
