@@ -1964,6 +1964,12 @@ int cu_count() {
   return n;
 }
 
+// Most 64 x 64 tiles of rows that belong to an expert.
+int64_t split_tiles(const GroupedDesc& d) {
+  return (std::min(d.groups, d.total_rows) + d.total_rows / 64) *
+         tiles_up(d.transpose_w ? d.k : d.n, 64);
+}
+
 // Tile and kernel of a call, from its sizes alone.
 enum class Kernel { Tile128, Split64, Rows, Ring, Big };
 struct Plan {
@@ -2014,6 +2020,13 @@ bool dma_ok(const GroupedDesc& d) {
 //   512x1024: 14 of k_grouped_ring / 24, 1024x2048 30 / 32, 512x4096 37 / 30; four of 1024, 512x512
 //   13 / 16, of 300, 2048x512 13 / 16, of 2048, 1024x512, two rounds, 28 / 18; over 734 sizes of 1 to 8
 //   experts of 300 to 8192 rows 2 % from the faster of the two, k_grouped_big alone 23 %).
+//   A layer of few tiles of 64 x 64 and a long reduction: k_grouped_split in parts (split_parts), with
+//   operands for the DMA too. Its time over that of k_grouped_ring or k_grouped_big, split or not (252 sizes
+//   of 1 to 16 experts, means for up to 64 / 128 / 256 tiles): input gradients, reduction 1024 1.15 / 1.24 /
+//   1.38, 2048 0.79 / 0.87 / 1.08, 4032 0.82 / 0.90 / 1.06, 8192 0.85 / 1.01 / 1.11; forwards 0.84 / 1.02 / 1.19 (26
+//   rows an expert: 1.2), 0.68 / 0.85 / 1.02, 0.81 / 0.99 / 1.05, 0.95 / 1.20 / 1.19 (us: 7 experts, 1 row, input
+//   gradient of 4992 x 1152 16.6 / 24.2; 58, 909 rows, 2560 x 64 16.8 / 32.8; 3, 624 rows, forward of 192 x 3968
+//   20.1 / 24.2).
 //   What the DMA cannot take: k_grouped_rows up to 96 rows each (forward); k_grouped_split up to 160
 //   tiles of 128 x 128 (float32, 1021 rows over 5 experts of 513x1277: forward 36 against 103,
 //   input gradient 37 / 47; bfloat16 45 / 62 and 26 / 26; 200 tiles: 142 / 124, 51 / 38), else
@@ -2037,6 +2050,13 @@ Plan plan_of(const GroupedDesc& d) {
     const int64_t ring_tiles = (used + d.total_rows / 128) * tiles_up(out, bn);
     const bool few = !d.transpose_w && d.total_rows <= 24 * used;
     const bool many = d.total_rows > 256 * d.groups;
+    const bool middling = red <= 4096;
+    if (d.layer && !few && (d.transpose_w && middling ? 2 : 4) * split_tiles(d) <= cus &&
+        (d.transpose_w ? red >= 2048 : red >= 1536 && middling)) {
+      p.kernel = Kernel::Split64;
+      p.bm = p.bn = 64;
+      return p;
+    }
     if (many && red <= 2048) {
       const int64_t row_tiles = used + d.total_rows / 128;
       p.bn = out <= 64 || row_tiles * tiles_up(out, 64) <= cus ? 64 : 128;
@@ -2104,19 +2124,15 @@ int64_t grouped_blocks(const GroupedDesc& d) {
   return (tiles_up(d.total_rows, p.bm) + ends + 2) * tiles_up(d.transpose_w ? d.k : d.n, p.bn);
 }
 
-// Most 64 x 64 tiles of rows that belong to an expert.
-static int64_t split_tiles(const GroupedDesc& d) {
-  return (std::min(d.groups, d.total_rows) + d.total_rows / 64) *
-         tiles_up(d.transpose_w ? d.k : d.n, 64);
-}
-
-// Parts of a layer's reduction on k_grouped_split: as many as fill the CUs' two blocks each, of at least 8
-// k-tiles (two a wave), where there are 32 or more.
+// Parts of a layer's reduction on k_grouped_split: as many as fill the CUs' two blocks each, of at least 5
+// k-tiles, where there are 16 or more (input gradients, us, in parts / not: float32, 141 rows over 2 experts of
+// 6080 x 320 30.6 / 167, 65 of 640 x 320, 20 k-tiles, 14.9 / 23.5; bfloat16, 2 experts, 300 rows, 2500 x 1001
+// 22.2 / 37; parts of at least 4 and 8 k-tiles: 46 k-tiles 16.0 and 16.8, 56 20.1 and 18.3).
 static int split_parts(const GroupedDesc& d) {
   if (!d.layer || plan_of(d).kernel != Kernel::Split64) return 1;
   const int64_t k_tiles = tiles_up(d.transpose_w ? d.n : d.k, d.store == Store::F32 ? 32 : 64);
-  if (k_tiles < 32) return 1;
-  const int64_t parts = std::min(2 * (int64_t)cu_count() / split_tiles(d), std::min<int64_t>(k_tiles / 8, 16));
+  if (k_tiles < 16) return 1;
+  const int64_t parts = std::min(2 * (int64_t)cu_count() / split_tiles(d), std::min<int64_t>(k_tiles / 5, 16));
   return parts < 2 ? 1 : (int)parts;
 }
 

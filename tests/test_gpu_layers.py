@@ -104,6 +104,7 @@ PARTS = [
     (([141], 0, 0), 70, 2100, BF), (([100, 130], 3, 70), 65, 1090, F32), (([300, 0, 200], 0, 1), 130, 2049, BF),
     (([1], 0, 0), 1, 2050, BF), (([0, 1, 0], 2, 66), 33, 1025, F32), (([1] * 9 + [0] * 60, 1, 2), 40, 1030, F32),
     (([64, 65, 32, 33], 0, 64), 64, 6500, BF), (([31, 97], 64, 0), 320, 6080, F32),
+    (([120, 1, 0, 300], 3, 0), 200, 2048, BF), (([130], 0, 5), 64, 4096, BF), (([45] * 5, 1, 0), 72, 3968, BF),
 ]
 
 
