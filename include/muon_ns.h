@@ -380,7 +380,7 @@ mns_status grad_norm(const mns_tensor* tensors, int count, float* norm, void* wo
 /* grad_norm, then out = in * min(1, max_norm / (norm + eps)) for every tensor, the factor formed in
  * float64 and rounded to float32, the product rounded to the dtype. A NaN norm gives NaN, an infinite one
  * zeros (and NaN where the gradient is infinite). A tensor scaled in place by 1 is not written.
- * max_norm >= 0 (may be infinite), eps >= 0 and finite, else MNS_ERR_PARAM; so is an output that overlaps
+ * max_norm >= 0 (infinite: by 1, unless the norm is NaN), eps >= 0 and finite, else MNS_ERR_PARAM; so is an output that overlaps
  * another output, another tensor's input, or its own input without being it. */
 mns_status clip_grad_norm(const mns_tensor* tensors, int count, float max_norm, float eps, float* norm,
                           void* workspace, size_t workspace_bytes, void* stream);

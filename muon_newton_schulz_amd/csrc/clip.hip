@@ -157,8 +157,8 @@ __device__ __forceinline__ float clip_factor(const double* partial, int partials
 #pragma unroll 4
   for (int i = threadIdx.x; i < partials; i += kThreads) sum += partial[i];
   total = sqrt(block_sum(sum));
-  const double floor = total + (double)eps, ratio = (double)max_norm / floor;
-  return ratio >= 1. || floor == 0. ? 1.f : (float)ratio;       // a NaN stays one
+  const double floor = total + (double)eps;
+  return (double)max_norm >= floor ? 1.f : (float)((double)max_norm / floor);   // a NaN stays one
 }
 
 __global__ __launch_bounds__(kThreads) void k_grad_norm(const double* partial, int partials,

@@ -92,6 +92,14 @@ def test_nan_and_infinity():
     assert grads[0][4321].isnan() and (grads[1] == 0).all() and (grads[0][:4000] == 0).all()
 
 
+def test_no_limit_keeps_infinite_gradients():
+    g = [torch.randn(300, device="cuda"), torch.randn(5, 7, device="cuda").bfloat16()]
+    g[0][17] = float("inf")
+    want, out = [t.clone() for t in g], [torch.empty_like(t) for t in g]
+    assert mns.clip_grad_norm(g, float("inf"), out=out).item() == float("inf")
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
 def test_unaligned_pieces_and_neighbours():
     """Gradients that are slices of one buffer, at odd addresses: what lies between stays."""
     for dtype in (BF, F32):

@@ -502,3 +502,30 @@ def test_two_streams_at_once():
     for pair in outs:
         for got in pair:
             assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_parts_in_place_captured_and_on_two_streams(dtype):
+    rows, e, n, k = 150, 3, 2500, 130
+    W, off = _rand((e, n, k), dtype, 1, 0.1), _offsets([0, 40, 41, 150])
+    dY, Z = _rand((rows, n), dtype, 2), _rand((rows, k), dtype, 3)
+
+    def step(out=None, stream=None):
+        return mns.grouped_input_grad(dY, W, off, activation="gelu", Z=Z if out is None else out, out=out,
+                                      stream=stream)
+
+    want = step()
+    assert torch.equal(step(), want) and torch.equal(step(Z.clone()), want)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [step(stream=s) for _ in range(4) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for bounds in ([0, 0, 0, 150], [3, 60, 130, 140], [0, 150, 150, 150]):
+        off.copy_(_offsets(bounds))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, step()), bounds
