@@ -242,7 +242,15 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs p) {
     s = sum_of(s);
     const float inv = z == 0.f ? 0.f : 1.f / z;
     s *= inv;
-    if (use && l == 0) total += (double)a * (double)s;
+    // What s is off by, sum_e p_te (c_e - s): where the counts are nearly equal, c_e - s is as small as the
+    // rounding of s, and the gradient of a balanced router would be noise without it.
+    float rest = 0.f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rest += x[q][i] * (c[q][i] - s);
+    rest = sum_of(rest) * inv;
+    if (use && l == 0) total += (double)a * ((double)s + (double)rest);
     if (p.grad && in) {
       const float f = use ? factor * (float)a * inv : 0.f;
 #pragma unroll
@@ -250,7 +258,7 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs p) {
         const int col = (q * G + l) * 4;
         T out[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) out[i] = (T)(use ? f * x[q][i] * (c[q][i] - s) : 0.f);
+        for (int i = 0; i < 4; ++i) out[i] = (T)(use ? f * x[q][i] * (c[q][i] - s - rest) : 0.f);
         T* dst = static_cast<T*>(p.grad) + t * p.ldg + col;
         if (col + 4 <= p.E) {
           __builtin_memcpy(dst, out, sizeof(out));

@@ -127,6 +127,21 @@ def test_gradient_against_differences():
         assert abs(mine - diff) <= 80 * 2.0 ** -23 * size + 1e-8, (mine, diff)
 
 
+@pytest.mark.parametrize("tokens,experts", [(53, 8), (300, 256), (7, 1)])
+def test_equal_counts_leave_no_gradient(tokens, experts):
+    """Every token to every expert: c_e - sum_j c_j p_j is 0. c_e - s is exact for s near c_e, off from 0 by
+    d <= (E + 8) 2^-23 c (a sum of E terms and a quotient), and what is left of d once sum_j p_j d, off by as much
+    relative to it, is taken away is at most c ((E + 8) 2^-23)^2."""
+    g = torch.Generator().manual_seed(tokens)
+    ids = torch.arange(experts).repeat(tokens, 1).cuda()
+    logits = (3 * torch.randn(tokens, experts, generator=g)).cuda()
+    counts, _, _ = mns.expert_order(ids, experts)
+    loss, grad = mns.balance_loss(logits, ids, counts)
+    n = tokens * experts
+    assert grad.abs().max().item() <= experts / n ** 2 * experts * tokens * ((experts + 8) * 2.0 ** -23) ** 2
+    assert abs(loss.item() - 1.0) <= 2.0 ** -23
+
+
 def test_captured_replayed_and_on_two_streams():
     ids, logits, counts = _balance(9000, 4, 100, BF, "holes", 1.0)
     side = torch.cuda.Stream()
