@@ -7,31 +7,35 @@ namespace mns {
 enum Act { ACT_NONE = 0, ACT_RELU = 1, ACT_RELU2 = 2, ACT_GELU = 3, ACT_SILU = 4 };
 
 // gelu and its slope, z Phi(z) and Phi(z) + z phi(z), Phi the normal distribution's mass below z and phi
-// its density. EXACT (float32 storage): by float32's erfc. Else (bfloat16 storage, whose rounding is up to
-// 2^-8 of a value) by two approximations of Q(a) = Phi(-a), a = |z|, fitted here to the least largest
-// relative error, in about 14 and 22 instructions' time where float32's erfc takes several times that (an
-// epilogue has 256 x 256 values a block and little to hide them behind):
-//   log2 Q as a polynomial of degree 7 in a: 2e-4 of Q up to a = 5, 6e-4 up to 8, 8e-3 up to 13.3, where
-//   Q leaves float32's normal numbers (it falls on from there); gelu = max(z, 0) - a Q;
-//   Q e^(a^2 / 2) as one of degree 5 in t = 1 / (1 + 0.53 a / sqrt 2): 2.9e-5 of Q; the slope is 1 - S or S
-//   with S = e^(-a^2 / 2) (that - a / sqrt(2 pi)), so both terms share the exponential.
-// A NaN stays one.
+// its density. EXACT (float32 storage): by float32's erfc. Else (bfloat16 storage) by two approximations of
+// Q(a) = Phi(-a), a = |z|, fitted here to the least largest relative error, in about 15 and 24 instructions'
+// time where float32's erfc takes several times that (an epilogue has 256 x 256 values a block and little to
+// hide them behind):
+//   log2 Q as a polynomial of degree 8 in a: 1.5e-5 of Q up to a = 5, 2.1e-4 up to 8 and 2.8e-3, below half a
+//   bfloat16 step, up to 13.2, where Q leaves float32's normal numbers; gelu = max(z, 0) - a Q;
+//   Q e^(a^2 / 2) as one of degree 7 in t = 1 / (1 + 0.5 a / sqrt 2): 1.3e-6 of Q, and z^2 2^-24 for the
+//   exponential's rounded argument; the slope is 1 - S or S with S = e^(-a^2 / 2) (that - a / sqrt(2 pi)), so
+//   both terms share the exponential.
+// They are this close because what is rounded to bfloat16 from a value that is off by r falls on the other
+// side for about r 2^8 of the elements: with 2e-4 and 2.9e-5 of Q (one and two terms fewer) 1.5 and 0.9 % of
+// normally distributed elements did, now 0.1 % and less. A NaN stays one.
 template <bool EXACT>
 __device__ __forceinline__ float gelu(float z) {
   if constexpr (EXACT) {
     return 0.5f * z * erfcf(z * -0.70710678119f);
   } else {
-    const float a = fabsf(z);
-    float p = -5.3191501e-07f;
-    p = fmaf(p, a, 2.6550542e-05f);
-    p = fmaf(p, a, -5.5683139e-04f);
-    p = fmaf(p, a, 6.5194792e-03f);
-    p = fmaf(p, a, -4.8504496e-02f);
-    p = fmaf(p, a, -4.6561548e-01f);
-    p = fmaf(p, a, -1.1477230f);
-    p = fmaf(p, a, -1.0002828f);
-    // (Q = 0 long before a = 64, and an infinite a would make a NaN of it)
-    return fmaf(-fminf(a, 64.f), __builtin_amdgcn_exp2f(p), fmaxf(z, 0.f));
+    // Q is 0 from a = 15 on (2^-167), where the polynomial turns; a NaN passes through this minimum
+    const float a = __builtin_elementwise_minimum(fabsf(z), 15.f);
+    float p = 5.07311775e-08f;
+    p = fmaf(p, a, -2.83297572e-06f);
+    p = fmaf(p, a, 6.81215533e-05f);
+    p = fmaf(p, a, -9.40051919e-04f);
+    p = fmaf(p, a, 8.43972154e-03f);
+    p = fmaf(p, a, -5.36463074e-02f);
+    p = fmaf(p, a, -4.58936363e-01f);
+    p = fmaf(p, a, -1.15100300e+00f);
+    p = fmaf(p, a, -1.00002003e+00f);
+    return fmaf(-a, __builtin_amdgcn_exp2f(p), fmaxf(z, 0.f));
   }
 }
 
@@ -42,12 +46,14 @@ __device__ __forceinline__ float gelu_slope(float z) {
     return fmaf(z, density, 0.5f * erfcf(z * -0.70710678119f));
   } else {
     const float a = fabsf(z), e = __builtin_amdgcn_exp2f(z * z * -0.72134752044f);
-    const float t = __builtin_amdgcn_rcpf(fmaf(a, 0.53f * 0.70710678119f, 1.f));
-    float q = 0.5f * -0.18196194364f;
-    q = fmaf(q, t, 0.5f * 0.40301403400f);
-    q = fmaf(q, t, 0.5f * 0.16524518902f);
-    q = fmaf(q, t, 0.5f * 0.31580967563f);
-    q = fmaf(q, t, 0.5f * 0.29788199973f);
+    const float t = __builtin_amdgcn_rcpf(fmaf(a, 0.5f * 0.70710678119f, 1.f));
+    float q = 4.4651631266e-02f;
+    q = fmaf(q, t, -1.8030735850e-01f);
+    q = fmaf(q, t, 1.9733217359e-01f);
+    q = fmaf(q, t, 1.7013832927e-02f);
+    q = fmaf(q, t, 1.4147923887e-01f);
+    q = fmaf(q, t, 1.3865421712e-01f);
+    q = fmaf(q, t, 1.4117570221e-01f);
     const float s = e * fmaf(q, t, a * -0.39894228040f);
     return z >= 0.f ? 1.f - s : s;
   }
