@@ -1989,8 +1989,9 @@ bool dma_ok(const GroupedDesc& d) {
   if (d.store != Store::BF16 || !on16(d.A) || !on16(d.B) || d.lda % 8) return false;
   if (d.weight_grad) return d.ldb % 8 == 0 && d.n % 2 == 0 && d.k % 2 == 0;
   const int64_t red = d.transpose_w ? d.n : d.k;
-  // a layer's epilogue moves whole chunks
+  // a layer's epilogue moves whole chunks, and four bias elements a load, which must start on a dword
   if (d.layer && ((d.transpose_w ? d.k : d.n) % 8 || !on16(d.C) || !on16(d.R) || !on16(d.Z) ||
+                  (reinterpret_cast<uintptr_t>(d.bias) & 3) ||
                   d.ldc % 8 || (d.R && d.ldr % 8) || (d.Z && d.ldz % 8)))
     return false;
   return red % 64 == 0 && red >= 128 && d.k % 8 == 0 && (d.n * d.k) % 8 == 0 &&
