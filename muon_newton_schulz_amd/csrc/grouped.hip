@@ -1433,7 +1433,10 @@ __global__ __launch_bounds__(512) void k_grouped_big(Args p) {
                          ((int64_t)(cur.m_valid < BM ? cur.m_valid - 1 : BM - 1) * ld +
                           (cur.n_valid < BN ? cur.n_valid : BN)) * 2);
       };
-      // byte offsets, below 2^30 for a tile's rows (pitches are at most 2^21); a column past the end: 7 2^28
+      // Byte offsets, below 2^30 for a tile's rows (pitches are at most 2^21); a column past the end: 7 2^28.
+      // They are the lanes' as a whole, none in a scalar register: the check takes a scalar offset off the
+      // resource's end first, and that of a row past a part tile's last one lies beyond it (no borrow is
+      // specified).
       auto lane_at = [&](int64_t ld) { return in ? unsigned(r8 * (int)ld + 8 * c) * 2u : 0x70000000u; };
       auto row_at = [&](int64_t ld, int i, int q) {
         return unsigned((wm * 128 + 32 * i + 8 * q) * (int)ld + wn * 64) * 2u;
@@ -1442,7 +1445,7 @@ __global__ __launch_bounds__(512) void k_grouped_big(Args p) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           v[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                               rows_of(base, ld), lane_at(ld), row_at(ld, i, q), 0));
+                                               rows_of(base, ld), lane_at(ld) + row_at(ld, i, q), 0, 0));
       };
       auto into_stage = [&](const u32x4 (&v)[4]) {
 #pragma unroll
@@ -1481,6 +1484,8 @@ __global__ __launch_bounds__(512) void k_grouped_big(Args p) {
       // beside them too many to keep, so loaded for every 32 rows there (from L1).
       u32x2 bias[FN][4];
       auto load_bias = [&] {
+        unsigned at = 8 * (ln >> 5) + wn * 128;
+        asm volatile("" : "+v"(at));       // computed here, not kept (spills of silu with a residual 112 -> 76 bytes)
         const __amdgpu_buffer_rsrc_t r =
             make_rsrc(static_cast<const __bf16*>(p.bias) + (int64_t)cur.expert * p.N + cur.col,
                       p.bias ? (cur.n_valid < BN ? cur.n_valid : BN) * 2 : 0);
@@ -1489,7 +1494,7 @@ __global__ __launch_bounds__(512) void k_grouped_big(Args p) {
 #pragma unroll
           for (int g = 0; g < 4; ++g)
             bias[j][g] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(
-                                                       r, 8 * (ln >> 5), (wn * 64 + 32 * j + 8 * g) * 2, 0));
+                                                       r, at + (32 * j + 8 * g) * 2, 0, 0));
       };
       constexpr bool gate = FORM == NN && ACT != ACT_NONE;
       u32x4 ahead[4];

@@ -12,8 +12,8 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 constexpr int kChunks = 8;                  // 16-byte chunks of a 128-byte LDS row (one k-tile)
 constexpr int kBufferFlags = 0x00020000;    // buffer resource word 3: raw loads, gfx9 family
 
-// Loads are checked dword by dword against `bytes` (>= 0), the scalar offset counted: one that starts at or
-// past the end, or that the end falls inside of, reads as zero.
+// Loads are checked dword by dword against `bytes` (>= 0), the scalar offset (at most `bytes`) counted: one
+// that starts at or past the end, or that the end falls inside of, reads as zero.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
   const int n = bytes > 0x7FFFFFFFLL ? 0x7FFFFFFF : (int)bytes;
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, n, kBufferFlags);
