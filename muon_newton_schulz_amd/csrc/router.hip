@@ -209,19 +209,25 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane % G;
   constexpr int ROWS = 64 / G;                     // rows of a wave
   auto sum_of = [](auto v) { return over_lanes<G>(v, [](auto a, auto b) { return a + b; }); };
-  float c[Q][4];
-  double n = 0.;
+  double count[Q][4], n = 0.;
 #pragma unroll
   for (int q = 0; q < Q; ++q)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int e = (q * G + l) * 4 + i;
-      const int64_t v = e < p.E ? p.counts[e] : 0;
-      c[q][i] = (float)v;
-      n += (double)v;
+      count[q][i] = e < p.E ? (double)p.counts[e] : 0.;
+      n += count[q][i];
     }
 #pragma unroll
   for (int o = G / 2; o > 0; o >>= 1) n += __shfl_xor(n, o, G);
+  // From here on what a count is off the mean by: float32 keeps whole numbers up to 2^24 only, and where the
+  // counts are larger but nearly equal, their differences are what the gradient is made of.
+  const double mean = n / p.E;
+  float c[Q][4];
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[q][i] = (q * G + l) * 4 + i < p.E ? (float)(count[q][i] - mean) : 0.f;
   const float factor = n > 0. ? (float)((double)p.scale * p.E / (n * n)) : 0.f;
   double total = 0.;
   for (int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * ROWS; t0 < p.T;
@@ -259,15 +265,16 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs p) {
     s = sum_of(s);
     const float inv = z == 0.f ? 0.f : 1.f / z;
     s *= inv;
-    // What s is off by, sum_e p_te (c_e - s): where the counts are nearly equal, c_e - s is as small as the
-    // rounding of s, and the gradient of a balanced router would be noise without it.
+    // What s is off by, sum_e p_te (c_e - s): where one expert has nearly all of a token's probability, c_e - s
+    // is as small as the rounding of s.
     float rest = 0.f;
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
       for (int i = 0; i < 4; ++i) rest += x[q][i] * (c[q][i] - s);
     rest = sum_of(rest) * inv;
-    if (use && l == 0) total += (double)a * ((double)s + (double)rest);
+    // (an s of 0 / 0, a row without probabilities, is not the mean but nothing)
+    if (use && l == 0) total += (double)a * ((double)s + (double)rest + (z == 0.f ? 0. : mean));
     if (p.grad && in) {
       const float f = use ? factor * (float)a * inv : 0.f;
 #pragma unroll

@@ -1,0 +1,42 @@
+"""The balance loss where an expert has more assignments than float32 counts one by one (2^24)."""
+import pytest
+import torch
+
+import grouped_ref
+import muon_newton_schulz_amd as mns
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+ULP = 2.0 ** -23
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_counts_beyond_float32(dtype):
+    """Two experts of 2^24 + 1 and 2^24 + 4 assignments: c_e - s is +-3 times the other's probability. With the
+    counts' distances from their mean, +-1.5, a row's s is off by at most (10 + 2 |x - max|) 2^-23 of 1.5 and the
+    gradient by twice that, by as much of itself, and by its factor's roundings."""
+    c0, c1 = (1 << 24) + 1, (1 << 24) + 4
+    tokens = c0 + c1
+    ids = torch.zeros(tokens, 1, dtype=torch.int64, device="cuda")
+    ids[c0:] = 1
+    logits = torch.empty(tokens, 2, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    logits = logits.to(dtype)
+    counts, offsets, order = mns.expert_order(ids, 2)
+    assert counts.tolist() == [c0, c1] and offsets.tolist() == [0, c0, tokens]
+    assert torch.equal(order, torch.arange(tokens, device="cuda"))
+    loss, grad = mns.balance_loss(logits, ids, counts, scale=float(tokens) * 1000)
+    factor = 1000.0 * 2 / tokens
+    total = 0.0
+    for part, got in zip(logits.split(1 << 22), grad.split(1 << 22)):
+        x = part.double()
+        p = torch.softmax(x, 1)
+        far = (x[:, 0] - x[:, 1]).abs()[:, None]
+        diff = p.flip(1) * torch.tensor([float(c0 - c1), float(c1 - c0)], dtype=torch.float64, device="cuda")
+        want = factor * p * diff
+        err = factor * p * (4 * 1.5 * (10 + 2 * far) * ULP + diff.abs() * (16 + 2 * far) * ULP)
+        over = ((got.double() - want).abs() - grouped_ref.stored(want, err, dtype)).max().item()
+        assert over <= 0, over
+        total += float((p[:, 0] * c0 + p[:, 1] * c1).sum())
+    want = factor * total
+    assert abs(loss.item() - want) <= 2.0 ** -23 * want
