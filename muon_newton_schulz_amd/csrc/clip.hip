@@ -183,12 +183,14 @@ __global__ __launch_bounds__(kThreads) void k_grad_scale(Table a, const double* 
   } else {
     double total;
     f = clip_factor(partial, partials, max_norm, eps, total);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
+    if (block_place() == 0 && threadIdx.x == 0) *norm = (float)total;
   }
+  const int64_t piece = block_place();
+  if (piece >= a.pieces) return;
   Cursor c;
-  c.to(a, blockIdx.x);
+  c.to(a, piece);
   if (f == 1.f && c.in == c.out) return;
-  const int64_t at = (blockIdx.x - c.first) * (kPieceBytes / (c.f32 ? 4 : 2));
+  const int64_t at = (piece - c.first) * (kPieceBytes / (c.f32 ? 4 : 2));
   if (c.f32)
     scale_piece<float, STREAM>(static_cast<const float*>(c.in) + at, static_cast<float*>(c.out) + at,
                                c.numel - at, f);
@@ -251,7 +253,7 @@ hipError_t clip_grads(const ClipTensor* list, int count, bool scale, float max_n
   for (int i = 0; scale && i < count; i += kClipPack) {
     if (count > kClipPack) fill_table(a, list + i, count - i < kClipPack ? count - i : kClipPack);
     if (a.pieces == 0) continue;
-    const dim3 grid((unsigned)a.pieces);
+    const dim3 grid = grid_of(a.pieces);
     const float* given = few ? nullptr : factor;
     if (stream) hipLaunchKernelGGL(k_grad_scale<true>, grid, block, 0, s, a, partial, partials, max_norm, eps, norm, given);
     else hipLaunchKernelGGL(k_grad_scale<false>, grid, block, 0, s, a, partial, partials, max_norm, eps, norm, given);

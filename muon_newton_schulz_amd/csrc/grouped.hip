@@ -346,8 +346,9 @@ __global__ __launch_bounds__(256) void k_grouped(Args p) {
                               : static_cast<const T*>(p.B) + p.groups * p.sB;
   int m_valid;
   if constexpr (FORM == TN) {
-    const int per = (p.N + BM - 1) / BM * p.tiles_n, t = (int)(blockIdx.x % per);
-    expert = (int)(blockIdx.x / per);
+    const int per = (p.N + BM - 1) / BM * p.tiles_n, t = block_place() % per;
+    expert = block_place() / per;
+    if (expert >= p.groups) return;
     m0 = t / p.tiles_n * BM;
     n0 = t % p.tiles_n * BN;
     expert_rows(p, expert, lo, hi);
@@ -358,7 +359,7 @@ __global__ __launch_bounds__(256) void k_grouped(Args p) {
   } else {
     Place at;
     if (!find_place(p, BM, p.tiles_n, p.fill_rest, walk_start(p, BM, p.tiles_n, p.fill_rest),
-                    (int)blockIdx.x, at))
+                    block_place(), at))
       return;
     expert = at.expert;
     m0 = at.lo + at.inside / p.tiles_n * BM;
@@ -543,7 +544,7 @@ __global__ __launch_bounds__(256) void k_grouped_split(Args p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   Place at;
   int slot, part = 0;
-  int lin = (int)blockIdx.x;
+  int lin = block_place();
   if constexpr (kLayer<Args>) {
     part = lin % p.parts;
     lin /= p.parts;
@@ -704,7 +705,7 @@ __global__ __launch_bounds__(256) void k_split_join(LayerArgs p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   Place at;
   int slot;
-  if (!split_place(p, (int)blockIdx.x, at, slot) || at.expert < 0) return;
+  if (!split_place(p, block_place(), at, slot) || at.expert < 0) return;
   const int m0 = at.lo + at.inside / p.tiles_n * 64, n0 = at.inside % p.tiles_n * 64;
   const int m_valid = at.hi - m0, n_valid = p.N - n0;
   const int mi = 32 * (wave >> 1), nj = 32 * (wave & 1);
@@ -767,7 +768,7 @@ __global__ __launch_bounds__(256) void k_grouped_rows(Args p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   Place at;
   if (!find_place(p, BM, p.tiles_n, p.fill_rest, walk_start(p, BM, p.tiles_n, p.fill_rest),
-                    (int)blockIdx.x, at))
+                    block_place(), at))
       return;
   const int expert = at.expert;
   const int row0 = at.lo + at.inside / p.tiles_n * BM;
@@ -1775,7 +1776,7 @@ __global__ __launch_bounds__(256) void k_grouped_ring(Args p) {
 
   Place at;
   if (!find_place(p, BM, p.tiles_n, p.fill_rest, walk_start(p, BM, p.tiles_n, p.fill_rest),
-                  (int)blockIdx.x, at))
+                  block_place(), at))
     return;
   const int m0 = at.lo + at.inside / p.tiles_n * BM, n0 = at.inside % p.tiles_n * BN;
   const int m_valid = at.hi - m0, n_valid = p.N - n0;
@@ -1925,7 +1926,7 @@ bool between_dwords(const GroupedArgs& a) {
 
 template <typename T, typename TO, int FORM, typename Args>
 hipError_t launch_grouped(const Args& a, int64_t blocks, hipStream_t s) {
-  const dim3 grid((unsigned)blocks), block(256);
+  const dim3 grid = grid_of(blocks), block(256);
   if constexpr (FORM == NN && sizeof(T) == 2) {
     if (between_dwords(a)) {
       hipLaunchKernelGGL((k_grouped<T, TO, FORM, Args, true>), grid, block, 0, s, a);
@@ -1939,8 +1940,8 @@ hipError_t launch_grouped(const Args& a, int64_t blocks, hipStream_t s) {
 template <typename T, typename Args>
 hipError_t launch_split(const Args& a, bool transpose_w, int64_t blocks, hipStream_t s) {
   const dim3 block(256);
-  dim3 grid((unsigned)blocks);
-  if constexpr (kLayer<Args>) grid.x *= (unsigned)a.parts;
+  dim3 grid = grid_of(blocks);
+  if constexpr (kLayer<Args>) grid = grid_of(blocks * a.parts);
   if (!transpose_w) hipLaunchKernelGGL((k_grouped_split<T, NT, Args, false>), grid, block, 0, s, a);
   else if (sizeof(T) == 2 && between_dwords(a))
     hipLaunchKernelGGL((k_grouped_split<T, NN, Args, sizeof(T) == 2>), grid, block, 0, s, a);
@@ -1948,7 +1949,7 @@ hipError_t launch_split(const Args& a, bool transpose_w, int64_t blocks, hipStre
   const hipError_t e = hipGetLastError();
   if constexpr (kLayer<Args>) {
     if (e != hipSuccess || a.parts == 1) return e;
-    grid.x = (unsigned)blocks;
+    grid = grid_of(blocks);
     if (transpose_w) hipLaunchKernelGGL((k_split_join<T, NN>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((k_split_join<T, NT>), grid, block, 0, s, a);
     return hipGetLastError();
@@ -2103,7 +2104,7 @@ Plan plan_of(const GroupedDesc& d) {
 
 template <typename T, int MT, typename Args>
 hipError_t launch_rows(const Args& a, const Plan& p, int64_t blocks, hipStream_t s) {
-  const dim3 grid((unsigned)blocks), block(256);
+  const dim3 grid = grid_of(blocks), block(256);
   if (p.ntw == 4 && p.wk == 1)
     hipLaunchKernelGGL((k_grouped_rows<T, MT, 4, 1, Args>), grid, block, 0, s, a);
   else if (p.ntw == 4)
@@ -2227,7 +2228,7 @@ static hipError_t launch_rowwise(const GroupedDesc& d, const Plan& pl, const Arg
     return d.store == Store::F32 ? launch_split<float>(a, d.transpose_w, blocks, s)
                                  : launch_split<__bf16>(a, d.transpose_w, blocks, s);
   if (pl.kernel == Kernel::Ring) {
-    const dim3 grid((unsigned)blocks), block(256);
+    const dim3 grid = grid_of(blocks), block(256);
     if (d.transpose_w && pl.bn == 128)
       hipLaunchKernelGGL((k_grouped_ring<NN, 128, Args>), grid, block, 0, s, a);
     else if (d.transpose_w)

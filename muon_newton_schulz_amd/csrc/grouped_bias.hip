@@ -28,7 +28,7 @@ template <typename T, typename TO, bool STREAM>
 __global__ __launch_bounds__(256) void k_bias_grad(BiasArgs p) {
   const int tid = threadIdx.x, cg = tid & 31, rg = tid >> 5;
   Place at;
-  const int lin = (int)blockIdx.x;
+  const int lin = block_place();
   if (!find_place(p, p.chunk, p.tiles_n, p.fill_rest,
                   walk_start(p, p.chunk, p.tiles_n, p.fill_rest, 1), lin, at, 1))
     return;
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(256) void k_bias_grad(BiasArgs p) {
 // from L2: 9 us for 32 experts of 8192, 27 with one block of 256 threads that walks all chunks.
 template <typename TO>
 __global__ __launch_bounds__(1024) void k_bias_join(BiasArgs p) {
-  const int expert = (int)(blockIdx.x / p.tiles_n), column_tile = (int)(blockIdx.x % p.tiles_n);
+  const int expert = (int)blockIdx.x, column_tile = (int)blockIdx.y;
   int lo, hi;
   expert_rows(p, expert, lo, hi);
   if (hi - lo <= p.chunk) return;
@@ -178,14 +178,14 @@ hipError_t bias_grad(const BiasGradDesc& d, hipStream_t s) {
   a.db = d.db;
   a.act = d.act;
   a.chunk = chunk_rows(d.total_rows, d.n);
-  const dim3 grid((unsigned)blocks);
+  const dim3 grid = grid_of(blocks);
   const bool out32 = d.out_store == Store::F32;
   const double bytes = (double)d.total_rows * d.n * (d.store == Store::F32 ? 4 : 2) *
                        (1 + (d.Z ? 1 : 0) + (d.dZ ? 1 : 0));
   const hipError_t e = bytes > kStreamBytes ? launch_bias<true>(a, d.store, out32, grid, s)
                                             : launch_bias<false>(a, d.store, out32, grid, s);
   if (e != hipSuccess || d.total_rows <= a.chunk) return e;
-  const dim3 joins((unsigned)(d.groups * a.tiles_n));
+  const dim3 joins((unsigned)d.groups, (unsigned)a.tiles_n);
   if (out32) hipLaunchKernelGGL(k_bias_join<float>, joins, dim3(1024), 0, s, a);
   else hipLaunchKernelGGL(k_bias_join<__bf16>, joins, dim3(1024), 0, s, a);
   return hipGetLastError();

@@ -24,6 +24,17 @@ struct PtrPack {
   void* p[kMaxPack];
 };
 
+// A list of blocks as a grid, and a block's place in the list: the threads along x of a launch must stay
+// below 2^32, so rows of 2^21 blocks (the last row's end lies past the list's: the kernels check).
+constexpr int kGridRowLog = 21;
+inline dim3 grid_of(int64_t blocks) {
+  constexpr int64_t row = int64_t(1) << kGridRowLog;
+  return blocks <= row ? dim3((unsigned)blocks) : dim3((unsigned)row, (unsigned)((blocks + row - 1) / row));
+}
+__device__ __forceinline__ int block_place() {
+  return (int)(blockIdx.y << kGridRowLog | blockIdx.x);
+}
+
 // Every NS-side matrix in the workspace is zero-padded to multiples of this size, so the
 // GEMM kernels run on whole tiles with no bounds checks; zero padding is invariant under
 // every product and polynomial the iterations form.
