@@ -29,7 +29,8 @@
  *   - Errors: arguments are validated synchronously, before anything is enqueued, and
  *     reported as an mns_status; nothing is enqueued when a call returns an error other
  *     than MNS_ERR_HIP. MNS_ERR_HIP means a kernel launch failed (the stream may hold
- *     part of the call's work). No C++ exception crosses this boundary.
+ *     part of the call's work). No C++ exception crosses this boundary; a call whose lists find
+ *     no host memory returns MNS_ERR_PARAM.
  *   - Streams: every call is asynchronous on `stream` (a hipStream_t; NULL = the null
  *     stream). Nothing synchronises; the results are ready when the stream reaches them.
  *   - Graph capture: a call may be recorded into a HIP graph by capturing `stream` (it only

@@ -67,7 +67,13 @@ hipError_t timed(const char* name, double flops, double bytes, hipStream_t s, F&
   const hipError_t e = launch();
   (void)hipEventRecord(r.b, s);
   std::lock_guard<std::mutex> lk(g_prof_mu);
-  g_prof.push_back(r);
+  try {
+    g_prof.push_back(r);
+  } catch (...) {                          // no host memory: the session fails, the call does not
+    (void)hipEventDestroy(r.a);
+    (void)hipEventDestroy(r.b);
+    g_prof_failed = true;
+  }
   return e;
 }
 
@@ -427,14 +433,14 @@ int64_t k_rows(double f, int64_t rows) {
   return k;
 }
 
-// Shape groups: matrices of equal (rows, cols), in order of first appearance.
+// Shape groups: matrices of equal (rows, cols), in order of first appearance. False where the host has no
+// memory for them.
 struct Group {
   int64_t rows, cols;
   std::vector<int> idx;
 };
 
-std::vector<Group> group_by_shape(const mns_matrix* mats, int count) {
-  std::vector<Group> gs;
+bool group_by_shape(const mns_matrix* mats, int count, std::vector<Group>& gs) try {
   for (int i = 0; i < count; ++i) {
     bool found = false;
     for (auto& g : gs)
@@ -445,7 +451,9 @@ std::vector<Group> group_by_shape(const mns_matrix* mats, int count) {
       }
     if (!found) gs.push_back(Group{mats[i].rows, mats[i].cols, {i}});
   }
-  return gs;
+  return true;
+} catch (...) {
+  return false;
 }
 
 mns_status validate_step(const mns_matrix* mats, int count, const mns_hparams* hp,
@@ -511,11 +519,11 @@ size_t carve_step(void* base, const Geo& g, int count, int64_t rows, int64_t col
   return cv.off + 256;
 }
 
-size_t step_bytes(const mns_matrix* mats, int count, const mns_hparams* hp) {
+size_t step_bytes(const std::vector<Group>& groups, const mns_hparams* hp) {
   const Store st = hp->dtype == MNS_BF16 ? Store::BF16 : Store::F32;
   const bool dion = hp->row_fraction < 1.0;
   size_t need = 0;
-  for (const Group& gr : group_by_shape(mats, count)) {
+  for (const Group& gr : groups) {
     const int c = (int)gr.idx.size() < kChunk ? (int)gr.idx.size() : kChunk;
     const int64_t k = dion ? k_rows(hp->row_fraction, gr.rows) : gr.rows;
     const Geo g = make_geo(k, gr.cols, st);
@@ -616,7 +624,9 @@ mns_status mns_step_workspace_size(const mns_matrix* mats, int count, const mns_
   if (!bytes) return MNS_ERR_NULL;
   const mns_status st = validate_step(mats, count, hp, false);
   if (st != MNS_OK) return st;
-  *bytes = step_bytes(mats, count, hp);
+  std::vector<Group> groups;
+  if (!group_by_shape(mats, count, groups)) return MNS_ERR_PARAM;
+  *bytes = step_bytes(groups, hp);
   return MNS_OK;
 }
 
@@ -624,13 +634,15 @@ mns_status muon_step(const mns_matrix* mats, int count, const mns_hparams* hp, v
                      size_t workspace_bytes, void* stream) {
   mns_status st = validate_step(mats, count, hp, true);
   if (st != MNS_OK) return st;
-  st = check_ws(workspace, workspace_bytes, step_bytes(mats, count, hp));
+  std::vector<Group> groups;
+  if (!group_by_shape(mats, count, groups)) return MNS_ERR_PARAM;
+  st = check_ws(workspace, workspace_bytes, step_bytes(groups, hp));
   if (st != MNS_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const Store sto = hp->dtype == MNS_BF16 ? Store::BF16 : Store::F32;
   const bool dion = hp->row_fraction < 1.0;
 
-  for (const Group& gr : group_by_shape(mats, count)) {
+  for (const Group& gr : groups) {
     const int64_t rows = gr.rows, cols = gr.cols;
     const int64_t k = dion ? k_rows(hp->row_fraction, rows) : rows;
     const Geo g = make_geo(k, cols, sto);      // the matrix NS runs on: k x cols
@@ -1330,7 +1342,7 @@ static mns_status run_clip(const mns_tensor* tensors, int count, bool scale, flo
   std::vector<Range> outs;
   try {
     list.resize(count);
-    outs.reserve(count);
+    outs.reserve(count + 1);               // and the norm
   } catch (...) {
     return MNS_ERR_PARAM;
   }
@@ -2016,7 +2028,12 @@ mns_status mns_profile_end(mns_kernel_stat* out, int capacity, int* count) {
     if (!st) {
       mns_kernel_stat z = {};
       std::strncpy(z.name, r.name, sizeof(z.name) - 1);
-      stats.push_back(z);
+      try {
+        stats.push_back(z);
+      } catch (...) {
+        ok = false;
+        continue;
+      }
       st = &stats.back();
     }
     st->launches += 1;
