@@ -46,6 +46,14 @@ __global__ __launch_bounds__(1024) void k_count(OrderArgs p) {
     p.hist[(int64_t)blockIdx.x * (p.E + 1) + e] = bins[e];
 }
 
+// What some lanes of a wave wrote to LDS before is what its other lanes read behind it: the LDS takes a
+// wave's accesses in order, and the compiler moves none across. No instruction.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // WAVES waves, whose counters for up to MOST experts fit the LDS: 16 for up to 512 (8192 assignments of 32
 // experts in one block 9.0 us, with 4 waves 22.6), 4 beyond.
 template <int WAVES, int MOST>
@@ -139,12 +147,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_order(OrderArgs p) {
       const unsigned long long set = __ballot((bin & bit) != 0);
       same &= (bin & bit) ? set : ~set;
     }
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    const int place = in ? cursor[wave][bin] : 0;
+    wave_order();
     if (in) {
-      const int rank = __popcll(same & ((1ull << lane) - 1));
-      const int place = cursor[wave][bin];
       p.order[place + rank] = i;
       if (rank == 0) cursor[wave][bin] = place + __popcll(same);
     }
+    wave_order();
   }
 }
 

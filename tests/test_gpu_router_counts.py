@@ -1,8 +1,10 @@
-"""The balance loss where an expert has more assignments than float32 counts one by one (2^24)."""
+"""Counts: the balance loss where an expert has more assignments than float32 counts one by one (2^24), and the
+order where a wave's steps find the place that the step before left."""
 import pytest
 import torch
 
 import grouped_ref
+import layer_ref
 import muon_newton_schulz_amd as mns
 
 pytestmark = pytest.mark.gpu
@@ -40,3 +42,16 @@ def test_counts_beyond_float32(dtype):
         total += float((p[:, 0] * c0 + p[:, 1] * c1).sum())
     want = factor * total
     assert abs(loss.item() - want) <= 2.0 ** -23 * want
+
+
+@pytest.mark.parametrize("experts", [3, 512, 513, 2048])
+@pytest.mark.parametrize("run", [1, 2, 63, 64, 65, 200])
+def test_order_of_runs(run, experts):
+    """Runs of one expert, and of two in turn, across a wave's steps of 64: every step's first place is the one that
+    another lane of the wave wrote a step before."""
+    m = 20011
+    i = torch.arange(m)
+    for ids in ((i // run) % experts, ((i // run) + (i & 1)) % experts, (i // run) % (experts + 1) - 1):
+        got = mns.expert_order(ids.cuda(), experts)
+        for name, g, w in zip(("counts", "offsets", "order"), got, layer_ref.order(ids, experts)):
+            assert torch.equal(g.cpu(), w), (name, run, experts)
