@@ -95,7 +95,8 @@ __global__ __launch_bounds__(256) void k_bias_grad(BiasArgs p) {
 // from L2: 9 us for 32 experts of 8192, 27 with one block of 256 threads that walks all chunks.
 template <typename TO>
 __global__ __launch_bounds__(1024) void k_bias_join(BiasArgs p) {
-  const int expert = (int)blockIdx.x, column_tile = (int)blockIdx.y;
+  const int expert = block_place() / p.tiles_n, column_tile = block_place() % p.tiles_n;
+  if (expert >= p.groups) return;
   int lo, hi;
   expert_rows(p, expert, lo, hi);
   if (hi - lo <= p.chunk) return;
@@ -185,7 +186,7 @@ hipError_t bias_grad(const BiasGradDesc& d, hipStream_t s) {
   const hipError_t e = bytes > kStreamBytes ? launch_bias<true>(a, d.store, out32, grid, s)
                                             : launch_bias<false>(a, d.store, out32, grid, s);
   if (e != hipSuccess || d.total_rows <= a.chunk) return e;
-  const dim3 joins((unsigned)d.groups, (unsigned)a.tiles_n);
+  const dim3 joins = grid_of(d.groups * a.tiles_n);
   if (out32) hipLaunchKernelGGL(k_bias_join<float>, joins, dim3(1024), 0, s, a);
   else hipLaunchKernelGGL(k_bias_join<__bf16>, joins, dim3(1024), 0, s, a);
   return hipGetLastError();
