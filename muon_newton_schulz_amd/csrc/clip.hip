@@ -9,9 +9,9 @@
 // Few pieces (kFewPieces): every block of the scaling adds the partial sums itself, which takes less than a
 // launch in between (four tensors, us, and with that launch: 64 KB 5.0, 6.3; 6.5 MB 6.0, 7.1; 24 MB 7.8, 8.4;
 // 32 MB 10.0, 9.9). More: a launch of one block adds them, and each block of the scaling takes one piece
-// (1.5 GB, out of place: 470 us; blocks that go from piece to piece 510 to 525). Lists beyond the 256 MB
-// last-level cache are read and written with non-temporal accesses (the norm 260 us instead of 300, the
-// scaling 470 instead of 517); smaller ones stay in the caches for the step that follows. Walking the
+// (1.5 GB, out of place: 490 us; blocks that go from piece to piece 8 to 11 % longer). Lists beyond the 256 MB
+// last-level cache are read and written with non-temporal accesses (1.5 GB: the norm 224 us, the scaling 490; with
+// ordinary ones 15 and 10 % longer); smaller ones stay in the caches for the step that follows. Walking the
 // pieces backwards, so that those read last are found in the caches, gained nothing.
 #include "mns_internal.h"
 #include "row_vectors.h"

@@ -119,15 +119,7 @@ __device__ __forceinline__ void store_fragments(const GroupedArgs& p, const floa
 }
 
 // ---- the epilogue of a layer ------------------------------------------------------------------
-//
-// A wave's fragments go through 4 KB of LDS of its own, 32 rows x 32 columns or 16 x 64 of float32 at a
-// time, so that a lane holds eight consecutive columns of a row: the addends and outputs then move as
-// whole pieces of 16 bytes, 128-byte lines of bfloat16, and one copy of the activation's code serves
-// all fragments of a row. Used by every grouped kernel but the one of 256 x 256 tiles. Latency of the
-// operands' loads is what it adds (613 rows, 9 experts of 777 x 331, float32, Z kept, a residual: 14.7 us,
-// the product alone 13.3; 1021 rows, 5 of 513 x 1277, silu, a residual: 20.5 and 18.4), so they are loaded a
-// step ahead (without: 1 and 2 us more). Everything is float32 until the output's one rounding; act sees the sum, not
-// Z as it is kept (the gradient then is that of the rounded Z, up to 2^-8 of it away).
+
 // Zeros over a tile of rows that belong to no expert (m_rows x n_cols of it, threads of one block).
 template <typename T, int FORM>
 __device__ __forceinline__ void zero_tile(const LayerArgs& p, int64_t row, int col, int m_rows,
@@ -139,6 +131,16 @@ __device__ __forceinline__ void zero_tile(const LayerArgs& p, int64_t row, int c
   }
 }
 
+// A wave's fragments go through 4 KB of LDS of its own, 32 rows x 32 columns or 16 x 64 of float32 at a
+// time, so that a lane holds eight consecutive columns of a row: the addends and outputs then move as
+// whole pieces of 16 bytes, 128-byte lines of bfloat16, and one copy of the activation's code serves
+// all fragments of a row. Used by every grouped kernel but those of 256 x 256 tiles (layer_rows) and of few
+// rows (k_grouped_rows, whose fragments lie four columns a lane as they are). Latency of the operands'
+// loads is what it adds (1021 rows, 5 experts of 513 x 1277, silu, a residual: 20.3 us, the product alone
+// 18.4), so they are loaded a step ahead (without: 2 us more). Everything is float32 until the output's one
+// rounding; act sees the sum, not Z as it is kept (the gradient then is that of the rounded Z, up to 2^-8 of it
+// away).
+//
 // The epilogue of a wave's FM x FN fragments (as in store_fragments) at rows m0, columns n0 of the tile
 // that starts at row `row`, column `col`, in FM * FN steps. load() takes a step's operands; a step's are
 // loaded before the one before it is finished, the first ones by the caller where its registers allow
@@ -1411,9 +1413,10 @@ __global__ __launch_bounds__(512) void k_grouped_big(Args p) {
   // written, and the number of accesses in flight is known (kStores). Which operands there are and the
   // activation are compile-time (as runtime branches the accumulators spill, up to 500 bytes a lane).
   // Bound by its vector instructions, about 4 us a pass over the 16384 x 8192 elements an instruction:
-  // both waves of a SIMD come to it together, so the matrix units wait. 32 experts of 8192 x 1024, us,
-  // hot: forward, product 313, bias 289, + relu 291, silu 310, gelu 328, + Z kept 357; input gradient,
-  // product 300, none 293, relu 328 (Z's 268 MB), silu 346, gelu 378.
+  // both waves of a SIMD come to it together, so the matrix units wait. 16384 rows, 32 experts of
+  // 8192 x 1024, us, one after the other in one process: forward, product 287, bias 288, + relu 294, silu 308,
+  // gelu 329, + Z kept 368; with a residual relu 339, silu 360, gelu 380; input gradient, product 297,
+  // none 293, relu 332 (Z's 268 MB), silu 351, gelu 381, with a residual 412.
   auto layer_rows = [&](int b) {
     if constexpr (kLayer<Args>) {
       int ln = lane;
