@@ -15,8 +15,8 @@ ULP = 2.0 ** -23
 
 @pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
 def test_counts_beyond_float32(dtype):
-    """Two experts of 2^24 + 1 and 2^24 + 4 assignments: c_e - s is +-3 times the other's probability. With the
-    counts' distances from their mean, +-1.5, a row's s is off by at most (10 + 2 |x - max|) 2^-23 of 1.5 and the
+    """Two experts of 2^24 + 1 and 2^24 + 4 assignments: c_e - s is +-3 times the other's probability. With what the
+    counts exceed the least one by, 0 and 3, a row's s is off by at most (10 + 2 |x - max|) 2^-23 of 3 and the
     gradient by twice that, by as much of itself, and by its factor's roundings."""
     c0, c1 = (1 << 24) + 1, (1 << 24) + 4
     tokens = c0 + c1
@@ -36,7 +36,7 @@ def test_counts_beyond_float32(dtype):
         far = (x[:, 0] - x[:, 1]).abs()[:, None]
         diff = p.flip(1) * torch.tensor([float(c0 - c1), float(c1 - c0)], dtype=torch.float64, device="cuda")
         want = factor * p * diff
-        err = factor * p * (4 * 1.5 * (10 + 2 * far) * ULP + diff.abs() * (16 + 2 * far) * ULP)
+        err = factor * p * (2 * 3 * (10 + 2 * far) * ULP + diff.abs() * (16 + 2 * far) * ULP)
         over = ((got.double() - want).abs() - grouped_ref.stored(want, err, dtype)).max().item()
         assert over <= 0, over
         total += float((p[:, 0] * c0 + p[:, 1] * c1).sum())
@@ -55,3 +55,20 @@ def test_order_of_runs(run, experts):
         got = mns.expert_order(ids.cuda(), experts)
         for name, g, w in zip(("counts", "offsets", "order"), got, layer_ref.order(ids, experts)):
             assert torch.equal(g.cpu(), w), (name, run, experts)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("tokens,experts", [(300, 4), (5000, 100)])
+def test_loss_of_probabilities_on_unassigned_experts(tokens, experts, dtype):
+    """Every token's probability lies on an expert without assignments, all but e^-20 of it: the loss is what is left,
+    and as exact as any (layer_ref's bound is relative to sum_e c_e p_te)."""
+    g = torch.Generator().manual_seed(experts)
+    logits = torch.randn(tokens, experts, generator=g)
+    logits[:, 0] = 20
+    logits = logits.to(dtype).cuda()
+    ids = torch.randint(1, experts, (tokens, 2), generator=g).cuda()
+    counts, _, _ = mns.expert_order(ids, experts)
+    loss, grad = mns.balance_loss(logits, ids, counts)
+    want, el, wg, eg = layer_ref.balance(logits, ids, counts, 1.0)
+    assert abs(loss.item() - want.item()) <= el.item(), (loss.item(), want.item(), el.item())
+    grouped_ref.check(grad, wg, eg, (tokens, experts))
