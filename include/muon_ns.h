@@ -277,8 +277,9 @@ mns_status grouped_weight_grad(const void* dY, int64_t lddy, const void* X, int6
  * above; a plain layer is a stack of one. Everything between the product and the output's one rounding
  * is float32. gelu and its slope are float32's erfc for MNS_F32; for MNS_BF16 they are fits, whatever the
  * output's type: z Phi(z) is off by up to 1.5e-5 |z| Phi(-|z|) for |z| <= 5, 2.1e-4 of it up to 8, 2.8e-3 of it
- * beyond, the slope by up to (2e-6 + z^2 2^-23) (Phi(-|z|) + |z| phi(z)). Rows of no expert are left as they are, or with fill_rest written as zeros, in every
- * row-wise output. NaN and infinities stay in their rows (bias: in their expert). */
+ * beyond, the slope by up to (2e-6 + z^2 2^-23) (Phi(-|z|) + |z| phi(z)), terms below 2^-126 as zeros.
+ * Rows of no expert are left as they are, or with fill_rest written as zeros, in every row-wise output.
+ * NaN and infinities stay in their rows (bias: in their expert). */
 
 /* Workspace bytes of grouped_linear (input_grad = 0) or grouped_input_grad (1). */
 mns_status mns_grouped_layer_workspace_size(int input_grad, int dtype, int64_t groups,
